@@ -44,6 +44,13 @@ class _SwaRingC(ctypes.Structure):
                 ("d", ctypes.c_int32), ("window", ctypes.c_int32), ("pos", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
+class _PagedKVC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("rope_base", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libyoco.so not found at {LIB_PATH}; build it with "
@@ -52,6 +59,7 @@ def _load():
     vp, i, f, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
     cp = ctypes.POINTER(_KVCacheC)
     rp = ctypes.POINTER(_SwaRingC)
+    pp = ctypes.POINTER(_PagedKVC)
     sigs = {
         "yoco_gret_prefill_chunkwise": (i, [vp, vp, vp, vp, f, vp, vp, i, i, i, i, i, i, i, i, vp, sz, vp]),
         "yoco_gret_prefill_workspace_size": (sz, [i, i, i, i, i, i, i]),
@@ -81,6 +89,10 @@ def _load():
         "yoco_gret_prefill_chunkwise_gn_gate": (i, [vp, vp, vp, vp, f, vp, vp, vp, f, vp, vp, i, i, i, i, i, i, vp, sz,
                                                     vp]),
         "yoco_selftest_occupy_sms": (i, [i, ctypes.c_uint64, vp]),
+        "yoco_paged_append": (i, [vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i, vp, i, pp, vp, sz, vp]),
+        "yoco_paged_attn_prefill": (i, [vp, i, vp, i, pp, f, i, i, vp, vp, sz, vp]),
+        "yoco_paged_attn_decode": (i, [vp, i, pp, f, i, i, vp, vp, sz, vp]),
+        "yoco_paged_attn_workspace_size": (sz, [i, i, pp]),
         "yoco_debug_checks": (i, [i, ctypes.POINTER(ctypes.c_uint32)]),
     }
     for name, (res, args) in sigs.items():
@@ -99,7 +111,8 @@ EXPORTED = ("yoco_gret_prefill_chunkwise", "yoco_gret_prefill_workspace_size", "
             "yoco_swa_prefill", "yoco_swa_decode", "yoco_swa_workspace_size", "yoco_gret_group_norm_gate",
             "yoco_rope_apply", "yoco_gret_qkvg_project", "yoco_gret_qkvg_workspace_size",
             "yoco_gret_decode_step_gn_gate", "yoco_cross_attn_decode_noalloc_status", "yoco_test_hook",
-            "yoco_selftest_occupy_sms", "yoco_gret_prefill_chunkwise_gn_gate", "yoco_debug_checks")
+            "yoco_selftest_occupy_sms", "yoco_gret_prefill_chunkwise_gn_gate", "yoco_debug_checks", "yoco_paged_append",
+            "yoco_paged_attn_prefill", "yoco_paged_attn_decode", "yoco_paged_attn_workspace_size")
 YOCO_HOOK_FAIL_NEXT_CALLS, YOCO_HOOK_GRET_SEG0_DELAY_NS, YOCO_HOOK_GRET_SEGMENTS = 1, 2, 3
 
 
@@ -386,3 +399,122 @@ def yoco_gret_qkvg_project(X, W, H, q, k, v, gate_logits, rope_base=0.0, pos0=0,
                                     _ptr(v), _ptr(gate_logits), _ptr(ws), ws.numel() * ws.element_size(),
                                     _stream(stream))
     _check(st, "yoco_gret_qkvg_project")
+
+
+# ------------------------------------- many sequences on pages of one cache
+
+class PagedKV:
+    """Caller-side holder of a paged cache: k, v [num_pages, Hkv, page_size, d],
+    page_table int32 [B, max_pages] and seq_lens int32 [B] on the device, and the C
+    descriptor that points at them.  The caller hands out pages and advances
+    seq_lens (to the lengths with a call's new rows) before the call."""
+
+    def __init__(self, k, v, page_table, seq_lens, rope_base=0.0):
+        for t, n in ((k, "k"), (v, "v"), (page_table, "page_table"), (seq_lens, "seq_lens")):
+            _need(t, n)
+            if t.device != k.device:
+                raise ValueError(f"{n} is on {t.device}, k on {k.device}")
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be [num_pages, Hkv, page_size, d] of one dtype")
+        if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+            raise TypeError("page_table and seq_lens must be int32")
+        if page_table.dim() != 2 or seq_lens.shape != page_table.shape[:1]:
+            raise ValueError("page_table must be [B, max_pages] and seq_lens [B]")
+        self.k, self.v, self.page_table, self.seq_lens = k, v, page_table, seq_lens
+        num_pages, Hkv, page_size, d = k.shape
+        B, max_pages = page_table.shape
+        self.c = _PagedKVC(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), B, Hkv, d, page_size,
+                           max_pages, num_pages, _dt(k), float(rope_base))
+        self.ref = ctypes.byref(self.c)
+
+
+def _on(t, name, cache):
+    if t.device != cache.k.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
+
+
+def _paged_call(fn, name, cache, *args, stream):
+    # the library launches on the current device; a stream belongs to its own
+    dev = cache.k.device
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), name)
+
+
+def yoco_paged_attn_workspace_size(Hq, rows, cache: PagedKV) -> int:
+    return lib.yoco_paged_attn_workspace_size(Hq, rows, cache.ref)
+
+
+def _paged_rows(cu_rows, cache):
+    if cu_rows.dtype != torch.int32 or cu_rows.shape != (cache.c.B + 1,):
+        raise ValueError("cu_rows must be int32 [B + 1]")
+    _need(cu_rows, "cu_rows")
+    _on(cu_rows, "cu_rows", cache)
+
+
+def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, workspace=None, stream=None):
+    """k, v [rows, Hkv, d] (or both None), q [rows, Hq, d] or None, each with any strides
+    that are multiples of 16 bytes; q_out [rows, Hq, d] (None: q in place).  cu_rows int32
+    [B + 1], or None for one row per sequence."""
+    d, dt = cache.c.d, cache.k.dtype
+    if q is not None and q_out is None:
+        q_out = q
+    rows, args = None, []
+    for t, n, heads in ((k, "k", cache.c.Hkv), (v, "v", cache.c.Hkv), (q, "q", None)):
+        if t is None:
+            args += [None, 0, 0]
+            continue
+        if not t.is_cuda or t.dtype != dt or t.dim() != 3 or t.shape[2] != d or (d > 1 and t.stride(2) != 1) or \
+                (heads is not None and t.shape[1] != heads) or (rows is not None and t.shape[0] != rows):
+            raise ValueError(f"{n} must be a CUDA tensor [rows, heads, {d}] of {dt} with adjacent channels")
+        _on(t, n, cache)
+        rows = t.shape[0]
+        args += [t.data_ptr(), t.stride(0), t.stride(1)]
+    if rows is None:
+        raise ValueError("neither k and v nor q given")
+    if q is not None:
+        if q_out.shape != q.shape or q_out.dtype != dt:
+            raise ValueError("q_out must have q's shape and dtype")
+        _need(q_out, "q_out")
+        _on(q_out, "q_out", cache)
+    if cu_rows is not None:
+        _paged_rows(cu_rows, cache)
+    ws = _workspace(256, cache.k.device, workspace)
+    _paged_call(lib.yoco_paged_append, "yoco_paged_append", cache, *args, _ptr(q_out), 0 if q is None else q.shape[1],
+                _ptr(cu_rows), rows, cache.ref, _ptr(ws), ws.numel() * ws.element_size(), stream=stream)
+
+
+def _paged_q(Q, O, cache):
+    _need(Q, "Q")
+    _need(O, "O")
+    if Q.dim() != 3 or Q.shape != O.shape or Q.shape[2] != cache.c.d or Q.dtype != cache.k.dtype or O.dtype != Q.dtype:
+        raise ValueError(f"Q and O must be [rows, Hq, {cache.c.d}] of {cache.k.dtype}")
+    _on(Q, "Q", cache)
+    _on(O, "O", cache)
+
+
+def yoco_paged_attn_prefill(Q, cache: PagedKV, cu_rows, O, scale=None, window=0, sinks=0, workspace=None, stream=None):
+    """Q, O [rows, Hq, d]; rows cu_rows[b] .. cu_rows[b + 1] - 1 are sequence b's newest."""
+    _paged_q(Q, O, cache)
+    _paged_rows(cu_rows, cache)
+    rows, Hq, d = Q.shape
+    ws = workspace if workspace is not None else _workspace(
+        lib.yoco_paged_attn_workspace_size(Hq, rows, cache.ref), Q.device, None)
+    _paged_call(lib.yoco_paged_attn_prefill, "yoco_paged_attn_prefill", cache, _ptr(Q), Hq, _ptr(cu_rows), rows,
+                cache.ref, d ** -0.5 if scale is None else scale, window, sinks, _ptr(O), _ptr(ws),
+                0 if ws is None else ws.numel() * ws.element_size(), stream=stream)
+
+
+def yoco_paged_attn_decode(Q, cache: PagedKV, O, scale=None, window=0, sinks=0, workspace=None, stream=None):
+    """Q, O [B, Hq, d]: one row per sequence, at position seq_lens[b] - 1."""
+    _paged_q(Q, O, cache)
+    rows, Hq, d = Q.shape
+    if rows != cache.c.B:
+        raise ValueError(f"Q has {rows} rows, the cache {cache.c.B} sequences")
+    ws = workspace if workspace is not None else _workspace(
+        lib.yoco_paged_attn_workspace_size(Hq, rows, cache.ref), Q.device, None)
+    _paged_call(lib.yoco_paged_attn_decode, "yoco_paged_attn_decode", cache, _ptr(Q), Hq, cache.ref,
+                d ** -0.5 if scale is None else scale, window, sinks, _ptr(O), _ptr(ws),
+                0 if ws is None else ws.numel() * ws.element_size(), stream=stream)

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paged.cuh"
 
 namespace yoco_host {
 
@@ -141,6 +142,12 @@ yoco_status yoco_workspace_status(void *workspace, int clear, void *stream) {
         if (e == cudaSuccess) e = cudaStreamSynchronize(st);
         if (e != cudaSuccess) return cuda_status(e, "workspace_status");
     }
+    if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedLen)
+        return fail(YOCO_ERR_INVALID_ARG, "a paged call met a sequence length that its page table cannot hold");
+    if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedPage)
+        return fail(YOCO_ERR_INVALID_ARG, "a paged call needed a page that the pool does not have");
+    if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedRows)
+        return fail(YOCO_ERR_INVALID_ARG, "a paged call met cu_rows that decrease or leave [0, rows]");
     if (hit) return fail(YOCO_ERR_TIMEOUT, "a bounded on-device wait gave up (site %u)", word & 0xFFu);
     g_last_error[0] = 0;
     return YOCO_OK;
@@ -532,6 +539,108 @@ yoco_status yoco_swa_decode(const void *q, const void *k, const void *v, int Hq,
     if (e != cudaSuccess) return cuda_status(e, "swa_decode");
     ring->pos += 1;
     return YOCO_OK;
+}
+
+// ------------------------------------------- many sequences on pages of one cache
+
+static yoco_status check_paged(const yoco_paged_kv *c) {
+    if (!c) return fail(YOCO_ERR_INVALID_ARG, "cache is NULL");
+    if (!c->k || !c->v || !c->page_table || !c->seq_lens)
+        return fail(YOCO_ERR_INVALID_ARG, "cache k, v, page_table and seq_lens must be set");
+    if (!valid_dt(c->dtype)) return fail(YOCO_ERR_INVALID_ARG, "cache dtype invalid");
+    if (c->B <= 0 || c->Hkv <= 0 || c->max_pages <= 0 || c->num_pages <= 0)
+        return fail(YOCO_ERR_INVALID_ARG, "cache B, Hkv, max_pages and num_pages must be positive");
+    if (c->d != 64 && c->d != 128) return fail(YOCO_ERR_UNSUPPORTED, "cache head size %d not in {64, 128}", c->d);
+    if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+        return fail(YOCO_ERR_UNSUPPORTED, "page size %d is not a power of two in [16, 1024]", c->page_size);
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(YOCO_ERR_INVALID_ARG, "cache k/v must be 16-byte aligned");
+    if (!aligned(c->page_table, 4) || !aligned(c->seq_lens, 4))
+        return fail(YOCO_ERR_INVALID_ARG, "page_table and seq_lens must be 4-byte aligned");
+    if (c->B > yoco::kPagedMaxB) return fail(YOCO_ERR_UNSUPPORTED, "more than %d sequences", yoco::kPagedMaxB);
+    const int64_t keys = (int64_t)c->max_pages * c->page_size;
+    if (keys > ((int64_t)1 << 30)) return fail(YOCO_ERR_UNSUPPORTED, "max_pages * page_size above 2^30");
+    if (c->Hkv > 65536 || (int64_t)c->B * c->Hkv * ((keys + yoco::kPagedTile - 1) / yoco::kPagedTile) > INT32_MAX)
+        return fail(YOCO_ERR_UNSUPPORTED, "B * Hkv * max_pages * page_size / %d above 2^31 - 1", yoco::kPagedTile);
+    if (!(c->rope_base == 0.0f || (c->rope_base > 1.0f && isfinite(c->rope_base))))
+        return fail(YOCO_ERR_INVALID_ARG, "rope_base must be 0 (off) or a finite base > 1");
+    return YOCO_OK;
+}
+
+static yoco_status check_paged_heads(const yoco_paged_kv *c, int Hq, int rows) {
+    if (Hq <= 0 || Hq % c->Hkv != 0) return fail(YOCO_ERR_UNSUPPORTED, "Hq must be a positive multiple of Hkv");
+    if (Hq / c->Hkv > 16) return fail(YOCO_ERR_UNSUPPORTED, "at most 16 query heads per kv head");
+    if (rows < 0) return fail(YOCO_ERR_INVALID_ARG, "rows must be >= 0");
+    if ((int64_t)rows * Hq > INT32_MAX) return fail(YOCO_ERR_UNSUPPORTED, "rows * Hq above 2^31 - 1");
+    return YOCO_OK;
+}
+
+size_t yoco_paged_attn_workspace_size(int Hq, int rows, const yoco_paged_kv *cache) {
+    if (check_paged(cache) != YOCO_OK || check_paged_heads(cache, Hq, rows) != YOCO_OK) return 0;
+    return paged_workspace(cache, Hq, rows);
+}
+
+yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                              int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out, int Hq,
+                              const int32_t *cu_rows, int rows, const yoco_paged_kv *cache, void *workspace,
+                              size_t ws_bytes, void *stream) {
+    yoco_status s = check_paged(cache);
+    if (s != YOCO_OK) return s;
+    if (rows < 0) return fail(YOCO_ERR_INVALID_ARG, "rows must be >= 0");
+    if (!k != !v) return fail(YOCO_ERR_INVALID_ARG, "k and v come together");
+    if (!q != !q_out) return fail(YOCO_ERR_INVALID_ARG, "q and q_out come together");
+    if (!k && !q) return fail(YOCO_ERR_INVALID_ARG, "neither k and v nor q given");
+    if (q && Hq <= 0) return fail(YOCO_ERR_INVALID_ARG, "Hq must be > 0");
+    if (rows > (1 << 30) || (q && (int64_t)rows * Hq > INT32_MAX)) return fail(YOCO_ERR_UNSUPPORTED, "size out of range");
+    if (!cu_rows && rows != cache->B)
+        return fail(YOCO_ERR_INVALID_ARG, "without cu_rows there is one row per sequence: rows %d, B %d", rows, cache->B);
+    if (cu_rows && !aligned(cu_rows, 4)) return fail(YOCO_ERR_INVALID_ARG, "cu_rows must be 4-byte aligned");
+    const int per16 = cache->dtype == YOCO_BF16 ? 8 : 4;
+    if (k && (!aligned(k, 16) || !aligned(v, 16) || k_row % per16 || k_head % per16 || v_row % per16 || v_head % per16))
+        return fail(YOCO_ERR_INVALID_ARG, "k, v and their strides must be multiples of 16 bytes");
+    if (q && (!aligned(q, 16) || !aligned(q_out, 16) || q_row % per16 || q_head % per16))
+        return fail(YOCO_ERR_INVALID_ARG, "q, q_out and q's strides must be multiples of 16 bytes");
+    if (q && q == q_out && (q_row != (int64_t)Hq * cache->d || q_head != cache->d))
+        return fail(YOCO_ERR_INVALID_ARG, "q may be turned in place only where it is dense");
+    if ((s = check_ws(workspace, ws_bytes, 256)) != YOCO_OK) return s;
+    if (rows == 0) return YOCO_OK;
+    YOCO_INJECTED_FAILURE("paged_append");
+    const PagedArgs a{q, q_out, cu_rows, rows, Hq, cache, 0.f, 0, 0, workspace, (int *)workspace};
+    const PagedSource src{k, v, k_row, k_head, v_row, v_head, q_row, q_head};
+    return cuda_status(paged_append(a, src, (cudaStream_t)stream), "paged_append");
+}
+
+static yoco_status paged_attn(const void *Q, int Hq, const int32_t *cu_rows, int rows, const yoco_paged_kv *cache,
+                              float scale, int window, int sinks, void *O, void *workspace, size_t ws_bytes,
+                              void *stream, bool one_row) {
+    yoco_status s = check_paged(cache);
+    if (s != YOCO_OK) return s;
+    if (one_row) rows = cache->B;
+    if (!Q || !O || (!one_row && !cu_rows)) return fail(YOCO_ERR_INVALID_ARG, "null tensor");
+    if ((s = check_paged_heads(cache, Hq, rows)) != YOCO_OK) return s;
+    if (!(scale > 0.0f) || !isfinite(scale)) return fail(YOCO_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (window < 0 || sinks < 0) return fail(YOCO_ERR_INVALID_ARG, "window and sinks must be >= 0");
+    if (!aligned(Q, 16) || !aligned(O, 16)) return fail(YOCO_ERR_INVALID_ARG, "Q/O must be 16-byte aligned");
+    if (cu_rows && !aligned(cu_rows, 4)) return fail(YOCO_ERR_INVALID_ARG, "cu_rows must be 4-byte aligned");
+    // no position or window edge leaves 32 bits
+    if (window > (1 << 30)) window = 1 << 30;
+    if (sinks > (1 << 30)) sinks = 1 << 30;
+    if ((s = check_ws(workspace, ws_bytes, paged_workspace(cache, Hq, rows))) != YOCO_OK) return s;
+    if (rows == 0) return YOCO_OK;
+    const char *name = one_row ? "paged_attn_decode" : "paged_attn_prefill";
+    YOCO_INJECTED_FAILURE(name);
+    const PagedArgs a{Q, O, cu_rows, rows, Hq, cache, scale, window, sinks, workspace, (int *)workspace};
+    return cuda_status(one_row ? paged_decode(a, (cudaStream_t)stream) : paged_prefill(a, (cudaStream_t)stream), name);
+}
+
+yoco_status yoco_paged_attn_prefill(const void *Q, int Hq, const int32_t *cu_rows, int rows,
+                                    const yoco_paged_kv *cache, float scale, int window, int sinks, void *O,
+                                    void *workspace, size_t ws_bytes, void *stream) {
+    return paged_attn(Q, Hq, cu_rows, rows, cache, scale, window, sinks, O, workspace, ws_bytes, stream, false);
+}
+
+yoco_status yoco_paged_attn_decode(const void *Q, int Hq, const yoco_paged_kv *cache, float scale, int window,
+                                   int sinks, void *O, void *workspace, size_t ws_bytes, void *stream) {
+    return paged_attn(Q, Hq, nullptr, 0, cache, scale, window, sinks, O, workspace, ws_bytes, stream, true);
 }
 
 }  // extern "C"

@@ -51,6 +51,8 @@ __device__ __forceinline__ float log_gate(float logit, float inv_tau) {
 //   0x53 attention (CUDA cores): output / partial row      0x54 split merge: output row
 //   0x58 gRet recurrent step: state element                0x5C GroupNorm + gate: row
 //   0x5D rotary encoding: row                              0x5E sliding-window ring: slot
+//   0x63 paged append: slot                                0x64 paged decode (CUDA cores): output / partial row
+//   0x65 paged prefill (CUDA cores): output row            0x66 paged prefill: merged row
 #ifdef YOCO_DEBUG_CHECKS
 static __device__ unsigned g_yoco_dbg_word;
 __device__ __forceinline__ bool dcheck(bool ok, unsigned site) {

@@ -119,9 +119,33 @@ cudaError_t rope_table(float2 *tab, int64_t pos0, int T, int d, float base, cuda
 cudaError_t qkvg_project(const void *X, const void *W, int B, int N, int dm, int H, int d, void *q, void *k, void *v,
                          float *logits, const float2 *rope_cs, int *err, cudaStream_t st);
 
+// paged_append.cu, paged_simt.cu: the paged cache
+struct PagedArgs {
+    const void *Q;
+    void *O;
+    const int32_t *cu;
+    int rows, Hq;
+    const yoco_paged_kv *cache;
+    float scale;
+    int window, sinks;
+    void *ws;
+    int *err;  // status word of ws
+};
+struct PagedSource {  // new rows, strides in elements (Q of PagedArgs has q_row, q_head)
+    const void *k, *v;
+    int64_t k_row, k_head, v_row, v_head, q_row, q_head;
+};
+cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t st);
+size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows);
+cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st);
+cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st);
+// the row blocks' splits of the keys into the output: R rows to a set, `sets` sets to a block
+cudaError_t paged_merge_rows(const PagedArgs &a, const float *part, int units, int splits, int R, int sets,
+                             cudaStream_t st);
+
 // debug builds: each kernel file's debug word (see YOCO_DEBUG_TU in common.cuh)
 #define YOCO_DEBUG_TUS(X) X(attn) X(attn_fa) X(attn_tc) X(gn_gate) X(gret_simt) X(gret_tc) X(kv_proj) \
-    X(kv_proj_tc) X(qkvg_tc) X(rope) X(swa)
+    X(kv_proj_tc) X(paged_append) X(paged_simt) X(qkvg_tc) X(rope) X(swa)
 #define YOCO_DECLARE_DEBUG_WORD(tu) cudaError_t debug_word_##tu(unsigned *w, int clear);
 YOCO_DEBUG_TUS(YOCO_DECLARE_DEBUG_WORD)
 

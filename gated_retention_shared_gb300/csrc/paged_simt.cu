@@ -1,0 +1,620 @@
+// paged_simt.cu -- attention over the paged cache on the CUDA cores, fp32 arithmetic: every
+// type and head size the library has (the tensor-core kernels take bf16 at head size 128),
+// and the merges of split keys that both paths share.
+//
+//   o = sum_m p_m v_m / sum_m p_m,   p_m = 2^(c q.k_m - r),  c = scale log2(e),
+//
+// over the slots m that the row sees, r a running maximum.  K and V of slots that no row
+// of a block sees are never loaded, so what those hold (nothing yet, NaN, another
+// sequence's rows) cannot reach a result.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace yoco {
+
+constexpr float kPagedLog2e = 1.4426950408889634f;
+
+// 4 or 8 consecutive elements (16 bytes) as floats
+template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16 / sizeof(T)]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            x[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- decode
+//
+// One row per sequence; a unit is one (sequence, kv head) with its G query heads.  Eight
+// lanes hold one key (16-byte chunk j of the row in lane j % 8), four keys to a warp, 32 to
+// the block: a key's score is summed over its lanes, and each group of eight lanes keeps a
+// running maximum, sum and weighted sum of its own, merged at the end of the unit.  K and V
+// go from global memory to registers once.  Groups with more than kDecQ heads take them
+// kDecQ at a time, reading K and V again (from L2).
+constexpr int kDecThreads = 256;
+constexpr int kDecWarps = kDecThreads / 32;
+constexpr int kDecQ = 8;      // query heads at a time
+constexpr int kDecKeys = 2;   // keys of a lane group in flight
+
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(kDecThreads)
+paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
+                         float *__restrict__ part, PagedCut *__restrict__ cuts, int Hq, const PagedView pv, float c2,
+                         int *err) {
+    constexpr int EV = 16 / (int)sizeof(T);
+    constexpr int NC = D / EV / 8;  // chunks of a key per lane
+    constexpr int EL = NC * EV;     // elements of a key per lane
+    static_assert(NC >= 1, "a key has at least one chunk per lane");
+    extern __shared__ int pre[];
+    __shared__ int sums[kDecWarps];
+    __shared__ float qs[NQ][D];
+    __shared__ float wm[kDecWarps][NQ], wl[kDecWarps][NQ], wo[kDecWarps][NQ][D];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j8 = lane & 7, grp = warp * 4 + (lane >> 3);
+    const int G = Hq / pv.Hkv, c = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    paged_prefix<kDecThreads>(pv, pre, sums, err);
+    const int total = pre[pv.B] * pv.Hkv;
+    const int each = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    // sequences without a key: zeros
+    for (int b = c; b < pv.B; b += gridDim.x)
+        if (pre[b + 1] == pre[b])
+            for (int e = tid; e < Hq * D; e += kDecThreads) O[(size_t)b * Hq * D + e] = from_f32<T>(0.f);
+    PagedWalk w;
+    PagedCut cut{-1, 0, 0, 0};
+    bool more = w.start(pv, pre, (int)min((int64_t)c * each, (int64_t)total), (int)min((int64_t)(c + 1) * each, (int64_t)total));
+    if (more && w.t0 > 0) cut = paged_cut(pv, pre, w, c, each);
+    if (tid == 0) cuts[c] = cut;
+    for (int seg = 0; more; ++seg, more = w.next(pv, pre)) {
+        const int p = paged_len(pv, w.b, err) - 1;
+        const PagedRange range = paged_range(pv, p, p);
+        for (int g0 = 0; g0 < G; g0 += NQ) {
+            const int nq = min(NQ, G - g0);
+            const size_t qrow = (size_t)w.b * Hq + w.hk * G + g0;
+            __syncthreads();
+            for (int e = tid; e < NQ * D; e += kDecThreads)
+                qs[e / D][e % D] = e < nq * D ? c2 * to_f32(Q[qrow * D + e]) : 0.f;
+            __syncthreads();
+            float m[NQ], l[NQ], acc[NQ][EL];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < EL; ++e) acc[i][e] = 0.f;
+            }
+            // this group's keys of the run: 4 of each 128-key tile
+            const int steps = (w.t1 - w.t0) * (kPagedTile / 32);
+            for (int st = 0; st < steps; st += kDecKeys) {
+                float kx[kDecKeys][EL], vx[kDecKeys][EL];
+                bool ok[kDecKeys];
+#pragma unroll
+                for (int x = 0; x < kDecKeys; ++x) {
+                    const int key = range.key0(w.t0 + (st + x) / 4) + ((st + x) % 4) * 32 + grp;
+                    ok[x] = key < range.hi && (key >= range.lo || key < pv.sinks);
+                    const int page = ok[x] ? paged_page(pv, w.b, key >> pv.shift, err) : -1;
+                    const size_t at = (((size_t)max(page, 0) * pv.Hkv + w.hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) {
+                        float t[EV], u[EV];
+#pragma unroll
+                        for (int e = 0; e < EV; ++e) t[e] = u[e] = 0.f;
+                        if (page >= 0) {
+                            load16(K + at * D + (n * 8 + j8) * EV, t);
+                            load16(V + at * D + (n * 8 + j8) * EV, u);
+                        }
+#pragma unroll
+                        for (int e = 0; e < EV; ++e) {
+                            kx[x][n * EV + e] = t[e];
+                            vx[x][n * EV + e] = u[e];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    float s[kDecKeys], top = m[i];
+#pragma unroll
+                    for (int x = 0; x < kDecKeys; ++x) {
+                        float d = 0.f;
+#pragma unroll
+                        for (int e = 0; e < EL; ++e) d = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d);
+#pragma unroll
+                        for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                        s[x] = ok[x] ? d : -INFINITY;
+                        top = fmaxf(top, s[x]);
+                    }
+                    if (top == -INFINITY) continue;
+                    const float old = exp2f(m[i] - top);
+                    m[i] = top;
+                    l[i] *= old;
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) acc[i][e] *= old;
+#pragma unroll
+                    for (int x = 0; x < kDecKeys; ++x) {
+                        const float pe = exp2f(s[x] - top);
+                        l[i] += pe;
+#pragma unroll
+                        for (int e = 0; e < EL; ++e) acc[i][e] = fmaf(pe, vx[x][e], acc[i][e]);
+                    }
+                }
+            }
+            // the warp's four groups, then the eight warps
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                float M = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+                const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - M);
+                float L = l[i] * f;
+                L += __shfl_xor_sync(0xffffffffu, L, 8);
+                L += __shfl_xor_sync(0xffffffffu, L, 16);
+                if (lane == 0) {
+                    wm[warp][i] = M;
+                    wl[warp][i] = L;
+                }
+#pragma unroll
+                for (int e = 0; e < EL; ++e) {
+                    float a = acc[i][e] * f;
+                    a += __shfl_xor_sync(0xffffffffu, a, 8);
+                    a += __shfl_xor_sync(0xffffffffu, a, 16);
+                    if (lane < 8) wo[warp][i][(e / EV * 8 + j8) * EV + e % EV] = a;
+                }
+            }
+            __syncthreads();
+            for (int e = tid; e < nq * D; e += kDecThreads) {
+                const int i = e / D, dd = e % D;
+                float M = -INFINITY, L = 0.f, A = 0.f;
+                for (int x = 0; x < kDecWarps; ++x) M = fmaxf(M, wm[x][i]);
+                for (int x = 0; x < kDecWarps; ++x) {
+                    const float f = wm[x][i] == -INFINITY ? 0.f : exp2f(wm[x][i] - M);
+                    L += wl[x][i] * f;
+                    A += wo[x][i][dd] * f;
+                }
+                if (!YOCO_DCHECK(w.b < pv.B && w.hk < pv.Hkv, 0x64)) continue;
+                if (w.whole()) {
+                    O[qrow * D + e] = from_f32<T>(A / L);
+                } else {
+                    float *pp = part + (((size_t)c * 2 + (seg > 0)) * G + g0 + i) * (D + 2);
+                    pp[dd] = A;
+                    if (dd == 0) {
+                        pp[D] = M;
+                        pp[D + 1] = L;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Joins the partial results of a unit that several blocks share: block x of the grid looks
+// at the cut before run x + 1, one query head per grid.y, thread = head dim.
+constexpr int kMergeBatch = 16;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(D)
+paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ cuts, T *__restrict__ O, int G) {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const PagedCut cut = cuts[blockIdx.x + 1];
+    if (cut.unit < 0) return;
+    const int g = blockIdx.y, dd = threadIdx.x;
+    float M = -INFINITY, L = 0.f, A = 0.f;
+    for (int c0 = cut.c_first; c0 <= cut.c_last; c0 += kMergeBatch) {
+        float m[kMergeBatch], l[kMergeBatch], a[kMergeBatch], top = M;
+#pragma unroll
+        for (int x = 0; x < kMergeBatch; ++x) {
+            const int c = min(c0 + x, cut.c_last);
+            const float *pp = part + (((size_t)c * 2 + (c == cut.c_first ? cut.slot_first : 0)) * G + g) * (D + 2);
+            m[x] = __ldcg(pp + D);
+            l[x] = __ldcg(pp + D + 1);
+            a[x] = __ldcg(pp + dd);
+            top = fmaxf(top, m[x]);
+        }
+        if (top == -INFINITY) continue;
+        const float old = exp2f(M - top);
+        M = top;
+        L *= old;
+        A *= old;
+#pragma unroll
+        for (int x = 0; x < kMergeBatch; ++x) {
+            const float f = c0 + x <= cut.c_last ? exp2f(m[x] - top) : 0.f;
+            L = fmaf(l[x], f, L);
+            A = fmaf(a[x], f, A);
+        }
+    }
+    O[((size_t)cut.unit * G + g) * D + dd] = from_f32<T>(A / L);
+}
+
+// ----------------------------------------------------------------- prefill
+//
+// 64 rows (tokens x the G query heads of one kv head) against 64-key tiles, 256 threads as
+// 16 x 16: thread (ty, tx) holds rows 4 ty .. and keys tx + 16 j of the scores, rows 4 ty ..
+// and dims 4 tx + 64 j .. of the output.  Everything the products read is in shared memory
+// as fp32, two blocks to an SM; bound by the fp32 pipe.
+constexpr int kPreRows = 64, kPreKeys = 64, kPreThreads = 256;
+
+template <int D> __host__ __device__ constexpr size_t pre_smem() {
+    return sizeof(float) * ((size_t)kPreRows * D + kPreKeys * (D + 4) + kPreKeys * D + kPreRows * kPreKeys);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPreThreads, 2)
+paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
+                          float *__restrict__ part, const int32_t *__restrict__ cu, int rows, int Hq,
+                          const PagedView pv, float c2, int splits, int *err) {
+    constexpr int EV = 16 / (int)sizeof(T), NJ = D / 64;
+    extern __shared__ float4 smem4[];
+    float *sq = reinterpret_cast<float *>(smem4);
+    float *sk = sq + kPreRows * D, *sv = sk + kPreKeys * (D + 4), *sp = sv + kPreKeys * D;
+    __shared__ PagedBlock blk;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int G = Hq / pv.Hkv, TS = kPreRows / G;
+    const int hk = (blockIdx.x / splits) % pv.Hkv, sp_i = blockIdx.x % splits, j = blockIdx.x / splits / pv.Hkv;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (tid < 32) {
+        PagedBlock o;
+        paged_block(pv, cu, rows, TS, j, hk, sp_i, splits, o, err);
+        if (tid == 0) blk = o;
+    }
+    __syncthreads();
+    if (blk.nrow == 0) return;
+    const int nr = blk.nrow * G;  // rows in use: (token, head) = (r / G, r % G)
+    const size_t row_stride = (size_t)Hq * D;
+    for (int e = tid; e < kPreRows * (D / EV); e += kPreThreads) {
+        const int r = e / (D / EV), ch = e % (D / EV);
+        float x[EV];
+#pragma unroll
+        for (int i = 0; i < EV; ++i) x[i] = 0.f;
+        if (r < nr) load16(Q + (blk.row0 + r / G) * row_stride + (size_t)(hk * G + r % G) * D + ch * EV, x);
+#pragma unroll
+        for (int i = 0; i < EV; ++i) sq[r * D + ch * EV + i] = c2 * x[i];
+    }
+    float m[4], l[4], acc[4][4 * NJ];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4 * NJ; ++e) acc[i][e] = 0.f;
+    }
+    for (int t2 = 2 * blk.i0; t2 < 2 * blk.i1; ++t2) {
+        const int key0 = blk.range.key0(t2 >> 1) + (t2 & 1) * kPreKeys;
+        __syncthreads();
+        for (int e = tid; e < kPreKeys * (D / EV); e += kPreThreads) {
+            const int r = e / (D / EV), ch = e % (D / EV), key = key0 + r;
+            float x[EV], y[EV];
+#pragma unroll
+            for (int i = 0; i < EV; ++i) x[i] = y[i] = 0.f;
+            if (key < blk.range.hi && (key >= blk.range.lo || key < pv.sinks)) {
+                const int page = paged_page(pv, blk.b, key >> pv.shift, err);
+                if (page >= 0) {
+                    const size_t at = (((size_t)page * pv.Hkv + hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
+                    load16(K + at * D + ch * EV, x);
+                    load16(V + at * D + ch * EV, y);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < EV; ++i) {
+                sk[r * (D + 4) + ch * EV + i] = x[i];
+                sv[r * D + ch * EV + i] = y[i];
+            }
+        }
+        __syncthreads();
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
+#pragma unroll 4
+        for (int dd = 0; dd < D; dd += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * D + dd);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * x) * (D + 4) + dd);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    s[i][x] = fmaf(a[i].x, b[x].x, fmaf(a[i].y, b[x].y, fmaf(a[i].z, b[x].z, fmaf(a[i].w, b[x].w, s[i][x]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pos = blk.pos0 + (4 * ty + i) / G;
+            float top = m[i];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int key = key0 + tx + 16 * x;
+                const bool seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
+                if (!seen) s[i][x] = -INFINITY;
+                top = fmaxf(top, s[i][x]);
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float old = exp2f(m[i] - ref);
+            m[i] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float pe = exp2f(s[i][x] - ref);
+                sum += pe;
+                sp[(4 * ty + i) * kPreKeys + tx + 16 * x] = pe;
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            l[i] = l[i] * old + sum;
+#pragma unroll
+            for (int e = 0; e < 4 * NJ; ++e) acc[i][e] *= old;
+        }
+        __syncwarp();  // a row's P is written and read by one half-warp
+#pragma unroll 2
+        for (int kk = 0; kk < kPreKeys; kk += 4) {
+            float pr[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 f = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * kPreKeys + kk);
+                pr[i][0] = f.x;
+                pr[i][1] = f.y;
+                pr[i][2] = f.z;
+                pr[i][3] = f.w;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int n = 0; n < NJ; ++n) {
+                    const float4 vv = *reinterpret_cast<const float4 *>(sv + (kk + x) * D + 64 * n + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[i][4 * n] = fmaf(pr[i][x], vv.x, acc[i][4 * n]);
+                        acc[i][4 * n + 1] = fmaf(pr[i][x], vv.y, acc[i][4 * n + 1]);
+                        acc[i][4 * n + 2] = fmaf(pr[i][x], vv.z, acc[i][4 * n + 2]);
+                        acc[i][4 * n + 3] = fmaf(pr[i][x], vv.w, acc[i][4 * n + 3]);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (blk.pieces > 1) {  // [unit][split][D + 2][row]
+            float *pp = part + ((size_t)(j * pv.Hkv + hk) * splits + sp_i) * (D + 2) * kPreRows + r;
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pp[(64 * n + 4 * tx + e) * kPreRows] = acc[i][4 * n + e];
+            if (tx == 0) {
+                pp[D * kPreRows] = m[i];
+                pp[(D + 1) * kPreRows] = l[i];
+            }
+        } else if (r < nr) {
+            const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+            T *op = O + (blk.row0 + r / G) * row_stride + (size_t)(hk * G + r % G) * D;
+            if (!YOCO_DCHECK(blk.row0 + r / G < rows && hk * G + r % G < Hq, 0x65)) continue;
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) op[64 * n + 4 * tx + e] = from_f32<T>(acc[i][4 * n + e] * inv);
+        }
+    }
+}
+
+// Joins the splits of a row block's keys: partials [unit][split][set][D + 2][R], one CTA per
+// (unit, set) and 32 head dims, thread = row.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(R)
+paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const int32_t *__restrict__ cu, int rows,
+                        int Hq, const PagedView pv, int splits, int sets, int *err) {
+    __shared__ PagedBlock blk;
+    const int r = threadIdx.x, G = Hq / pv.Hkv, TS = R / G;
+    const int set = blockIdx.x % sets, unit = blockIdx.x / sets, hk = unit % pv.Hkv, d0 = blockIdx.y * 32;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (r < 32) {
+        PagedBlock o;
+        paged_block(pv, cu, rows, TS * sets, unit / pv.Hkv, hk, 0, splits, o, err);
+        if (r == 0) blk = o;
+    }
+    __syncthreads();
+    const int tok = set * TS + r / G;
+    if (blk.nrow == 0 || blk.pieces == 1 || r >= TS * G || tok >= blk.nrow) return;
+    float M = -INFINITY, L = 0.f, A[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) A[e] = 0.f;
+    for (int s = 0; s < blk.pieces; ++s) {
+        const float *pp = part + (((size_t)unit * splits + s) * sets + set) * (D + 2) * R + r;
+        const float m = __ldcg(pp + D * R), l = __ldcg(pp + (D + 1) * R);
+        float x[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = __ldcg(pp + (d0 + e) * R);
+        if (m == -INFINITY) continue;
+        const float top = fmaxf(M, m), old = exp2f(M - top), f = exp2f(m - top);
+        M = top;
+        L = fmaf(l, f, L * old);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) A[e] = fmaf(x[e], f, A[e] * old);
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    T *op = O + (size_t)(blk.row0 + tok) * Hq * D + (size_t)(hk * G + r % G) * D + d0;
+    if (!YOCO_DCHECK(blk.row0 + tok < rows, 0x66)) return;
+#pragma unroll
+    for (int e = 0; e < 32; e += 16 / (int)sizeof(T)) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(A[e + 2 * i] * inv, A[e + 2 * i + 1] * inv);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h2);
+            } else {
+                w[i] = __float_as_uint(A[e + i] * inv);
+            }
+        }
+        *reinterpret_cast<uint4 *>(op + e) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+}  // namespace yoco
+
+namespace yoco_host {
+using namespace yoco;
+
+constexpr size_t kPagedHead = 256;                    // status word
+constexpr size_t kPagedCuts = 16384;                  // PagedCut per block of a decode grid
+constexpr int kMaxDecodeBlocks = (int)(kPagedCuts / sizeof(PagedCut));
+
+bool paged_on_tc(const yoco_paged_kv *c) { (void)c; return false; }
+
+int paged_decode_blocks(const yoco_paged_kv *c) {
+    const int per_sm = paged_on_tc(c) ? 1 : 2;
+    return std::min(kMaxDecodeBlocks, per_sm * device_sm_count());
+}
+
+// rows of a prefill block, and its partial results per split
+static int pre_rows(bool tc) { return tc ? 256 : kPreRows; }
+
+static int64_t prefill_units(const yoco_paged_kv *c, int Hq, int rows, bool tc) {
+    const int G = Hq / c->Hkv, TR = tc ? 2 * (128 / G) : kPreRows / G;
+    const int64_t blocks = c->B == 1 ? ((int64_t)rows + TR - 1) / TR : (int64_t)rows / TR + std::min(c->B, rows);
+    return std::max<int64_t>(blocks, 1) * c->Hkv;
+}
+
+// Key splits of a prefill: none while the row blocks alone give every SM two blocks, else
+// the smallest count whose last wave is at least 95 % full, a split being four tiles or more.
+static int prefill_splits(const yoco_paged_kv *c, int64_t units, int per_sm) {
+    const int64_t slots = (int64_t)per_sm * device_sm_count();
+    const int64_t tiles = ((int64_t)c->max_pages * c->page_size + kPagedTile - 1) / kPagedTile;
+    const int64_t cap = std::min<int64_t>(64, (tiles + kPagedMinTiles - 1) / kPagedMinTiles);
+    if (units >= 2 * slots || cap <= 1) return 1;
+    int64_t best = 1;
+    double best_eff = -1.0;
+    for (int64_t s = std::min(cap, (slots + units - 1) / units); s <= std::min(cap, 4 * ((slots + units - 1) / units)); ++s) {
+        const int64_t n = units * s;
+        const double eff = (double)n / (double)(slots * ((n + slots - 1) / slots));
+        if (eff >= 0.95) return (int)s;
+        if (eff > best_eff) {
+            best_eff = eff;
+            best = s;
+        }
+    }
+    return (int)best;
+}
+
+size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows) {
+    const int G = Hq / c->Hkv;
+    const size_t dec = (size_t)paged_decode_blocks(c) * 2 * G * (c->d + 2) * sizeof(float);
+    const bool tc = paged_on_tc(c);
+    const int64_t units = prefill_units(c, Hq, rows, tc);
+    const int splits = prefill_splits(c, units, tc ? 1 : 2);
+    const size_t pre = splits > 1 ? (size_t)units * splits * pre_rows(tc) * (c->d + 2) * sizeof(float) : 0;
+    return kPagedHead + kPagedCuts + std::max(dec, pre);
+}
+
+static void pdl_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, size_t smem,
+                       cudaStream_t st) {
+    cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+}
+
+template <typename T, int D, int NQ>
+static cudaError_t decode_simt(const PagedArgs &a, const PagedView &pv, PagedCut *cuts, float *part, int blocks,
+                               cudaStream_t st) {
+    const size_t smem = ((size_t)pv.B + 1) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D, NQ>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (kPagedMaxB + 1) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    pdl_config(cfg, attr, dim3(blocks), kDecThreads, smem, st);
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, paged_decode_simt_kernel<T, D, NQ>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
+                              (const T *)a.cache->v, part, cuts, a.Hq, pv, a.scale * kPagedLog2e, a.err);
+}
+
+template <typename T, int D>
+static cudaError_t decode(const PagedArgs &a, cudaStream_t st) {
+    const PagedView pv = paged_view(a);
+    const int G = a.Hq / pv.Hkv, blocks = paged_decode_blocks(a.cache);
+    PagedCut *cuts = (PagedCut *)((char *)a.ws + kPagedHead);
+    float *part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
+    cudaError_t e = G <= 1   ? decode_simt<T, D, 1>(a, pv, cuts, part, blocks, st)
+                    : G <= 2 ? decode_simt<T, D, 2>(a, pv, cuts, part, blocks, st)
+                    : G <= 4 ? decode_simt<T, D, 4>(a, pv, cuts, part, blocks, st)
+                             : decode_simt<T, D, kDecQ>(a, pv, cuts, part, blocks, st);
+    if (e != cudaSuccess || blocks < 2) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    pdl_config(cfg, attr, dim3(blocks - 1, G), D, 0, st);
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, (const float *)part, (const PagedCut *)cuts, (T *)a.O, G);
+}
+
+template <typename T, int D>
+static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
+    const PagedView pv = paged_view(a);
+    const int64_t units = prefill_units(a.cache, a.Hq, a.rows, false);
+    const int splits = prefill_splits(a.cache, units, 2);
+    float *part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
+    if (units * splits > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)pre_smem<D>());
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    pdl_config(cfg, attr, dim3((unsigned)(units * splits)), kPreThreads, pre_smem<D>(), st);
+    count_launches(1);
+    e = cudaLaunchKernelEx(&cfg, paged_prefill_simt_kernel<T, D>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
+                           (const T *)a.cache->v, part, a.cu, a.rows, a.Hq, pv, a.scale * kPagedLog2e, splits, a.err);
+    if (e != cudaSuccess || splits == 1) return e;
+    return paged_merge_rows(a, part, (int)units, splits, kPreRows, 1, st);
+}
+
+template <typename T, int D, int R>
+static cudaError_t merge_rows(const PagedArgs &a, const float *part, int units, int splits, int sets, cudaStream_t st) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    pdl_config(cfg, attr, dim3((unsigned)(units * sets), D / 32), R, 0, st);
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, part, (T *)a.O, a.cu, a.rows, a.Hq, paged_view(a),
+                              splits, sets, a.err);
+}
+
+cudaError_t paged_merge_rows(const PagedArgs &a, const float *part, int units, int splits, int R, int sets,
+                             cudaStream_t st) {
+    if (R == 128) return merge_rows<bf16_t, 128, 128>(a, part, units, splits, sets, st);
+    if (a.cache->dtype == YOCO_BF16)
+        return a.cache->d == 64 ? merge_rows<bf16_t, 64, 64>(a, part, units, splits, sets, st)
+                                : merge_rows<bf16_t, 128, 64>(a, part, units, splits, sets, st);
+    return a.cache->d == 64 ? merge_rows<float, 64, 64>(a, part, units, splits, sets, st)
+                            : merge_rows<float, 128, 64>(a, part, units, splits, sets, st);
+}
+
+cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st) {
+    if (a.cache->dtype == YOCO_BF16) return a.cache->d == 64 ? decode<bf16_t, 64>(a, st) : decode<bf16_t, 128>(a, st);
+    return a.cache->d == 64 ? decode<float, 64>(a, st) : decode<float, 128>(a, st);
+}
+
+cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st) {
+    if (a.cache->dtype == YOCO_BF16) return a.cache->d == 64 ? prefill<bf16_t, 64>(a, st) : prefill<bf16_t, 128>(a, st);
+    return a.cache->d == 64 ? prefill<float, 64>(a, st) : prefill<float, 128>(a, st);
+}
+
+}  // namespace yoco_host
+
+YOCO_DEBUG_TU(paged_simt)

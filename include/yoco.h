@@ -377,6 +377,103 @@ YOCO_API yoco_status yoco_swa_decode(const void *q, const void *k, const void *v
 /* Workspace bytes for yoco_swa_decode (also enough for yoco_swa_prefill). */
 YOCO_API size_t yoco_swa_workspace_size(int B, int Hq, const yoco_swa_ring *ring);
 
+/* ------------------------------------ many sequences on pages of one cache */
+
+/*
+ * The shared K^/V^ cache (or a self-decoder layer's own) of B sequences of
+ * different lengths, kept in pages that a caller hands out and takes back as
+ * sequences grow and end.  Slot p of sequence b is row p % page_size of page
+ * page_table[b][p / page_size].
+ *   k, v        [num_pages, Hkv, page_size, d] of `dtype`, 16-byte aligned
+ *   page_table  device int32 [B, max_pages]; only entries that hold a slot the
+ *               call writes or some row sees are used, the others may hold
+ *               anything.  Two sequences may name the same page (a shared
+ *               prefix) as long as neither appends to it.
+ *   seq_lens    device int32 [B]: each sequence's length, the call's own new
+ *               rows included.  No call changes it.
+ *   page_size   a power of two in [16, 1024]; max_pages * page_size <= 2^30
+ *   rope_base   0, or > 1: yoco_paged_append turns k and q.  The attention
+ *               calls take queries as they are (a query turned at its append is
+ *               rounded once, and not turned again by every block of every call).
+ * Lengths, table and cu_rows are read on the device when the call runs, so a
+ * captured graph replays with whatever they hold by then.  A length below 0 or
+ * above max_pages * page_size counts as 0, a page outside the pool as a page of
+ * zeros that nothing is written to, a sequence whose cu_rows decrease or leave
+ * [0, rows] as one without rows; each is recorded in the workspace and
+ * yoco_workspace_status then returns YOCO_ERR_INVALID_ARG.
+ * B <= 4096, and B * Hkv * max_pages * page_size / 128 < 2^31.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    int32_t B;
+    int32_t Hkv;
+    int32_t d;
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t num_pages;
+    yoco_dtype dtype;
+    float rope_base;
+} yoco_paged_kv;
+
+/*
+ * New rows of every sequence into their slots: row i of sequence b, which is
+ * row cu_rows[b] + i of the call, belongs at position
+ * p = seq_lens[b] - T_b + i, T_b = cu_rows[b + 1] - cu_rows[b].
+ *   k, v [rows, Hkv, d] with the given strides, in elements, between rows and
+ *        between heads (channels adjacent): token-major, a part of a fused
+ *        projection, or a head-major staging cache.  Both NULL: q alone.
+ *   q    [rows, Hq, d] likewise, or NULL; q_out [rows, Hq, d] dense, may be q
+ *        itself where q is dense.
+ * With rope_base, pairs (2i, 2i+1) of k and q turn by p * rope_base^(-2i/d)
+ * before they are rounded; v is copied.
+ *   cu_rows  device int32 [B + 1], not decreasing, within [0, rows], or NULL:
+ *            one row per sequence, rows == B.
+ * Rows at negative positions and rows behind the last sequence are left out.
+ * Pointers and strides are multiples of 16 bytes.  Two rows for the same slot
+ * (a page named twice) leave either's values.
+ *   workspace  >= 256 bytes, 256-byte aligned (status word)
+ */
+YOCO_API yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                                       int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out,
+                                       int Hq, const int32_t *cu_rows, int rows, const yoco_paged_kv *cache,
+                                       void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Causal grouped-query attention of a chunk of new rows of every sequence over
+ * its pages (the rows' own k and v appended before): with p as in
+ * yoco_paged_append,
+ *     o = sum_m softmax_m(scale * q . k_m) v_m   over the slots m that p sees:
+ *     m <= p and, with window > 0, (p - window < m or m < sinks).
+ * window = 0: no window (sinks is then of no effect).  A page that no row sees
+ * may have been given back.  Query head h reads kv head h / (Hq / Hkv).
+ *   Q, O [rows, Hq, d] cache dtype, dense; cu_rows as above, not NULL.
+ * Rows at negative positions see nothing and come out as zeros; rows of O
+ * behind the last sequence are not written.  Slots that no row of a sequence
+ * sees may hold anything, NaN among it.
+ * Supported: Hq / Hkv <= 16; scale > 0.
+ *   workspace  >= yoco_paged_attn_workspace_size(Hq, rows, cache) bytes,
+ *              256-byte aligned.  Calls that share it must be ordered on one
+ *              stream.
+ */
+YOCO_API yoco_status yoco_paged_attn_prefill(const void *Q, int Hq, const int32_t *cu_rows, int rows,
+                                             const yoco_paged_kv *cache, float scale, int window, int sinks, void *O,
+                                             void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The same for one row per sequence, at its newest position seq_lens[b] - 1:
+ * Q, O [B, Hq, d].  A sequence of length 0 gets zeros.  The keys of all
+ * sequences are shared out evenly over the GPU, whatever their lengths.
+ *   workspace  >= yoco_paged_attn_workspace_size(Hq, B, cache) bytes
+ */
+YOCO_API yoco_status yoco_paged_attn_decode(const void *Q, int Hq, const yoco_paged_kv *cache, float scale, int window,
+                                            int sinks, void *O, void *workspace, size_t ws_bytes, void *stream);
+
+/* Workspace bytes for any paged call with up to `rows` rows (0 for a cache or head count the calls refuse). */
+YOCO_API size_t yoco_paged_attn_workspace_size(int Hq, int rows, const yoco_paged_kv *cache);
+
 /* ------------------------------------------------------------ utilities */
 
 YOCO_API const char *yoco_status_string(yoco_status s);
@@ -389,7 +486,9 @@ YOCO_API int yoco_version(void);
  * the first bytes of the workspace they were given.  This call waits for
  * `stream`, reads that word and returns YOCO_OK or YOCO_ERR_TIMEOUT (the
  * detail is in yoco_last_error()); with clear != 0 it also resets the word.
- * A freshly allocated workspace needs no initialisation.
+ * A freshly allocated workspace needs no initialisation.  After a paged call it
+ * also reports what that call found wrong in the lengths, the page table or
+ * cu_rows (YOCO_ERR_INVALID_ARG).
  */
 YOCO_API yoco_status yoco_workspace_status(void *workspace, int clear, void *stream);
 
