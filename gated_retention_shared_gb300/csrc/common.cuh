@@ -53,6 +53,7 @@ __device__ __forceinline__ float log_gate(float logit, float inv_tau) {
 //   0x5D rotary encoding: row                              0x5E sliding-window ring: slot
 //   0x63 paged append: slot                                0x64 paged decode (CUDA cores): output / partial row
 //   0x65 paged prefill (CUDA cores): output row            0x66 paged prefill: merged row
+//   0x67 paged decode (tensor cores): output / partial row  0x68 paged prefill (tensor cores): output row
 #ifdef YOCO_DEBUG_CHECKS
 static __device__ unsigned g_yoco_dbg_word;
 __device__ __forceinline__ bool dcheck(bool ok, unsigned site) {

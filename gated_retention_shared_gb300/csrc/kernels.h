@@ -139,13 +139,17 @@ cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t 
 size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows);
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st);
 cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st);
+// paged_decode_tc.cu: bf16, d = 128; cuts and part as paged_decode lays them out
+cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blocks, cudaStream_t st);
+// paged_prefill_tc.cu: bf16, d = 128; row blocks x kv heads `units`, keys in `splits`
+cudaError_t paged_prefill_tc(const PagedArgs &a, float *part, int64_t units, int splits, cudaStream_t st);
 // the row blocks' splits of the keys into the output: R rows to a set, `sets` sets to a block
 cudaError_t paged_merge_rows(const PagedArgs &a, const float *part, int units, int splits, int R, int sets,
                              cudaStream_t st);
 
 // debug builds: each kernel file's debug word (see YOCO_DEBUG_TU in common.cuh)
 #define YOCO_DEBUG_TUS(X) X(attn) X(attn_fa) X(attn_tc) X(gn_gate) X(gret_simt) X(gret_tc) X(kv_proj) \
-    X(kv_proj_tc) X(paged_append) X(paged_simt) X(qkvg_tc) X(rope) X(swa)
+    X(kv_proj_tc) X(paged_append) X(paged_decode_tc) X(paged_prefill_tc) X(paged_simt) X(qkvg_tc) X(rope) X(swa)
 #define YOCO_DECLARE_DEBUG_WORD(tu) cudaError_t debug_word_##tu(unsigned *w, int clear);
 YOCO_DEBUG_TUS(YOCO_DECLARE_DEBUG_WORD)
 

@@ -7,6 +7,7 @@
 // rows than the sequence holds) see nothing and come out as zeros.
 #pragma once
 
+#include <cuda.h>
 #include <stdint.h>
 
 #include "common.cuh"
@@ -253,4 +254,9 @@ __device__ __forceinline__ PagedCut paged_cut(const PagedView &pv, const int *pr
 namespace yoco_host {
 struct PagedArgs;
 yoco::PagedView paged_view(const PagedArgs &a);
+// bf16, 128-byte swizzle, what lies outside reads as zeros
+bool paged_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+               const uint32_t *box);
+// a pool's k or v as {d, slot of the page, kv head, page}, boxes of 64 channels x up to a tile's slots
+bool paged_kv_map(CUtensorMap *m, const void *ptr, const yoco_paged_kv *c);
 }  // namespace yoco_host

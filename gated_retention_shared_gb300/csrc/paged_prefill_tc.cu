@@ -1,0 +1,536 @@
+// paged_prefill_tc.cu -- attention of chunks of new rows over the paged cache on the tensor
+// cores, bf16, head size 128, up to 16 query heads to a kv head.
+//
+// A row of the MMA is one (token, query head of the kv head's group): 128 rows are
+// TS = 128 / G tokens with their G heads, so the group reads each K and V tile once, and a
+// block of 2 TS tokens meets the diagonal over 2 TS + 128 keys, not over 256 + 128.  A block
+// has two such sets, A and B, each with a softmax warpgroup of its own, so that the tensor
+// cores work on one set while the other's softmax runs.  Per 128-key tile i and set X:
+//     S_X  = Q_X K_i^T                    (TMEM)
+//     P_X  = 2^(c S_X - m)   masked       (bf16, shared memory)
+//     O_X += P_X V_i                      (TMEM)
+// with c = scale log2(e) and m a reference per row that moves only when a tile's maximum
+// passes it by more than 8 / ln 2, O_X being rescaled then.  P is rounded to bf16 for the
+// second product, its sum is kept in fp32 before that rounding.
+//
+// The sets take one P buffer in turn by 64-key halves (set B writes P(i) as P_A V(i) reads
+// its halves, set A P(i + 1) as P_B V(i) does).  A block whose tokens fit set A (a short
+// chunk, the end of a long one) leaves set B out and uses Q_B's place as a second P buffer, so
+// that the softmax of tile i + 1 runs while P V(i) does.
+//
+// Pages, rows out of sight and pages that are not there: as in paged_decode_tc.cu; set A's
+// warps clear the V rows that no row of the block sees.  With few row blocks the keys are
+// split (paged.cuh) and the unnormalised sums joined by paged_merge_rows_kernel; the
+// partials lie column by column, so a warp's 32 rows store side by side.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 2-5 set A, 6-9 set B (thread = TMEM lane = row).
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace yoco {
+
+using namespace tc;
+
+constexpr int kCD = 128;                       // head size
+constexpr int kCRows = 128;                    // rows of a set
+constexpr int kCStages = 2;
+constexpr int kCTile = kPagedTile * kCD * 2;   // 32 KB
+constexpr int kCHalf = kCTile / 2;             // 64 channels (or keys) of 128 rows
+constexpr int kCThreads = 320;
+constexpr float kCLog2e = 1.4426950408889634f;
+constexpr float kCGap = 8.f * kCLog2e;
+
+struct PagedPreSmem {
+    uint64_t q_full;
+    uint64_t kfull[kCStages], kempty[kCStages], vfull[kCStages], vempty[kCStages];
+    uint64_t s_full[2], s_free[2];          // per set
+    uint64_t p_ready[2][2], pv_done[2][2];  // per set (one set: per P buffer) and 64-key half
+    int walive[2][4];
+    uint32_t tmem_base;
+    int abort_flag;
+    int go[2];
+    PagedBlock blk;
+};
+
+constexpr size_t kCTileBytes = (size_t)3 * kCTile + (size_t)kCStages * 2 * kCTile;  // Q_A, Q_B, P, K/V rings
+constexpr size_t kCSmem = kCTileBytes + sizeof(PagedPreSmem) + 1024;
+static_assert(kCSmem <= 232448, "paged prefill tiles must fit shared memory");
+
+__device__ __forceinline__ void cbar(int id) {  // the four warps of a set
+    __syncwarp();
+    asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ uint32_t c_chunk(int r, int c) {  // 16-byte chunk c (0..15) of row r, 128-byte swizzle
+    return (uint32_t)(c >> 3) * kCHalf + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) * 16);
+}
+
+__device__ __forceinline__ uint32_t c_pack(float lo, float hi) {
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h2);
+}
+
+__device__ __forceinline__ float c_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// the low `n` of 32 bits (n clamped to [0, 32])
+__device__ __forceinline__ uint32_t c_below(int n) {
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+__global__ void __launch_bounds__(kCThreads, 1)
+paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
+                        const int32_t *__restrict__ cu, int rows, int Hq, const PagedView pv, float c2, int splits,
+                        int *err) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    uint8_t *tiles = smem_raw + pad;
+    uint8_t *sQ = tiles;                 // Q_A, Q_B
+    uint8_t *sP = tiles + 2 * kCTile;
+    uint8_t *ring = tiles + 3 * kCTile;  // stage s: K at ring + 2 s kCTile, V after it
+    PagedPreSmem &sm = *reinterpret_cast<PagedPreSmem *>(tiles + kCTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = Hq / pv.Hkv, TS = kCRows / G;
+    const int unit = blockIdx.x / splits, sp_i = blockIdx.x % splits;
+    const int hk = unit % pv.Hkv, j = unit / pv.Hkv;
+
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        for (int s = 0; s < kCStages; ++s) {
+            mbar_init(&sm.kfull[s], 1);
+            mbar_init(&sm.kempty[s], 1);
+            mbar_init(&sm.vfull[s], 1);
+            mbar_init(&sm.vempty[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sm.s_full[x], 1);
+            mbar_init(&sm.s_free[x], 4);
+            for (int hh = 0; hh < 2; ++hh) {
+                mbar_init(&sm.p_ready[x][hh], 4);
+                mbar_init(&sm.pv_done[x][hh], 1);
+            }
+        }
+        sm.abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (warp == 0) {
+        PagedBlock o;
+        paged_block(pv, cu, rows, 2 * TS, j, hk, sp_i, splits, o, err);
+        if (lane == 0) sm.blk = o;
+    }
+    __syncthreads();
+    const PagedBlock &blk = sm.blk;
+    if (blk.nrow == 0) return;
+    const int ntiles = blk.i1 - blk.i0;
+    if (ntiles == 0) {  // nothing to see: zeros
+        for (int e = tid; e < blk.nrow * G * (kCD / 8); e += kCThreads)
+            *reinterpret_cast<uint4 *>(O + ((size_t)(blk.row0 + e / (G * 16)) * Hq + hk * G) * kCD + (e % (G * 16)) * 8) =
+                make_uint4(0, 0, 0, 0);
+        return;
+    }
+    if (warp == 0) {
+        tmem_alloc(&sm.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const bool two = blk.nrow > TS;  // set B has rows
+    volatile int *abort_flag = &sm.abort_flag;
+    auto fail = [&](int code) {
+        *abort_flag = 1;
+        paged_report(err, code);
+    };
+    // P buffer and barriers of set x at tile i, and how often they were used before
+    auto p_slot = [&](int x, int i) { return two ? x : (i & 1); };
+    auto p_use = [&](int i) { return two ? i : (i >> 1); };
+    auto p_buf = [&](int i) { return !two && (i & 1) ? sQ + kCTile : sP; };
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- TMA
+        const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
+        const int mine = (lane >> 1) * psz, half = lane & 1;
+        auto look_up = [&](int i) -> int {  // this lane's box of tile i: its page, or the one past the pool
+            const int first = blk.range.key0(blk.i0 + i) + mine;
+            int page = -1;
+            if (lane < boxes && first < blk.range.hi && (first + psz > blk.range.lo || first < pv.sinks))
+                page = paged_page(pv, blk.b, first >> pv.shift, err);
+            return page < 0 ? pv.num_pages : page;
+        };
+        int nk = 0, nv = 0;  // tiles whose K / V copy was issued
+        bool ok = true;
+        auto load = [&](int i, bool is_v, int page) {
+            const int s = i % kCStages;
+            uint8_t *st = ring + (size_t)s * 2 * kCTile + (is_v ? kCTile : 0);
+            uint64_t *full = is_v ? &sm.vfull[s] : &sm.kfull[s];
+            if (i >= kCStages) ok = mbar_wait(is_v ? &sm.vempty[s] : &sm.kempty[s], ((i / kCStages) + 1) & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            if (lane == 0) mbar_arrive_expect_tx(full, kCTile);
+            __syncwarp();
+            const int row = (blk.range.key0(blk.i0 + i) + mine) & ((1 << pv.shift) - 1);
+            if (lane < boxes)
+                tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
+            ++(is_v ? nv : nk);
+        };
+        int pg0 = look_up(0), pg1 = ntiles > 1 ? look_up(1) : 0;
+        if (lane == 0) {
+            const int sets = two ? 2 : 1;
+            mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(sets * 2 * TS * G * 128));
+            for (int x = 0; x < sets; ++x)
+                for (int hf = 0; hf < 2; ++hf)
+                    tma_load_3d(sQ + x * kCTile + hf * kCHalf, &tm_q, &sm.q_full, hf * 64, hk * G, blk.row0 + x * TS);
+        }
+        // K runs one tile ahead of V: its slot is free first
+        load(0, false, pg0);
+        for (int i = 0; i < ntiles && ok; ++i) {
+            const int pg2 = i + 2 < ntiles ? look_up(i + 2) : 0;
+            if (i + 1 < ntiles) load(i + 1, false, pg1);
+            if (ok) load(i, true, pg0);
+            pg0 = pg1;
+            pg1 = pg2;
+        }
+        if (lane == 0) {
+            if (!ok) fail(51);
+            // leave no copy in flight (only the last two of each kind can be)
+            volatile int no_abort = 0;
+            mbar_wait(&sm.q_full, 0, &no_abort, 200000000ull);
+            for (int k = max(0, nk - kCStages); k < nk; ++k)
+                mbar_wait(&sm.kfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
+            for (int k = max(0, nv - kCStages); k < nv; ++k)
+                mbar_wait(&sm.vfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA
+        if (lane == 0) {
+            const uint32_t id_s = idesc_bf16_f32(kCRows, kPagedTile, false, false);  // A = Q, B = K (K-major)
+            const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);          // A = P (K-major), B = V (N-major)
+            bool ok = mbar_wait(&sm.q_full, 0, abort_flag);
+            auto issue_s = [&](int x, int i) -> bool {
+                if (i > 0 && !mbar_wait(&sm.s_free[x], (i - 1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
+                const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)(i % kCStages) * 2 * kCTile), 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t off = ((kk >> 2) * kCHalf + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + 256 * x, dq + off, dk + off, id_s, kk > 0);
+                }
+                mma_commit(&sm.s_full[x]);
+                return true;
+            };
+            auto issue_pv = [&](int x, int i) -> bool {
+                if (x == 0 && !mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag)) return false;
+                const int b = p_slot(x, i);
+                const uint64_t dp = smem_desc_sw128(smem_u32(p_buf(i)), 16, 1024);
+                const uint64_t dv =
+                    smem_desc_sw128(smem_u32(ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile), kCHalf, 1024);
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (!mbar_wait(&sm.p_ready[b][hh], p_use(i) & 1, abort_flag)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        const int kk = 4 * hh + k4;
+                        mma_ss(tmem + 256 * x + 128, dp + (uint64_t)((hh * kCHalf + k4 * 32) >> 4),
+                               dv + (uint64_t)((kk * 2048) >> 4), id_o, (i > 0 || kk > 0));
+                    }
+                    mma_commit(&sm.pv_done[b][hh]);
+                }
+                return true;
+            };
+            // S_A(0), S_B(0), then per tile i: S_A(i + 1), P_A V(i), S_B(i + 1), P_B V(i)
+            if (ok) {
+                ok = mbar_wait(&sm.kfull[0], 0, abort_flag) && issue_s(0, 0) && (!two || issue_s(1, 0));
+                if (ok) mma_commit(&sm.kempty[0]);
+            }
+            for (int i = 0; i < ntiles && ok; ++i) {
+                const bool next = i + 1 < ntiles;
+                const int s1 = (i + 1) % kCStages;
+                if (next && !(ok = mbar_wait(&sm.kfull[s1], ((i + 1) / kCStages) & 1, abort_flag))) break;
+                if (next && !(ok = issue_s(0, i + 1))) break;
+                if (next && !two) mma_commit(&sm.kempty[s1]);
+                if (!(ok = issue_pv(0, i))) break;
+                if (two) {
+                    if (next) {
+                        if (!(ok = issue_s(1, i + 1))) break;
+                        mma_commit(&sm.kempty[s1]);
+                    }
+                    if (!(ok = issue_pv(1, i))) break;
+                }
+                mma_commit(&sm.vempty[i % kCStages]);
+            }
+            if (!ok) fail(52);
+        }
+    } else if (warp < 6 || two) {
+        // ------------------------------------------ softmax, rescale, output
+        const int x = (warp - 2) / 4;  // set
+        const int q4 = warp & 3;       // TMEM lane quarter of this warp
+        const int r = q4 * 32 + lane;  // row of the set = TMEM lane
+        const int bar_id = 1 + x;
+        const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+        const uint32_t colS = 256 * x, colO = 256 * x + 128;
+        const int toks = min(TS, blk.nrow - x * TS);       // tokens of the set
+        const int set_lo = blk.pos0 + x * TS, set_hi = set_lo + toks - 1;
+        const bool used = r < toks * G;
+        const int pos = set_lo + r / G;
+        float m_ref = -INFINITY, l = 0.f;  // base-2 units
+        bool alive = true;
+        for (int i = 0; i < ntiles && alive; ++i) {
+            bool okw = true;
+            if (lane == 0) {
+                okw = mbar_wait(&sm.s_full[x], i & 1, abort_flag);
+                if (!okw) fail(53);
+                okw = okw && !*abort_flag;
+            }
+            if (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) == 0) {
+                alive = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t s_t = tmem + colS + lane_base;
+            uint32_t sv[128];
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) tmem_ld32(s_t + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * cb));
+            tmem_wait_ld();
+            // S is in registers: the MMA may write S(i + 1) over it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_free[x]);
+            const int key0 = blk.range.key0(blk.i0 + i);
+            // every row of the set sees every key of the tile
+            const bool full = key0 + kPagedTile - 1 <= set_lo &&
+                              (pv.window <= 0 || key0 > set_hi - pv.window || key0 + kPagedTile <= pv.sinks);
+            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (full) {
+#pragma unroll
+                for (int c = 0; c < kPagedTile; c += 2)
+                    mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            } else {
+                // the keys this row sees of the tile: a run up to its own position from the window's
+                // first slot on, and the sinks
+                const int hi_c = pos + 1 - key0;
+                const int lo_c = pv.window > 0 ? pos + 1 - pv.window - key0 : -1;
+                const int sk_c = min(pv.sinks - key0, hi_c);
+                uint32_t bits[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    bits[w] = (c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w);
+#pragma unroll
+                for (int c = 0; c < kPagedTile; c += 2) {
+                    const float v0 = (bits[c >> 5] & (1u << (c & 31))) ? __uint_as_float(sv[c]) : -INFINITY;
+                    const float v1 = (bits[c >> 5] & (2u << (c & 31))) ? __uint_as_float(sv[c + 1]) : -INFINITY;
+                    sv[c] = __float_as_uint(v0);
+                    sv[c + 1] = __float_as_uint(v1);
+                    mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], v0, v1);
+                }
+            }
+            // rows past the set's tokens hold whatever shared memory held: they never move the
+            // reference (no rescaling for their sake) and are never stored
+            const float mt = used ? fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * c2 : -INFINITY;
+            float alpha = 1.f;
+            const bool move = (mt > m_ref + kCGap) || (m_ref == -INFINITY && mt > -INFINITY);
+            if (move) {
+                alpha = (m_ref == -INFINITY) ? 0.f : c_ex2(m_ref - mt);
+                m_ref = mt;
+            }
+            const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
+            const uint64_t c2x2 = f2_pack(c2, c2), nmu2 = f2_pack(-mu, -mu);
+            uint64_t acc2 = f2_pack(0.f, 0.f);
+            uint32_t pk[kPagedTile / 2];
+#pragma unroll
+            for (int c = 0; c < kPagedTile / 2; ++c) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), c2x2, nmu2), x0, x1);
+                const float e0 = c_ex2(x0), e1 = c_ex2(x1);
+                acc2 = f2_add(acc2, f2_pack(e0, e1));
+                pk[c] = c_pack(e0, e1);
+            }
+            float ls0, ls1;
+            f2_unpack(acc2, ls0, ls1);
+            l = fmaf(l, alpha, ls0 + ls1);
+            // O_X holds tiles < i; rows whose reference moved rescale it before P V(i)
+            if (i > 0 && __any_sync(0xffffffffu, move)) {
+                bool ok = true;
+                if (lane == 0) ok = mbar_wait(&sm.pv_done[p_slot(x, i - 1)][1], p_use(i - 1) & 1, abort_flag);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) {
+                    if (lane == 0) fail(54);
+                } else {
+                    tc_fence_after();
+                    const uint32_t o_t = tmem + colO + lane_base;
+#pragma unroll 1
+                    for (int cb = 0; cb < 8; ++cb) {
+                        uint32_t ov[16];
+                        tmem_ld16(o_t + cb * 16, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tmem_st16(o_t + cb * 16, ov);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            // V rows that no row of the block sees: zero, once the tile has come
+            bool okb = true;
+            if (x == 0 && (key0 + kPagedTile > blk.range.hi ||
+                           (key0 < blk.range.lo && key0 + kPagedTile > pv.sinks))) {
+                if (lane == 0) okb = mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
+                okb = __shfl_sync(0xffffffffu, okb ? 1 : 0, 0) != 0;
+                const int key = key0 + r;
+                if (okb && !(key < blk.range.hi && (key >= blk.range.lo || key < pv.sinks))) {
+                    uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
+#pragma unroll 1
+                    for (int ch = 0; ch < 16; ++ch)
+                        *reinterpret_cast<uint4 *>(vr + (ch >> 3) * kCHalf + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            // the P buffer's halves are free once the product that read them last is done: with two
+            // sets the other set's latest, with one the product two tiles back
+            uint8_t *pb = p_buf(i);
+            const int b = p_slot(x, i);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                if (okb && (two ? (x == 1 || i > 0) : i > 1)) {
+                    bool ok = true;
+                    if (lane == 0)
+                        ok = two ? mbar_wait(&sm.pv_done[1 - x][hh], (x == 0 ? i - 1 : i) & 1, abort_flag)
+                                 : mbar_wait(&sm.pv_done[b][hh], (p_use(i) - 1) & 1, abort_flag);
+                    okb = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                }
+                if (!okb) break;
+#pragma unroll
+                for (int c8 = 0; c8 < kPagedTile / 16; ++c8) {
+                    const int ch = hh * (kPagedTile / 16) + c8;
+                    *reinterpret_cast<uint4 *>(pb + c_chunk(r, ch)) =
+                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready[b][hh]);
+            }
+            if (!okb) {
+                if (lane == 0) fail(55);
+                alive = false;
+                break;
+            }
+        }
+        // the set agrees on going on
+        if (lane == 0) sm.walive[x][q4] = alive ? 1 : 0;
+        cbar(bar_id);
+        alive = sm.walive[x][0] && sm.walive[x][1] && sm.walive[x][2] && sm.walive[x][3];
+        if (alive) {
+            if (r == 0) {
+                const bool ok = mbar_wait(&sm.pv_done[p_slot(x, ntiles - 1)][1], p_use(ntiles - 1) & 1, abort_flag);
+                if (!ok) fail(56);
+                sm.go[x] = ok && !*abort_flag;
+            }
+            cbar(bar_id);
+            if (sm.go[x]) {
+                tc_fence_after();
+                const uint32_t o_t = tmem + colO + lane_base;
+                if (blk.pieces > 1) {
+                    float *pp = part + (((size_t)unit * splits + sp_i) * 2 + x) * (kCD + 2) * kCRows + r;
+#pragma unroll 1
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t ov[32];
+                        tmem_ld32(o_t + cb * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) pp[(size_t)(cb * 32 + e) * kCRows] = __uint_as_float(ov[e]);
+                    }
+                    pp[(size_t)kCD * kCRows] = m_ref;
+                    pp[(size_t)(kCD + 1) * kCRows] = l;
+                } else {
+                    // o = O / l as bf16, staged in this set's Q tile (every S product is done), then rows
+                    // of 256 bytes side by side
+                    uint8_t *stg = sQ + x * kCTile;
+                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t ov[32];
+                        tmem_ld32(o_t + cb * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = c_pack(__uint_as_float(ov[8 * q + 2 * e]) * inv,
+                                              __uint_as_float(ov[8 * q + 2 * e + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(stg + c_chunk(r, cb * 4 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                    cbar(bar_id);
+                    const int ch = r & 15;
+                    for (int row = r >> 4; row < toks * G; row += 8) {
+                        const int tok = blk.row0 + x * TS + row / G, h = hk * G + row % G;
+                        if (!YOCO_DCHECK(tok < rows && h < Hq, 0x68)) continue;
+                        *reinterpret_cast<uint4 *>(O + ((size_t)tok * Hq + h) * kCD + ch * 8) =
+                            *reinterpret_cast<const uint4 *>(stg + c_chunk(row, ch));
+                    }
+                }
+                tc_fence_before();
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace yoco
+
+namespace yoco_host {
+using namespace yoco;
+
+cudaError_t paged_prefill_tc(const PagedArgs &a, float *part, int64_t units, int splits, cudaStream_t st) {
+    const PagedView pv = paged_view(a);
+    const int G = a.Hq / pv.Hkv, TS = kCRows / G;
+    CUtensorMap mq, mk, mv;
+    // Q [rows, Hq, 128] by boxes of TS tokens x G heads x 64 channels
+    const uint64_t dims[3] = {(uint64_t)kCD, (uint64_t)a.Hq, (uint64_t)a.rows};
+    const uint64_t strides[2] = {(uint64_t)kCD * 2, (uint64_t)a.Hq * kCD * 2};
+    const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)TS};
+    if (!paged_map(&mq, a.Q, 3, dims, strides, box) || !paged_kv_map(&mk, a.cache->k, a.cache) ||
+        !paged_kv_map(&mv, a.cache->v, a.cache))
+        return cudaErrorInvalidValue;
+    // the shared-memory opt-in is set on every launch (it belongs to the current device)
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.blockDim = dim3(kCThreads);
+    cfg.dynamicSmemBytes = kCSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    e = cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, part, a.cu, a.rows, a.Hq, pv,
+                           a.scale * kCLog2e, splits, a.err);
+    if (e != cudaSuccess || splits == 1) return e;
+    return paged_merge_rows(a, part, (int)units, splits, kCRows, 2, st);
+}
+
+}  // namespace yoco_host
+
+YOCO_DEBUG_TU(paged_prefill_tc)

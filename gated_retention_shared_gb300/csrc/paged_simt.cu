@@ -472,9 +472,11 @@ constexpr size_t kPagedHead = 256;                    // status word
 constexpr size_t kPagedCuts = 16384;                  // PagedCut per block of a decode grid
 constexpr int kMaxDecodeBlocks = (int)(kPagedCuts / sizeof(PagedCut));
 
-bool paged_on_tc(const yoco_paged_kv *c) { (void)c; return false; }
+// the tensor-core kernels take what fits their tiles
+static bool paged_on_tc(const yoco_paged_kv *c) { return c->dtype == YOCO_BF16 && c->d == 128; }
 
-int paged_decode_blocks(const yoco_paged_kv *c) {
+// blocks of a decode grid: what stays resident, one per SM for the tensor-core kernel
+static int paged_decode_blocks(const yoco_paged_kv *c) {
     const int per_sm = paged_on_tc(c) ? 1 : 2;
     return std::min(kMaxDecodeBlocks, per_sm * device_sm_count());
 }
@@ -553,10 +555,14 @@ static cudaError_t decode(const PagedArgs &a, cudaStream_t st) {
     const int G = a.Hq / pv.Hkv, blocks = paged_decode_blocks(a.cache);
     PagedCut *cuts = (PagedCut *)((char *)a.ws + kPagedHead);
     float *part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
-    cudaError_t e = G <= 1   ? decode_simt<T, D, 1>(a, pv, cuts, part, blocks, st)
-                    : G <= 2 ? decode_simt<T, D, 2>(a, pv, cuts, part, blocks, st)
-                    : G <= 4 ? decode_simt<T, D, 4>(a, pv, cuts, part, blocks, st)
-                             : decode_simt<T, D, kDecQ>(a, pv, cuts, part, blocks, st);
+    cudaError_t e;
+    if constexpr (sizeof(T) == 2 && D == 128)
+        e = paged_decode_tc(a, cuts, part, blocks, st);
+    else
+        e = G <= 1   ? decode_simt<T, D, 1>(a, pv, cuts, part, blocks, st)
+            : G <= 2 ? decode_simt<T, D, 2>(a, pv, cuts, part, blocks, st)
+            : G <= 4 ? decode_simt<T, D, 4>(a, pv, cuts, part, blocks, st)
+                     : decode_simt<T, D, kDecQ>(a, pv, cuts, part, blocks, st);
     if (e != cudaSuccess || blocks < 2) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
@@ -566,12 +572,8 @@ static cudaError_t decode(const PagedArgs &a, cudaStream_t st) {
 }
 
 template <typename T, int D>
-static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
-    const PagedView pv = paged_view(a);
-    const int64_t units = prefill_units(a.cache, a.Hq, a.rows, false);
-    const int splits = prefill_splits(a.cache, units, 2);
-    float *part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
-    if (units * splits > 0x7fffffff) return cudaErrorInvalidValue;
+static cudaError_t prefill_simt(const PagedArgs &a, const PagedView &pv, float *part, int64_t units, int splits,
+                                cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(paged_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)pre_smem<D>());
     if (e != cudaSuccess) return e;
@@ -583,6 +585,17 @@ static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
                            (const T *)a.cache->v, part, a.cu, a.rows, a.Hq, pv, a.scale * kPagedLog2e, splits, a.err);
     if (e != cudaSuccess || splits == 1) return e;
     return paged_merge_rows(a, part, (int)units, splits, kPreRows, 1, st);
+}
+
+template <typename T, int D>
+static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
+    constexpr bool tc = sizeof(T) == 2 && D == 128;
+    const int64_t units = prefill_units(a.cache, a.Hq, a.rows, tc);
+    const int splits = prefill_splits(a.cache, units, tc ? 1 : 2);
+    float *part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
+    if (units * splits > 0x7fffffff) return cudaErrorInvalidValue;
+    if constexpr (tc) return paged_prefill_tc(a, part, units, splits, st);
+    else return prefill_simt<T, D>(a, paged_view(a), part, units, splits, st);
 }
 
 template <typename T, int D, int R>
@@ -598,9 +611,7 @@ static cudaError_t merge_rows(const PagedArgs &a, const float *part, int units, 
 cudaError_t paged_merge_rows(const PagedArgs &a, const float *part, int units, int splits, int R, int sets,
                              cudaStream_t st) {
     if (R == 128) return merge_rows<bf16_t, 128, 128>(a, part, units, splits, sets, st);
-    if (a.cache->dtype == YOCO_BF16)
-        return a.cache->d == 64 ? merge_rows<bf16_t, 64, 64>(a, part, units, splits, sets, st)
-                                : merge_rows<bf16_t, 128, 64>(a, part, units, splits, sets, st);
+    if (a.cache->dtype == YOCO_BF16) return merge_rows<bf16_t, 64, 64>(a, part, units, splits, sets, st);
     return a.cache->d == 64 ? merge_rows<float, 64, 64>(a, part, units, splits, sets, st)
                             : merge_rows<float, 128, 64>(a, part, units, splits, sets, st);
 }
