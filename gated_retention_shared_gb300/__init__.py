@@ -426,95 +426,101 @@ class PagedKV:
         self.c = _PagedKVC(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), B, Hkv, d, page_size,
                            max_pages, num_pages, _dt(k), float(rope_base))
         self.ref = ctypes.byref(self.c)
+        # what every call's checks ask for, in plain attributes: a call of one token per sequence
+        # takes the GPU a few microseconds, so the binding must not take more
+        self._dtype, self._dev, self._B, self._Hkv, self._d = k.dtype, k.get_device(), B, Hkv, d
 
 
-def _on(t, name, cache):
-    if t.device != cache.k.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
-
-
-def _paged_call(fn, name, cache, *args, stream):
-    # the library launches on the current device; a stream belongs to its own
-    dev = cache.k.device
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), name)
-    else:
+def _paged_call(fn, name, cache, stream, *args):
+    dev = cache._dev
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:  # the library launches on the current device
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), name)
+            status = fn(*args, raw)
+    if status:
+        _check(status, name)
+
+
+def _paged_workspace(nbytes, cache, workspace):
+    """(pointer, bytes) of the caller's workspace, or of a new one that the caller's reference keeps."""
+    if workspace is None:
+        workspace = torch.empty(nbytes() if callable(nbytes) else nbytes, dtype=torch.uint8, device=cache.k.device)
+    elif workspace.get_device() != cache._dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def yoco_paged_attn_workspace_size(Hq, rows, cache: PagedKV) -> int:
     return lib.yoco_paged_attn_workspace_size(Hq, rows, cache.ref)
 
 
-def _paged_rows(cu_rows, cache):
-    if cu_rows.dtype != torch.int32 or cu_rows.shape != (cache.c.B + 1,):
-        raise ValueError("cu_rows must be int32 [B + 1]")
-    _need(cu_rows, "cu_rows")
-    _on(cu_rows, "cu_rows", cache)
+def _paged_cu(cu_rows, cache):
+    if cu_rows.dtype != torch.int32 or cu_rows.shape != (cache._B + 1,) or cu_rows.get_device() != cache._dev or \
+            not cu_rows.is_contiguous():
+        raise ValueError("cu_rows must be a contiguous int32 [B + 1] on the cache's device")
+    return cu_rows.data_ptr()
+
+
+def _paged_source(t, name, cache, heads, rows):
+    shape, stride = t.shape, t.stride()
+    if t.dtype != cache._dtype or t.get_device() != cache._dev or len(shape) != 3 or shape[2] != cache._d or \
+            stride[2] != 1 or (heads is not None and shape[1] != heads) or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be [rows, heads, {cache._d}] of {cache._dtype} with adjacent channels on the "
+                         "cache's device")
+    return shape[0], shape[1], t.data_ptr(), stride[0], stride[1]
 
 
 def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, workspace=None, stream=None):
     """k, v [rows, Hkv, d] (or both None), q [rows, Hq, d] or None, each with any strides
     that are multiples of 16 bytes; q_out [rows, Hq, d] (None: q in place).  cu_rows int32
     [B + 1], or None for one row per sequence."""
-    d, dt = cache.c.d, cache.k.dtype
-    if q is not None and q_out is None:
-        q_out = q
-    rows, args = None, []
-    for t, n, heads in ((k, "k", cache.c.Hkv), (v, "v", cache.c.Hkv), (q, "q", None)):
-        if t is None:
-            args += [None, 0, 0]
-            continue
-        if not t.is_cuda or t.dtype != dt or t.dim() != 3 or t.shape[2] != d or (d > 1 and t.stride(2) != 1) or \
-                (heads is not None and t.shape[1] != heads) or (rows is not None and t.shape[0] != rows):
-            raise ValueError(f"{n} must be a CUDA tensor [rows, heads, {d}] of {dt} with adjacent channels")
-        _on(t, n, cache)
-        rows = t.shape[0]
-        args += [t.data_ptr(), t.stride(0), t.stride(1)]
+    rows, Hq, qo = None, 0, None
+    kp = vp = qp = (None, 0, 0)
+    if k is not None:
+        rows, _, *kp = _paged_source(k, "k", cache, cache._Hkv, None)
+    if v is not None:
+        rows, _, *vp = _paged_source(v, "v", cache, cache._Hkv, rows)
+    if q is not None:
+        rows, Hq, *qp = _paged_source(q, "q", cache, None, rows)
+        if q_out is None:
+            q_out = q
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != cache._dev or \
+                not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous with q's shape and dtype on its device")
+        qo = q_out.data_ptr()
     if rows is None:
         raise ValueError("neither k and v nor q given")
-    if q is not None:
-        if q_out.shape != q.shape or q_out.dtype != dt:
-            raise ValueError("q_out must have q's shape and dtype")
-        _need(q_out, "q_out")
-        _on(q_out, "q_out", cache)
-    if cu_rows is not None:
-        _paged_rows(cu_rows, cache)
-    ws = _workspace(256, cache.k.device, workspace)
-    _paged_call(lib.yoco_paged_append, "yoco_paged_append", cache, *args, _ptr(q_out), 0 if q is None else q.shape[1],
-                _ptr(cu_rows), rows, cache.ref, _ptr(ws), ws.numel() * ws.element_size(), stream=stream)
+    cu = None if cu_rows is None else _paged_cu(cu_rows, cache)
+    ws, wp, wn = _paged_workspace(256, cache, workspace)
+    _paged_call(lib.yoco_paged_append, "yoco_paged_append", cache, stream, *kp, *vp, *qp, qo, Hq, cu, rows, cache.ref, wp,
+                wn)
 
 
 def _paged_q(Q, O, cache):
-    _need(Q, "Q")
-    _need(O, "O")
-    if Q.dim() != 3 or Q.shape != O.shape or Q.shape[2] != cache.c.d or Q.dtype != cache.k.dtype or O.dtype != Q.dtype:
-        raise ValueError(f"Q and O must be [rows, Hq, {cache.c.d}] of {cache.k.dtype}")
-    _on(Q, "Q", cache)
-    _on(O, "O", cache)
+    shape = Q.shape
+    if len(shape) != 3 or shape[2] != cache._d or O.shape != shape or Q.dtype != cache._dtype or \
+            O.dtype != cache._dtype or Q.get_device() != cache._dev or O.get_device() != cache._dev or \
+            not Q.is_contiguous() or not O.is_contiguous():
+        raise ValueError(f"Q and O must be contiguous [rows, Hq, {cache._d}] of {cache._dtype} on the cache's device")
+    return shape[0], shape[1]
 
 
 def yoco_paged_attn_prefill(Q, cache: PagedKV, cu_rows, O, scale=None, window=0, sinks=0, workspace=None, stream=None):
     """Q, O [rows, Hq, d]; rows cu_rows[b] .. cu_rows[b + 1] - 1 are sequence b's newest."""
-    _paged_q(Q, O, cache)
-    _paged_rows(cu_rows, cache)
-    rows, Hq, d = Q.shape
-    ws = workspace if workspace is not None else _workspace(
-        lib.yoco_paged_attn_workspace_size(Hq, rows, cache.ref), Q.device, None)
-    _paged_call(lib.yoco_paged_attn_prefill, "yoco_paged_attn_prefill", cache, _ptr(Q), Hq, _ptr(cu_rows), rows,
-                cache.ref, d ** -0.5 if scale is None else scale, window, sinks, _ptr(O), _ptr(ws),
-                0 if ws is None else ws.numel() * ws.element_size(), stream=stream)
+    rows, Hq = _paged_q(Q, O, cache)
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace)
+    _paged_call(lib.yoco_paged_attn_prefill, "yoco_paged_attn_prefill", cache, stream, Q.data_ptr(), Hq,
+                _paged_cu(cu_rows, cache), rows, cache.ref, cache._d ** -0.5 if scale is None else scale, window, sinks,
+                O.data_ptr(), wp, wn)
 
 
 def yoco_paged_attn_decode(Q, cache: PagedKV, O, scale=None, window=0, sinks=0, workspace=None, stream=None):
     """Q, O [B, Hq, d]: one row per sequence, at position seq_lens[b] - 1."""
-    _paged_q(Q, O, cache)
-    rows, Hq, d = Q.shape
-    if rows != cache.c.B:
-        raise ValueError(f"Q has {rows} rows, the cache {cache.c.B} sequences")
-    ws = workspace if workspace is not None else _workspace(
-        lib.yoco_paged_attn_workspace_size(Hq, rows, cache.ref), Q.device, None)
-    _paged_call(lib.yoco_paged_attn_decode, "yoco_paged_attn_decode", cache, _ptr(Q), Hq, cache.ref,
-                d ** -0.5 if scale is None else scale, window, sinks, _ptr(O), _ptr(ws),
-                0 if ws is None else ws.numel() * ws.element_size(), stream=stream)
+    rows, Hq = _paged_q(Q, O, cache)
+    if rows != cache._B:
+        raise ValueError(f"Q has {rows} rows, the cache {cache._B} sequences")
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace)
+    _paged_call(lib.yoco_paged_attn_decode, "yoco_paged_attn_decode", cache, stream, Q.data_ptr(), Hq, cache.ref,
+                cache._d ** -0.5 if scale is None else scale, window, sinks, O.data_ptr(), wp, wn)

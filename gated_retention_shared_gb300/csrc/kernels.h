@@ -14,6 +14,7 @@ namespace yoco_host {
 // can be queried (workspace-size queries on a machine without a GPU).
 constexpr int kDefaultSmCount = 152;
 int device_sm_count();
+int64_t device_l2_bytes();  // of the current device, queried once; 0 where none can be
 
 // Test hooks (yoco_test_hook): process-wide values that tests set to reach paths
 // ordinary inputs cannot force; all are 0 (off) unless a test sets them.
@@ -141,11 +142,14 @@ cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st);
 cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st);
 // paged_decode_tc.cu: bf16, d = 128; cuts and part as paged_decode lays them out
 cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blocks, cudaStream_t st);
-// paged_prefill_tc.cu: bf16, d = 128; row blocks x kv heads `units`, keys in `splits`
-cudaError_t paged_prefill_tc(const PagedArgs &a, float *part, int64_t units, int splits, cudaStream_t st);
-// the row blocks' splits of the keys into the output: R rows to a set, `sets` sets to a block
-cudaError_t paged_merge_rows(const PagedArgs &a, const float *part, int units, int splits, int R, int sets,
-                             cudaStream_t st);
+// paged_prefill_tc.cu: bf16, d = 128
+struct PagedGrid {  // of a prefill, and where its pieces' partial results go
+    int64_t blocks;
+    int slots, max_split;  // blocks resident at a time, pieces there may be
+    int *plan_q;
+    float *part;
+};
+cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
 
 // debug builds: each kernel file's debug word (see YOCO_DEBUG_TU in common.cuh)
 #define YOCO_DEBUG_TUS(X) X(attn) X(attn_fa) X(attn_tc) X(gn_gate) X(gret_simt) X(gret_tc) X(kv_proj) \

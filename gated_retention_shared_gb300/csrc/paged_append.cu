@@ -162,6 +162,21 @@ static cudaError_t append_launch(const PagedAppend &p, const PagedView &pv, cons
     return cudaGetLastError();
 }
 
+// The turns of a base and head size; a thread keeps the last ones (64 powers take longer
+// than the rest of the call).
+static const RopeTurns &rope_turns(float base, int d) {
+    static thread_local RopeTurns t{};
+    static thread_local float t_base = 0.f;
+    static thread_local int t_d = 0;
+    if (base != t_base || d != t_d) {
+        const RopeFreq f = make_rope_freq(base, d);
+        for (int i = 0; i < 64; ++i) t.f[i] = (uint64_t)std::ldexp(f.theta[i] / kRopeTwoPi, 64);
+        t_base = base;
+        t_d = d;
+    }
+    return t;
+}
+
 cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t st) {
     const int es = a.cache->dtype == YOCO_BF16 ? 2 : 4, d = a.cache->d;
     PagedAppend p{};
@@ -182,11 +197,7 @@ cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t 
     p.Hq = a.Hq;
     p.err = a.err;
     p.turn = a.cache->rope_base > 0.f;
-    RopeTurns t{};
-    if (p.turn) {
-        const RopeFreq f = make_rope_freq(a.cache->rope_base, d);
-        for (int i = 0; i < d / 2; ++i) t.f[i] = (uint64_t)std::ldexp(f.theta[i] / kRopeTwoPi, 64);
-    }
+    const RopeTurns &t = rope_turns(a.cache->rope_base, d);
     const PagedView pv = paged_view(a);
     if (es == 2) return d == 64 ? append_launch<bf16_t, 64>(p, pv, t, st) : append_launch<bf16_t, 128>(p, pv, t, st);
     return d == 64 ? append_launch<float, 64>(p, pv, t, st) : append_launch<float, 128>(p, pv, t, st);

@@ -137,14 +137,15 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         const int boxes = 2 * (kPagedTile / psz);        // per tile: (page, 64-channel half)
         const uint64_t pol_keep = l2_policy_evict_normal(), pol_stream = l2_policy_evict_first();
         PagedRange range{};
-        int t = 0, key0 = 0, page = 0;
+        int t = 0, slot = 0, page = 0;
         // this lane's box of the tile at (w, t): its page, or the one past the pool
         auto look_up = [&]() {
-            key0 = range.key0(t);
-            const int first = key0 + (lane >> 1) * psz;
+            const int v = t * kPagedTile + (lane >> 1) * psz;
             page = -1;
-            if (lane < boxes && first < range.hi && (first + psz > range.lo || first < pv.sinks))
-                page = paged_page(pv, w.b, first >> pv.shift, err);
+            if (lane < boxes && v < range.places) {
+                slot = range.slot(v);
+                page = paged_page(pv, w.b, slot >> pv.shift, err);
+            }
             if (page < 0) page = pv.num_pages;
         };
         auto enter = [&]() {
@@ -161,7 +162,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         for (; more; ++i) {
             const int s = i % kPStages;
             const uint32_t par = ((i / kPStages) + 1) & 1;
-            const int my_page = page, my_row = (key0 + (lane >> 1) * psz) & ((1 << pv.shift) - 1), hk = w.hk;
+            const int my_page = page, my_row = slot & ((1 << pv.shift) - 1), hk = w.hk;
             if (++t == w.t1) {
                 more = w.next(pv, pre);
                 if (more) enter();
@@ -363,8 +364,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 tmem_ld16(tmem + kPColS + 16 * (i & 1) + lane_base, sv);
                 tmem_wait_ld();
                 tc_fence_before();
-                const int key0 = range.key0(t), key = key0 + r;
-                const bool seen = key < range.hi && (key >= range.lo || key < pv.sinks);
+                const bool seen = range.seen(range.slot(t * kPagedTile + r), pv.sinks);
                 float sc[NQ];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
@@ -375,7 +375,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     if (lane == 0) sm.wmax[q4][n] = x;
                 }
                 // V rows out of sight: zero, once the tile has come
-                const bool edge = key0 + kPagedTile > range.hi || (key0 < range.lo && key0 + kPagedTile > pv.sinks);
+                const bool edge = range.edge(t, pv.sinks);
                 if (edge && r == 0) {
                     const bool ok = mbar_wait(&sm.full_v[i % kPStages], (i / kPStages) & 1, abort_flag);
                     if (!ok) fail(46);
@@ -494,9 +494,7 @@ cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blo
     const PagedView pv = paged_view(a);
     // pages up to half the L2's size keep normal priority and stay cached for the next layer's
     // call over the same pool, the rest streams through
-    int dev = 0, l2 = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) != cudaSuccess)
-        l2 = 0;
+    const int64_t l2 = device_l2_bytes();
     const int64_t page_bytes = (int64_t)a.cache->page_size * a.cache->Hkv * kPD * 2 * 2;
     const int keep = (int)(l2 / 2 / page_bytes);
     const int G = a.Hq / pv.Hkv;

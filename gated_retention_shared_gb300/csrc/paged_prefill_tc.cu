@@ -20,7 +20,7 @@
 //
 // Pages, rows out of sight and pages that are not there: as in paged_decode_tc.cu; set A's
 // warps clear the V rows that no row of the block sees.  With few row blocks the keys are
-// split (paged.cuh) and the unnormalised sums joined by paged_merge_rows_kernel; the
+// cut into pieces (paged.cuh) and the unnormalised sums joined by paged_merge_rows_kernel; the
 // partials lie column by column, so a warp's 32 rows store side by side.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2-5 set A, 6-9 set B (thread = TMEM lane = row).
@@ -88,8 +88,8 @@ __device__ __forceinline__ uint32_t c_below(int n) {
 __global__ void __launch_bounds__(kCThreads, 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
-                        const int32_t *__restrict__ cu, int rows, int Hq, const PagedView pv, float c2, int splits,
-                        int *err) {
+                        const int32_t *__restrict__ cu, int rows, int Hq, const PagedView pv, float c2, int slots,
+                        int max_split, int *plan_q, int *err) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
@@ -99,8 +99,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     PagedPreSmem &sm = *reinterpret_cast<PagedPreSmem *>(tiles + kCTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = Hq / pv.Hkv, TS = kCRows / G;
-    const int unit = blockIdx.x / splits, sp_i = blockIdx.x % splits;
-    const int hk = unit % pv.Hkv, j = unit / pv.Hkv;
 
     if (tid == 0) {
         mbar_init(&sm.q_full, 1);
@@ -128,12 +126,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (warp == 0) {
         PagedBlock o;
-        paged_block(pv, cu, rows, 2 * TS, j, hk, sp_i, splits, o, err);
+        const PagedSeq s = paged_seq(pv, cu, rows, 2 * TS, pv.B - 1 - lane, err);
+        const int tiles_q = paged_plan(pv, cu, rows, 2 * TS, slots, max_split, s, err);
+        paged_block<false>(pv, cu, rows, 2 * TS, tiles_q, blockIdx.x, s, o, err);
         if (lane == 0) sm.blk = o;
+        if (blockIdx.x == 0 && lane == 0) *plan_q = tiles_q;
     }
     __syncthreads();
     const PagedBlock &blk = sm.blk;
     if (blk.nrow == 0) return;
+    const int hk = blk.hk;
     const int ntiles = blk.i1 - blk.i0;
     if (ntiles == 0) {  // nothing to see: zeros
         for (int e = tid; e < blk.nrow * G * (kCD / 8); e += kCThreads)
@@ -165,10 +167,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
         const int mine = (lane >> 1) * psz, half = lane & 1;
         auto look_up = [&](int i) -> int {  // this lane's box of tile i: its page, or the one past the pool
-            const int first = blk.range.key0(blk.i0 + i) + mine;
+            const int v = (blk.i0 + i) * kPagedTile + mine;
             int page = -1;
-            if (lane < boxes && first < blk.range.hi && (first + psz > blk.range.lo || first < pv.sinks))
-                page = paged_page(pv, blk.b, first >> pv.shift, err);
+            if (lane < boxes && v < blk.range.places) page = paged_page(pv, blk.b, blk.range.slot(v) >> pv.shift, err);
             return page < 0 ? pv.num_pages : page;
         };
         int nk = 0, nv = 0;  // tiles whose K / V copy was issued
@@ -182,7 +183,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (!ok) return;
             if (lane == 0) mbar_arrive_expect_tx(full, kCTile);
             __syncwarp();
-            const int row = (blk.range.key0(blk.i0 + i) + mine) & ((1 << pv.shift) - 1);
+            const int row = blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
             if (lane < boxes)
                 tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
             ++(is_v ? nv : nk);
@@ -287,6 +288,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int set_lo = blk.pos0 + x * TS, set_hi = set_lo + toks - 1;
         const bool used = r < toks * G;
         const int pos = set_lo + r / G;
+        const int sink_slots = blk.range.sink_slots, delta = blk.range.base - sink_slots;
         float m_ref = -INFINITY, l = 0.f;  // base-2 units
         bool alive = true;
         for (int i = 0; i < ntiles && alive; ++i) {
@@ -310,9 +312,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.s_free[x]);
-            const int key0 = blk.range.key0(blk.i0 + i);
-            // every row of the set sees every key of the tile
-            const bool full = key0 + kPagedTile - 1 <= set_lo &&
+            // place 0 of the tile, and what its slot is where it lies past the sinks' chunks
+            const int v0 = (blk.i0 + i) * kPagedTile, key0 = v0 + delta;
+            // every row of the set sees every slot of the tile
+            const bool full = v0 >= sink_slots && key0 + kPagedTile - 1 <= set_lo &&
                               (pv.window <= 0 || key0 > set_hi - pv.window || key0 + kPagedTile <= pv.sinks);
             float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (full) {
@@ -320,15 +323,17 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 for (int c = 0; c < kPagedTile; c += 2)
                     mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
             } else {
-                // the keys this row sees of the tile: a run up to its own position from the window's
-                // first slot on, and the sinks
+                // the places this row sees of the tile: sinks in the sinks' chunks, then a run up to its
+                // own position from the window's first slot on, and sinks that lie in those chunks
                 const int hi_c = pos + 1 - key0;
                 const int lo_c = pv.window > 0 ? pos + 1 - pv.window - key0 : -1;
                 const int sk_c = min(pv.sinks - key0, hi_c);
+                const int ch_c = sink_slots - v0, sc_c = min(ch_c, min(pv.sinks, pos + 1) - v0);
                 uint32_t bits[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    bits[w] = (c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w);
+                    bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w)) &
+                               ~c_below(ch_c - 32 * w)) | c_below(sc_c - 32 * w);
 #pragma unroll
                 for (int c = 0; c < kPagedTile; c += 2) {
                     const float v0 = (bits[c >> 5] & (1u << (c & 31))) ? __uint_as_float(sv[c]) : -INFINITY;
@@ -386,12 +391,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             }
             // V rows that no row of the block sees: zero, once the tile has come
             bool okb = true;
-            if (x == 0 && (key0 + kPagedTile > blk.range.hi ||
-                           (key0 < blk.range.lo && key0 + kPagedTile > pv.sinks))) {
+            if (x == 0 && blk.range.edge(blk.i0 + i, pv.sinks)) {
                 if (lane == 0) okb = mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
                 okb = __shfl_sync(0xffffffffu, okb ? 1 : 0, 0) != 0;
-                const int key = key0 + r;
-                if (okb && !(key < blk.range.hi && (key >= blk.range.lo || key < pv.sinks))) {
+                if (okb && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
 #pragma unroll 1
                     for (int ch = 0; ch < 16; ++ch)
@@ -444,7 +447,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tc_fence_after();
                 const uint32_t o_t = tmem + colO + lane_base;
                 if (blk.pieces > 1) {
-                    float *pp = part + (((size_t)unit * splits + sp_i) * 2 + x) * (kCD + 2) * kCRows + r;
+                    float *pp = part + ((size_t)blk.slot * 2 + x) * (kCD + 2) * kCRows + r;
 #pragma unroll 1
                     for (int cb = 0; cb < 4; ++cb) {
                         uint32_t ov[32];
@@ -500,9 +503,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 namespace yoco_host {
 using namespace yoco;
 
-cudaError_t paged_prefill_tc(const PagedArgs &a, float *part, int64_t units, int splits, cudaStream_t st) {
-    const PagedView pv = paged_view(a);
-    const int G = a.Hq / pv.Hkv, TS = kCRows / G;
+cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
+    const int G = a.Hq / a.cache->Hkv, TS = kCRows / G;
     CUtensorMap mq, mk, mv;
     // Q [rows, Hq, 128] by boxes of TS tokens x G heads x 64 channels
     const uint64_t dims[3] = {(uint64_t)kCD, (uint64_t)a.Hq, (uint64_t)a.rows};
@@ -515,7 +517,7 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, float *part, int64_t units, int
     cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.gridDim = dim3((unsigned)g.blocks);
     cfg.blockDim = dim3(kCThreads);
     cfg.dynamicSmemBytes = kCSmem;
     cfg.stream = st;
@@ -525,10 +527,8 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, float *part, int64_t units, int
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    e = cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, part, a.cu, a.rows, a.Hq, pv,
-                           a.scale * kCLog2e, splits, a.err);
-    if (e != cudaSuccess || splits == 1) return e;
-    return paged_merge_rows(a, part, (int)units, splits, kCRows, 2, st);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, g.part, a.cu, a.rows, a.Hq,
+                              paged_view(a), a.scale * kCLog2e, g.slots, g.max_split, g.plan_q, a.err);
 }
 
 }  // namespace yoco_host

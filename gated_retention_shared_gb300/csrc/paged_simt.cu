@@ -100,8 +100,8 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                 bool ok[kDecKeys];
 #pragma unroll
                 for (int x = 0; x < kDecKeys; ++x) {
-                    const int key = range.key0(w.t0 + (st + x) / 4) + ((st + x) % 4) * 32 + grp;
-                    ok[x] = key < range.hi && (key >= range.lo || key < pv.sinks);
+                    const int key = range.slot(w.t0 * kPagedTile + (st + x) * 32 + grp);
+                    ok[x] = range.seen(key, pv.sinks);
                     const int page = ok[x] ? paged_page(pv, w.b, key >> pv.shift, err) : -1;
                     const size_t at = (((size_t)max(page, 0) * pv.Hkv + w.hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
 #pragma unroll
@@ -250,7 +250,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 2)
 paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
                           float *__restrict__ part, const int32_t *__restrict__ cu, int rows, int Hq,
-                          const PagedView pv, float c2, int splits, int *err) {
+                          const PagedView pv, float c2, int slots, int max_split, int *plan_q, int *err) {
     constexpr int EV = 16 / (int)sizeof(T), NJ = D / 64;
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4);
@@ -258,16 +258,19 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     __shared__ PagedBlock blk;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int G = Hq / pv.Hkv, TS = kPreRows / G;
-    const int hk = (blockIdx.x / splits) % pv.Hkv, sp_i = blockIdx.x % splits, j = blockIdx.x / splits / pv.Hkv;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (tid < 32) {
         PagedBlock o;
-        paged_block(pv, cu, rows, TS, j, hk, sp_i, splits, o, err);
+        const PagedSeq s = paged_seq(pv, cu, rows, TS, pv.B - 1 - tid, err);
+        const int tiles_q = paged_plan(pv, cu, rows, TS, slots, max_split, s, err);
+        paged_block<false>(pv, cu, rows, TS, tiles_q, blockIdx.x, s, o, err);
         if (tid == 0) blk = o;
+        if (blockIdx.x == 0 && tid == 0) *plan_q = tiles_q;
     }
     __syncthreads();
     if (blk.nrow == 0) return;
+    const int hk = blk.hk;
     const int nr = blk.nrow * G;  // rows in use: (token, head) = (r / G, r % G)
     const size_t row_stride = (size_t)Hq * D;
     for (int e = tid; e < kPreRows * (D / EV); e += kPreThreads) {
@@ -288,14 +291,14 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         for (int e = 0; e < 4 * NJ; ++e) acc[i][e] = 0.f;
     }
     for (int t2 = 2 * blk.i0; t2 < 2 * blk.i1; ++t2) {
-        const int key0 = blk.range.key0(t2 >> 1) + (t2 & 1) * kPreKeys;
+        const int v0 = t2 * kPreKeys;
         __syncthreads();
         for (int e = tid; e < kPreKeys * (D / EV); e += kPreThreads) {
-            const int r = e / (D / EV), ch = e % (D / EV), key = key0 + r;
+            const int r = e / (D / EV), ch = e % (D / EV), key = blk.range.slot(v0 + r);
             float x[EV], y[EV];
 #pragma unroll
             for (int i = 0; i < EV; ++i) x[i] = y[i] = 0.f;
-            if (key < blk.range.hi && (key >= blk.range.lo || key < pv.sinks)) {
+            if (blk.range.seen(key, pv.sinks)) {
                 const int page = paged_page(pv, blk.b, key >> pv.shift, err);
                 if (page >= 0) {
                     const size_t at = (((size_t)page * pv.Hkv + hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
@@ -334,7 +337,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
             float top = m[i];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int key = key0 + tx + 16 * x;
+                const int key = blk.range.slot(v0 + tx + 16 * x);
                 const bool seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
                 if (!seen) s[i][x] = -INFINITY;
                 top = fmaxf(top, s[i][x]);
@@ -387,8 +390,8 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
-        if (blk.pieces > 1) {  // [unit][split][D + 2][row]
-            float *pp = part + ((size_t)(j * pv.Hkv + hk) * splits + sp_i) * (D + 2) * kPreRows + r;
+        if (blk.pieces > 1) {  // [slot][D + 2][row]
+            float *pp = part + (size_t)blk.slot * (D + 2) * kPreRows + r;
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
 #pragma unroll
@@ -409,30 +412,34 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     }
 }
 
-// Joins the splits of a row block's keys: partials [unit][split][set][D + 2][R], one CTA per
-// (unit, set) and 32 head dims, thread = row.
+// Joins the pieces of a row block: partials [slot][set][D + 2][R], one CTA per (row block and
+// kv head that is cut, set) and 32 head dims, thread = row.
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(R)
 paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const int32_t *__restrict__ cu, int rows,
-                        int Hq, const PagedView pv, int splits, int sets, int *err) {
+                        int Hq, const PagedView pv, const int *__restrict__ plan_q, int sets, int *err) {
     __shared__ PagedBlock blk;
     const int r = threadIdx.x, G = Hq / pv.Hkv, TS = R / G;
-    const int set = blockIdx.x % sets, unit = blockIdx.x / sets, hk = unit % pv.Hkv, d0 = blockIdx.y * 32;
+    const int set = blockIdx.x % sets, d0 = blockIdx.y * 32;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int tiles_q = *plan_q;
+    if (tiles_q == kPagedNoSplit) return;
     if (r < 32) {
         PagedBlock o;
-        paged_block(pv, cu, rows, TS * sets, unit / pv.Hkv, hk, 0, splits, o, err);
+        const PagedSeq s = paged_seq(pv, cu, rows, TS * sets, pv.B - 1 - r, err);
+        paged_block<true>(pv, cu, rows, TS * sets, tiles_q, blockIdx.x / sets, s, o, err);
         if (r == 0) blk = o;
     }
     __syncthreads();
+    const int hk = blk.hk;
     const int tok = set * TS + r / G;
     if (blk.nrow == 0 || blk.pieces == 1 || r >= TS * G || tok >= blk.nrow) return;
     float M = -INFINITY, L = 0.f, A[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) A[e] = 0.f;
     for (int s = 0; s < blk.pieces; ++s) {
-        const float *pp = part + (((size_t)unit * splits + s) * sets + set) * (D + 2) * R + r;
+        const float *pp = part + (((size_t)blk.slot + (size_t)s * blk.stride) * sets + set) * (D + 2) * R + r;
         const float m = __ldcg(pp + D * R), l = __ldcg(pp + (D + 1) * R);
         float x[32];
 #pragma unroll
@@ -468,56 +475,38 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
 namespace yoco_host {
 using namespace yoco;
 
-constexpr size_t kPagedHead = 256;                    // status word
-constexpr size_t kPagedCuts = 16384;                  // PagedCut per block of a decode grid
+// workspace: status word, Q of a prefill, cuts of a decode, then partial results
+constexpr size_t kPagedPlan = 128;
+constexpr size_t kPagedHead = 256;
+constexpr size_t kPagedCuts = 16384;  // PagedCut per block of a decode grid
 constexpr int kMaxDecodeBlocks = (int)(kPagedCuts / sizeof(PagedCut));
 
 // the tensor-core kernels take what fits their tiles
 static bool paged_on_tc(const yoco_paged_kv *c) { return c->dtype == YOCO_BF16 && c->d == 128; }
 
-// blocks of a decode grid: what stays resident, one per SM for the tensor-core kernel
-static int paged_decode_blocks(const yoco_paged_kv *c) {
-    const int per_sm = paged_on_tc(c) ? 1 : 2;
-    return std::min(kMaxDecodeBlocks, per_sm * device_sm_count());
-}
+// resident blocks of the decode and prefill kernels: one per SM of the tensor-core ones
+static int paged_slots(const yoco_paged_kv *c) { return (paged_on_tc(c) ? 1 : 2) * device_sm_count(); }
+static int paged_decode_blocks(const yoco_paged_kv *c) { return std::min(kMaxDecodeBlocks, paged_slots(c)); }
 
-// rows of a prefill block, and its partial results per split
-static int pre_rows(bool tc) { return tc ? 256 : kPreRows; }
-
-static int64_t prefill_units(const yoco_paged_kv *c, int Hq, int rows, bool tc) {
-    const int G = Hq / c->Hkv, TR = tc ? 2 * (128 / G) : kPreRows / G;
+// (row block, kv head) pairs of a prefill, at most; and pieces of such that there may be
+static int64_t prefill_units(const yoco_paged_kv *c, int Hq, int rows) {
+    const int G = Hq / c->Hkv, TR = paged_on_tc(c) ? 2 * (128 / G) : kPreRows / G;
     const int64_t blocks = c->B == 1 ? ((int64_t)rows + TR - 1) / TR : (int64_t)rows / TR + std::min(c->B, rows);
     return std::max<int64_t>(blocks, 1) * c->Hkv;
 }
 
-// Key splits of a prefill: none while the row blocks alone give every SM two blocks, else
-// the smallest count whose last wave is at least 95 % full, a split being four tiles or more.
-static int prefill_splits(const yoco_paged_kv *c, int64_t units, int per_sm) {
-    const int64_t slots = (int64_t)per_sm * device_sm_count();
+// No cuts where the row blocks alone come to eight rounds, else up to three rounds of pieces
+static int prefill_max_split(const yoco_paged_kv *c, int64_t units) {
+    const int64_t slots = paged_slots(c);
     const int64_t tiles = ((int64_t)c->max_pages * c->page_size + kPagedTile - 1) / kPagedTile;
-    const int64_t cap = std::min<int64_t>(64, (tiles + kPagedMinTiles - 1) / kPagedMinTiles);
-    if (units >= 2 * slots || cap <= 1) return 1;
-    int64_t best = 1;
-    double best_eff = -1.0;
-    for (int64_t s = std::min(cap, (slots + units - 1) / units); s <= std::min(cap, 4 * ((slots + units - 1) / units)); ++s) {
-        const int64_t n = units * s;
-        const double eff = (double)n / (double)(slots * ((n + slots - 1) / slots));
-        if (eff >= 0.95) return (int)s;
-        if (eff > best_eff) {
-            best_eff = eff;
-            best = s;
-        }
-    }
-    return (int)best;
+    if (units >= 8 * slots || tiles <= kPagedMinPiece) return 0;
+    return (int)std::min(3 * slots, units * ((tiles + kPagedMinPiece - 1) / kPagedMinPiece));
 }
 
 size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows) {
-    const int G = Hq / c->Hkv;
-    const size_t dec = (size_t)paged_decode_blocks(c) * 2 * G * (c->d + 2) * sizeof(float);
-    const bool tc = paged_on_tc(c);
-    const int64_t units = prefill_units(c, Hq, rows, tc);
-    const int splits = prefill_splits(c, units, tc ? 1 : 2);
-    const size_t pre = splits > 1 ? (size_t)units * splits * pre_rows(tc) * (c->d + 2) * sizeof(float) : 0;
+    const size_t dec = (size_t)paged_decode_blocks(c) * 2 * (Hq / c->Hkv) * (c->d + 2) * sizeof(float);
+    const size_t pre = (size_t)prefill_max_split(c, prefill_units(c, Hq, rows)) * (paged_on_tc(c) ? 256 : kPreRows) *
+                       (c->d + 2) * sizeof(float);
     return kPagedHead + kPagedCuts + std::max(dec, pre);
 }
 
@@ -572,48 +561,43 @@ static cudaError_t decode(const PagedArgs &a, cudaStream_t st) {
 }
 
 template <typename T, int D>
-static cudaError_t prefill_simt(const PagedArgs &a, const PagedView &pv, float *part, int64_t units, int splits,
-                                cudaStream_t st) {
+static cudaError_t prefill_simt(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(paged_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)pre_smem<D>());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    pdl_config(cfg, attr, dim3((unsigned)(units * splits)), kPreThreads, pre_smem<D>(), st);
+    pdl_config(cfg, attr, dim3((unsigned)g.blocks), kPreThreads, pre_smem<D>(), st);
     count_launches(1);
-    e = cudaLaunchKernelEx(&cfg, paged_prefill_simt_kernel<T, D>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
-                           (const T *)a.cache->v, part, a.cu, a.rows, a.Hq, pv, a.scale * kPagedLog2e, splits, a.err);
-    if (e != cudaSuccess || splits == 1) return e;
-    return paged_merge_rows(a, part, (int)units, splits, kPreRows, 1, st);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_simt_kernel<T, D>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
+                              (const T *)a.cache->v, g.part, a.cu, a.rows, a.Hq, paged_view(a), a.scale * kPagedLog2e,
+                              g.slots, g.max_split, g.plan_q, a.err);
 }
 
 template <typename T, int D>
 static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
     constexpr bool tc = sizeof(T) == 2 && D == 128;
-    const int64_t units = prefill_units(a.cache, a.Hq, a.rows, tc);
-    const int splits = prefill_splits(a.cache, units, tc ? 1 : 2);
-    float *part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
-    if (units * splits > 0x7fffffff) return cudaErrorInvalidValue;
-    if constexpr (tc) return paged_prefill_tc(a, part, units, splits, st);
-    else return prefill_simt<T, D>(a, paged_view(a), part, units, splits, st);
-}
-
-template <typename T, int D, int R>
-static cudaError_t merge_rows(const PagedArgs &a, const float *part, int units, int splits, int sets, cudaStream_t st) {
+    constexpr int R = tc ? 128 : kPreRows, sets = tc ? 2 : 1;
+    const int64_t units = prefill_units(a.cache, a.Hq, a.rows);
+    PagedGrid g{};
+    g.slots = paged_slots(a.cache);
+    g.max_split = prefill_max_split(a.cache, units);
+    if (units + g.max_split > 0x7fffffff) return cudaErrorInvalidValue;
+    g.blocks = units + g.max_split;
+    g.plan_q = (int *)((char *)a.ws + kPagedPlan);
+    g.part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
+    cudaError_t e;
+    if constexpr (tc) e = paged_prefill_tc(a, g, st);
+    else e = prefill_simt<T, D>(a, g, st);
+    if (e != cudaSuccess || g.max_split == 0) return e;
+    // what is cut has two pieces or more
+    const int64_t cut = std::min<int64_t>(units, g.max_split / 2);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    pdl_config(cfg, attr, dim3((unsigned)(units * sets), D / 32), R, 0, st);
+    pdl_config(cfg, attr, dim3((unsigned)(cut * sets), D / 32), R, 0, st);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, part, (T *)a.O, a.cu, a.rows, a.Hq, paged_view(a),
-                              splits, sets, a.err);
-}
-
-cudaError_t paged_merge_rows(const PagedArgs &a, const float *part, int units, int splits, int R, int sets,
-                             cudaStream_t st) {
-    if (R == 128) return merge_rows<bf16_t, 128, 128>(a, part, units, splits, sets, st);
-    if (a.cache->dtype == YOCO_BF16) return merge_rows<bf16_t, 64, 64>(a, part, units, splits, sets, st);
-    return a.cache->d == 64 ? merge_rows<float, 64, 64>(a, part, units, splits, sets, st)
-                            : merge_rows<float, 128, 64>(a, part, units, splits, sets, st);
+    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, (const float *)g.part, (T *)a.O, a.cu, a.rows, a.Hq,
+                              paged_view(a), (const int *)g.plan_q, sets, a.err);
 }
 
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st) {
