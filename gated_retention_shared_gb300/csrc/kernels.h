@@ -143,6 +143,8 @@ cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st);
 // paged_decode_tc.cu: bf16, d = 128; cuts and part as paged_decode lays them out
 cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blocks, cudaStream_t st);
 // paged_prefill_tc.cu: bf16, d = 128
+constexpr int kPagedMinPiece = 2;       // tiles
+constexpr float kPagedBlockCost = 5.f;  // a block's start and end, in tiles: 6-7 us
 struct PagedGrid {  // of a prefill, and where its pieces' partial results go
     int64_t blocks;
     int slots, max_split;  // blocks resident at a time, pieces there may be

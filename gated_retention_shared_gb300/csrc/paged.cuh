@@ -125,9 +125,6 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedView &pv, const int32_t
 __device__ __forceinline__ int paged_pieces(const PagedSeq &s, int Q) { return max(1, (s.tiles + Q - 1) / Q); }
 
 constexpr int kPagedNoSplit = 1 << 30;
-constexpr int kPagedMinPiece = 2;     // tiles
-constexpr float kPagedBlockCost = 5;  // what a thread block costs beside its tiles, in tiles (measured: 6-7 us)
-
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -135,13 +132,15 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // Q for the call; one whole warp, `s` its lanes' sequences B - 1 - lane.  `slots` blocks are
-// resident at a time, at most max_split may be pieces of something.  Nothing is cut where
+// resident at a time, at most max_split may be pieces of something; a piece has min_piece
+// tiles or more, and a block costs block_cost tiles beside its own.  Nothing is cut where
 // the row blocks keep the slots busy for two rounds and none is longer than a slot's share.
 // Else the smallest Q with which all blocks fit one, two or three rounds of `slots` is
 // compared with no cut: by the tiles and blocks to a slot, the last round's idle part, and
 // never less than the longest block.
 __device__ __forceinline__ int paged_plan(const PagedView &pv, const int32_t *cu, int rows, int T_R, int slots,
-                                          int max_split, const PagedSeq &s, int *err) {
+                                          int max_split, int min_piece, float block_cost, const PagedSeq &s,
+                                          int *err) {
     if (max_split == 0) return kPagedNoSplit;
     const int lane = threadIdx.x & 31;
     int units = s.blocks * pv.Hkv, longest = s.tiles;
@@ -157,21 +156,21 @@ __device__ __forceinline__ int paged_plan(const PagedView &pv, const int32_t *cu
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (units >= 2 * slots && (float)longest * (float)slots <= W) return kPagedNoSplit;
     if (pv.B > 32)  // many sequences: pieces of 1 / 1.5 of a slot's share (at most max_split of them)
-        return max(kPagedMinPiece, (int)ceilf(min(1e9f, 2.f * W / (float)max_split)) + 1);
+        return max(min_piece, (int)ceilf(min(1e9f, 2.f * W / (float)max_split)) + 1);
     auto cost = [&](int items, int most) {
-        const float x = (float)items / (float)slots, one = (float)most + kPagedBlockCost;
-        return max(one, (W + (float)items * kPagedBlockCost) / (float)slots + (ceilf(x) - x) * one);
+        const float x = (float)items / (float)slots, one = (float)most + block_cost;
+        return max(one, (W + (float)items * block_cost) / (float)slots + (ceilf(x) - x) * one);
     };
     int best_q = kPagedNoSplit;
     float best = cost(units, longest);
     for (int k = 1; k <= 3; ++k) {
-        int Q = max(kPagedMinPiece, (int)ceilf(W / (float)(slots * k)));
+        int Q = max(min_piece, (int)ceilf(W / (float)(slots * k)));
         for (int it = 0; it < 6; ++it) {
             const int pc = paged_pieces(s, Q), mine = s.blocks * pv.Hkv * pc;
             const int items = __reduce_add_sync(0xffffffffu, mine);
             const int split = __reduce_add_sync(0xffffffffu, pc > 1 ? mine : 0);
             if (items <= slots * k && split <= max_split) {
-                const float c = cost(items, __reduce_max_sync(0xffffffffu, (s.tiles + pc - 1) / pc)) + kPagedBlockCost;
+                const float c = cost(items, __reduce_max_sync(0xffffffffu, (s.tiles + pc - 1) / pc)) + block_cost;
                 if (c < best) {
                     best = c;
                     best_q = Q;

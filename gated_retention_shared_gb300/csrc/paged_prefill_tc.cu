@@ -127,7 +127,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (warp == 0) {
         PagedBlock o;
         const PagedSeq s = paged_seq(pv, cu, rows, 2 * TS, pv.B - 1 - lane, err);
-        const int tiles_q = paged_plan(pv, cu, rows, 2 * TS, slots, max_split, s, err);
+        const int tiles_q = paged_plan(pv, cu, rows, 2 * TS, slots, max_split, yoco_host::kPagedMinPiece,
+                                       yoco_host::kPagedBlockCost, s, err);
         paged_block<false>(pv, cu, rows, 2 * TS, tiles_q, blockIdx.x, s, o, err);
         if (lane == 0) sm.blk = o;
         if (blockIdx.x == 0 && lane == 0) *plan_q = tiles_q;

@@ -236,15 +236,60 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
 
 // ----------------------------------------------------------------- prefill
 //
-// 64 rows (tokens x the G query heads of one kv head) against 64-key tiles, 256 threads as
+// 64 rows (tokens x the G query heads of one kv head) against 64-key steps, 256 threads as
 // 16 x 16: thread (ty, tx) holds rows 4 ty .. and keys tx + 16 j of the scores, rows 4 ty ..
 // and dims 4 tx + 64 j .. of the output.  Everything the products read is in shared memory
-// as fp32, two blocks to an SM; bound by the fp32 pipe.
+// as fp32, two blocks to an SM.  K and V have one buffer each: the next step's K comes in
+// while this step's softmax and P V run, its V while the next scores do (asynchronous copies
+// for fp32, registers for bf16, which is widened on the way).  Bound by the fp32 pipe.
 constexpr int kPreRows = 64, kPreKeys = 64, kPreThreads = 256;
+constexpr int kPreMinPiece = 1;       // tiles
+constexpr float kPreBlockCost = 1.f;  // a block's start and end take about as long as a tile
 
 template <int D> __host__ __device__ constexpr size_t pre_smem() {
     return sizeof(float) * ((size_t)kPreRows * D + kPreKeys * (D + 4) + kPreKeys * D + kPreRows * kPreKeys);
 }
+
+// One 64-key step of K or V on its way from the pages to shared memory (rows PITCH floats apart)
+template <typename T, int D, int PITCH> struct PreStage {
+    static constexpr int EV = 16 / (int)sizeof(T), CH = D / EV, N = kPreKeys * CH / kPreThreads;
+    uint4 r[sizeof(T) == 2 ? N : 1];
+    // `at`: the step's slots, in rows of the pool, -1: not to be read
+    __device__ __forceinline__ void issue(const T *src, float *dst, const int64_t *at) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int e = threadIdx.x + n * kPreThreads, row = e / CH, ch = e % CH;
+            const int64_t o = at[row];
+            if constexpr (sizeof(T) == 2) {
+                r[n] = make_uint4(0, 0, 0, 0);
+                if (o >= 0) r[n] = __ldg(reinterpret_cast<const uint4 *>(src + o * D + ch * EV));
+            } else {
+                // 0 bytes are read and 16 zeros written where the slot is not to be read
+                const unsigned s = (unsigned)__cvta_generic_to_shared(dst + row * PITCH + ch * EV);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(src + max(o, (int64_t)0) * D + ch * EV),
+                             "r"(o >= 0 ? 16 : 0));
+            }
+        }
+        asm volatile("cp.async.commit_group;\n" ::);
+    }
+    // all but the newest issue() of the two stages has come; the caller synchronises
+    __device__ __forceinline__ void land(float *dst) {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int e = threadIdx.x + n * kPreThreads, row = e / CH, ch = e % CH;
+                const uint32_t w[4] = {r[n].x, r[n].y, r[n].z, r[n].w};
+                float4 *p = reinterpret_cast<float4 *>(dst + row * PITCH + ch * EV);
+                p[0] = make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+                                   __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u));
+                p[1] = make_float4(__uint_as_float(w[2] << 16), __uint_as_float(w[2] & 0xFFFF0000u),
+                                   __uint_as_float(w[3] << 16), __uint_as_float(w[3] & 0xFFFF0000u));
+            }
+        } else {
+            asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+        }
+    }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 2)
@@ -256,6 +301,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     float *sq = reinterpret_cast<float *>(smem4);
     float *sk = sq + kPreRows * D, *sv = sk + kPreKeys * (D + 4), *sp = sv + kPreKeys * D;
     __shared__ PagedBlock blk;
+    __shared__ int64_t at[2][kPreKeys];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int G = Hq / pv.Hkv, TS = kPreRows / G;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -263,7 +309,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     if (tid < 32) {
         PagedBlock o;
         const PagedSeq s = paged_seq(pv, cu, rows, TS, pv.B - 1 - tid, err);
-        const int tiles_q = paged_plan(pv, cu, rows, TS, slots, max_split, s, err);
+        const int tiles_q = paged_plan(pv, cu, rows, TS, slots, max_split, kPreMinPiece, kPreBlockCost, s, err);
         paged_block<false>(pv, cu, rows, TS, tiles_q, blockIdx.x, s, o, err);
         if (tid == 0) blk = o;
         if (blockIdx.x == 0 && tid == 0) *plan_q = tiles_q;
@@ -273,6 +319,27 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     const int hk = blk.hk;
     const int nr = blk.nrow * G;  // rows in use: (token, head) = (r / G, r % G)
     const size_t row_stride = (size_t)Hq * D;
+    const int t0 = 2 * blk.i0, t1 = min(2 * blk.i1, (blk.range.places + kPreKeys - 1) / kPreKeys);
+    auto look_up = [&](int t) {  // the slots of step t
+        if (tid < kPreKeys) {
+            const int key = blk.range.slot(t * kPreKeys + tid);
+            int64_t o = -1;
+            if (t < t1 && blk.range.seen(key, pv.sinks)) {
+                const int page = paged_page(pv, blk.b, key >> pv.shift, err);
+                if (page >= 0) o = (((int64_t)page * pv.Hkv + hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
+            }
+            at[t & 1][tid] = o;
+        }
+    };
+    look_up(t0);
+    look_up(t0 + 1);
+    __syncthreads();
+    PreStage<T, D, D + 4> stage_k;
+    PreStage<T, D, D> stage_v;
+    if (t0 < t1) {
+        stage_k.issue(K, sk, at[t0 & 1]);
+        stage_v.issue(V, sv, at[t0 & 1]);
+    }
     for (int e = tid; e < kPreRows * (D / EV); e += kPreThreads) {
         const int r = e / (D / EV), ch = e % (D / EV);
         float x[EV];
@@ -290,28 +357,9 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 #pragma unroll
         for (int e = 0; e < 4 * NJ; ++e) acc[i][e] = 0.f;
     }
-    for (int t2 = 2 * blk.i0; t2 < 2 * blk.i1; ++t2) {
-        const int v0 = t2 * kPreKeys;
-        __syncthreads();
-        for (int e = tid; e < kPreKeys * (D / EV); e += kPreThreads) {
-            const int r = e / (D / EV), ch = e % (D / EV), key = blk.range.slot(v0 + r);
-            float x[EV], y[EV];
-#pragma unroll
-            for (int i = 0; i < EV; ++i) x[i] = y[i] = 0.f;
-            if (blk.range.seen(key, pv.sinks)) {
-                const int page = paged_page(pv, blk.b, key >> pv.shift, err);
-                if (page >= 0) {
-                    const size_t at = (((size_t)page * pv.Hkv + hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
-                    load16(K + at * D + ch * EV, x);
-                    load16(V + at * D + ch * EV, y);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < EV; ++i) {
-                sk[r * (D + 4) + ch * EV + i] = x[i];
-                sv[r * D + ch * EV + i] = y[i];
-            }
-        }
+    for (int t = t0; t < t1; ++t) {
+        const int v0 = t * kPreKeys;
+        stage_k.land(sk);
         __syncthreads();
         float s[4][4];
 #pragma unroll
@@ -331,6 +379,8 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
                 for (int x = 0; x < 4; ++x)
                     s[i][x] = fmaf(a[i].x, b[x].x, fmaf(a[i].y, b[x].y, fmaf(a[i].z, b[x].z, fmaf(a[i].w, b[x].w, s[i][x]))));
         }
+        __syncthreads();  // K read by everyone
+        stage_k.issue(K, sk, at[(t + 1) & 1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pos = blk.pos0 + (4 * ty + i) / G;
@@ -360,7 +410,8 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 #pragma unroll
             for (int e = 0; e < 4 * NJ; ++e) acc[i][e] *= old;
         }
-        __syncwarp();  // a row's P is written and read by one half-warp
+        stage_v.land(sv);
+        __syncthreads();  // V and P there
 #pragma unroll 2
         for (int kk = 0; kk < kPreKeys; kk += 4) {
             float pr[4][4];
@@ -386,7 +437,11 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
                     }
                 }
         }
+        __syncthreads();  // V and P read by everyone
+        stage_v.issue(V, sv, at[(t + 1) & 1]);
+        look_up(t + 2);
     }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
@@ -499,8 +554,9 @@ static int64_t prefill_units(const yoco_paged_kv *c, int Hq, int rows) {
 static int prefill_max_split(const yoco_paged_kv *c, int64_t units) {
     const int64_t slots = paged_slots(c);
     const int64_t tiles = ((int64_t)c->max_pages * c->page_size + kPagedTile - 1) / kPagedTile;
-    if (units >= 8 * slots || tiles <= kPagedMinPiece) return 0;
-    return (int)std::min(3 * slots, units * ((tiles + kPagedMinPiece - 1) / kPagedMinPiece));
+    const int least = paged_on_tc(c) ? kPagedMinPiece : kPreMinPiece;
+    if (units >= 8 * slots || tiles <= least) return 0;
+    return (int)std::min(3 * slots, units * ((tiles + least - 1) / least));
 }
 
 size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows) {
