@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libyoco.so")
 DEBUG_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB = os.path.join(DEBUG_DIR, "libyoco.so")
-SOURCES = ["api.cu", "gret_simt.cu", "gret_tc.cu", "kv_proj.cu", "attn.cu", "attn_noalloc.cu", "kv_proj_tc.cu", "attn_tc.cu", "attn_fa.cu", "swa.cu", "gn_gate.cu", "rope.cu", "qkvg_tc.cu", "paged_append.cu", "paged_decode_tc.cu", "paged_prefill_tc.cu", "paged_simt.cu", "selftest.cu"]
+SOURCES = ["api.cu", "gret_simt.cu", "gret_tc.cu", "kv_proj.cu", "attn.cu", "attn_noalloc.cu", "kv_proj_tc.cu", "attn_tc.cu", "attn_fa.cu", "swa.cu", "gn_gate.cu", "rope.cu", "qkvg_tc.cu", "paged_append.cu", "paged_decode_tc.cu", "paged_plan.cu", "paged_prefill_tc.cu", "paged_simt.cu", "selftest.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

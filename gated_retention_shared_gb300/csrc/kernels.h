@@ -142,20 +142,25 @@ cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st);
 cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st);
 // paged_decode_tc.cu: bf16, d = 128; cuts and part as paged_decode lays them out
 cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blocks, cudaStream_t st);
-// paged_prefill_tc.cu: bf16, d = 128
-constexpr int kPagedMinPiece = 2;       // tiles
-constexpr float kPagedBlockCost = 5.f;  // a block's start and end, in tiles: 6-7 us
-struct PagedGrid {  // of a prefill, and where its pieces' partial results go
-    int64_t blocks;
-    int slots, max_split;  // blocks resident at a time, pieces there may be
-    int *plan_q;
+// a prefill's plan and where it lies in the workspace
+struct PagedGrid {
+    int rows;              // tokens to a row block
+    int cap;               // entries the list has room for
+    int slots, max_split;  // thread blocks resident at a time; pieces of row blocks there may be
+    int min_piece;         // tiles
+    float entry_cost;      // an entry's start and end, in tiles
+    void *plan, *entries, *cuts;
     float *part;
 };
+cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
+// paged_prefill_tc.cu: bf16, d = 128
+constexpr int kPagedMinPiece = 2;       // tiles
+constexpr float kPagedEntryCost = 3.f;  // an entry's start and end, in tiles
 cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
 
 // debug builds: each kernel file's debug word (see YOCO_DEBUG_TU in common.cuh)
 #define YOCO_DEBUG_TUS(X) X(attn) X(attn_fa) X(attn_tc) X(gn_gate) X(gret_simt) X(gret_tc) X(kv_proj) \
-    X(kv_proj_tc) X(paged_append) X(paged_decode_tc) X(paged_prefill_tc) X(paged_simt) X(qkvg_tc) X(rope) X(swa)
+    X(kv_proj_tc) X(paged_append) X(paged_decode_tc) X(paged_plan) X(paged_prefill_tc) X(paged_simt) X(qkvg_tc) X(rope) X(swa)
 #define YOCO_DECLARE_DEBUG_WORD(tu) cudaError_t debug_word_##tu(unsigned *w, int clear);
 YOCO_DEBUG_TUS(YOCO_DECLARE_DEBUG_WORD)
 

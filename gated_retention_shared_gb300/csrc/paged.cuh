@@ -102,157 +102,24 @@ __device__ __forceinline__ PagedRange paged_range(const PagedView &pv, int p_lo,
 // ---------------------------------------------- chunks of rows (prefill)
 //
 // Rows of a sequence go to blocks of T_R; where that leaves SMs idle or one sequence much
-// longer than the rest, a sequence's tiles are cut into pieces of at most Q tiles, each
-// (piece, kv head, block) a thread block of its own.  Q is chosen on the device from the
-// lengths as they are (nothing on the host needs to know them) by every thread block alike.
-
-// one sequence's part of a call: its rows, its row blocks and the tiles of its last block
-struct PagedSeq {
-    int first, n, pos, blocks, tiles;
-};
-
-__device__ __forceinline__ PagedSeq paged_seq(const PagedView &pv, const int32_t *cu, int rows, int T_R, int b, int *err) {
-    PagedSeq s{0, 0, 0, 0, 0};
-    if (b < 0 || b >= pv.B) return s;
-    s.n = paged_rows(cu, rows, b, s.first, err);
-    if (s.n == 0) return s;
-    s.blocks = (s.n + T_R - 1) / T_R;
-    s.pos = paged_len(pv, b, err) - s.n;
-    s.tiles = paged_range(pv, s.pos + (s.blocks - 1) * T_R, s.pos + s.n - 1).ntiles;
-    return s;
-}
-
-__device__ __forceinline__ int paged_pieces(const PagedSeq &s, int Q) { return max(1, (s.tiles + Q - 1) / Q); }
-
-constexpr int kPagedNoSplit = 1 << 30;
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
-}
-
-// Q for the call; one whole warp, `s` its lanes' sequences B - 1 - lane.  `slots` blocks are
-// resident at a time, at most max_split may be pieces of something; a piece has min_piece
-// tiles or more, and a block costs block_cost tiles beside its own.  Nothing is cut where
-// the row blocks keep the slots busy for two rounds and none is longer than a slot's share.
-// Else the smallest Q with which all blocks fit one, two or three rounds of `slots` is
-// compared with no cut: by the tiles and blocks to a slot, the last round's idle part, and
-// never less than the longest block.
-__device__ __forceinline__ int paged_plan(const PagedView &pv, const int32_t *cu, int rows, int T_R, int slots,
-                                          int max_split, int min_piece, float block_cost, const PagedSeq &s,
-                                          int *err) {
-    if (max_split == 0) return kPagedNoSplit;
-    const int lane = threadIdx.x & 31;
-    int units = s.blocks * pv.Hkv, longest = s.tiles;
-    float W = (float)units * (float)s.tiles;
-    for (int b = pv.B - 33 - lane; b + lane >= 0; b -= 32) {
-        const PagedSeq o = paged_seq(pv, cu, rows, T_R, b, err);
-        units += o.blocks * pv.Hkv;
-        longest = max(longest, o.tiles);
-        W += (float)(o.blocks * pv.Hkv) * (float)o.tiles;
-    }
-    W = warp_sum(W);
-    units = __reduce_add_sync(0xffffffffu, units);
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (units >= 2 * slots && (float)longest * (float)slots <= W) return kPagedNoSplit;
-    if (pv.B > 32)  // many sequences: pieces of 1 / 1.5 of a slot's share (at most max_split of them)
-        return max(min_piece, (int)ceilf(min(1e9f, 2.f * W / (float)max_split)) + 1);
-    auto cost = [&](int items, int most) {
-        const float x = (float)items / (float)slots, one = (float)most + block_cost;
-        return max(one, (W + (float)items * block_cost) / (float)slots + (ceilf(x) - x) * one);
-    };
-    int best_q = kPagedNoSplit;
-    float best = cost(units, longest);
-    for (int k = 1; k <= 3; ++k) {
-        int Q = max(min_piece, (int)ceilf(W / (float)(slots * k)));
-        for (int it = 0; it < 6; ++it) {
-            const int pc = paged_pieces(s, Q), mine = s.blocks * pv.Hkv * pc;
-            const int items = __reduce_add_sync(0xffffffffu, mine);
-            const int split = __reduce_add_sync(0xffffffffu, pc > 1 ? mine : 0);
-            if (items <= slots * k && split <= max_split) {
-                const float c = cost(items, __reduce_max_sync(0xffffffffu, (s.tiles + pc - 1) / pc)) + block_cost;
-                if (c < best) {
-                    best = c;
-                    best_q = Q;
-                }
-                break;
-            }
-            Q = max(Q + 1, (int)min(1e9f, (float)Q * (float)items / (float)(slots * k)));
-        }
-    }
-    return best_q;
-}
-
-// What one thread block of the prefill kernels works on: rows [row0, row0 + nrow) of the
-// call, at positions pos0 .., all query heads of kv head hk, and tiles [i0, i1) of what they
-// see.  `pieces` blocks share the rows (1: nothing to join); this one's partial result goes
-// to `slot`, piece p's to slot + (p - piece) stride.
-struct PagedBlock {
-    int b, hk, row0, nrow, pos0, i0, i1, pieces, slot, stride;
+// longer than the rest, a sequence's tiles are cut into pieces.  paged_plan_kernel writes
+// the list of (row block, piece) from the lengths as they are on the device; the prefill
+// kernels take its entries, once for every kv head.
+struct alignas(16) PagedEntry {
+    int b, row0, nrow, pos0;   // rows [row0, row0 + nrow) of the call, at positions pos0 ..
+    int i0, i1;                // tiles of what they see
+    int pieces, slot, stride;  // pieces > 1: this one's partial result is `slot`, piece 0's
+                               // neighbour slot + stride (each times Hkv, plus the kv head)
     PagedRange range;
+    int pad;
 };
+static_assert(sizeof(PagedEntry) == 64, "entries are read by 16 lanes");
 
-// Block `item` of the call, or with SPLIT the item-th (row block, kv head) of the sequences
-// that are cut, as its first piece.  From the last sequence to the first; within a
-// sequence that is cut all row blocks of one (piece, kv head) are neighbours (they read the
-// same keys), within one that is not the row blocks that see most come first.  One whole
-// warp, `s` its lanes' sequences B - 1 - lane; nrow = 0 when there is no such block.
-template <bool SPLIT>
-__device__ __forceinline__ void paged_block(const PagedView &pv, const int32_t *cu, int rows, int T_R, int Q, int item,
-                                            PagedSeq s, PagedBlock &o, int *err) {
-    const int lane = threadIdx.x & 31;
-    o.nrow = 0;
-    o.pieces = 1;
-    int before = 0, slots = 0;
-    for (int hi = pv.B; hi > 0; hi -= 32) {
-        if (hi < pv.B) s = paged_seq(pv, cu, rows, T_R, hi - 1 - lane, err);
-        const int pc = paged_pieces(s, Q), units = s.blocks * pv.Hkv;
-        const int mine = SPLIT ? (pc > 1 ? units : 0) : units * pc, cut = pc > 1 ? units * pc : 0;
-        int inc = mine, inc_s = cut;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, off), u = __shfl_up_sync(0xffffffffu, inc_s, off);
-            if (lane >= off) {
-                inc += v;
-                inc_s += u;
-            }
-        }
-        const int total = __shfl_sync(0xffffffffu, inc, 31);
-        if (item < before + total) {
-            const int src = __ffs(__ballot_sync(0xffffffffu, before + inc > item)) - 1;
-            const int first = __shfl_sync(0xffffffffu, s.first, src), n = __shfl_sync(0xffffffffu, s.n, src);
-            const int pos = __shfl_sync(0xffffffffu, s.pos, src), nb = __shfl_sync(0xffffffffu, s.blocks, src);
-            const int tiles = __shfl_sync(0xffffffffu, s.tiles, src), p = __shfl_sync(0xffffffffu, pc, src);
-            const int idx = item - before - __shfl_sync(0xffffffffu, inc - mine, src);
-            slots += __shfl_sync(0xffffffffu, inc_s - cut, src);
-            int piece = 0, j;
-            if (p > 1) {
-                j = nb - 1 - idx % nb;
-                o.hk = idx / nb % pv.Hkv;
-                piece = idx / nb / pv.Hkv;
-            } else {
-                o.hk = idx % pv.Hkv;
-                j = nb - 1 - idx / pv.Hkv;
-            }
-            const int per = (tiles + p - 1) / p;
-            o.b = hi - 1 - src;
-            o.row0 = first + j * T_R;
-            o.pos0 = pos + j * T_R;
-            o.stride = pv.Hkv * nb;
-            o.slot = slots + idx;
-            const int nr = min(T_R, n - j * T_R);
-            o.range = paged_range(pv, o.pos0, o.pos0 + nr - 1);
-            // a block may see a tile more or less than the last one: the last piece takes what is left
-            o.pieces = min(p, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
-            o.i0 = min(piece * per, o.range.ntiles);
-            o.i1 = piece == p - 1 ? o.range.ntiles : min(o.i0 + per, o.range.ntiles);
-            if (piece < o.pieces) o.nrow = nr;
-            return;
-        }
-        before += total;
-        slots += __shfl_sync(0xffffffffu, inc_s, 31);
-    }
-}
+struct PagedPlan {
+    int entries;  // in the list
+    int cut;      // row blocks in more than one piece: entries cuts[0 .. cut) are their first
+    int next;     // work counter of the persistent kernel
+};
 
 // ------------------------------------------------ one row per sequence (decode)
 //

@@ -1,0 +1,256 @@
+// paged_plan.cu -- the work list of a prefill over the paged cache, from the lengths on the
+// device: one thread block, a few microseconds, so that neither the host nor each of the
+// prefill's thread blocks has to look for its rows.
+//
+// A sequence's tiles are cut into pieces of at most Q tiles where that pays.  Q is chosen
+// for the whole call: nothing is cut where the row blocks keep every SM busy for two rounds
+// and none is longer than an SM's share; else the smallest Q with which all entries fit one,
+// two or three rounds of the SMs is compared with no cut, by the tiles and entries to an SM,
+// the last round's idle part and never less than the longest entry.  Sequences with the
+// longest entries come first (a short entry at the end leaves less idle than a long one).
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace yoco {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanRanked = 256;  // sequences that are ordered by length, and tried with three Qs
+constexpr int kPlanNoCut = 1 << 30;
+
+struct PlanSeq {
+    int first, n, pos, blocks, tiles;  // tiles: of the last row block
+};
+
+__device__ __forceinline__ PlanSeq plan_seq(const PagedView &pv, const int32_t *cu, int rows, int T_R, int b, int *err) {
+    PlanSeq s{0, 0, 0, 0, 0};
+    s.n = paged_rows(cu, rows, b, s.first, err);
+    if (s.n == 0) return s;
+    s.blocks = (s.n + T_R - 1) / T_R;
+    s.pos = paged_len(pv, b, err) - s.n;
+    s.tiles = paged_range(pv, s.pos + (s.blocks - 1) * T_R, s.pos + s.n - 1).ntiles;
+    return s;
+}
+
+__device__ __forceinline__ int plan_pieces(int tiles, int Q) { return max(1, (tiles + Q - 1) / Q); }
+
+template <typename T> __device__ __forceinline__ T plan_sum(T x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, int T_R, int slots, int max_split,
+                  int min_piece, float entry_cost, int cap, PagedPlan *plan, PagedEntry *entries, int *cuts, int *err) {
+    extern __shared__ int sh[];
+    int *tiles = sh, *blocks = tiles + pv.B, *order = blocks + pv.B;
+    int *start = order + pv.B, *slot0 = start + pv.B + 1, *cut0 = slot0 + pv.B + 1;
+    __shared__ float r_W[kPlanThreads / 32], c_cost[4];
+    __shared__ long long r_sum[3][kPlanThreads / 32];
+    __shared__ int r_longest[kPlanThreads / 32], c_q[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = pv.B;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+
+    float W = 0.f;
+    long long nblocks = 0;
+    int longest = 0;
+    for (int b = tid; b < B; b += kPlanThreads) {
+        const PlanSeq s = plan_seq(pv, cu, rows, T_R, b, err);
+        tiles[b] = s.tiles;
+        blocks[b] = s.blocks;
+        W += (float)s.blocks * (float)s.tiles;
+        nblocks += s.blocks;
+        longest = max(longest, s.tiles);
+    }
+    W = plan_sum(W);
+    nblocks = plan_sum(nblocks);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+        r_W[warp] = W;
+        r_sum[0][warp] = nblocks;
+        r_longest[warp] = longest;
+    }
+    __syncthreads();
+    W = 0.f;
+    nblocks = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        W += r_W[w];
+        nblocks += r_sum[0][w];
+        longest = max(longest, r_longest[w]);
+    }
+    W *= (float)pv.Hkv;  // tiles of all heads
+    int Q = kPlanNoCut;
+    // (rows counted twice by overlapping cu_rows may pass the list's end: then nothing is cut)
+    if (max_split > 0 && nblocks * pv.Hkv <= (1 << 30) &&
+        !(nblocks * pv.Hkv >= 2 * slots && (float)longest * (float)slots <= W)) {
+        if (B > kPlanRanked) {
+            // pieces of 1 / 1.5 of an SM's share: at most max_split of them
+            Q = max(min_piece, (int)ceilf(min(1e9f, 2.f * W / (float)max_split)) + 1);
+        } else {
+            if (warp < 4) {
+                const int k = warp;  // rounds; 0: no cut
+                int q = k == 0 ? kPlanNoCut : max(min_piece, (int)ceilf(W / (float)(slots * k)));
+                float cost = 3e38f;
+                for (int it = 0; it < 6; ++it) {
+                    int n = 0, split = 0, most = 0;
+                    for (int b = lane; b < B; b += 32) {
+                        const int pc = plan_pieces(tiles[b], q);
+                        n += blocks[b] * pc;
+                        split += pc > 1 ? blocks[b] * pc : 0;
+                        most = max(most, blocks[b] > 0 ? (tiles[b] + pc - 1) / pc : 0);
+                    }
+                    n = __reduce_add_sync(0xffffffffu, n) * pv.Hkv;
+                    split = __reduce_add_sync(0xffffffffu, split) * pv.Hkv;
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    if (k == 0 || (n <= slots * k && split <= max_split)) {
+                        const float x = (float)n / (float)slots, one = (float)most + entry_cost;
+                        cost = max(one, (W + (float)n * entry_cost) / (float)slots + (ceilf(x) - x) * one) +
+                               (split > 0 ? 2.f * entry_cost : 0.f);
+                        break;
+                    }
+                    q = max(q + 1, (int)min(1e9f, (float)q * (float)n / (float)(slots * k)));
+                }
+                if (lane == 0) {
+                    c_cost[k] = cost;
+                    c_q[k] = q;
+                }
+            }
+            __syncthreads();
+            int best = 0;
+            for (int k = 1; k < 4; ++k)
+                if (c_cost[k] < c_cost[best]) best = k;
+            Q = c_q[best];
+        }
+    }
+    // longest entries first
+    int *length = slot0;  // (its own use comes later)
+    for (int b = tid; b < B; b += kPlanThreads) {
+        const int pc = plan_pieces(tiles[b], Q);
+        length[b] = (tiles[b] + pc - 1) / pc;
+    }
+    __syncthreads();
+    for (int b = tid; b < B; b += kPlanThreads) {
+        int at = B - 1 - b;
+        if (B <= kPlanRanked) {
+            const int mine = length[b];
+            at = 0;
+            for (int o = 0; o < B; ++o) at += length[o] > mine || (length[o] == mine && o < b);
+        }
+        order[at] = b;
+    }
+    __syncthreads();
+    // where each sequence's entries, partial results and cut row blocks start
+    const int each = (B + kPlanThreads - 1) / kPlanThreads;
+    const int p0 = min(B, tid * each), p1 = min(B, p0 + each);
+    long long sum[3] = {0, 0, 0}, inc[3];
+    for (int p = p0; p < p1; ++p) {
+        const int b = order[p], pc = plan_pieces(tiles[b], Q);
+        const long long n = (long long)blocks[b] * pc;
+        sum[0] += n;
+        sum[1] += pc > 1 ? n : 0;
+        sum[2] += pc > 1 ? blocks[b] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        inc[k] = sum[k];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc[k], off);
+            if (lane >= off) inc[k] += v;
+        }
+        if (lane == 31) r_sum[k][warp] = inc[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        long long run = inc[k] - sum[k];
+        for (int w = 0; w < warp; ++w) run += r_sum[k][w];
+        sum[k] = run;
+    }
+    const long long top = 0x7fffffff;
+    for (int p = p0; p <= p1; ++p) {
+        if (p == p1 && p1 != B) break;  // the next thread's
+        start[p] = (int)min(sum[0], top);
+        slot0[p] = (int)min(sum[1], top);
+        cut0[p] = (int)min(sum[2], top);
+        if (p == p1) break;
+        const int b = order[p], pc = plan_pieces(tiles[b], Q);
+        const long long n = (long long)blocks[b] * pc;
+        sum[0] += n;
+        sum[1] += pc > 1 ? n : 0;
+        sum[2] += pc > 1 ? blocks[b] : 0;
+    }
+    __syncthreads();
+    const int total = min(start[B], cap);
+    if (tid == 0) {
+        plan->entries = total;
+        plan->cut = cut0[B];
+        plan->next = 0;
+    }
+    for (int e = tid; e < total; e += kPlanThreads) {
+        int lo = 0, hi = B;  // the sequence: start[lo] <= e < start[lo + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= e) lo = mid;
+            else hi = mid;
+        }
+        const int b = order[lo], idx = e - start[lo];
+        const PlanSeq s = plan_seq(pv, cu, rows, T_R, b, err);
+        const int pc = plan_pieces(s.tiles, Q), per = (s.tiles + pc - 1) / pc;
+        // the row blocks that see most come first; a cut sequence's row blocks of one piece are
+        // neighbours (they read the same keys)
+        const int j = s.blocks - 1 - idx % s.blocks, piece = idx / s.blocks;
+        PagedEntry o;
+        o.b = b;
+        o.row0 = s.first + j * T_R;
+        o.nrow = min(T_R, s.n - j * T_R);
+        o.pos0 = s.pos + j * T_R;
+        o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
+        // a block may see a tile more or less than the last one: the last piece takes what is left
+        o.pieces = min(pc, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
+        o.i0 = min(piece * per, o.range.ntiles);
+        o.i1 = piece == pc - 1 ? o.range.ntiles : min(o.i0 + per, o.range.ntiles);
+        if (piece >= o.pieces) o.nrow = 0;
+        o.slot = slot0[lo] + idx;
+        o.stride = s.blocks;
+        o.pad = 0;
+        const int4 *from = reinterpret_cast<const int4 *>(&o);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(entries + e)[x] = from[x];
+        if (pc > 1 && piece == 0) cuts[cut0[lo] + idx] = e;
+    }
+}
+
+}  // namespace yoco
+
+namespace yoco_host {
+using namespace yoco;
+
+cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
+    const size_t smem = (6 * (size_t)a.cache->B + 3) * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)((6 * (size_t)kPagedMaxB + 3) * sizeof(int)));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, paged_view(a), a.cu, a.rows, g.rows, g.slots, g.max_split,
+                              g.min_piece, g.entry_cost, g.cap, (PagedPlan *)g.plan, (PagedEntry *)g.entries,
+                              (int *)g.cuts, a.err);
+}
+
+}  // namespace yoco_host
+
+YOCO_DEBUG_TU(paged_plan)

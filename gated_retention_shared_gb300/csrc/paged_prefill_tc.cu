@@ -19,11 +19,25 @@
 // that the softmax of tile i + 1 runs while P V(i) does.
 //
 // Pages, rows out of sight and pages that are not there: as in paged_decode_tc.cu; set A's
-// warps clear the V rows that no row of the block sees.  With few row blocks the keys are
-// cut into pieces (paged.cuh) and the unnormalised sums joined by paged_merge_rows_kernel; the
-// partials lie column by column, so a warp's 32 rows store side by side.
+// warps clear the V rows that no row of the block sees.  Where the plan (paged_plan.cu) cuts a
+// row block's keys into pieces, the unnormalised sums are joined by paged_merge_rows_kernel;
+// the partials lie column by column, so a warp's 32 rows store side by side.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2-5 set A, 6-9 set B (thread = TMEM lane = row).
+// Warps: 0 TMA producer, 1 issues S products, 2 issues P V products, 4-7 set A, 8-11 set B
+// (thread = TMEM lane = row).  S and P V have issuers of their own so that S_X(i + 1) goes as
+// soon as S_X(i) has been read, whatever P the other issuer waits for.
+//
+// What bounds it (512 rows over 131072 keys, 1.65 us a tile of 2 x 128 rows; the products
+// alone are 1.08): the softmax warps' own chain, about 3150 cycles a tile from S to P with no
+// pipe above a third.  What counted there, each timed on that case:
+//   - no register spilled in the tile loop: shared memory leaves next to no L1, so each reload
+//     is an L2 round trip (140 bytes of spills: 1.5 x the time).  Hence the 120 / 192 split;
+//   - the exponentials in steps over 32 columns, not element by element (740 -> 690 us);
+//   - one copy of the tile loop's code for both sets (a copy for each: 2 x the time, the
+//     instruction cache), and waits whose polls fall through (690 -> 674 us);
+//   - S and P V issuers apart (757 -> 740 us).
+// Tried and slower: two warps to a row (half the columns each, 808 us), S read twice by halves
+// (739 us), weights before the maximum is known (752 us), one persistent block per SM (965 us).
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -40,7 +54,7 @@ constexpr int kCRows = 128;                    // rows of a set
 constexpr int kCStages = 2;
 constexpr int kCTile = kPagedTile * kCD * 2;   // 32 KB
 constexpr int kCHalf = kCTile / 2;             // 64 channels (or keys) of 128 rows
-constexpr int kCThreads = 320;
+constexpr int kCThreads = 384;
 constexpr float kCLog2e = 1.4426950408889634f;
 constexpr float kCGap = 8.f * kCLog2e;
 
@@ -53,7 +67,7 @@ struct PagedPreSmem {
     uint32_t tmem_base;
     int abort_flag;
     int go[2];
-    PagedBlock blk;
+    PagedEntry blk;
 };
 
 constexpr size_t kCTileBytes = (size_t)3 * kCTile + (size_t)kCStages * 2 * kCTile;  // Q_A, Q_B, P, K/V rings
@@ -80,6 +94,32 @@ __device__ __forceinline__ float c_ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ void c_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n"); }
+
+// 8 consecutive columns of lane (taddr.lane + t)
+__device__ __forceinline__ void c_tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void c_tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// mbar_wait with the polls in a loop that falls through into what follows: the tile loops are
+// long straight code, and each jump out of line costs an instruction fetch of 100-200 cycles
+__device__ __forceinline__ bool c_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    bool ok;
+    int n = 1 << 14;
+    do {
+        ok = mbar_try_wait(bar, parity);
+    } while (!ok && --n);
+    if (__builtin_expect(!ok, 0)) ok = mbar_wait(bar, parity, abort);
+    return ok;
+}
+
 // the low `n` of 32 bits (n clamped to [0, 32])
 __device__ __forceinline__ uint32_t c_below(int n) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -88,8 +128,8 @@ __device__ __forceinline__ uint32_t c_below(int n) {
 __global__ void __launch_bounds__(kCThreads, 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
-                        const int32_t *__restrict__ cu, int rows, int Hq, const PagedView pv, float c2, int slots,
-                        int max_split, int *plan_q, int *err) {
+                        const PagedPlan *__restrict__ plan, const PagedEntry *__restrict__ entries, int rows, int Hq,
+                        const PagedView pv, float c2, int *err) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
@@ -124,19 +164,12 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    if (warp == 0) {
-        PagedBlock o;
-        const PagedSeq s = paged_seq(pv, cu, rows, 2 * TS, pv.B - 1 - lane, err);
-        const int tiles_q = paged_plan(pv, cu, rows, 2 * TS, slots, max_split, yoco_host::kPagedMinPiece,
-                                       yoco_host::kPagedBlockCost, s, err);
-        paged_block<false>(pv, cu, rows, 2 * TS, tiles_q, blockIdx.x, s, o, err);
-        if (lane == 0) sm.blk = o;
-        if (blockIdx.x == 0 && lane == 0) *plan_q = tiles_q;
-    }
+    const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
+    if (entry >= plan->entries) return;
+    if (tid < 16) reinterpret_cast<int *>(&sm.blk)[tid] = reinterpret_cast<const int *>(entries + entry)[tid];
     __syncthreads();
-    const PagedBlock &blk = sm.blk;
+    const PagedEntry &blk = sm.blk;
     if (blk.nrow == 0) return;
-    const int hk = blk.hk;
     const int ntiles = blk.i1 - blk.i0;
     if (ntiles == 0) {  // nothing to see: zeros
         for (int e = tid; e < blk.nrow * G * (kCD / 8); e += kCThreads)
@@ -165,6 +198,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 
     if (warp == 0) {
         // -------------------------------------------------------------- TMA
+        c_regs_dec();
         const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
         const int mine = (lane >> 1) * psz, half = lane & 1;
         auto look_up = [&](int i) -> int {  // this lane's box of tile i: its page, or the one past the pool
@@ -217,69 +251,67 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 mbar_wait(&sm.vfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
         }
     } else if (warp == 1) {
-        // -------------------------------------------------------------- MMA
+        // ------------------------------------------------------- MMA: S = Q K^T
+        c_regs_dec();
         if (lane == 0) {
             const uint32_t id_s = idesc_bf16_f32(kCRows, kPagedTile, false, false);  // A = Q, B = K (K-major)
-            const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);          // A = P (K-major), B = V (N-major)
-            bool ok = mbar_wait(&sm.q_full, 0, abort_flag);
-            auto issue_s = [&](int x, int i) -> bool {
-                if (i > 0 && !mbar_wait(&sm.s_free[x], (i - 1) & 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
-                const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)(i % kCStages) * 2 * kCTile), 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t off = ((kk >> 2) * kCHalf + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + 256 * x, dq + off, dk + off, id_s, kk > 0);
-                }
-                mma_commit(&sm.s_full[x]);
-                return true;
-            };
-            auto issue_pv = [&](int x, int i) -> bool {
-                if (x == 0 && !mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag)) return false;
-                const int b = p_slot(x, i);
-                const uint64_t dp = smem_desc_sw128(smem_u32(p_buf(i)), 16, 1024);
-                const uint64_t dv =
-                    smem_desc_sw128(smem_u32(ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile), kCHalf, 1024);
-                for (int hh = 0; hh < 2; ++hh) {
-                    if (!mbar_wait(&sm.p_ready[b][hh], p_use(i) & 1, abort_flag)) return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4) {
-                        const int kk = 4 * hh + k4;
-                        mma_ss(tmem + 256 * x + 128, dp + (uint64_t)((hh * kCHalf + k4 * 32) >> 4),
-                               dv + (uint64_t)((kk * 2048) >> 4), id_o, (i > 0 || kk > 0));
-                    }
-                    mma_commit(&sm.pv_done[b][hh]);
-                }
-                return true;
-            };
-            // S_A(0), S_B(0), then per tile i: S_A(i + 1), P_A V(i), S_B(i + 1), P_B V(i)
-            if (ok) {
-                ok = mbar_wait(&sm.kfull[0], 0, abort_flag) && issue_s(0, 0) && (!two || issue_s(1, 0));
-                if (ok) mma_commit(&sm.kempty[0]);
-            }
+            bool ok = c_wait(&sm.q_full, 0, abort_flag);
             for (int i = 0; i < ntiles && ok; ++i) {
-                const bool next = i + 1 < ntiles;
-                const int s1 = (i + 1) % kCStages;
-                if (next && !(ok = mbar_wait(&sm.kfull[s1], ((i + 1) / kCStages) & 1, abort_flag))) break;
-                if (next && !(ok = issue_s(0, i + 1))) break;
-                if (next && !two) mma_commit(&sm.kempty[s1]);
-                if (!(ok = issue_pv(0, i))) break;
-                if (two) {
-                    if (next) {
-                        if (!(ok = issue_s(1, i + 1))) break;
-                        mma_commit(&sm.kempty[s1]);
+                const int s = i % kCStages;
+                if (!(ok = c_wait(&sm.kfull[s], (i / kCStages) & 1, abort_flag))) break;
+                for (int x = 0; x < (two ? 2 : 1); ++x) {
+                    // S_X(i) goes over S_X(i - 1) as soon as that has been read out
+                    if (i > 0 && !(ok = c_wait(&sm.s_free[x], (i - 1) & 1, abort_flag))) break;
+                    tc_fence_after();
+                    const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
+                    const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint64_t off = ((kk >> 2) * kCHalf + (kk & 3) * 32) >> 4;
+                        mma_ss(tmem + 256 * x, dq + off, dk + off, id_s, kk > 0);
                     }
-                    if (!(ok = issue_pv(1, i))) break;
+                    mma_commit(&sm.s_full[x]);
                 }
-                mma_commit(&sm.vempty[i % kCStages]);
+                if (ok) mma_commit(&sm.kempty[s]);
             }
             if (!ok) fail(52);
         }
-    } else if (warp < 6 || two) {
+    } else if (warp == 2) {
+        // ------------------------------------------------------ MMA: O += P V
+        c_regs_dec();
+        if (lane == 0) {
+            const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);  // A = P (K-major), B = V (N-major)
+            bool ok = true;
+            for (int i = 0; i < ntiles && ok; ++i) {
+                const int s = i % kCStages;
+                if (!(ok = c_wait(&sm.vfull[s], (i / kCStages) & 1, abort_flag))) break;
+                const uint64_t dp = smem_desc_sw128(smem_u32(p_buf(i)), 16, 1024);
+                const uint64_t dv = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile + kCTile), kCHalf, 1024);
+                for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
+                    const int b = p_slot(x, i);
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (!(ok = c_wait(&sm.p_ready[b][hh], p_use(i) & 1, abort_flag))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const int kk = 4 * hh + k4;
+                            mma_ss(tmem + 256 * x + 128, dp + (uint64_t)((hh * kCHalf + k4 * 32) >> 4),
+                                   dv + (uint64_t)((kk * 2048) >> 4), id_o, (i > 0 || kk > 0));
+                        }
+                        mma_commit(&sm.pv_done[b][hh]);
+                    }
+                }
+                if (ok) mma_commit(&sm.vempty[s]);
+            }
+            if (!ok) fail(58);
+        }
+    } else if (warp == 3) {
+        c_regs_dec();
+    } else if (warp < 8 || two) {
         // ------------------------------------------ softmax, rescale, output
-        const int x = (warp - 2) / 4;  // set
+        const bool two = *(volatile int *)&sm.blk.nrow > TS;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
+        const int x = (warp - 4) / 4;  // set
         const int q4 = warp & 3;       // TMEM lane quarter of this warp
         const int r = q4 * 32 + lane;  // row of the set = TMEM lane
         const int bar_id = 1 + x;
@@ -290,19 +322,22 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const bool used = r < toks * G;
         const int pos = set_lo + r / G;
         const int sink_slots = blk.range.sink_slots, delta = blk.range.base - sink_slots;
+        // tiles of which some place is no row's are those before e_lo and from e_hi on; set A clears
+        // their V rows.  (A parity can only tell a phase from the one before: with two sets P(i - 1)
+        // waited for P_B V(i - 2), so V(i - 2) has come; with one set every tile waits for V)
+        int e_lo = 0, e_hi = 0x7fffffff;
+        if (x == 0) {
+            const PagedRange &rg = blk.range;
+            const int from = rg.sink_slots + rg.lo - rg.base;  // the first place that is seen for being in the window
+            e_lo = (from + kPagedTile - 1) / kPagedTile - blk.i0;
+            e_hi = rg.places / kPagedTile - blk.i0;
+        }
         float m_ref = -INFINITY, l = 0.f;  // base-2 units
+        // One exit from the tile loop: a wait that gave up makes what follows garbage (the status word
+        // says so), but every barrier is still served.
         bool alive = true;
         for (int i = 0; i < ntiles && alive; ++i) {
-            bool okw = true;
-            if (lane == 0) {
-                okw = mbar_wait(&sm.s_full[x], i & 1, abort_flag);
-                if (!okw) fail(53);
-                okw = okw && !*abort_flag;
-            }
-            if (__shfl_sync(0xffffffffu, okw ? 1 : 0, 0) == 0) {
-                alive = false;
-                break;
-            }
+            alive = c_wait(&sm.s_full[x], i & 1, abort_flag);
             tc_fence_after();
             const uint32_t s_t = tmem + colS + lane_base;
             uint32_t sv[128];
@@ -318,12 +353,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             // every row of the set sees every slot of the tile
             const bool full = v0 >= sink_slots && key0 + kPagedTile - 1 <= set_lo &&
                               (pv.window <= 0 || key0 > set_hi - pv.window || key0 + kPagedTile <= pv.sinks);
-            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (full) {
-#pragma unroll
-                for (int c = 0; c < kPagedTile; c += 2)
-                    mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            } else {
+            if (__builtin_expect(!full, 0)) {
                 // the places this row sees of the tile: sinks in the sinks' chunks, then a run up to its
                 // own position from the window's first slot on, and sinks that lie in those chunks
                 const int hi_c = pos + 1 - key0;
@@ -336,103 +366,100 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w)) &
                                ~c_below(ch_c - 32 * w)) | c_below(sc_c - 32 * w);
 #pragma unroll
-                for (int c = 0; c < kPagedTile; c += 2) {
-                    const float v0 = (bits[c >> 5] & (1u << (c & 31))) ? __uint_as_float(sv[c]) : -INFINITY;
-                    const float v1 = (bits[c >> 5] & (2u << (c & 31))) ? __uint_as_float(sv[c + 1]) : -INFINITY;
-                    sv[c] = __float_as_uint(v0);
-                    sv[c + 1] = __float_as_uint(v1);
-                    mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], v0, v1);
-                }
+                for (int c = 0; c < kPagedTile; ++c)
+                    sv[c] = (bits[c >> 5] & (1u << (c & 31))) ? sv[c] : 0xff800000u;  // -inf
             }
+            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kPagedTile; c += 2)
+                mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
             // rows past the set's tokens hold whatever shared memory held: they never move the
             // reference (no rescaling for their sake) and are never stored
             const float mt = used ? fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * c2 : -INFINITY;
-            float alpha = 1.f;
             const bool move = (mt > m_ref + kCGap) || (m_ref == -INFINITY && mt > -INFINITY);
-            if (move) {
-                alpha = (m_ref == -INFINITY) ? 0.f : c_ex2(m_ref - mt);
-                m_ref = mt;
-            }
+            const float m_old = m_ref;
+            m_ref = move ? mt : m_ref;
+            const float alpha = move ? (m_old == -INFINITY ? 0.f : c_ex2(m_old - mt)) : 1.f;
             const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
             const uint64_t c2x2 = f2_pack(c2, c2), nmu2 = f2_pack(-mu, -mu);
-            uint64_t acc2 = f2_pack(0.f, 0.f);
+            uint64_t acc2[4] = {0, 0, 0, 0};  // packed zeros
             uint32_t pk[kPagedTile / 2];
 #pragma unroll
-            for (int c = 0; c < kPagedTile / 2; ++c) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), c2x2, nmu2), x0, x1);
-                const float e0 = c_ex2(x0), e1 = c_ex2(x1);
-                acc2 = f2_add(acc2, f2_pack(e0, e1));
-                pk[c] = c_pack(e0, e1);
-            }
-            float ls0, ls1;
-            f2_unpack(acc2, ls0, ls1);
-            l = fmaf(l, alpha, ls0 + ls1);
-            // O_X holds tiles < i; rows whose reference moved rescale it before P V(i)
-            if (i > 0 && __any_sync(0xffffffffu, move)) {
-                bool ok = true;
-                if (lane == 0) ok = mbar_wait(&sm.pv_done[p_slot(x, i - 1)][1], p_use(i - 1) & 1, abort_flag);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) {
-                    if (lane == 0) fail(54);
-                } else {
-                    tc_fence_after();
-                    const uint32_t o_t = tmem + colO + lane_base;
-#pragma unroll 1
-                    for (int cb = 0; cb < 8; ++cb) {
-                        uint32_t ov[16];
-                        tmem_ld16(o_t + cb * 16, ov);
-                        tmem_wait_ld();
+            for (int q = 0; q < 4; ++q) {  // 32 columns at a time, each step for all of them: element by element
+                                           // they come out as chains of latencies
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        tmem_st16(o_t + cb * 16, ov);
-                    }
-                    tmem_wait_st();
+                for (int c = 16 * q; c < 16 * q + 16; ++c) {
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), c2x2, nmu2), x0, x1);
+                    sv[2 * c] = __float_as_uint(x0);
+                    sv[2 * c + 1] = __float_as_uint(x1);
+                }
+#pragma unroll
+                for (int c = 32 * q; c < 32 * q + 32; ++c) sv[c] = __float_as_uint(c_ex2(__uint_as_float(sv[c])));
+#pragma unroll
+                for (int c = 16 * q; c < 16 * q + 16; ++c) {
+                    const float e0 = __uint_as_float(sv[2 * c]), e1 = __uint_as_float(sv[2 * c + 1]);
+                    acc2[c & 3] = f2_add(acc2[c & 3], f2_pack(e0, e1));
+                    pk[c] = c_pack(e0, e1);
                 }
             }
+            float ls0, ls1;
+            f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), ls0, ls1);
+            l = fmaf(l, alpha, ls0 + ls1);
+            // O_X holds tiles < i; rows whose reference moved rescale it before P V(i)
+            if (__builtin_expect(i > 0 && __any_sync(0xffffffffu, move), 0)) {
+                alive &= mbar_wait(&sm.pv_done[p_slot(x, i - 1)][1], p_use(i - 1) & 1, abort_flag);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t o_t = tmem + colO + lane_base;
+#pragma unroll 1
+                for (int cb = 0; cb < kCD; cb += 8) {  // (in small steps: it is rare, and registers are not)
+                    uint32_t ov[8];
+                    c_tmem_ld8(o_t + cb, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                    c_tmem_st8(o_t + cb, ov);
+                }
+                tmem_wait_st();
+            }
             // V rows that no row of the block sees: zero, once the tile has come
-            bool okb = true;
-            if (x == 0 && blk.range.edge(blk.i0 + i, pv.sinks)) {
-                if (lane == 0) okb = mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
-                okb = __shfl_sync(0xffffffffu, okb ? 1 : 0, 0) != 0;
-                if (okb && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
+            if (__builtin_expect(i < e_lo || i >= e_hi || !two, 0)) {
+                alive &= mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
+                if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
 #pragma unroll 1
                     for (int ch = 0; ch < 16; ++ch)
                         *reinterpret_cast<uint4 *>(vr + (ch >> 3) * kCHalf + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
+                __syncwarp();
             }
             // the P buffer's halves are free once the product that read them last is done: with two
-            // sets the other set's latest, with one the product two tiles back
-            uint8_t *pb = p_buf(i);
+            // sets the other set's latest, with one the product two tiles back (before the first use of
+            // a barrier the other parity counts as done)
             const int b = p_slot(x, i);
+            uint64_t *done = sm.pv_done[two ? 1 - x : b];
+            const uint32_t par = two ? (uint32_t)(x == 0 ? i + 1 : i) & 1u : (uint32_t)((i >> 1) + 1) & 1u;
+            const uint32_t pb = smem_u32(sP) - (!two && (i & 1) ? (uint32_t)kCTile : 0u) + (uint32_t)r * 128u;  // (Q_B lies before P)
+            uint32_t swz = (uint32_t)(r & 7) * 16u;
+            asm volatile("" : "+r"(swz));  // (eight addresses kept over the loop would spill)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                if (okb && (two ? (x == 1 || i > 0) : i > 1)) {
-                    bool ok = true;
-                    if (lane == 0)
-                        ok = two ? mbar_wait(&sm.pv_done[1 - x][hh], (x == 0 ? i - 1 : i) & 1, abort_flag)
-                                 : mbar_wait(&sm.pv_done[b][hh], (p_use(i) - 1) & 1, abort_flag);
-                    okb = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                }
-                if (!okb) break;
+                alive &= c_wait(done + hh, par, abort_flag);
 #pragma unroll
-                for (int c8 = 0; c8 < kPagedTile / 16; ++c8) {
-                    const int ch = hh * (kPagedTile / 16) + c8;
-                    *reinterpret_cast<uint4 *>(pb + c_chunk(r, ch)) =
-                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                for (int c8 = 0; c8 < 8; ++c8) {
+                    const int ch = hh * 8 + c8;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(pb + hh * kCHalf + ((c8 * 16) ^ swz)),
+                                 "r"(pk[4 * ch]), "r"(pk[4 * ch + 1]), "r"(pk[4 * ch + 2]), "r"(pk[4 * ch + 3])
+                                 : "memory");
                 }
-                fence_proxy_async_smem();
+                fence_proxy_async_smem();  // P as the tensor cores read it
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_ready[b][hh]);
             }
-            if (!okb) {
-                if (lane == 0) fail(55);
-                alive = false;
-                break;
-            }
         }
+        if (!alive && lane == 0) fail(53);
         // the set agrees on going on
         if (lane == 0) sm.walive[x][q4] = alive ? 1 : 0;
         cbar(bar_id);
@@ -448,7 +475,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tc_fence_after();
                 const uint32_t o_t = tmem + colO + lane_base;
                 if (blk.pieces > 1) {
-                    float *pp = part + ((size_t)blk.slot * 2 + x) * (kCD + 2) * kCRows + r;
+                    float *pp = part + (((size_t)blk.slot * pv.Hkv + hk) * 2 + x) * (kCD + 2) * kCRows + r;
 #pragma unroll 1
                     for (int cb = 0; cb < 4; ++cb) {
                         uint32_t ov[32];
@@ -518,7 +545,9 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
     cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)g.blocks);
+    const int64_t items = (int64_t)g.cap * a.cache->Hkv;
+    if (items > 0x7fffffff) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)items);
     cfg.blockDim = dim3(kCThreads);
     cfg.dynamicSmemBytes = kCSmem;
     cfg.stream = st;
@@ -528,8 +557,8 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, g.part, a.cu, a.rows, a.Hq,
-                              paged_view(a), a.scale * kCLog2e, g.slots, g.max_split, g.plan_q, a.err);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, g.part, (const PagedPlan *)g.plan,
+                              (const PagedEntry *)g.entries, a.rows, a.Hq, paged_view(a), a.scale * kCLog2e, a.err);
 }
 
 }  // namespace yoco_host

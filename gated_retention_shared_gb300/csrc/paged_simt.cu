@@ -244,7 +244,7 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
 // for fp32, registers for bf16, which is widened on the way).  Bound by the fp32 pipe.
 constexpr int kPreRows = 64, kPreKeys = 64, kPreThreads = 256;
 constexpr int kPreMinPiece = 1;       // tiles
-constexpr float kPreBlockCost = 1.f;  // a block's start and end take about as long as a tile
+constexpr float kPreEntryCost = 1.f;  // a block's start and end take about as long as a tile
 
 template <int D> __host__ __device__ constexpr size_t pre_smem() {
     return sizeof(float) * ((size_t)kPreRows * D + kPreKeys * (D + 4) + kPreKeys * D + kPreRows * kPreKeys);
@@ -294,29 +294,23 @@ template <typename T, int D, int PITCH> struct PreStage {
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 2)
 paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
-                          float *__restrict__ part, const int32_t *__restrict__ cu, int rows, int Hq,
-                          const PagedView pv, float c2, int slots, int max_split, int *plan_q, int *err) {
+                          float *__restrict__ part, const PagedPlan *__restrict__ plan,
+                          const PagedEntry *__restrict__ entries, int rows, int Hq, const PagedView pv, float c2, int *err) {
     constexpr int EV = 16 / (int)sizeof(T), NJ = D / 64;
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4);
     float *sk = sq + kPreRows * D, *sv = sk + kPreKeys * (D + 4), *sp = sv + kPreKeys * D;
-    __shared__ PagedBlock blk;
+    __shared__ PagedEntry blk;
     __shared__ int64_t at[2][kPreKeys];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int G = Hq / pv.Hkv, TS = kPreRows / G;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    if (tid < 32) {
-        PagedBlock o;
-        const PagedSeq s = paged_seq(pv, cu, rows, TS, pv.B - 1 - tid, err);
-        const int tiles_q = paged_plan(pv, cu, rows, TS, slots, max_split, kPreMinPiece, kPreBlockCost, s, err);
-        paged_block<false>(pv, cu, rows, TS, tiles_q, blockIdx.x, s, o, err);
-        if (tid == 0) blk = o;
-        if (blockIdx.x == 0 && tid == 0) *plan_q = tiles_q;
-    }
+    const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
+    if (entry >= plan->entries) return;
+    if (tid < 16) reinterpret_cast<int *>(&blk)[tid] = reinterpret_cast<const int *>(entries + entry)[tid];
     __syncthreads();
     if (blk.nrow == 0) return;
-    const int hk = blk.hk;
     const int nr = blk.nrow * G;  // rows in use: (token, head) = (r / G, r % G)
     const size_t row_stride = (size_t)Hq * D;
     const int t0 = 2 * blk.i0, t1 = min(2 * blk.i1, (blk.range.places + kPreKeys - 1) / kPreKeys);
@@ -445,8 +439,8 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
-        if (blk.pieces > 1) {  // [slot][D + 2][row]
-            float *pp = part + (size_t)blk.slot * (D + 2) * kPreRows + r;
+        if (blk.pieces > 1) {  // [slot][kv head][D + 2][row]
+            float *pp = part + ((size_t)blk.slot * pv.Hkv + hk) * (D + 2) * kPreRows + r;
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
 #pragma unroll
@@ -467,34 +461,26 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     }
 }
 
-// Joins the pieces of a row block: partials [slot][set][D + 2][R], one CTA per (row block and
-// kv head that is cut, set) and 32 head dims, thread = row.
+// Joins the pieces of the row blocks that are cut: partials [slot][kv head][set][D + 2][R], one
+// CTA per (row block, kv head, set) and 32 head dims, thread = row.
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(R)
-paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const int32_t *__restrict__ cu, int rows,
-                        int Hq, const PagedView pv, const int *__restrict__ plan_q, int sets, int *err) {
-    __shared__ PagedBlock blk;
-    const int r = threadIdx.x, G = Hq / pv.Hkv, TS = R / G;
-    const int set = blockIdx.x % sets, d0 = blockIdx.y * 32;
+paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const PagedPlan *__restrict__ plan,
+                        const PagedEntry *__restrict__ entries, const int *__restrict__ cuts, int rows, int Hq, int Hkv,
+                        int sets) {
+    const int r = threadIdx.x, G = Hq / Hkv, TS = R / G;
+    const int set = blockIdx.x % sets, unit = blockIdx.x / sets, hk = unit % Hkv, d0 = blockIdx.y * 32;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int tiles_q = *plan_q;
-    if (tiles_q == kPagedNoSplit) return;
-    if (r < 32) {
-        PagedBlock o;
-        const PagedSeq s = paged_seq(pv, cu, rows, TS * sets, pv.B - 1 - r, err);
-        paged_block<true>(pv, cu, rows, TS * sets, tiles_q, blockIdx.x / sets, s, o, err);
-        if (r == 0) blk = o;
-    }
-    __syncthreads();
-    const int hk = blk.hk;
+    if (unit / Hkv >= plan->cut) return;
+    const PagedEntry &blk = entries[cuts[unit / Hkv]];
     const int tok = set * TS + r / G;
     if (blk.nrow == 0 || blk.pieces == 1 || r >= TS * G || tok >= blk.nrow) return;
     float M = -INFINITY, L = 0.f, A[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) A[e] = 0.f;
     for (int s = 0; s < blk.pieces; ++s) {
-        const float *pp = part + (((size_t)blk.slot + (size_t)s * blk.stride) * sets + set) * (D + 2) * R + r;
+        const float *pp = part + ((((size_t)blk.slot + (size_t)s * blk.stride) * Hkv + hk) * sets + set) * (D + 2) * R + r;
         const float m = __ldcg(pp + D * R), l = __ldcg(pp + (D + 1) * R);
         float x[32];
 #pragma unroll
@@ -530,8 +516,9 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
 namespace yoco_host {
 using namespace yoco;
 
-// workspace: status word, Q of a prefill, cuts of a decode, then partial results
-constexpr size_t kPagedPlan = 128;
+// workspace: status word and plan, then the cuts of a decode or the entries and cut row
+// blocks of a prefill, then partial results
+constexpr size_t kPagedPlanAt = 128;
 constexpr size_t kPagedHead = 256;
 constexpr size_t kPagedCuts = 16384;  // PagedCut per block of a decode grid
 constexpr int kMaxDecodeBlocks = (int)(kPagedCuts / sizeof(PagedCut));
@@ -543,27 +530,39 @@ static bool paged_on_tc(const yoco_paged_kv *c) { return c->dtype == YOCO_BF16 &
 static int paged_slots(const yoco_paged_kv *c) { return (paged_on_tc(c) ? 1 : 2) * device_sm_count(); }
 static int paged_decode_blocks(const yoco_paged_kv *c) { return std::min(kMaxDecodeBlocks, paged_slots(c)); }
 
-// (row block, kv head) pairs of a prefill, at most; and pieces of such that there may be
-static int64_t prefill_units(const yoco_paged_kv *c, int Hq, int rows) {
-    const int G = Hq / c->Hkv, TR = paged_on_tc(c) ? 2 * (128 / G) : kPreRows / G;
-    const int64_t blocks = c->B == 1 ? ((int64_t)rows + TR - 1) / TR : (int64_t)rows / TR + std::min(c->B, rows);
-    return std::max<int64_t>(blocks, 1) * c->Hkv;
-}
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// No cuts where the row blocks alone come to eight rounds, else up to three rounds of pieces
-static int prefill_max_split(const yoco_paged_kv *c, int64_t units) {
-    const int64_t slots = paged_slots(c);
+// the plan of a prefill of `rows` rows, with offsets into the workspace for pointers; its bytes
+static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &g, char *ws) {
+    const bool tc = paged_on_tc(c);
+    const int G = Hq / c->Hkv;
+    g.rows = tc ? 2 * (128 / G) : kPreRows / G;
+    g.slots = paged_slots(c);
+    g.min_piece = tc ? kPagedMinPiece : kPreMinPiece;
+    g.entry_cost = tc ? kPagedEntryCost : kPreEntryCost;
+    const int64_t blocks = std::max<int64_t>(
+        1, c->B == 1 ? ((int64_t)rows + g.rows - 1) / g.rows : (int64_t)rows / g.rows + std::min(c->B, rows));
+    // no cuts where the row blocks alone come to eight rounds of the SMs, else up to three rounds of pieces
     const int64_t tiles = ((int64_t)c->max_pages * c->page_size + kPagedTile - 1) / kPagedTile;
-    const int least = paged_on_tc(c) ? kPagedMinPiece : kPreMinPiece;
-    if (units >= 8 * slots || tiles <= least) return 0;
-    return (int)std::min(3 * slots, units * ((tiles + least - 1) / least));
+    g.max_split = 0;
+    if (blocks * c->Hkv < 8 * (int64_t)g.slots && tiles > g.min_piece)
+        g.max_split = (int)std::min<int64_t>(3 * g.slots, blocks * c->Hkv * ((tiles + g.min_piece - 1) / g.min_piece));
+    const int64_t split = g.max_split / c->Hkv;
+    g.cap = (int)(blocks + split);
+    size_t at = kPagedHead;
+    g.plan = ws + kPagedPlanAt;
+    g.entries = ws + at;
+    at += align256((size_t)g.cap * sizeof(PagedEntry));
+    g.cuts = ws + at;
+    at += align256((size_t)(split / 2) * sizeof(int));
+    g.part = (float *)(ws + at);
+    return at + (size_t)split * c->Hkv * (tc ? 256 : kPreRows) * (c->d + 2) * sizeof(float);
 }
 
 size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows) {
+    PagedGrid g;
     const size_t dec = (size_t)paged_decode_blocks(c) * 2 * (Hq / c->Hkv) * (c->d + 2) * sizeof(float);
-    const size_t pre = (size_t)prefill_max_split(c, prefill_units(c, Hq, rows)) * (paged_on_tc(c) ? 256 : kPreRows) *
-                       (c->d + 2) * sizeof(float);
-    return kPagedHead + kPagedCuts + std::max(dec, pre);
+    return std::max(kPagedHead + kPagedCuts + dec, prefill_grid(c, Hq, rows, g, nullptr));
 }
 
 static void pdl_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, size_t smem,
@@ -623,37 +622,34 @@ static cudaError_t prefill_simt(const PagedArgs &a, const PagedGrid &g, cudaStre
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    pdl_config(cfg, attr, dim3((unsigned)g.blocks), kPreThreads, pre_smem<D>(), st);
+    const int64_t blocks = (int64_t)g.cap * a.cache->Hkv;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    pdl_config(cfg, attr, dim3((unsigned)blocks), kPreThreads, pre_smem<D>(), st);
     count_launches(1);
     return cudaLaunchKernelEx(&cfg, paged_prefill_simt_kernel<T, D>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
-                              (const T *)a.cache->v, g.part, a.cu, a.rows, a.Hq, paged_view(a), a.scale * kPagedLog2e,
-                              g.slots, g.max_split, g.plan_q, a.err);
+                              (const T *)a.cache->v, g.part, (const PagedPlan *)g.plan, (const PagedEntry *)g.entries,
+                              a.rows, a.Hq, paged_view(a), a.scale * kPagedLog2e, a.err);
 }
 
 template <typename T, int D>
 static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
     constexpr bool tc = sizeof(T) == 2 && D == 128;
     constexpr int R = tc ? 128 : kPreRows, sets = tc ? 2 : 1;
-    const int64_t units = prefill_units(a.cache, a.Hq, a.rows);
     PagedGrid g{};
-    g.slots = paged_slots(a.cache);
-    g.max_split = prefill_max_split(a.cache, units);
-    if (units + g.max_split > 0x7fffffff) return cudaErrorInvalidValue;
-    g.blocks = units + g.max_split;
-    g.plan_q = (int *)((char *)a.ws + kPagedPlan);
-    g.part = (float *)((char *)a.ws + kPagedHead + kPagedCuts);
-    cudaError_t e;
+    (void)prefill_grid(a.cache, a.Hq, a.rows, g, (char *)a.ws);
+    cudaError_t e = paged_plan(a, g, st);
+    if (e != cudaSuccess) return e;
     if constexpr (tc) e = paged_prefill_tc(a, g, st);
     else e = prefill_simt<T, D>(a, g, st);
-    if (e != cudaSuccess || g.max_split == 0) return e;
-    // what is cut has two pieces or more
-    const int64_t cut = std::min<int64_t>(units, g.max_split / 2);
+    const int cut = g.max_split / a.cache->Hkv / 2;  // what is cut has two pieces or more
+    if (e != cudaSuccess || cut == 0) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    pdl_config(cfg, attr, dim3((unsigned)(cut * sets), D / 32), R, 0, st);
+    pdl_config(cfg, attr, dim3((unsigned)(cut * a.cache->Hkv * sets), D / 32), R, 0, st);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, (const float *)g.part, (T *)a.O, a.cu, a.rows, a.Hq,
-                              paged_view(a), (const int *)g.plan_q, sets, a.err);
+    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, (const float *)g.part, (T *)a.O,
+                              (const PagedPlan *)g.plan, (const PagedEntry *)g.entries, (const int *)g.cuts, a.rows, a.Hq,
+                              a.cache->Hkv, sets);
 }
 
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st) {
