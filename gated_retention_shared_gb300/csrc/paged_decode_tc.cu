@@ -21,7 +21,12 @@
 // Warps: 0 TMA producer, 1 MMA issuer, 2-5 softmax and sums (thread = TMEM lane = key of the
 // tile / head dim), 6-7 the units' query rows into one of two shared-memory tiles.  A unit's
 // last sums wait until the next unit's first weights are out, so that the tensor cores and
-// the rings never stand still between units.
+// the rings never stand still between units.  The softmax warps meet once a tile; every
+// thread waits for what it reads itself, so no warp waits for another's wait as well.
+//
+// What bounds it: DRAM reads of K and V (32 sequences of 100 to 60000 keys 120 us, 6.3 TB/s;
+// one of 10^6 keys 602 us, 7.1 TB/s).  Short calls (700 keys: 8.8 us) are the launch, two
+// dependent tiles and the merge.  Four barriers a tile in place of one: 130 us for the 32.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -48,9 +53,9 @@ struct PagedDecSmem {
     uint64_t s_full[2], s_free[2], p_ready[2], o_full[2], o_free[2], q_full[2], q_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
-    int go, go_v;
     int sums[kPThreads / 32];
-    float wmax[4][kPN];
+    int4 dead[2];             // per tile parity: softmax warps that have given up
+    float wmax[2][4][kPN];    // per tile parity and softmax warp
     float wsum[4][kPN];
 };
 
@@ -93,10 +98,10 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.s_full[s], 1);
-            mbar_init(&sm.s_free[s], 1);
-            mbar_init(&sm.p_ready[s], 1);
+            mbar_init(&sm.s_free[s], 4);   // one arrival per softmax warp
+            mbar_init(&sm.p_ready[s], 4);
             mbar_init(&sm.o_full[s], 1);
-            mbar_init(&sm.o_free[s], 1);
+            mbar_init(&sm.o_free[s], 4);
             mbar_init(&sm.q_full[s], 64);
             mbar_init(&sm.q_empty[s], 1);
         }
@@ -292,14 +297,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         int done_b = 0, done_hk = 0, done_slot = 0;  // the unit whose last tile is not added yet
         bool done_whole = false, alive = true;
         // acc = acc corr + O^T(i); corr belongs to tile i
-        auto accumulate = [&](int i) -> bool {
-            if (r == 0) {
-                const bool ok = mbar_wait(&sm.o_full[i & 1], (i / 2) & 1, abort_flag);
-                if (!ok) fail(44);
-                sm.go = ok && !*abort_flag;
-            }
-            pbar(128);
-            if (!sm.go) return false;
+        auto accumulate = [&](int i) {
+            alive &= mbar_wait(&sm.o_full[i & 1], (i / 2) & 1, abort_flag);
+            __syncwarp();
             tc_fence_after();
             uint32_t o[16];
             tmem_ld16(tmem + kPColO + 16 * (i & 1) + lane_base, o);
@@ -307,9 +307,8 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll
             for (int n = 0; n < NQ; ++n) acc[n] = fmaf(acc[n], corr[n], __uint_as_float(o[n]));
             tc_fence_before();
-            pbar(128);
-            if (r == 0) mbar_arrive(&sm.o_free[i & 1]);
-            return true;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_free[i & 1]);
         };
         // the finished unit's output, or its partial result
         auto flush = [&]() {
@@ -339,8 +338,11 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             }
             pbar(128);  // wsum may be written again
         };
+        // One barrier of the four warps a tile: it makes their maxima known, and with them which warps
+        // have given up a wait, so that all leave together.
         int i = 0;
-        for (int unit = 0; more && alive; ++unit, more = w.next(pv, pre)) {
+        bool all = true;
+        for (int unit = 0; more && all; ++unit, more = w.next(pv, pre)) {
             const int p = paged_len(pv, w.b, nullptr) - 1;
             const PagedRange range = paged_range(pv, p, p);
 #pragma unroll
@@ -349,21 +351,15 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 l[n] = 0.f;
             }
             for (int t = w.t0; t < w.t1; ++t, ++i) {
-                if (r == 0) {
-                    const bool ok = mbar_wait(&sm.s_full[i & 1], (i / 2) & 1, abort_flag);
-                    if (!ok) fail(45);
-                    sm.go = ok && !*abort_flag;
-                }
-                pbar(128);
-                if (!sm.go) {
-                    alive = false;
-                    break;
-                }
+                alive &= mbar_wait(&sm.s_full[i & 1], (i / 2) & 1, abort_flag);
+                __syncwarp();
                 tc_fence_after();
                 uint32_t sv[16];
                 tmem_ld16(tmem + kPColS + 16 * (i & 1) + lane_base, sv);
                 tmem_wait_ld();
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.s_free[i & 1]);
                 const bool seen = range.seen(range.slot(t * kPagedTile + r), pv.sinks);
                 float sc[NQ];
 #pragma unroll
@@ -372,32 +368,32 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                     float x = sc[n];
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                    if (lane == 0) sm.wmax[q4][n] = x;
+                    if (lane == 0) sm.wmax[i & 1][q4][n] = x;
                 }
-                // V rows out of sight: zero, once the tile has come
-                const bool edge = range.edge(t, pv.sinks);
-                if (edge && r == 0) {
-                    const bool ok = mbar_wait(&sm.full_v[i % kPStages], (i / kPStages) & 1, abort_flag);
-                    if (!ok) fail(46);
-                    sm.go_v = ok && !*abort_flag;
-                }
-                pbar(128);  // S^T read by everyone; warp maxima (and go_v) visible
-                if (edge && !sm.go_v) {
-                    alive = false;
-                    break;
-                }
-                if (r == 0) mbar_arrive(&sm.s_free[i & 1]);
-                if (edge && !seen) {
-                    uint8_t *vr = tiles + (size_t)(i % kPStages) * 2 * kPTile + kPTile + r * 128;
+                // V rows out of sight: zero, once the tile has come (V(i - 3), the phase before, was used by
+                // a product that this warp has seen the end of)
+                if (range.edge(t, pv.sinks)) {
+                    alive &= mbar_wait(&sm.full_v[i % kPStages], (i / kPStages) & 1, abort_flag);
+                    if (alive && !seen) {
+                        uint8_t *vr = tiles + (size_t)(i % kPStages) * 2 * kPTile + kPTile + r * 128;
 #pragma unroll
-                    for (int ch = 0; ch < 16; ++ch)
-                        *reinterpret_cast<uint4 *>(vr + (ch >> 3) * kPHalf + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int ch = 0; ch < 16; ++ch)
+                            *reinterpret_cast<uint4 *>(vr + (ch >> 3) * kPHalf + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (lane == 0) reinterpret_cast<int *>(&sm.dead[i & 1])[q4] = alive ? 0 : 1;
+                pbar(128);
+                const int4 dead = sm.dead[i & 1];
+                if (dead.x | dead.y | dead.z | dead.w) {
+                    all = false;
+                    break;
                 }
                 uint8_t *pb = sP + (i & 1) * kPQBytes;
                 float now[NQ];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    const float mt = fmaxf(fmaxf(sm.wmax[0][n], sm.wmax[1][n]), fmaxf(sm.wmax[2][n], sm.wmax[3][n]));
+                    const float(&wm)[4][kPN] = sm.wmax[i & 1];
+                    const float mt = fmaxf(fmaxf(wm[0][n], wm[1][n]), fmaxf(wm[2][n], wm[3][n]));
                     const float mn = fmaxf(m[n], mt);
                     now[n] = (mn == -INFINITY) ? 1.f : pex2(m[n] - mn);
                     const float pe = (sc[n] == -INFINITY) ? 0.f : pex2(sc[n] - mn);
@@ -407,9 +403,9 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                         *reinterpret_cast<__nv_bfloat16 *>(pb + sw128_offset(n, r, kPN)) = __float2bfloat16_rn(pe);
                 }
                 fence_proxy_async_smem();
-                pbar(128);  // P complete; wmax may be written again
-                if (r == 0) mbar_arrive(&sm.p_ready[i & 1]);
-                if (i > 0 && !(alive = accumulate(i - 1))) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_ready[i & 1]);
+                if (i > 0) accumulate(i - 1);
                 if (unit > 0 && t == w.t0) {
                     flush();
 #pragma unroll
@@ -428,7 +424,12 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 m_done[n] = m[n];
             }
         }
-        if (alive && i > 0 && accumulate(i - 1)) flush();
+        if (all && i > 0) {
+            accumulate(i - 1);
+            if (!alive) fail(45);
+            flush();
+        }
+        if (!all && lane == 0) fail(44);
     }
 
     tc_fence_before();
