@@ -27,17 +27,20 @@
 // (thread = TMEM lane = row).  S and P V have issuers of their own so that S_X(i + 1) goes as
 // soon as S_X(i) has been read, whatever P the other issuer waits for.
 //
-// What bounds it (512 rows over 131072 keys, 1.65 us a tile of 2 x 128 rows; the products
-// alone are 1.08): the softmax warps' own chain, about 3150 cycles a tile from S to P with no
-// pipe above a third.  What counted there, each timed on that case:
+// What bounds it (512 rows over 131072 keys: 586 us, 1.46 us a tile of 2 x 128 rows; the
+// products alone are 1.08): the softmax warps' own chain, about 2800 cycles a tile from S to P
+// with no pipe above a third.  What counted there, each timed on that case as it then was:
 //   - no register spilled in the tile loop: shared memory leaves next to no L1, so each reload
 //     is an L2 round trip (140 bytes of spills: 1.5 x the time).  Hence the 120 / 192 split;
 //   - the exponentials in steps over 32 columns, not element by element (740 -> 690 us);
 //   - one copy of the tile loop's code for both sets (a copy for each: 2 x the time, the
-//     instruction cache), and waits whose polls fall through (690 -> 674 us);
+//     instruction cache);
+//   - waits that look at the abort flag and the clock between polls: a tight loop of polls
+//     takes issue slots from the softmax (663 -> 586 us);
 //   - S and P V issuers apart (757 -> 740 us).
-// Tried and slower: two warps to a row (half the columns each, 808 us), S read twice by halves
-// (739 us), weights before the maximum is known (752 us), one persistent block per SM (965 us).
+// Tried and slower: two warps to a row (half the columns each, 808 against 740 us), weights
+// before the maximum is known (752), one persistent block per SM (965); S read twice by
+// halves made no difference.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
@@ -106,18 +109,6 @@ __device__ __forceinline__ void c_tmem_st8(uint32_t taddr, const uint32_t (&r)[8
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
-}
-
-// mbar_wait with the polls in a loop that falls through into what follows: the tile loops are
-// long straight code, and each jump out of line costs an instruction fetch of 100-200 cycles
-__device__ __forceinline__ bool c_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    bool ok;
-    int n = 1 << 14;
-    do {
-        ok = mbar_try_wait(bar, parity);
-    } while (!ok && --n);
-    if (__builtin_expect(!ok, 0)) ok = mbar_wait(bar, parity, abort);
-    return ok;
 }
 
 // the low `n` of 32 bits (n clamped to [0, 32])
@@ -255,13 +246,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         c_regs_dec();
         if (lane == 0) {
             const uint32_t id_s = idesc_bf16_f32(kCRows, kPagedTile, false, false);  // A = Q, B = K (K-major)
-            bool ok = c_wait(&sm.q_full, 0, abort_flag);
+            bool ok = mbar_wait(&sm.q_full, 0, abort_flag);
             for (int i = 0; i < ntiles && ok; ++i) {
                 const int s = i % kCStages;
-                if (!(ok = c_wait(&sm.kfull[s], (i / kCStages) & 1, abort_flag))) break;
+                if (!(ok = mbar_wait(&sm.kfull[s], (i / kCStages) & 1, abort_flag))) break;
                 for (int x = 0; x < (two ? 2 : 1); ++x) {
                     // S_X(i) goes over S_X(i - 1) as soon as that has been read out
-                    if (i > 0 && !(ok = c_wait(&sm.s_free[x], (i - 1) & 1, abort_flag))) break;
+                    if (i > 0 && !(ok = mbar_wait(&sm.s_free[x], (i - 1) & 1, abort_flag))) break;
                     tc_fence_after();
                     const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
                     const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile), 16, 1024);
@@ -284,13 +275,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             bool ok = true;
             for (int i = 0; i < ntiles && ok; ++i) {
                 const int s = i % kCStages;
-                if (!(ok = c_wait(&sm.vfull[s], (i / kCStages) & 1, abort_flag))) break;
+                if (!(ok = mbar_wait(&sm.vfull[s], (i / kCStages) & 1, abort_flag))) break;
                 const uint64_t dp = smem_desc_sw128(smem_u32(p_buf(i)), 16, 1024);
                 const uint64_t dv = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile + kCTile), kCHalf, 1024);
                 for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
                     const int b = p_slot(x, i);
                     for (int hh = 0; hh < 2; ++hh) {
-                        if (!(ok = c_wait(&sm.p_ready[b][hh], p_use(i) & 1, abort_flag))) break;
+                        if (!(ok = mbar_wait(&sm.p_ready[b][hh], p_use(i) & 1, abort_flag))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
@@ -337,7 +328,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // says so), but every barrier is still served.
         bool alive = true;
         for (int i = 0; i < ntiles && alive; ++i) {
-            alive = c_wait(&sm.s_full[x], i & 1, abort_flag);
+            alive = mbar_wait(&sm.s_full[x], i & 1, abort_flag);
             tc_fence_after();
             const uint32_t s_t = tmem + colS + lane_base;
             uint32_t sv[128];
@@ -445,7 +436,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             asm volatile("" : "+r"(swz));  // (eight addresses kept over the loop would spill)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                alive &= c_wait(done + hh, par, abort_flag);
+                alive &= mbar_wait(done + hh, par, abort_flag);
 #pragma unroll
                 for (int c8 = 0; c8 < 8; ++c8) {
                     const int ch = hh * 8 + c8;
