@@ -156,8 +156,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
+    // (both loads at once: the list has room for every entry of the grid)
+    const int word = tid < 16 ? reinterpret_cast<const int *>(entries + entry)[tid] : 0;
     if (entry >= plan->entries) return;
-    if (tid < 16) reinterpret_cast<int *>(&sm.blk)[tid] = reinterpret_cast<const int *>(entries + entry)[tid];
+    if (tid < 16) reinterpret_cast<int *>(&sm.blk)[tid] = word;
     __syncthreads();
     const PagedEntry &blk = sm.blk;
     if (blk.nrow == 0) return;
@@ -168,7 +170,49 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 make_uint4(0, 0, 0, 0);
         return;
     }
-    if (warp == 0) {
+    const bool two = blk.nrow > TS;  // set B has rows
+    volatile int *abort_flag = &sm.abort_flag;
+    // the TMA warp's lanes: a tile is `boxes` boxes of pages, 64 channels each
+    const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
+    const int mine = (lane >> 1) * psz;
+    // what the table says of this lane's box of tile i (fetched ahead of use, so not yet looked
+    // at); -1 past the last place
+    auto look_up = [&](int i) -> int {
+        const int v = (blk.i0 + i) * kPagedTile + mine, e = blk.range.slot(v) >> pv.shift;
+        const bool there = lane < boxes && v < blk.range.places && e < pv.max_pages;
+        return there ? pv.table[(size_t)blk.b * pv.max_pages + e] : -1;
+    };
+    // that page, or the one past the pool
+    auto page_of = [&](int i, int entry_of_table) -> int {
+        if ((unsigned)entry_of_table < (unsigned)pv.num_pages) return entry_of_table;
+        if (lane < boxes && (blk.i0 + i) * kPagedTile + mine < blk.range.places) paged_report(err, kErrPagedPage);
+        return pv.num_pages;
+    };
+    auto copy = [&](int i, bool is_v, int page) {  // K or V tile i into its (free) slot
+        const int s = i % kCStages;
+        uint8_t *st = ring + (size_t)s * 2 * kCTile + (is_v ? kCTile : 0);
+        uint64_t *full = is_v ? &sm.vfull[s] : &sm.kfull[s];
+        if (lane == 0) mbar_arrive_expect_tx(full, kCTile);
+        __syncwarp();
+        const int half = lane & 1, row = blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
+        if (lane < boxes)
+            tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
+    };
+    int pg0 = 0, pg1 = 0;
+    if (warp == 0) {  // the first copies are on their way while tensor memory is taken
+        pg0 = look_up(0);
+        pg1 = ntiles > 1 ? look_up(1) : -1;
+        if (lane == 0) {
+            const int sets = two ? 2 : 1;
+            mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(sets * 2 * TS * G * 128));
+            for (int x = 0; x < sets; ++x)
+                for (int hf = 0; hf < 2; ++hf)
+                    tma_load_3d(sQ + x * kCTile + hf * kCHalf, &tm_q, &sm.q_full, hf * 64, hk * G, blk.row0 + x * TS);
+        }
+        __syncwarp();
+        pg0 = page_of(0, pg0);
+        copy(0, false, pg0);
+    } else if (warp == 3) {
         tmem_alloc(&sm.tmem_base, 512);
         tmem_relinquish();
     }
@@ -176,8 +220,6 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    const bool two = blk.nrow > TS;  // set B has rows
-    volatile int *abort_flag = &sm.abort_flag;
     auto fail = [&](int code) {
         *abort_flag = 1;
         paged_report(err, code);
@@ -190,43 +232,20 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (warp == 0) {
         // -------------------------------------------------------------- TMA
         c_regs_dec();
-        const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
-        const int mine = (lane >> 1) * psz, half = lane & 1;
-        auto look_up = [&](int i) -> int {  // this lane's box of tile i: its page, or the one past the pool
-            const int v = (blk.i0 + i) * kPagedTile + mine;
-            int page = -1;
-            if (lane < boxes && v < blk.range.places) page = paged_page(pv, blk.b, blk.range.slot(v) >> pv.shift, err);
-            return page < 0 ? pv.num_pages : page;
-        };
-        int nk = 0, nv = 0;  // tiles whose K / V copy was issued
+        int nk = 1, nv = 0;  // tiles whose K / V copy was issued
         bool ok = true;
         auto load = [&](int i, bool is_v, int page) {
             const int s = i % kCStages;
-            uint8_t *st = ring + (size_t)s * 2 * kCTile + (is_v ? kCTile : 0);
-            uint64_t *full = is_v ? &sm.vfull[s] : &sm.kfull[s];
             if (i >= kCStages) ok = mbar_wait(is_v ? &sm.vempty[s] : &sm.kempty[s], ((i / kCStages) + 1) & 1, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
-            if (lane == 0) mbar_arrive_expect_tx(full, kCTile);
-            __syncwarp();
-            const int row = blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
-            if (lane < boxes)
-                tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
+            copy(i, is_v, page);
             ++(is_v ? nv : nk);
         };
-        int pg0 = look_up(0), pg1 = ntiles > 1 ? look_up(1) : 0;
-        if (lane == 0) {
-            const int sets = two ? 2 : 1;
-            mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(sets * 2 * TS * G * 128));
-            for (int x = 0; x < sets; ++x)
-                for (int hf = 0; hf < 2; ++hf)
-                    tma_load_3d(sQ + x * kCTile + hf * kCHalf, &tm_q, &sm.q_full, hf * 64, hk * G, blk.row0 + x * TS);
-        }
         // K runs one tile ahead of V: its slot is free first
-        load(0, false, pg0);
         for (int i = 0; i < ntiles && ok; ++i) {
-            const int pg2 = i + 2 < ntiles ? look_up(i + 2) : 0;
-            if (i + 1 < ntiles) load(i + 1, false, pg1);
+            const int pg2 = i + 2 < ntiles ? look_up(i + 2) : -1;
+            if (i + 1 < ntiles) load(i + 1, false, pg1 = page_of(i + 1, pg1));
             if (ok) load(i, true, pg0);
             pg0 = pg1;
             pg1 = pg2;
@@ -499,9 +518,12 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     }
                     cbar(bar_id);
                     const int ch = r & 15;
-                    for (int row = r >> 4; row < toks * G; row += 8) {
-                        const int tok = blk.row0 + x * TS + row / G, h = hk * G + row % G;
-                        if (!YOCO_DCHECK(tok < rows && h < Hq, 0x68)) continue;
+                    const uint32_t by_g = 0x10000u / (uint32_t)G + 1;  // row / G for rows below 128
+#pragma unroll 8
+                    for (int k = 0; k < kCRows / 8; ++k) {
+                        const int row = (r >> 4) + 8 * k, t = (int)((uint32_t)row * by_g >> 16);
+                        const int tok = blk.row0 + x * TS + t, h = hk * G + row - t * G;
+                        if (row >= toks * G || !YOCO_DCHECK(tok < rows && h < Hq, 0x68)) continue;
                         *reinterpret_cast<uint4 *>(O + ((size_t)tok * Hq + h) * kCD + ch * 8) =
                             *reinterpret_cast<const uint4 *>(stg + c_chunk(row, ch));
                     }
@@ -514,7 +536,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 3) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace yoco
