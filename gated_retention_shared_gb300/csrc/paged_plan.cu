@@ -26,10 +26,11 @@ struct PlanSeq {
 
 __device__ __forceinline__ PlanSeq plan_seq(const PagedView &pv, const int32_t *cu, int rows, int T_R, int b, int *err) {
     PlanSeq s{0, 0, 0, 0, 0};
+    const int len = paged_len(pv, b, err);  // (asked for before the rows are known: one latency, not two)
     s.n = paged_rows(cu, rows, b, s.first, err);
     if (s.n == 0) return s;
     s.blocks = (s.n + T_R - 1) / T_R;
-    s.pos = paged_len(pv, b, err) - s.n;
+    s.pos = len - s.n;
     s.tiles = paged_range(pv, s.pos + (s.blocks - 1) * T_R, s.pos + s.n - 1).ntiles;
     return s;
 }
@@ -85,7 +86,7 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     W *= (float)pv.Hkv;  // tiles of all heads
     int Q = kPlanNoCut;
     // (rows counted twice by overlapping cu_rows may pass the list's end: then nothing is cut)
-    if (max_split > 0 && nblocks * pv.Hkv <= (1 << 30) &&
+    if (max_split > 0 && nblocks <= cap - max_split / pv.Hkv &&
         !(nblocks * pv.Hkv >= 2 * slots && (float)longest * (float)slots <= W)) {
         if (B > kPlanRanked) {
             // pieces of 1 / 1.5 of an SM's share: at most max_split of them

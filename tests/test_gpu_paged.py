@@ -391,6 +391,23 @@ def test_bad_row_bounds_are_reported(Y):
         assert bool(torch.isfinite(O.float()).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_overlapping_row_bounds_stay_within_the_work_list(Y, dtype):
+    """cu_rows that fall back to 0 count the call's rows many times over, more row blocks than
+    the list of work has room for; what follows the output and the workspace stays as it was."""
+    B, rows = 64, 640
+    pool = Pool(Y, [2500] * 2 + [700] * (B - 2), 1, 128, 64, dtype)
+    Q = torch.randn(rows, 4, 128).to(DT[dtype]).cuda()
+    n = Y.yoco_paged_attn_workspace_size(4, rows, pool.dev)
+    ws = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    ws[n:] = 0x5A
+    O = torch.full((rows + 8, 4, 128), 7.0, dtype=DT[dtype], device="cuda")
+    cu = torch.tensor([0, rows] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+    Y.yoco_paged_attn_prefill(Q, pool.dev, cu, O[:rows], workspace=ws[:n])
+    assert status(Y, ws[:n]) == Y.YOCO_ERR_INVALID_ARG
+    assert bool(torch.isfinite(O.float()).all()) and bool((O[rows:] == 7.0).all()) and bool((ws[n:] == 0x5A).all())
+
+
 def test_more_new_rows_than_the_sequence_holds(Y):
     """Rows at negative positions see nothing: zeros from attention, left out by the append."""
     pool = Pool(Y, [10, 100], 2, 128, 16, "bf16", rope=1e4)
