@@ -443,10 +443,12 @@ def _paged_call(fn, name, cache, stream, *args):
         _check(status, name)
 
 
-def _paged_workspace(nbytes, cache, workspace):
-    """(pointer, bytes) of the caller's workspace, or of a new one that the caller's reference keeps."""
+def _paged_workspace(nbytes, cache, workspace, stream):
+    """The caller's workspace, or a new one that is kept until `stream` is done with it, its pointer and bytes."""
     if workspace is None:
         workspace = torch.empty(nbytes() if callable(nbytes) else nbytes, dtype=torch.uint8, device=cache.k.device)
+        if stream is not None:
+            workspace.record_stream(stream)
     elif workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     return workspace, workspace.data_ptr(), workspace.nbytes
@@ -493,7 +495,7 @@ def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, wo
     if rows is None:
         raise ValueError("neither k and v nor q given")
     cu = None if cu_rows is None else _paged_cu(cu_rows, cache)
-    ws, wp, wn = _paged_workspace(256, cache, workspace)
+    ws, wp, wn = _paged_workspace(256, cache, workspace, stream)
     _paged_call(lib.yoco_paged_append, "yoco_paged_append", cache, stream, *kp, *vp, *qp, qo, Hq, cu, rows, cache.ref, wp,
                 wn)
 
@@ -510,7 +512,7 @@ def _paged_q(Q, O, cache):
 def yoco_paged_attn_prefill(Q, cache: PagedKV, cu_rows, O, scale=None, window=0, sinks=0, workspace=None, stream=None):
     """Q, O [rows, Hq, d]; rows cu_rows[b] .. cu_rows[b + 1] - 1 are sequence b's newest."""
     rows, Hq = _paged_q(Q, O, cache)
-    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace)
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
     _paged_call(lib.yoco_paged_attn_prefill, "yoco_paged_attn_prefill", cache, stream, Q.data_ptr(), Hq,
                 _paged_cu(cu_rows, cache), rows, cache.ref, cache._d ** -0.5 if scale is None else scale, window, sinks,
                 O.data_ptr(), wp, wn)
@@ -521,6 +523,6 @@ def yoco_paged_attn_decode(Q, cache: PagedKV, O, scale=None, window=0, sinks=0, 
     rows, Hq = _paged_q(Q, O, cache)
     if rows != cache._B:
         raise ValueError(f"Q has {rows} rows, the cache {cache._B} sequences")
-    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace)
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
     _paged_call(lib.yoco_paged_attn_decode, "yoco_paged_attn_decode", cache, stream, Q.data_ptr(), Hq, cache.ref,
                 cache._d ** -0.5 if scale is None else scale, window, sinks, O.data_ptr(), wp, wn)

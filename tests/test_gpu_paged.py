@@ -547,6 +547,23 @@ def test_two_streams_with_workspaces_of_their_own(Y):
         check(Os[i], pools[i], Qs[i], [0, 1, 2], 128 ** -0.5, 0, 0)
 
 
+def test_a_call_on_another_stream_keeps_its_own_workspace(Y):
+    """Without a workspace the binding makes one; memory freed on the current stream must not be
+    handed out again while the other stream still uses it."""
+    pool = Pool(Y, [6000, 40], 2, 128, 64, "bf16")
+    Q = torch.randn(2, 8, 128).bfloat16().cuda()
+    want, side = torch.empty_like(Q), torch.cuda.Stream()
+    Y.yoco_paged_attn_decode(Q, pool.dev, want)
+    n = Y.yoco_paged_attn_workspace_size(8, 2, pool.dev)
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(Q) for _ in range(8)]
+    for o in outs:
+        Y.yoco_paged_attn_decode(Q, pool.dev, o, stream=side)
+        torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_results_do_not_change_from_call_to_call(Y):
     pool = Pool(Y, [5000, 30, 900], 2, 128, 64, "bf16")
     Q = torch.randn(3, 6, 128).bfloat16().cuda()
