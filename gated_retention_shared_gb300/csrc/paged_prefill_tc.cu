@@ -39,8 +39,10 @@
 //     takes issue slots from the softmax (663 -> 586 us);
 //   - S and P V issuers apart (757 -> 740 us).
 // Tried and slower: two warps to a row (half the columns each, 808 against 740 us), weights
-// before the maximum is known (752), one persistent block per SM (965); S read twice by
-// halves made no difference.
+// before the maximum is known (752); S read twice by halves made no difference.  A block also
+// costs about 8 us around its tiles (start, first K and S, last P V, rows out).  One block per
+// SM that takes entries from a counter and fetches the next one's K early saves some of that and
+// slows the tile loop: 3 windows 129 -> 123 us, 12 mixed sequences 67.5 -> 71 us, the rest level.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
