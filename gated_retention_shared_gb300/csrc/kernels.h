@@ -149,13 +149,15 @@ struct PagedGrid {
     int slots, max_split;  // thread blocks resident at a time; pieces of row blocks there may be
     int min_piece;         // tiles
     float entry_cost;      // an entry's start and end, in tiles
+    float split_cost;      // a piece's partial result, written and read, in tiles of one SM's time over all SMs
     void *plan, *entries, *cuts;
     float *part;
 };
 cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
 // paged_prefill_tc.cu: bf16, d = 128
 constexpr int kPagedMinPiece = 2;       // tiles
-constexpr float kPagedEntryCost = 3.f;  // an entry's start and end, in tiles
+constexpr float kPagedEntryCost = 5.5f;  // an entry's start and end, in tiles
+constexpr float kPagedSplitCost = .026f;  // 2 x 133 KB at 7 TB/s
 cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
 
 // debug builds: each kernel file's debug word (see YOCO_DEBUG_TU in common.cuh)

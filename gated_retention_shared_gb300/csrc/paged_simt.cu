@@ -244,6 +244,7 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
 // for fp32, registers for bf16, which is widened on the way).  Bound by the fp32 pipe.
 constexpr int kPreRows = 64, kPreKeys = 64, kPreThreads = 256;
 constexpr int kPreMinPiece = 1;       // tiles
+constexpr float kPreSplitCost = .002f;
 constexpr float kPreEntryCost = 1.f;  // a block's start and end take about as long as a tile
 
 template <int D> __host__ __device__ constexpr size_t pre_smem() {
@@ -561,6 +562,7 @@ static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &
     g.slots = paged_slots(c);
     g.min_piece = tc ? kPagedMinPiece : kPreMinPiece;
     g.entry_cost = tc ? kPagedEntryCost : kPreEntryCost;
+    g.split_cost = tc ? kPagedSplitCost : kPreSplitCost;
     const int64_t blocks = std::max<int64_t>(
         1, c->B == 1 ? ((int64_t)rows + g.rows - 1) / g.rows : (int64_t)rows / g.rows + std::min(c->B, rows));
     // no cuts where the row blocks alone come to eight rounds of the SMs, else up to three rounds of pieces

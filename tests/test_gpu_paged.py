@@ -320,6 +320,11 @@ def test_prefill_many_rows(Y):
     run_prefill(Y, [2100], [0], 6, 2, 128, 64, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_one_long_sequence_among_many_short_ones(Y, dtype):
+    run_prefill(Y, [30] * 40 + [100], [50] * 40 + [9000], 8, 8, 128, 64, dtype)
+
+
 @pytest.mark.parametrize("dtype,d", TYPES)
 def test_prefill_peaked_scores(Y, dtype, d):
     run_prefill(Y, [300, 20], [200, 1500], 6, 2, d, 64, dtype, std=12.0)
