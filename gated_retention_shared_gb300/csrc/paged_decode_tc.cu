@@ -24,7 +24,7 @@
 // the rings never stand still between units.  The softmax warps meet once a tile; every
 // thread waits for what it reads itself, so no warp waits for another's wait as well.
 //
-// What bounds it: DRAM reads of K and V (32 sequences of 100 to 60000 keys 120 us, 6.3 TB/s;
+// What bounds it: DRAM reads of K and V (32 sequences of 60 to 32000 keys 120 us, 6.3 TB/s;
 // one of 10^6 keys 602 us, 7.1 TB/s).  Short calls (700 keys: 8.8 us) are the launch, two
 // dependent tiles and the merge.  Four barriers a tile in place of one: 130 us for the 32.
 #include <cudaTypedefs.h>

@@ -10,7 +10,7 @@
 //     lengths a: entries of that length have to be taken in that many rounds;
 // plus the merge of the pieces.  Longest entries come first.  Against the best of twenty Qs in a
 // simulation of that order over 120 random batches the choice costs 0.5 % on average and 10 % at
-// worst.  (Sizes that fill one, two or three whole rounds, as the rule was before, cost 10 % and up
+// worst.  (Qs that fill one, two or three whole rounds, as the rule was before, cost 10 % and up
 // to 5 x: a long sequence among many short ones was not cut.  12 mixed sequences: 67.5 -> 62.5 us.)
 #include <algorithm>
 
