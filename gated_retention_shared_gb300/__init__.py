@@ -471,7 +471,9 @@ def _paged_source(t, name, cache, heads, rows):
             stride[2] != 1 or (heads is not None and shape[1] != heads) or (rows is not None and shape[0] != rows):
         raise ValueError(f"{name} must be [rows, heads, {cache._d}] of {cache._dtype} with adjacent channels on the "
                          "cache's device")
-    return shape[0], shape[1], t.data_ptr(), stride[0], stride[1]
+    # (the stride of an axis of one element means nothing, and may be anything)
+    return shape[0], shape[1], t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2], \
+        stride[1] if shape[1] > 1 else shape[2]
 
 
 def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, workspace=None, stream=None):

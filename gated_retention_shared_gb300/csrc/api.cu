@@ -577,8 +577,8 @@ static yoco_status check_paged(const yoco_paged_kv *c) {
     if (c->B > yoco::kPagedMaxB) return fail(YOCO_ERR_UNSUPPORTED, "more than %d sequences", yoco::kPagedMaxB);
     const int64_t keys = (int64_t)c->max_pages * c->page_size;
     if (keys > ((int64_t)1 << 30)) return fail(YOCO_ERR_UNSUPPORTED, "max_pages * page_size above 2^30");
-    if (c->Hkv > 65536 || (int64_t)c->B * c->Hkv * ((keys + yoco::kPagedTile - 1) / yoco::kPagedTile) > INT32_MAX)
-        return fail(YOCO_ERR_UNSUPPORTED, "B * Hkv * max_pages * page_size / %d above 2^31 - 1", yoco::kPagedTile);
+    if (c->Hkv > 65536 || (int64_t)c->B * c->Hkv * ((keys + yoco::kPagedTile - 1) / yoco::kPagedTile) > (1 << 30))
+        return fail(YOCO_ERR_UNSUPPORTED, "B * Hkv * max_pages * page_size / %d above 2^30", yoco::kPagedTile);
     if (!(c->rope_base == 0.0f || (c->rope_base > 1.0f && isfinite(c->rope_base))))
         return fail(YOCO_ERR_INVALID_ARG, "rope_base must be 0 (off) or a finite base > 1");
     return YOCO_OK;
@@ -606,7 +606,7 @@ yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_head, cons
     if (rows < 0) return fail(YOCO_ERR_INVALID_ARG, "rows must be >= 0");
     if (!k != !v) return fail(YOCO_ERR_INVALID_ARG, "k and v come together");
     if (!q != !q_out) return fail(YOCO_ERR_INVALID_ARG, "q and q_out come together");
-    if (!k && !q) return fail(YOCO_ERR_INVALID_ARG, "neither k and v nor q given");
+    if (!k && !q && rows > 0) return fail(YOCO_ERR_INVALID_ARG, "neither k and v nor q given");
     if (q && Hq <= 0) return fail(YOCO_ERR_INVALID_ARG, "Hq must be > 0");
     if (rows > (1 << 30) || (q && (int64_t)rows * Hq > INT32_MAX)) return fail(YOCO_ERR_UNSUPPORTED, "size out of range");
     if (!cu_rows && rows != cache->B)
@@ -633,7 +633,7 @@ static yoco_status paged_attn(const void *Q, int Hq, const int32_t *cu_rows, int
     yoco_status s = check_paged(cache);
     if (s != YOCO_OK) return s;
     if (one_row) rows = cache->B;
-    if (!Q || !O || (!one_row && !cu_rows)) return fail(YOCO_ERR_INVALID_ARG, "null tensor");
+    if (((!Q || !O) && rows != 0) || (!one_row && !cu_rows)) return fail(YOCO_ERR_INVALID_ARG, "null tensor");
     if ((s = check_paged_heads(cache, Hq, rows)) != YOCO_OK) return s;
     if (!(scale > 0.0f) || !isfinite(scale)) return fail(YOCO_ERR_INVALID_ARG, "scale must be finite and > 0");
     if (window < 0 || sinks < 0) return fail(YOCO_ERR_INVALID_ARG, "window and sinks must be >= 0");

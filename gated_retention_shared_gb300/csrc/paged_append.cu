@@ -163,12 +163,12 @@ static cudaError_t append_launch(const PagedAppend &p, const PagedView &pv, cons
 }
 
 // The turns of a base and head size; a thread keeps the last ones (64 powers take longer
-// than the rest of the call).
+// than the rest of the call).  base 0: none, nothing is turned.
 static const RopeTurns &rope_turns(float base, int d) {
     static thread_local RopeTurns t{};
     static thread_local float t_base = 0.f;
     static thread_local int t_d = 0;
-    if (base != t_base || d != t_d) {
+    if (base > 0.f && (base != t_base || d != t_d)) {
         const RopeFreq f = make_rope_freq(base, d);
         for (int i = 0; i < 64; ++i) t.f[i] = (uint64_t)std::ldexp(f.theta[i] / kRopeTwoPi, 64);
         t_base = base;

@@ -401,7 +401,8 @@ YOCO_API size_t yoco_swa_workspace_size(int B, int Hq, const yoco_swa_ring *ring
  * zeros that nothing is written to, a sequence whose cu_rows decrease or leave
  * [0, rows] as one without rows; each is recorded in the workspace and
  * yoco_workspace_status then returns YOCO_ERR_INVALID_ARG.
- * B <= 4096, and B * Hkv * max_pages * page_size / 128 < 2^31.
+ * B <= 4096, and B * Hkv * max_pages * page_size / 128 <= 2^30.  A call of
+ * no rows does nothing; its tensors may be NULL.
  */
 typedef struct {
     void *k;

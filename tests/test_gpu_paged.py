@@ -242,6 +242,29 @@ def test_append_one_row_each_q_in_place_and_q_alone(Y):
 
 # ------------------------------------------------------------------ decode
 
+def test_calls_of_no_rows_do_nothing(Y):
+    pool = Pool(Y, [7, 0], 2, 128, 16, "bf16")
+    before = pool.dev.k.clone()
+    none = torch.empty(0, 4, 128, dtype=torch.bfloat16, device="cuda")
+    kv = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    Y.yoco_paged_append(kv, kv, pool.dev, cu, q=none)
+    Y.yoco_paged_attn_prefill(none, pool.dev, cu, torch.empty_like(none))
+    assert torch.equal(torch.nan_to_num(before), torch.nan_to_num(pool.dev.k))
+
+
+def test_append_of_one_row_and_one_head_with_any_stride_on_those_axes(Y):
+    pool = Pool(Y, [7], 1, 128, 16, "bf16", rope=1e4)
+    k, v, q = (torch.randn(1, h, 128).bfloat16() for h in (1, 1, 4))
+    odd = [torch.as_strided(x.cuda(), x.shape, (3, 128 if x.shape[1] > 1 else 5, 1)) for x in (k, v, q)]
+    Y.yoco_paged_append(odd[0], odd[1], pool.dev, q=odd[2])
+    page = int(pool.table[0, 0])
+    pos = torch.tensor([6])
+    close_turn(pool.dev.k.cpu()[page, :, 6][None], k, pos, 1e4, "bf16")
+    close_turn(odd[2].cpu(), q, pos, 1e4, "bf16")
+    assert torch.equal(pool.dev.v.cpu()[page, :, 6][None], v)
+
+
 TYPES = [("bf16", 128), ("bf16", 64), ("f32", 128), ("f32", 64)]
 
 

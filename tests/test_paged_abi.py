@@ -50,6 +50,20 @@ def test_bad_cache_is_refused_by_every_call(Y, field, value, status):
     assert Y.lib.yoco_paged_attn_workspace_size(Hq, 10, ctypes.byref(c)) == 0
 
 
+def test_tiles_of_all_sequences_stay_below_2_30(Y):
+    most = dict(B=4096, Hkv=16, page_size=128)
+    assert prefill(Y, cache(Y, max_pages=1 << 14, **most), Hq=16, rows=0) == Y.YOCO_OK
+    assert prefill(Y, cache(Y, max_pages=(1 << 14) + 1, **most), Hq=16, rows=0) == Y.YOCO_ERR_UNSUPPORTED
+
+
+def test_calls_of_no_rows_take_null_tensors(Y):
+    """What a binding hands over for an empty tensor."""
+    assert prefill(Y, cache(Y), rows=0, Q=None, O=None) == Y.YOCO_OK
+    assert prefill(Y, cache(Y), rows=0, Q=None, O=None, cu=None) == Y.YOCO_ERR_INVALID_ARG
+    assert append(Y, cache(Y), k=None, v=None, rows=0) == Y.YOCO_OK
+    assert append(Y, cache(Y), k=None, v=None, rows=1) == Y.YOCO_ERR_INVALID_ARG
+
+
 def test_null_cache(Y):
     L = Y.lib
     assert L.yoco_paged_attn_decode(FAKE, 4, None, 0.1, 0, 0, FAKE, FAKE, 1 << 30, None) == Y.YOCO_ERR_INVALID_ARG
