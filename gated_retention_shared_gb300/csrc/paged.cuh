@@ -118,7 +118,6 @@ static_assert(sizeof(PagedEntry) == 64, "entries are read by 16 lanes");
 struct PagedPlan {
     int entries;  // in the list
     int cut;      // row blocks in more than one piece: entries cuts[0 .. cut) are their first
-    int next;     // work counter of the persistent kernel
 };
 
 // ------------------------------------------------ one row per sequence (decode)

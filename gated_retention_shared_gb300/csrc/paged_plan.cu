@@ -10,8 +10,10 @@
 //     lengths a: entries of that length have to be taken in that many rounds;
 // plus the merge of the pieces.  Longest entries come first.  Against the best of twenty Qs in a
 // simulation of that order over 120 random batches the choice costs 0.5 % on average and 10 % at
-// worst.  (Qs that fill one, two or three whole rounds, as the rule was before, cost 10 % and up
-// to 5 x: a long sequence among many short ones was not cut.  12 mixed sequences: 67.5 -> 62.5 us.)
+// worst.  Where an SM's share is twice the longest entry cutting gained nothing (in none of 37
+// such batches), and the search is left out.  (Qs that fill one, two or three whole rounds, as
+// the rule was before, cost 10 % on average and up to 5 x: a long sequence among many short ones
+// was not cut.  12 mixed sequences 67.5 -> 62.5 us, one of 64000 keys among 256 of 110 690 -> 196.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -58,7 +60,7 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     int *start = order + pv.B, *slot0 = start + pv.B + 1, *cut0 = slot0 + pv.B + 1;
     __shared__ float r_W[kPlanThreads / 32], c_cost[kPlanTries];
     __shared__ long long r_sum[3][kPlanThreads / 32];
-    __shared__ int c_q[kPlanTries];
+    __shared__ int r_longest[kPlanThreads / 32], c_q[kPlanTries];
     static_assert(kPlanTries <= kPlanThreads / 32, "a warp for each");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = pv.B;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -66,6 +68,7 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
 
     float W = 0.f;
     long long nblocks = 0;
+    int longest = 0;
 #pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) {
         const PlanSeq s = plan_seq(pv, cu, rows, T_R, b, err);
@@ -73,10 +76,13 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
         blocks[b] = s.blocks;
         W += (float)s.blocks * (float)s.tiles;
         nblocks += s.blocks;
+        longest = max(longest, s.tiles);
     }
     W = plan_sum(W);
     nblocks = plan_sum(nblocks);
+    longest = __reduce_max_sync(0xffffffffu, longest);
     if (lane == 0) {
+        r_longest[warp] = longest;
         r_W[warp] = W;
         r_sum[0][warp] = nblocks;
     }
@@ -86,11 +92,13 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     for (int w = 0; w < kPlanThreads / 32; ++w) {
         W += r_W[w];
         nblocks += r_sum[0][w];
+        longest = max(longest, r_longest[w]);
     }
     W *= (float)pv.Hkv;  // tiles of all heads
     int Q = kPlanNoCut;
     // (rows counted twice by overlapping cu_rows may pass the list's end: then nothing is cut)
-    if (max_split > 0 && nblocks <= cap - max_split / pv.Hkv) {
+    if (max_split > 0 && nblocks <= cap - max_split / pv.Hkv &&
+        2.f * ((float)longest + entry_cost) > (W + (float)(nblocks * pv.Hkv) * entry_cost) / (float)slots) {
         if (warp < kPlanTries) {
             const float share = kPlanShare[warp];
             const int q = warp == 0 ? kPlanNoCut : max(min_piece, (int)ceilf(min(W / (float)slots * share, 1e9f)));
@@ -133,21 +141,44 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
             if (c_cost[k] < c_cost[best]) best = k;
         Q = c_q[best];
     }
-    // longest entries first
+    // longest entries first: ranked, or, of many sequences, by 32nds of the longest (in a class
+    // the order is any: it decides who runs when, not what comes out)
     int *length = slot0;  // (its own use comes later)
+    __shared__ int at_class[32];
+    if (tid < 32) at_class[tid] = 0;
+    __syncthreads();
+    const int cut_longest = max(1, min(longest, Q));
 #pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) {
         const int pc = plan_pieces(tiles[b], Q);
         length[b] = (tiles[b] + pc - 1) / pc;
+        if (B > kPlanRanked) {
+            length[b] = 31 - (int)(31ll * length[b] / cut_longest);
+            atomicAdd(&at_class[length[b]], 1);
+        }
     }
     __syncthreads();
+    if (B > kPlanRanked) {
+        if (warp == 0) {
+            const int n = at_class[lane];
+            int inc = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += v;
+            }
+            at_class[lane] = inc - n;
+        }
+        __syncthreads();
+    }
 #pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) {
-        int at = B - 1 - b;
+        int at = 0;
         if (B <= kPlanRanked) {
             const int mine = length[b];
-            at = 0;
             for (int o = 0; o < B; ++o) at += length[o] > mine || (length[o] == mine && o < b);
+        } else {
+            at = atomicAdd(&at_class[length[b]], 1);
         }
         order[at] = b;
     }
@@ -198,7 +229,6 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     if (tid == 0) {
         plan->entries = total;
         plan->cut = cut0[B];
-        plan->next = 0;
     }
     for (int e = tid; e < total; e += kPlanThreads) {
         int lo = 0, hi = B;  // the sequence: start[lo] <= e < start[lo + 1]

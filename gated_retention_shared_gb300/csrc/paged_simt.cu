@@ -565,10 +565,10 @@ static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &
     g.split_cost = tc ? kPagedSplitCost : kPreSplitCost;
     const int64_t blocks = std::max<int64_t>(
         1, c->B == 1 ? ((int64_t)rows + g.rows - 1) / g.rows : (int64_t)rows / g.rows + std::min(c->B, rows));
-    // no cuts where the row blocks alone come to eight rounds of the SMs, else up to three rounds of pieces
+    // up to three rounds of pieces, however many row blocks there are: one of them may see far more than the rest
     const int64_t tiles = ((int64_t)c->max_pages * c->page_size + kPagedTile - 1) / kPagedTile;
     g.max_split = 0;
-    if (blocks * c->Hkv < 8 * (int64_t)g.slots && tiles > g.min_piece)
+    if (tiles > g.min_piece)
         g.max_split = (int)std::min<int64_t>(3 * g.slots, blocks * c->Hkv * ((tiles + g.min_piece - 1) / g.min_piece));
     const int64_t split = g.max_split / c->Hkv;
     g.cap = (int)(blocks + split);

@@ -348,6 +348,10 @@ def test_prefill_one_long_sequence_among_many_short_ones(Y, dtype):
     run_prefill(Y, [30] * 40 + [100], [50] * 40 + [9000], 8, 8, 128, 64, dtype)
 
 
+def test_prefill_of_hundreds_of_sequences_and_a_long_one(Y):
+    run_prefill(Y, [2, 0, 1] * 100 + [70, 3], [3, 40, 0] * 100 + [6000, 900], 2, 1, 128, 16, "bf16")
+
+
 @pytest.mark.parametrize("dtype,d", TYPES)
 def test_prefill_peaked_scores(Y, dtype, d):
     run_prefill(Y, [300, 20], [200, 1500], 6, 2, d, 64, dtype, std=12.0)
