@@ -156,7 +156,7 @@ struct PagedGrid {
 cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
 // paged_prefill_tc.cu: bf16, d = 128
 constexpr int kPagedMinPiece = 2;       // tiles
-constexpr float kPagedEntryCost = 5.5f;  // an entry's start and end, in tiles
+constexpr float kPagedEntryCost = 4.f;  // an entry's start and end, in tiles
 constexpr float kPagedSplitCost = .026f;  // 2 x 133 KB at 7 TB/s
 cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
 

@@ -229,6 +229,7 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     if (tid == 0) {
         plan->entries = total;
         plan->cut = cut0[B];
+        plan->next = 0;
     }
     for (int e = tid; e < total; e += kPlanThreads) {
         int lo = 0, hi = B;  // the sequence: start[lo] <= e < start[lo + 1]

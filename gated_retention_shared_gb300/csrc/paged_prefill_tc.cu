@@ -23,13 +23,19 @@
 // row block's keys into pieces, the unnormalised sums are joined by paged_merge_rows_kernel;
 // the partials lie column by column, so a warp's 32 rows store side by side.
 //
-// Warps: 0 TMA producer, 1 issues S products, 2 issues P V products, 4-7 set A, 8-11 set B
-// (thread = TMEM lane = row).  S and P V have issuers of their own so that S_X(i + 1) goes as
-// soon as S_X(i) has been read, whatever P the other issuer waits for.
+// One block per SM; it takes entry after entry of the plan's list from a counter, longest first.
+// The next entry is chosen three tiles before this one's end, gets barriers of its own (two
+// groups in turn, set up anew while the other is in use) and its first K tile while this one's
+// rows are written; then all warps meet.
 //
-// What bounds it (512 rows over 131072 keys: 586 us, 1.46 us a tile of 2 x 128 rows; the
+// Warps: 0 TMA producer, 1 issues S products, 2 issues P V products, 3 the next entry, 4-7 set
+// A, 8-11 set B (thread = TMEM lane = row).  S and P V have issuers of their own so that
+// S_X(i + 1) goes as soon as S_X(i) has been read, whatever P the other issuer waits for.
+//
+// What bounds it (512 rows over 131072 keys: 590 us, 1.46 us a tile of 2 x 128 rows; the
 // products alone are 1.08): the softmax warps' own chain, about 2800 cycles a tile from S to P
-// with no pipe above a third.  What counted there, each timed on that case as it then was:
+// with no pipe above a third; and some 6 us an entry around its tiles (first Q, K, S; last P V;
+// rows out).  What counted, each timed as the kernel then was, on the long chunk if not said:
 //   - no register spilled in the tile loop: shared memory leaves next to no L1, so each reload
 //     is an L2 round trip (140 bytes of spills: 1.5 x the time).  Hence the 120 / 192 split;
 //   - the exponentials in steps over 32 columns, not element by element (740 -> 690 us);
@@ -37,13 +43,18 @@
 //     instruction cache);
 //   - waits that look at the abort flag and the clock between polls: a tight loop of polls
 //     takes issue slots from the softmax (663 -> 586 us);
-//   - S and P V issuers apart (757 -> 740 us).
+//   - S and P V issuers apart (757 -> 740 us);
+//   - little between a slot's release and its next copy (12 mixed sequences 63.4 -> 61.3 us);
+//   - blocks that stay instead of one per entry: 600 short sequences 218 -> 172 us, 3 windows 129
+//     -> 123, 16 prompts of 100 to 900 rows 67 -> 62; 12 mixed sequences, about one entry to a
+//     block, 61.3 -> 62.  The next kernel is let in when a block has found no further entry, not
+//     at once (2 us).
 // Tried and slower: two warps to a row (half the columns each, 808 against 740 us), weights
-// before the maximum is known (752); S read twice by halves made no difference.  A block also
-// costs about 8 us around its tiles (start, first K and S, last P V, rows out).  One block per
-// SM that takes entries from a counter and fetches the next one's K early saves some of that and
-// slows the tile loop: 3 windows 129 -> 123 us, 12 mixed sequences 67.5 -> 71 us, the rest level.
+// before the maximum is known (752); S read twice by halves made no difference, nor did both
+// sets on one set's rows, tile by tile, where the rows fit one (its time is the reads').
 #include <cudaTypedefs.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -63,16 +74,27 @@ constexpr int kCThreads = 384;
 constexpr float kCLog2e = 1.4426950408889634f;
 constexpr float kCGap = 8.f * kCLog2e;
 
-struct PagedPreSmem {
+struct PagedPreBars {
     uint64_t q_full;
     uint64_t kfull[kCStages], kempty[kCStages], vfull[kCStages], vempty[kCStages];
     uint64_t s_full[2], s_free[2];          // per set
     uint64_t p_ready[2][2], pv_done[2][2];  // per set (one set: per P buffer) and 64-key half
+};
+
+// what an entry needs; the next entry's is filled while this one's runs
+struct PagedPreTask {
+    PagedPreBars bar;
+    PagedEntry blk;
+    int hk;
+    int more;  // there is such an entry
+};
+
+struct PagedPreSmem {
+    PagedPreTask task[2];
     int walive[2][4];
     uint32_t tmem_base;
     int abort_flag;
     int go[2];
-    PagedEntry blk;
 };
 
 constexpr size_t kCTileBytes = (size_t)3 * kCTile + (size_t)kCStages * 2 * kCTile;  // Q_A, Q_B, P, K/V rings
@@ -99,6 +121,41 @@ __device__ __forceinline__ float c_ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ void c_bars_init(PagedPreBars &bar) {
+    mbar_init(&bar.q_full, 1);
+    for (int s = 0; s < kCStages; ++s) {
+        mbar_init(&bar.kfull[s], 1);
+        mbar_init(&bar.kempty[s], 1);
+        mbar_init(&bar.vfull[s], 1);
+        mbar_init(&bar.vempty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+        mbar_init(&bar.s_full[x], 1);
+        mbar_init(&bar.s_free[x], 4);
+        for (int hh = 0; hh < 2; ++hh) {
+            mbar_init(&bar.p_ready[x][hh], 4);
+            mbar_init(&bar.pv_done[x][hh], 1);
+        }
+    }
+    fence_mbar_init();
+}
+
+// end of an entry for every warp; false when one of them has seen the abort flag
+__device__ __forceinline__ bool c_end(volatile int *abort_flag) {
+    uint32_t gone = *abort_flag != 0;
+    __syncwarp();
+    tc_fence_before();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+        "bar.red.or.pred q, 9, 384, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        : "+r"(gone)
+        :
+        : "memory");
+    tc_fence_after();
+    return gone == 0;
+}
+static_assert(kCThreads == 384, "c_end counts the block's threads");
+
 __device__ __forceinline__ void c_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n"); }
 
 // 8 consecutive columns of lane (taddr.lane + t)
@@ -121,8 +178,8 @@ __device__ __forceinline__ uint32_t c_below(int n) {
 __global__ void __launch_bounds__(kCThreads, 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
-                        const PagedPlan *__restrict__ plan, const PagedEntry *__restrict__ entries, int rows, int Hq,
-                        const PagedView pv, float c2, int *err) {
+                        PagedPlan *plan, const PagedEntry *__restrict__ entries, int cap, int rows, int Hq, const PagedView pv,
+                        float c2, int *err) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
@@ -134,86 +191,97 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     const int G = Hq / pv.Hkv, TS = kCRows / G;
 
     if (tid == 0) {
-        mbar_init(&sm.q_full, 1);
-        for (int s = 0; s < kCStages; ++s) {
-            mbar_init(&sm.kfull[s], 1);
-            mbar_init(&sm.kempty[s], 1);
-            mbar_init(&sm.vfull[s], 1);
-            mbar_init(&sm.vempty[s], 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&sm.s_full[x], 1);
-            mbar_init(&sm.s_free[x], 4);
-            for (int hh = 0; hh < 2; ++hh) {
-                mbar_init(&sm.p_ready[x][hh], 4);
-                mbar_init(&sm.pv_done[x][hh], 1);
-            }
-        }
+        c_bars_init(sm.task[0].bar);
+        c_bars_init(sm.task[1].bar);
         sm.abort_flag = 0;
-        fence_mbar_init();
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int entry0 = (int)blockIdx.x / pv.Hkv;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
-    // (both loads at once: the list has room for every entry of the grid)
-    const int word = tid < 16 ? reinterpret_cast<const int *>(entries + entry)[tid] : 0;
-    if (entry >= plan->entries) return;
-    if (tid < 16) reinterpret_cast<int *>(&sm.blk)[tid] = word;
-    __syncthreads();
-    const PagedEntry &blk = sm.blk;
-    if (blk.nrow == 0) return;
-    const int ntiles = blk.i1 - blk.i0;
-    if (ntiles == 0) {  // nothing to see: zeros
-        for (int e = tid; e < blk.nrow * G * (kCD / 8); e += kCThreads)
-            *reinterpret_cast<uint4 *>(O + ((size_t)(blk.row0 + e / (G * 16)) * Hq + hk * G) * kCD + (e % (G * 16)) * 8) =
-                make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const bool two = blk.nrow > TS;  // set B has rows
     volatile int *abort_flag = &sm.abort_flag;
+    auto fail = [&](int code) {
+        *abort_flag = 1;
+        paged_report(err, code);
+    };
+    // warp 3: the first entry with rows from `item` on, item by item of all blocks' common counter
+    auto fetch = [&](int item, int entry, PagedPreTask &task) {
+        for (;;) {
+            // (both loads at once: the list has room for `cap` entries)
+            const int word = lane < 16 ? reinterpret_cast<const int *>(entries + min(entry, cap - 1))[lane] : 0;
+            const int count = plan->entries;
+            if (entry >= count) {
+                if (lane == 0) task.more = 0;
+                break;
+            }
+            if (lane < 16) reinterpret_cast<int *>(&task.blk)[lane] = word;
+            if (lane == 0) {
+                task.hk = item - entry * pv.Hkv;
+                task.more = 1;
+            }
+            if (__shfl_sync(0xffffffffu, word, 2) > 0) break;  // nrow
+            if (lane == 0) item = (int)gridDim.x + atomicAdd(&plan->next, 1);
+            item = __shfl_sync(0xffffffffu, item, 0);
+            entry = item / pv.Hkv;
+        }
+        __syncwarp();
+    };
+    if (warp == 3) fetch(blockIdx.x, entry0, sm.task[0]);
+    __syncthreads();
+    if (!sm.task[0].more) return;
     // the TMA warp's lanes: a tile is `boxes` boxes of pages, 64 channels each
     const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
     const int mine = (lane >> 1) * psz;
     // what the table says of this lane's box of tile i (fetched ahead of use, so not yet looked
     // at); -1 past the last place
-    auto look_up = [&](int i) -> int {
+    auto look_up = [&](const PagedEntry &blk, int i) -> int {
         const int v = (blk.i0 + i) * kPagedTile + mine, e = blk.range.slot(v) >> pv.shift;
         const bool there = lane < boxes && v < blk.range.places && e < pv.max_pages;
         return there ? pv.table[(size_t)blk.b * pv.max_pages + e] : -1;
     };
     // that page, or the one past the pool
-    auto page_of = [&](int i, int entry_of_table) -> int {
+    auto page_of = [&](const PagedEntry &blk, int i, int entry_of_table) -> int {
         if ((unsigned)entry_of_table < (unsigned)pv.num_pages) return entry_of_table;
         if (lane < boxes && (blk.i0 + i) * kPagedTile + mine < blk.range.places) paged_report(err, kErrPagedPage);
         return pv.num_pages;
     };
-    auto copy = [&](int i, bool is_v, int page) {  // K or V tile i into its (free) slot
+    const int half = lane & 1;
+    auto row_of = [&](const PagedEntry &blk, int i) -> int {  // of tile i's box in its page
+        return blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
+    };
+    auto copy = [&](PagedPreTask &task, int hk, int i, bool is_v, int page, int row) {  // K or V tile i into its (free) slot
         const int s = i % kCStages;
         uint8_t *st = ring + (size_t)s * 2 * kCTile + (is_v ? kCTile : 0);
-        uint64_t *full = is_v ? &sm.vfull[s] : &sm.kfull[s];
+        uint64_t *full = is_v ? &task.bar.vfull[s] : &task.bar.kfull[s];
         if (lane == 0) mbar_arrive_expect_tx(full, kCTile);
         __syncwarp();
-        const int half = lane & 1, row = blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
         if (lane < boxes)
             tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
     };
-    int pg0 = 0, pg1 = 0;
-    if (warp == 0) {  // the first copies are on their way while tensor memory is taken
-        pg0 = look_up(0);
-        pg1 = ntiles > 1 ? look_up(1) : -1;
+    auto copy_q = [&](PagedPreTask &task) {
         if (lane == 0) {
-            const int sets = two ? 2 : 1;
-            mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(sets * 2 * TS * G * 128));
+            const int sets = task.blk.nrow > TS ? 2 : 1;
+            mbar_arrive_expect_tx(&task.bar.q_full, (uint32_t)(sets * 2 * TS * G * 128));
             for (int x = 0; x < sets; ++x)
                 for (int hf = 0; hf < 2; ++hf)
-                    tma_load_3d(sQ + x * kCTile + hf * kCHalf, &tm_q, &sm.q_full, hf * 64, hk * G, blk.row0 + x * TS);
+                    tma_load_3d(sQ + x * kCTile + hf * kCHalf, &tm_q, &task.bar.q_full, hf * 64, task.hk * G,
+                                task.blk.row0 + x * TS);
         }
         __syncwarp();
-        pg0 = page_of(0, pg0);
-        copy(0, false, pg0);
+    };
+    int pg0 = -1, pg1 = -1;
+    // the entry's first pages and K tile
+    auto first_k = [&](PagedPreTask &task) {
+        if (task.blk.i1 == task.blk.i0) return;
+        pg0 = look_up(task.blk, 0);
+        pg1 = task.blk.i1 - task.blk.i0 > 1 ? look_up(task.blk, 1) : -1;
+        pg0 = page_of(task.blk, 0, pg0);
+        copy(task, task.hk, 0, false, pg0, row_of(task.blk, 0));
+    };
+    if (warp == 0) {  // the first copies are on their way while tensor memory is taken
+        if (sm.task[0].blk.i1 > sm.task[0].blk.i0) copy_q(sm.task[0]);
+        first_k(sm.task[0]);
     } else if (warp == 3) {
         tmem_alloc(&sm.tmem_base, 512);
         tmem_relinquish();
@@ -222,106 +290,167 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    auto fail = [&](int code) {
-        *abort_flag = 1;
-        paged_report(err, code);
-    };
     // P buffer and barriers of set x at tile i, and how often they were used before
-    auto p_slot = [&](int x, int i) { return two ? x : (i & 1); };
-    auto p_use = [&](int i) { return two ? i : (i >> 1); };
-    auto p_buf = [&](int i) { return !two && (i & 1) ? sQ + kCTile : sP; };
+    auto p_slot = [](bool two, int x, int i) { return two ? x : (i & 1); };
+    auto p_use = [](bool two, int i) { return two ? i : (i >> 1); };
 
     if (warp == 0) {
         // -------------------------------------------------------------- TMA
         c_regs_dec();
-        int nk = 1, nv = 0;  // tiles whose K / V copy was issued
-        bool ok = true;
-        auto load = [&](int i, bool is_v, int page) {
-            const int s = i % kCStages;
-            if (i >= kCStages) ok = mbar_wait(is_v ? &sm.vempty[s] : &sm.kempty[s], ((i / kCStages) + 1) & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            copy(i, is_v, page);
-            ++(is_v ? nv : nk);
-        };
-        // K runs one tile ahead of V: its slot is free first
-        for (int i = 0; i < ntiles && ok; ++i) {
-            const int pg2 = i + 2 < ntiles ? look_up(i + 2) : -1;
-            if (i + 1 < ntiles) load(i + 1, false, pg1 = page_of(i + 1, pg1));
-            if (ok) load(i, true, pg0);
-            pg0 = pg1;
-            pg1 = pg2;
-        }
-        if (lane == 0) {
-            if (!ok) fail(51);
-            // leave no copy in flight (only the last two of each kind can be)
+        for (int n = 0;; ++n) {
+            PagedPreTask &task = sm.task[n & 1], &next = sm.task[(n + 1) & 1];
+            const PagedEntry &blk = task.blk;
+            const int ntiles = blk.i1 - blk.i0;
             volatile int no_abort = 0;
-            mbar_wait(&sm.q_full, 0, &no_abort, 200000000ull);
-            for (int k = max(0, nk - kCStages); k < nk; ++k)
-                mbar_wait(&sm.kfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
-            for (int k = max(0, nv - kCStages); k < nv; ++k)
-                mbar_wait(&sm.vfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
+            bool told = false;  // warp 3 takes the next entry late: who is done first takes the longest
+            auto tell = [&]() {
+                if (!told) asm volatile("bar.arrive 11, 64;\n" ::: "memory");
+                told = true;
+            };
+            if (ntiles > 0) {
+                if (n > 0) copy_q(task);
+                int nk = 1, nv = 0;  // tiles whose K / V copy was issued
+                const int c_i0 = blk.i0, c_sink = blk.range.sink_slots, c_delta = blk.range.base - c_sink, c_hk = task.hk;
+                bool ok = true;
+                auto load = [&](int i, bool is_v, int page) {
+                    const int s = i % kCStages, v = (c_i0 + i) * kPagedTile + mine;
+                    const int row = (v < c_sink ? v : v + c_delta) & ((1 << pv.shift) - 1);
+                    if (i >= kCStages)
+                        ok = mbar_wait(is_v ? &task.bar.vempty[s] : &task.bar.kempty[s], ((i / kCStages) + 1) & 1, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
+                    copy(task, c_hk, i, is_v, page, row);
+                    ++(is_v ? nv : nk);
+                };
+                // K runs one tile ahead of V: its slot is free first
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    const int pg2 = i + 2 < ntiles ? look_up(blk, i + 2) : -1;
+                    if (i + 3 >= ntiles) tell();
+                    if (i + 1 < ntiles) load(i + 1, false, pg1 = page_of(blk, i + 1, pg1));
+                    if (ok) load(i, true, pg0);
+                    pg0 = pg1;
+                    pg1 = pg2;
+                }
+                tell();
+                if (lane == 0) {
+                    // leave no copy in flight (only the last two of each kind can be)
+                    mbar_wait(&task.bar.q_full, 0, &no_abort, 200000000ull);
+                    for (int k = max(0, nk - kCStages); k < nk; ++k)
+                        mbar_wait(&task.bar.kfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
+                    for (int k = max(0, nv - kCStages); k < nv; ++k)
+                        mbar_wait(&task.bar.vfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
+                    // nor a tile in use, nor a commit on its way to a barrier that is set up anew
+                    for (int k = max(0, nk - kCStages); k < nk && ok; ++k)
+                        ok = mbar_wait(&task.bar.kempty[k % kCStages], (k / kCStages) & 1, abort_flag);
+                    for (int k = max(0, nv - kCStages); k < nv && ok; ++k)
+                        ok = mbar_wait(&task.bar.vempty[k % kCStages], (k / kCStages) & 1, abort_flag);
+                    if (!ok) fail(51);
+                }
+                __syncwarp();
+            }
+            tell();
+            // the next entry's first K tile comes in while this one's rows are written
+            asm volatile("bar.sync 10, 64;\n" ::: "memory");
+            const bool ahead = next.more && next.blk.i1 > next.blk.i0 && __all_sync(0xffffffffu, !*abort_flag);
+            if (ahead) first_k(next);
+            if (!c_end(abort_flag)) {
+                if (ahead && lane == 0) mbar_wait(&next.bar.kfull[0], 0, &no_abort, 200000000ull);
+                break;
+            }
+            if (!next.more) break;
         }
     } else if (warp == 1) {
         // ------------------------------------------------------- MMA: S = Q K^T
         c_regs_dec();
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16_f32(kCRows, kPagedTile, false, false);  // A = Q, B = K (K-major)
-            bool ok = mbar_wait(&sm.q_full, 0, abort_flag);
-            for (int i = 0; i < ntiles && ok; ++i) {
-                const int s = i % kCStages;
-                if (!(ok = mbar_wait(&sm.kfull[s], (i / kCStages) & 1, abort_flag))) break;
-                for (int x = 0; x < (two ? 2 : 1); ++x) {
-                    // S_X(i) goes over S_X(i - 1) as soon as that has been read out
-                    if (i > 0 && !(ok = mbar_wait(&sm.s_free[x], (i - 1) & 1, abort_flag))) break;
-                    tc_fence_after();
-                    const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
-                    const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile), 16, 1024);
+        for (int n = 0;; ++n) {
+            PagedPreBars &bar = sm.task[n & 1].bar;
+            const PagedEntry &blk = sm.task[n & 1].blk;
+            const int ntiles = blk.i1 - blk.i0;
+            const bool two = blk.nrow > TS;
+            if (lane == 0 && ntiles > 0) {
+                const uint32_t id_s = idesc_bf16_f32(kCRows, kPagedTile, false, false);  // A = Q, B = K (K-major)
+                bool ok = mbar_wait(&bar.q_full, 0, abort_flag);
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    const int s = i % kCStages;
+                    if (!(ok = mbar_wait(&bar.kfull[s], (i / kCStages) & 1, abort_flag))) break;
+                    for (int x = 0; x < (two ? 2 : 1); ++x) {
+                        // S_X(i) goes over S_X(i - 1) as soon as that has been read out
+                        if (i > 0 && !(ok = mbar_wait(&bar.s_free[x], (i - 1) & 1, abort_flag))) break;
+                        tc_fence_after();
+                        const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
+                        const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile), 16, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint64_t off = ((kk >> 2) * kCHalf + (kk & 3) * 32) >> 4;
-                        mma_ss(tmem + 256 * x, dq + off, dk + off, id_s, kk > 0);
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint64_t off = ((kk >> 2) * kCHalf + (kk & 3) * 32) >> 4;
+                            mma_ss(tmem + 256 * x, dq + off, dk + off, id_s, kk > 0);
+                        }
+                        mma_commit(&bar.s_full[x]);
                     }
-                    mma_commit(&sm.s_full[x]);
+                    if (ok) mma_commit(&bar.kempty[s]);
                 }
-                if (ok) mma_commit(&sm.kempty[s]);
+                if (!ok) fail(52);
             }
-            if (!ok) fail(52);
+            if (!c_end(abort_flag) || !sm.task[(n + 1) & 1].more) break;
         }
     } else if (warp == 2) {
         // ------------------------------------------------------ MMA: O += P V
         c_regs_dec();
-        if (lane == 0) {
-            const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);  // A = P (K-major), B = V (N-major)
-            bool ok = true;
-            for (int i = 0; i < ntiles && ok; ++i) {
-                const int s = i % kCStages;
-                if (!(ok = mbar_wait(&sm.vfull[s], (i / kCStages) & 1, abort_flag))) break;
-                const uint64_t dp = smem_desc_sw128(smem_u32(p_buf(i)), 16, 1024);
-                const uint64_t dv = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile + kCTile), kCHalf, 1024);
-                for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
-                    const int b = p_slot(x, i);
-                    for (int hh = 0; hh < 2; ++hh) {
-                        if (!(ok = mbar_wait(&sm.p_ready[b][hh], p_use(i) & 1, abort_flag))) break;
-                        tc_fence_after();
+        for (int n = 0;; ++n) {
+            PagedPreBars &bar = sm.task[n & 1].bar;
+            const PagedEntry &blk = sm.task[n & 1].blk;
+            const int ntiles = blk.i1 - blk.i0;
+            const bool two = blk.nrow > TS;
+            if (lane == 0) {
+                const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);  // A = P (K-major), B = V (N-major)
+                bool ok = true;
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    const int s = i % kCStages;
+                    if (!(ok = mbar_wait(&bar.vfull[s], (i / kCStages) & 1, abort_flag))) break;
+                    const uint64_t dp = smem_desc_sw128(smem_u32(!two && (i & 1) ? sQ + kCTile : sP), 16, 1024);
+                    const uint64_t dv = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile + kCTile), kCHalf, 1024);
+                    for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
+                        const int b = p_slot(two, x, i);
+                        for (int hh = 0; hh < 2; ++hh) {
+                            if (!(ok = mbar_wait(&bar.p_ready[b][hh], p_use(two, i) & 1, abort_flag))) break;
+                            tc_fence_after();
 #pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            const int kk = 4 * hh + k4;
-                            mma_ss(tmem + 256 * x + 128, dp + (uint64_t)((hh * kCHalf + k4 * 32) >> 4),
-                                   dv + (uint64_t)((kk * 2048) >> 4), id_o, (i > 0 || kk > 0));
+                            for (int k4 = 0; k4 < 4; ++k4) {
+                                const int kk = 4 * hh + k4;
+                                mma_ss(tmem + 256 * x + 128, dp + (uint64_t)((hh * kCHalf + k4 * 32) >> 4),
+                                       dv + (uint64_t)((kk * 2048) >> 4), id_o, (i > 0 || kk > 0));
+                            }
+                            mma_commit(&bar.pv_done[b][hh]);
                         }
-                        mma_commit(&sm.pv_done[b][hh]);
                     }
+                    if (ok) mma_commit(&bar.vempty[s]);
                 }
-                if (ok) mma_commit(&sm.vempty[s]);
+                if (!ok) fail(58);
             }
-            if (!ok) fail(58);
+            if (!c_end(abort_flag) || !sm.task[(n + 1) & 1].more) break;
         }
     } else if (warp == 3) {
+        // -------------------------------------------- the next entry and its barriers
         c_regs_dec();
-    } else if (warp < 8 || two) {
+        for (int n = 0;; ++n) {
+            PagedPreTask &next = sm.task[(n + 1) & 1];
+            asm volatile("bar.sync 11, 64;\n" ::: "memory");
+            int item = 0;
+            if (lane == 0) item = (int)gridDim.x + atomicAdd(&plan->next, 1);
+            item = __shfl_sync(0xffffffffu, item, 0);
+            fetch(item, item / pv.Hkv, next);
+            // (let in before that the next kernel's blocks wait on SMs that other entries could use)
+            if (!next.more) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+            if (n > 0 && lane == 0) {
+                uint64_t *bars = reinterpret_cast<uint64_t *>(&next.bar);
+                for (int k = 0; k < (int)(sizeof(PagedPreBars) / sizeof(uint64_t)); ++k) mbar_inval(bars + k);
+                c_bars_init(next.bar);
+            }
+            __syncwarp();
+            asm volatile("bar.sync 10, 64;\n" ::: "memory");
+            if (!c_end(abort_flag) || !next.more) break;
+        }
+    } else {
         // ------------------------------------------ softmax, rescale, output
-        const bool two = *(volatile int *)&sm.blk.nrow > TS;
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
         const int x = (warp - 4) / 4;  // set
         const int q4 = warp & 3;       // TMEM lane quarter of this warp
@@ -329,6 +458,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int bar_id = 1 + x;
         const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
         const uint32_t colS = 256 * x, colO = 256 * x + 128;
+        for (int n = 0;; ++n) {
+        PagedPreBars &bar = sm.task[n & 1].bar;
+        const PagedEntry &blk = sm.task[n & 1].blk;
+        const int hk = sm.task[n & 1].hk, ntiles = blk.i1 - blk.i0;
+        const bool two = *(const volatile int *)&blk.nrow > TS;
+        if (ntiles == 0) {  // nothing to see: zeros
+            for (int e = tid - 128; e < blk.nrow * G * (kCD / 8); e += 256)
+                *reinterpret_cast<uint4 *>(O + ((size_t)(blk.row0 + e / (G * 16)) * Hq + hk * G) * kCD + (e % (G * 16)) * 8) =
+                    make_uint4(0, 0, 0, 0);
+        } else if (x == 0 || two) {
         const int toks = min(TS, blk.nrow - x * TS);       // tokens of the set
         const int set_lo = blk.pos0 + x * TS, set_hi = set_lo + toks - 1;
         const bool used = r < toks * G;
@@ -349,7 +488,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // says so), but every barrier is still served.
         bool alive = true;
         for (int i = 0; i < ntiles && alive; ++i) {
-            alive = mbar_wait(&sm.s_full[x], i & 1, abort_flag);
+            alive = mbar_wait(&bar.s_full[x], i & 1, abort_flag);
             tc_fence_after();
             const uint32_t s_t = tmem + colS + lane_base;
             uint32_t sv[128];
@@ -359,7 +498,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             // S is in registers: the MMA may write S(i + 1) over it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_free[x]);
+            if (lane == 0) mbar_arrive(&bar.s_free[x]);
             // place 0 of the tile, and what its slot is where it lies past the sinks' chunks
             const int v0 = (blk.i0 + i) * kPagedTile, key0 = v0 + delta;
             // every row of the set sees every slot of the tile
@@ -420,7 +559,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             l = fmaf(l, alpha, ls0 + ls1);
             // O_X holds tiles < i; rows whose reference moved rescale it before P V(i)
             if (__builtin_expect(i > 0 && __any_sync(0xffffffffu, move), 0)) {
-                alive &= mbar_wait(&sm.pv_done[p_slot(x, i - 1)][1], p_use(i - 1) & 1, abort_flag);
+                alive &= mbar_wait(&bar.pv_done[p_slot(two, x, i - 1)][1], p_use(two, i - 1) & 1, abort_flag);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t o_t = tmem + colO + lane_base;
@@ -437,7 +576,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             }
             // V rows that no row of the block sees: zero, once the tile has come
             if (__builtin_expect(i < e_lo || i >= e_hi || !two, 0)) {
-                alive &= mbar_wait(&sm.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
+                alive &= mbar_wait(&bar.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
                 if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
 #pragma unroll 1
@@ -449,8 +588,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             // the P buffer's halves are free once the product that read them last is done: with two
             // sets the other set's latest, with one the product two tiles back (before the first use of
             // a barrier the other parity counts as done)
-            const int b = p_slot(x, i);
-            uint64_t *done = sm.pv_done[two ? 1 - x : b];
+            const int b = p_slot(two, x, i);
+            uint64_t *done = bar.pv_done[two ? 1 - x : b];
             const uint32_t par = two ? (uint32_t)(x == 0 ? i + 1 : i) & 1u : (uint32_t)((i >> 1) + 1) & 1u;
             const uint32_t pb = smem_u32(sP) - (!two && (i & 1) ? (uint32_t)kCTile : 0u) + (uint32_t)r * 128u;  // (Q_B lies before P)
             uint32_t swz = (uint32_t)(r & 7) * 16u;
@@ -468,7 +607,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 fence_proxy_async_smem();  // P as the tensor cores read it
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_ready[b][hh]);
+                if (lane == 0) mbar_arrive(&bar.p_ready[b][hh]);
             }
         }
         if (!alive && lane == 0) fail(53);
@@ -478,7 +617,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         alive = sm.walive[x][0] && sm.walive[x][1] && sm.walive[x][2] && sm.walive[x][3];
         if (alive) {
             if (r == 0) {
-                const bool ok = mbar_wait(&sm.pv_done[p_slot(x, ntiles - 1)][1], p_use(ntiles - 1) & 1, abort_flag);
+                const bool ok = mbar_wait(&bar.pv_done[p_slot(two, x, ntiles - 1)][1], p_use(two, ntiles - 1) & 1, abort_flag);
                 if (!ok) fail(56);
                 sm.go[x] = ok && !*abort_flag;
             }
@@ -533,6 +672,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tc_fence_before();
             }
         }
+        }
+        fence_proxy_async_smem();  // the next entry's copies go where this one's rows were staged
+        if (!c_end(abort_flag) || !sm.task[(n + 1) & 1].more) break;
+        }
     }
 
     tc_fence_before();
@@ -562,7 +705,7 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
     cudaLaunchConfig_t cfg = {};
     const int64_t items = (int64_t)g.cap * a.cache->Hkv;
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)items);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, g.slots));
     cfg.blockDim = dim3(kCThreads);
     cfg.dynamicSmemBytes = kCSmem;
     cfg.stream = st;
@@ -572,8 +715,8 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, g.part, (const PagedPlan *)g.plan,
-                              (const PagedEntry *)g.entries, a.rows, a.Hq, paged_view(a), a.scale * kCLog2e, a.err);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, g.part, (PagedPlan *)g.plan,
+                              (const PagedEntry *)g.entries, g.cap, a.rows, a.Hq, paged_view(a), a.scale * kCLog2e, a.err);
 }
 
 }  // namespace yoco_host
