@@ -458,6 +458,49 @@ def test_more_new_rows_than_the_sequence_holds(Y):
     assert torch.equal(pool.dev.v[int(pool.table[0, 0]), :, :10].transpose(0, 1), kv[15:25])
 
 
+# ------------------------------------------------------------- large extents
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_pools_past_32_bits_of_elements(Y, dtype, d):
+    """The sequence's pages lie behind 2^31 elements of each tensor (2^32 bytes and more)."""
+    pool = Pool(Y, [300, 77], 2, d, 64, dtype)
+    lead = (2 ** 31) // (2 * 64 * d)
+    n = lead + pool.k.shape[0]
+    big = [torch.empty(n, 2, 64, d, dtype=DT[dtype], device="cuda") for _ in range(2)]
+    for t, small in zip(big, (pool.k, pool.v)):
+        t[:2] = math.nan
+        t[lead:] = small.cuda()
+    table = torch.where(pool.table >= 0, pool.table + lead, pool.table)
+    dev = Y.PagedKV(big[0], big[1], table.cuda(), pool.dev.seq_lens)
+    Q = torch.randn(2, 6, d, generator=torch.Generator().manual_seed(3)).to(DT[dtype]).cuda()
+    O = torch.empty_like(Q)
+    Y.yoco_paged_attn_decode(Q, dev, O)
+    check(O, pool, Q, [0, 1, 2], d ** -0.5, 0, 0)
+    O.fill_(math.nan)
+    Y.yoco_paged_attn_prefill(Q, dev, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), O)
+    check(O, pool, Q, [0, 1, 2], d ** -0.5, 0, 0)
+    kv = torch.randn(2, 2, d).to(DT[dtype]).cuda()
+    Y.yoco_paged_append(kv, kv, dev)
+    for b, L in enumerate(pool.lens):
+        assert torch.equal(big[0][int(table[b, (L - 1) // 64]), :, (L - 1) % 64], kv[b])
+    assert bool(big[0][:2].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_as_many_sequences_as_a_call_takes(Y, dtype):
+    lens = [(7 * b) % 40 for b in range(4096)]
+    run_decode(Y, lens, 1, 1, 128, 16, dtype)
+    new = [min(n, b % 3) for b, n in enumerate(lens)]
+    run_prefill(Y, new, [n - t for n, t in zip(lens, new)], 1, 1, 128, 16, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(15000, 100), (9000, 0), (300, 12000)])
+def test_long_windows_and_many_sinks_are_split_and_joined(Y, dtype, window, sinks):
+    run_prefill(Y, [5, 1], [20000, 100], 2, 1, 128, 64, dtype, window=window, sinks=sinks)
+    run_decode(Y, [20000, 100], 2, 1, 128, 64, dtype, window=window, sinks=sinks)
+
+
 # ----------------------------------------------------------- used together
 
 def serve(Y, pool, steps, k, v, q, window, sinks):
