@@ -52,9 +52,162 @@ template <typename T> __device__ __forceinline__ T plan_sum(T x) {
     return x;
 }
 
+struct PlanArgs {
+    const int32_t *cu;
+    int rows, T_R, slots, max_split, min_piece;
+    float entry_cost, split_cost;
+    int cap;
+    PagedPlan *plan;
+    PagedEntry *entries;
+    int *cuts, *err;
+};
+
+// sizes are tried where something may be gained by them, and where the list has room for cuts
+// (rows counted twice by overlapping cu_rows may pass its end: then nothing is cut)
+__device__ __forceinline__ bool plan_tries(const PlanArgs &a, int Hkv, float W, long long nblocks, int longest) {
+    return a.max_split > 0 && nblocks <= a.cap - a.max_split / Hkv &&
+           2.f * ((float)longest + a.entry_cost) > (W + (float)(nblocks * Hkv) * a.entry_cost) / (float)a.slots;
+}
+
+// A warp's try: its Q, and what the call is estimated to take with it, in tiles of an SM; seq(b)
+// is {row blocks, tiles} of sequence b
+template <typename Seq>
+__device__ __forceinline__ float plan_cost(const PlanArgs &a, int B, int Hkv, int warp, float W, Seq seq, int &q) {
+    const int lane = threadIdx.x & 31;
+    q = warp == 0 ? kPlanNoCut : max(a.min_piece, (int)ceilf(min(W / (float)a.slots * kPlanShare[warp], 1e9f)));
+    int n = 0, split = 0, most = 0;
+#pragma unroll 1
+    for (int b = lane; b < B; b += 32) {
+        const int2 s = seq(b);
+        if (s.x == 0) continue;
+        const int pc = plan_pieces(s.y, q);
+        n += s.x * pc;
+        split += pc > 1 ? s.x * pc : 0;
+        most = max(most, (s.y + pc - 1) / pc);
+    }
+    n = __reduce_add_sync(0xffffffffu, n) * Hkv;
+    split = __reduce_add_sync(0xffffffffu, split) * Hkv;
+    most = __reduce_max_sync(0xffffffffu, most);
+    float cost = (W + (float)n * a.entry_cost) / (float)a.slots;
+    int over[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // entries of at least that part of the longest
+    constexpr float part[8] = {1.f, .85f, .7f, .6f, .5f, .42f, .34f, .25f};
+#pragma unroll 1
+    for (int b = lane; b < B; b += 32) {
+        const int2 s = seq(b);
+        if (s.x == 0) continue;
+        const int pc = plan_pieces(s.y, q), len = (s.y + pc - 1) / pc;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) over[k] += (float)len >= part[k] * (float)most ? s.x * pc : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int rounds = (__reduce_add_sync(0xffffffffu, over[k]) * Hkv + a.slots - 1) / a.slots;
+        cost = max(cost, (float)rounds * (part[k] * (float)most + a.entry_cost));
+    }
+    cost += split > 0 ? .75f * a.entry_cost + (float)split * a.split_cost : 0.f;
+    return split <= a.max_split ? cost : 3e38f;
+}
+
+// entry e: number idx of sequence b's, whose partial results and cut row blocks start at slot0, cut0
+__device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &pv, const PlanSeq &s, int b, int pc, int idx,
+                                           int e, int slot0, int cut0) {
+    const int per = (s.tiles + pc - 1) / pc;
+    // the row blocks that see most come first; a cut sequence's row blocks of one piece are
+    // neighbours (they read the same keys)
+    const int piece = idx / s.blocks, j = s.blocks - 1 - (idx - piece * s.blocks);
+    PagedEntry o;
+    o.b = b;
+    o.row0 = s.first + j * a.T_R;
+    o.nrow = min(a.T_R, s.n - j * a.T_R);
+    o.pos0 = s.pos + j * a.T_R;
+    o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
+    // a block may see a tile more or less than the last one: the last piece takes what is left
+    o.pieces = min(pc, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
+    o.i0 = min(piece * per, o.range.ntiles);
+    o.i1 = piece == pc - 1 ? o.range.ntiles : min(o.i0 + per, o.range.ntiles);
+    if (piece >= o.pieces) o.nrow = 0;
+    o.slot = slot0 + idx;
+    o.stride = s.blocks;
+    o.pad = 0;
+    const int4 *from = reinterpret_cast<const int4 *>(&o);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(a.entries + e)[x] = from[x];
+    if (pc > 1 && piece == 0) a.cuts[cut0 + idx] = e;
+}
+
+// Up to 32 sequences: lane b of every warp has sequence b in registers, one barrier (for the tries).
 __global__ void __launch_bounds__(kPlanThreads)
-paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, int T_R, int slots, int max_split,
-                  int min_piece, float entry_cost, float split_cost, int cap, PagedPlan *plan, PagedEntry *entries, int *cuts, int *err) {
+paged_plan_small_kernel(const PagedView pv, const PlanArgs a) {
+    __shared__ float c_cost[kPlanTries];
+    __shared__ int c_q[kPlanTries];
+    static_assert(kPlanTries <= kPlanThreads / 32 && kPlanTries <= 32, "a warp for each try, a lane for each cost");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = pv.B;
+    constexpr int kWarps = kPlanThreads / 32;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    PlanSeq s{0, 0, 0, 0, 0};
+    if (lane < B) s = plan_seq(pv, a.cu, a.rows, a.T_R, lane, warp == 0 ? a.err : nullptr);
+    const float W = plan_sum((float)s.blocks * (float)s.tiles) * (float)pv.Hkv;
+    const long long nblocks = plan_sum((long long)s.blocks);
+    const int longest = __reduce_max_sync(0xffffffffu, s.tiles);
+    int Q = kPlanNoCut;
+    if (plan_tries(a, pv.Hkv, W, nblocks, longest)) {
+        if (warp < kPlanTries) {
+            int q;
+            const float cost = plan_cost(a, B, pv.Hkv, warp, W, [&](int) { return make_int2(s.blocks, s.tiles); }, q);
+            if (lane == 0) {
+                c_cost[warp] = cost;
+                c_q[warp] = q;
+            }
+        }
+        __syncthreads();
+        // (costs are positive: their bits are in their order)
+        const unsigned mine = lane < kPlanTries ? __float_as_uint(c_cost[lane]) : 0xffffffffu;
+        const unsigned least = __reduce_min_sync(0xffffffffu, mine);
+        Q = c_q[__ffs(__ballot_sync(0xffffffffu, mine == least)) - 1];
+    }
+    // longest entries first: where this lane's sequence starts is what all before it take
+    const int pc = plan_pieces(s.tiles, Q), len = s.blocks > 0 ? (s.tiles + pc - 1) / pc : -1;
+    long long start = 0, slot0 = 0, cut0 = 0, all = 0, all_cut = 0;
+#pragma unroll 4
+    for (int o = 0; o < B; ++o) {
+        const int o_len = __shfl_sync(0xffffffffu, len, o), o_blocks = __shfl_sync(0xffffffffu, s.blocks, o);
+        const int o_pc = __shfl_sync(0xffffffffu, pc, o);
+        const long long n = (long long)o_blocks * o_pc;
+        all += n;
+        all_cut += o_pc > 1 ? o_blocks : 0;
+        if (o_len > len || (o_len == len && o < lane)) {
+            start += n;
+            slot0 += o_pc > 1 ? n : 0;
+            cut0 += o_pc > 1 ? o_blocks : 0;
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.plan->entries = (int)min(all, (long long)a.cap);
+        a.plan->cut = (int)min(all_cut, (long long)a.cap);
+        a.plan->next = 0;
+    }
+    // sequences to warps, or several warps to each of a few
+    const int share = max(1, kWarps / (B > 1 ? 1 << (32 - __clz(B - 1)) : 1));
+    const int first = (int)min(start, (long long)a.cap), slot = (int)min(slot0, (long long)a.cap);
+    const int cut = (int)min(cut0, (long long)a.cap);
+    for (int k = warp / share; k < B; k += kWarps / share) {
+        PlanSeq t;
+        t.first = __shfl_sync(0xffffffffu, s.first, k);
+        t.n = __shfl_sync(0xffffffffu, s.n, k);
+        t.pos = __shfl_sync(0xffffffffu, s.pos, k);
+        t.blocks = __shfl_sync(0xffffffffu, s.blocks, k);
+        t.tiles = __shfl_sync(0xffffffffu, s.tiles, k);
+        const int t_pc = __shfl_sync(0xffffffffu, pc, k), t_first = __shfl_sync(0xffffffffu, first, k);
+        const int t_slot = __shfl_sync(0xffffffffu, slot, k), t_cut = __shfl_sync(0xffffffffu, cut, k);
+        const int n = (int)min((long long)t.blocks * t_pc, (long long)(a.cap - t_first));
+        for (int idx = (warp % share) * 32 + lane; idx < n; idx += 32 * share)
+            plan_entry(a, pv, t, k, t_pc, idx, t_first + idx, t_slot, t_cut);
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(const PagedView pv, const PlanArgs a) {
     extern __shared__ int sh[];
     int *tiles = sh, *blocks = tiles + pv.B, *order = blocks + pv.B;
     int *start = order + pv.B, *slot0 = start + pv.B + 1, *cut0 = slot0 + pv.B + 1;
@@ -71,7 +224,7 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     int longest = 0;
 #pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) {
-        const PlanSeq s = plan_seq(pv, cu, rows, T_R, b, err);
+        const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
         tiles[b] = s.tiles;
         blocks[b] = s.blocks;
         W += (float)s.blocks * (float)s.tiles;
@@ -96,42 +249,12 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
     }
     W *= (float)pv.Hkv;  // tiles of all heads
     int Q = kPlanNoCut;
-    // (rows counted twice by overlapping cu_rows may pass the list's end: then nothing is cut)
-    if (max_split > 0 && nblocks <= cap - max_split / pv.Hkv &&
-        2.f * ((float)longest + entry_cost) > (W + (float)(nblocks * pv.Hkv) * entry_cost) / (float)slots) {
+    if (plan_tries(a, pv.Hkv, W, nblocks, longest)) {
         if (warp < kPlanTries) {
-            const float share = kPlanShare[warp];
-            const int q = warp == 0 ? kPlanNoCut : max(min_piece, (int)ceilf(min(W / (float)slots * share, 1e9f)));
-            int n = 0, split = 0, most = 0;
-#pragma unroll 1
-            for (int b = lane; b < B; b += 32) {
-                if (blocks[b] == 0) continue;
-                const int pc = plan_pieces(tiles[b], q);
-                n += blocks[b] * pc;
-                split += pc > 1 ? blocks[b] * pc : 0;
-                most = max(most, (tiles[b] + pc - 1) / pc);
-            }
-            n = __reduce_add_sync(0xffffffffu, n) * pv.Hkv;
-            split = __reduce_add_sync(0xffffffffu, split) * pv.Hkv;
-            most = __reduce_max_sync(0xffffffffu, most);
-            float cost = (W + (float)n * entry_cost) / (float)slots;
-            int over[8] = {0, 0, 0, 0, 0, 0, 0, 0};  // entries of at least that part of the longest
-            constexpr float part[8] = {1.f, .85f, .7f, .6f, .5f, .42f, .34f, .25f};
-#pragma unroll 1
-            for (int b = lane; b < B; b += 32) {
-                if (blocks[b] == 0) continue;
-                const int pc = plan_pieces(tiles[b], q), len = (tiles[b] + pc - 1) / pc;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) over[k] += (float)len >= part[k] * (float)most ? blocks[b] * pc : 0;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int rounds = (__reduce_add_sync(0xffffffffu, over[k]) * pv.Hkv + slots - 1) / slots;
-                cost = max(cost, (float)rounds * (part[k] * (float)most + entry_cost));
-            }
-            cost += split > 0 ? .75f * entry_cost + (float)split * split_cost : 0.f;
+            int q;
+            const float cost = plan_cost(a, B, pv.Hkv, warp, W, [&](int b) { return make_int2(blocks[b], tiles[b]); }, q);
             if (lane == 0) {
-                c_cost[warp] = split <= max_split ? cost : 3e38f;
+                c_cost[warp] = cost;
                 c_q[warp] = q;
             }
         }
@@ -225,11 +348,11 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
         sum[2] += pc > 1 ? blocks[b] : 0;
     }
     __syncthreads();
-    const int total = min(start[B], cap);
+    const int total = min(start[B], a.cap);
     if (tid == 0) {
-        plan->entries = total;
-        plan->cut = cut0[B];
-        plan->next = 0;
+        a.plan->entries = total;
+        a.plan->cut = cut0[B];
+        a.plan->next = 0;
     }
     for (int e = tid; e < total; e += kPlanThreads) {
         int lo = 0, hi = B;  // the sequence: start[lo] <= e < start[lo + 1]
@@ -239,29 +362,8 @@ paged_plan_kernel(const PagedView pv, const int32_t *__restrict__ cu, int rows, 
             else hi = mid;
         }
         const int b = order[lo], idx = e - start[lo];
-        const PlanSeq s = plan_seq(pv, cu, rows, T_R, b, err);
-        const int pc = plan_pieces(s.tiles, Q), per = (s.tiles + pc - 1) / pc;
-        // the row blocks that see most come first; a cut sequence's row blocks of one piece are
-        // neighbours (they read the same keys)
-        const int j = s.blocks - 1 - idx % s.blocks, piece = idx / s.blocks;
-        PagedEntry o;
-        o.b = b;
-        o.row0 = s.first + j * T_R;
-        o.nrow = min(T_R, s.n - j * T_R);
-        o.pos0 = s.pos + j * T_R;
-        o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
-        // a block may see a tile more or less than the last one: the last piece takes what is left
-        o.pieces = min(pc, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
-        o.i0 = min(piece * per, o.range.ntiles);
-        o.i1 = piece == pc - 1 ? o.range.ntiles : min(o.i0 + per, o.range.ntiles);
-        if (piece >= o.pieces) o.nrow = 0;
-        o.slot = slot0[lo] + idx;
-        o.stride = s.blocks;
-        o.pad = 0;
-        const int4 *from = reinterpret_cast<const int4 *>(&o);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(entries + e)[x] = from[x];
-        if (pc > 1 && piece == 0) cuts[cut0[lo] + idx] = e;
+        const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
+        plan_entry(a, pv, s, b, plan_pieces(s.tiles, Q), idx, e, slot0[lo], cut0[lo]);
     }
 }
 
@@ -271,14 +373,15 @@ namespace yoco_host {
 using namespace yoco;
 
 cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
-    const size_t smem = (6 * (size_t)a.cache->B + 3) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((6 * (size_t)kPagedMaxB + 3) * sizeof(int)));
+    const bool small = a.cache->B <= 32;
+    cudaError_t e = small ? cudaSuccess
+                          : cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)((6 * (size_t)kPagedMaxB + 3) * sizeof(int)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = small ? 0 : (6 * (size_t)a.cache->B + 3) * sizeof(int);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -286,9 +389,9 @@ cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, paged_view(a), a.cu, a.rows, g.rows, g.slots, g.max_split,
-                              g.min_piece, g.entry_cost, g.split_cost, g.cap, (PagedPlan *)g.plan, (PagedEntry *)g.entries,
-                              (int *)g.cuts, a.err);
+    const PlanArgs p{a.cu, a.rows, g.rows, g.slots, g.max_split, g.min_piece, g.entry_cost, g.split_cost, g.cap,
+                     (PagedPlan *)g.plan, (PagedEntry *)g.entries, (int *)g.cuts, a.err};
+    return cudaLaunchKernelEx(&cfg, small ? paged_plan_small_kernel : paged_plan_kernel, paged_view(a), p);
 }
 
 }  // namespace yoco_host
