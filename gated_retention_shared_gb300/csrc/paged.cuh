@@ -118,7 +118,7 @@ static_assert(sizeof(PagedEntry) == 64, "entries are read by 16 lanes");
 struct PagedPlan {
     int entries;  // in the list
     int next;     // entry x kv head that a block takes next, counted from the grid's size
-    int cut;      // row blocks in more than one piece: entries cuts[0 .. cut) are their first
+    int cut;      // row blocks in more than one piece: cuts[0 .. cut) are their first entries
 };
 
 // ------------------------------------------------ one row per sequence (decode)

@@ -58,8 +58,8 @@ struct PlanArgs {
     float entry_cost, split_cost;
     int cap;
     PagedPlan *plan;
-    PagedEntry *entries;
-    int *cuts, *err;
+    PagedEntry *entries, *cuts;
+    int *err;
 };
 
 // sizes are tried where something may be gained by them, and where the list has room for cuts
@@ -132,7 +132,10 @@ __device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &p
     const int4 *from = reinterpret_cast<const int4 *>(&o);
 #pragma unroll
     for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(a.entries + e)[x] = from[x];
-    if (pc > 1 && piece == 0) a.cuts[cut0 + idx] = e;
+    if (pc > 1 && piece == 0) {  // for the merge
+#pragma unroll
+        for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(a.cuts + cut0 + idx)[x] = from[x];
+    }
 }
 
 // Up to 32 sequences: lane b of every warp has sequence b in registers, one barrier (for the tries).
@@ -390,7 +393,7 @@ cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) 
     cfg.numAttrs = 1;
     count_launches(1);
     const PlanArgs p{a.cu, a.rows, g.rows, g.slots, g.max_split, g.min_piece, g.entry_cost, g.split_cost, g.cap,
-                     (PagedPlan *)g.plan, (PagedEntry *)g.entries, (int *)g.cuts, a.err};
+                     (PagedPlan *)g.plan, (PagedEntry *)g.entries, (PagedEntry *)g.cuts, a.err};
     return cudaLaunchKernelEx(&cfg, small ? paged_plan_small_kernel : paged_plan_kernel, paged_view(a), p);
 }
 

@@ -463,47 +463,59 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 }
 
 // Joins the pieces of the row blocks that are cut: partials [slot][kv head][set][D + 2][R], a
-// part of the work is (row block, kv head, set) and kMergeCols head dims, thread = row.  The
-// pieces' maxima first, then kMergePieces pieces' values at a time: two rounds of L2 latency and
-// a stream, not a round for each piece.  The grid does not grow with what the call might have
-// cut, so a call that cuts nothing does not launch thousands of blocks to find that out.
-// (12 mixed sequences, up to ten pieces: 13 us; nothing cut: 4 us, 9 with a block for each part)
+// part of the work is (row block, kv head, set) and kMergeCols head dims, thread = row.
+// kMergePieces pieces' maxima, sums and values come in at a time: a latency for so many pieces,
+// not for each.  The grid does not grow with what the call might have cut, so a call that cuts
+// nothing does not launch thousands of blocks to find that out.
 constexpr int kMergeCols = 8, kMergePieces = 4, kMergeBlocks = 12;
 
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(R)
 paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const PagedPlan *__restrict__ plan,
-                        const PagedEntry *__restrict__ entries, const int *__restrict__ cuts, int rows, int Hq, int Hkv,
-                        int sets) {
+                        const PagedEntry *__restrict__ cuts, int rows, int Hq, int Hkv, int sets) {
     const int r = threadIdx.x, G = Hq / Hkv, TS = R / G;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    // (the first part's row block and how many there are, in one latency)
+    int row0, nrow, pieces, slot, stride;
+    auto look_up = [&](int64_t w) {
+        const int *c = reinterpret_cast<const int *>(cuts + w / (D / kMergeCols) / sets / Hkv);
+        row0 = c[1], nrow = c[2], pieces = c[6], slot = c[7], stride = c[8];
+    };
+    int64_t w = blockIdx.x;
+    look_up(w);
     const int64_t parts = (int64_t)plan->cut * Hkv * sets * (D / kMergeCols);
-    for (int64_t w = blockIdx.x; w < parts; w += gridDim.x) {
+    for (; w < parts; w += gridDim.x) {
+        if (w != blockIdx.x) look_up(w);
         const int d0 = (int)(w % (D / kMergeCols)) * kMergeCols, unit = (int)(w / (D / kMergeCols));
         const int set = unit % sets, hk = unit / sets % Hkv;
-        const PagedEntry &blk = entries[cuts[unit / sets / Hkv]];
-        const int tok = set * TS + r / G, pieces = blk.pieces;
-        if (blk.nrow == 0 || pieces == 1 || r >= TS * G || tok >= blk.nrow) continue;
-        const size_t step = (size_t)blk.stride * Hkv * sets * (D + 2) * R;  // from piece to piece
-        const float *pp = part + (((size_t)blk.slot * Hkv + hk) * sets + set) * (D + 2) * R + r;
-        float M = -INFINITY;
-#pragma unroll 8
-        for (int s = 0; s < pieces; ++s) M = fmaxf(M, __ldcg(pp + s * step + D * R));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f, A[kMergeCols];
+        const int tok = set * TS + r / G;
+        if (nrow == 0 || pieces == 1 || r >= TS * G || tok >= nrow) continue;
+        const size_t step = (size_t)stride * Hkv * sets * (D + 2) * R;  // from piece to piece
+        const float *pp = part + (((size_t)slot * Hkv + hk) * sets + set) * (D + 2) * R + r;
+        float M = -INFINITY, L = 0.f, A[kMergeCols];
 #pragma unroll
         for (int e = 0; e < kMergeCols; ++e) A[e] = 0.f;
         for (int s0 = 0; s0 < pieces; s0 += kMergePieces) {
-            float m[kMergePieces], l[kMergePieces], x[kMergePieces][kMergeCols];
+            float m[kMergePieces], l[kMergePieces], x[kMergePieces][kMergeCols], top = M;
 #pragma unroll
             for (int k = 0; k < kMergePieces; ++k) {
                 const float *q = pp + min(s0 + k, pieces - 1) * step;
-                m[k] = s0 + k < pieces ? __ldcg(q + D * R) : -INFINITY;
+                m[k] = __ldcg(q + D * R);
                 l[k] = __ldcg(q + (D + 1) * R);
 #pragma unroll
                 for (int e = 0; e < kMergeCols; ++e) x[k][e] = __ldcg(q + (d0 + e) * R);
             }
+#pragma unroll
+            for (int k = 0; k < kMergePieces; ++k) {
+                if (s0 + k >= pieces) m[k] = -INFINITY;
+                top = fmaxf(top, m[k]);
+            }
+            const float ref = top == -INFINITY ? 0.f : top, old = exp2f(M - ref);
+            M = top;
+            L *= old;
+#pragma unroll
+            for (int e = 0; e < kMergeCols; ++e) A[e] *= old;
 #pragma unroll
             for (int k = 0; k < kMergePieces; ++k) {
                 const float f = exp2f(m[k] - ref);
@@ -514,8 +526,8 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
             }
         }
         const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-        T *op = O + (size_t)(blk.row0 + tok) * Hq * D + (size_t)(hk * G + r % G) * D + d0;
-        if (!YOCO_DCHECK(blk.row0 + tok < rows, 0x66)) continue;
+        T *op = O + (size_t)(row0 + tok) * Hq * D + (size_t)(hk * G + r % G) * D + d0;
+        if (!YOCO_DCHECK(row0 + tok < rows, 0x66)) continue;
 #pragma unroll
         for (int e = 0; e < kMergeCols; e += 16 / (int)sizeof(T)) {
             uint32_t w[4];
@@ -577,7 +589,7 @@ static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &
     g.entries = ws + at;
     at += align256((size_t)g.cap * sizeof(PagedEntry));
     g.cuts = ws + at;
-    at += align256((size_t)(split / 2) * sizeof(int));
+    at += align256((size_t)(split / 2) * sizeof(PagedEntry));
     g.part = (float *)(ws + at);
     return at + (size_t)split * c->Hkv * (tc ? 256 : kPreRows) * (c->d + 2) * sizeof(float);
 }
@@ -671,8 +683,7 @@ static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
     pdl_config(cfg, attr, dim3((unsigned)std::min<int64_t>(cut * a.cache->Hkv * sets * (D / kMergeCols), kMergeBlocks * g.slots)), R, 0, st);
     count_launches(1);
     return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, (const float *)g.part, (T *)a.O,
-                              (const PagedPlan *)g.plan, (const PagedEntry *)g.entries, (const int *)g.cuts, a.rows, a.Hq,
-                              a.cache->Hkv, sets);
+                              (const PagedPlan *)g.plan, (const PagedEntry *)g.cuts, a.rows, a.Hq, a.cache->Hkv, sets);
 }
 
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st) {
