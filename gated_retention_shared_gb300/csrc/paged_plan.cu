@@ -1,6 +1,7 @@
 // paged_plan.cu -- the work list of a prefill over the paged cache, from the lengths on the
-// device: one thread block, a few microseconds, so that neither the host nor each of the
-// prefill's thread blocks has to look for its rows.
+// device: one thread block, about 3 us for up to 32 sequences and 5 us for more (latencies one
+// after the other), so that neither the host nor each of the prefill's thread blocks has to look
+// for its rows.
 //
 // A sequence's tiles are cut into pieces of at most Q tiles where that pays.  Q is chosen for
 // the whole call: each warp takes one share of the tiles that an SM gets on average (0.15 to 3

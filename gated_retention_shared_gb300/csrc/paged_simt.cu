@@ -241,7 +241,10 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
 // and dims 4 tx + 64 j .. of the output.  Everything the products read is in shared memory
 // as fp32, two blocks to an SM.  K and V have one buffer each: the next step's K comes in
 // while this step's softmax and P V run, its V while the next scores do (asynchronous copies
-// for fp32, registers for bf16, which is widened on the way).  Bound by the fp32 pipe.
+// for fp32, registers for bf16, which is widened on the way).  Bound by shared-memory reads and
+// the fp32 pipe, about half of its peak (4096 fp32 rows, 8 over 4 heads x 64: 475 us, 36 TFLOP/s;
+// 8 x 8 values to a thread and half the reads: 480 us).  Four chunks of 99 to 470 rows, 31 us: the
+// plan 3, two to four steps of 5 us each after 3 us of start, the merge 4.
 constexpr int kPreRows = 64, kPreKeys = 64, kPreThreads = 256;
 constexpr int kPreMinPiece = 1;       // tiles
 constexpr float kPreSplitCost = .002f;
@@ -308,8 +311,10 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
+    // (both loads at once: the list has room for every entry of the grid)
+    const int word = tid < 16 ? reinterpret_cast<const int *>(entries + entry)[tid] : 0;
     if (entry >= plan->entries) return;
-    if (tid < 16) reinterpret_cast<int *>(&blk)[tid] = reinterpret_cast<const int *>(entries + entry)[tid];
+    if (tid < 16) reinterpret_cast<int *>(&blk)[tid] = word;
     __syncthreads();
     if (blk.nrow == 0) return;
     const int nr = blk.nrow * G;  // rows in use: (token, head) = (r / G, r % G)
@@ -361,7 +366,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int dd = 0; dd < D; dd += 4) {
             float4 a[4], b[4];
 #pragma unroll
@@ -407,7 +412,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         }
         stage_v.land(sv);
         __syncthreads();  // V and P there
-#pragma unroll 2
+#pragma unroll 4
         for (int kk = 0; kk < kPreKeys; kk += 4) {
             float pr[4][4];
 #pragma unroll
