@@ -348,6 +348,12 @@ def test_prefill_one_long_sequence_among_many_short_ones(Y, dtype):
     run_prefill(Y, [30] * 40 + [100], [50] * 40 + [9000], 8, 8, 128, 64, dtype)
 
 
+@pytest.mark.parametrize("B", [2, 16, 31, 32, 33, 256, 257])
+def test_prefill_of_as_many_sequences_as_a_way_of_planning_takes(Y, B):
+    new = [(5 * b + 2) % 9 for b in range(B - 1)] + [90]
+    run_prefill(Y, new, [(31 * b) % 200 for b in range(B - 1)] + [5000], 2, 1, 128, 16, "bf16")
+
+
 def test_prefill_of_hundreds_of_sequences_and_a_long_one(Y):
     run_prefill(Y, [2, 0, 1] * 100 + [70, 3], [3, 40, 0] * 100 + [6000, 900], 2, 1, 128, 16, "bf16")
 
