@@ -24,6 +24,14 @@ struct PagedView {
 
 constexpr int kPagedTile = 128;  // keys per tile
 
+// What one kernel of a call leaves for the next: that one may be running already when it is
+// written, which a load through the read-only path does not allow for.
+__device__ __forceinline__ int paged_ld(const int *p) {
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // workspace status codes of bad metadata (kErrMagic | code); the call goes on without
 // touching what they name
 constexpr int kErrPagedLen = 0x60;   // a length below zero or past the table

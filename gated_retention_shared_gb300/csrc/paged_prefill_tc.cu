@@ -209,8 +209,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     auto fetch = [&](int item, int entry, PagedPreTask &task) {
         for (;;) {
             // (both loads at once: the list has room for `cap` entries)
-            const int word = lane < 16 ? reinterpret_cast<const int *>(entries + min(entry, cap - 1))[lane] : 0;
-            const int count = plan->entries;
+            const int word = lane < 16 ? paged_ld(reinterpret_cast<const int *>(entries + min(entry, cap - 1)) + lane) : 0;
+            const int count = paged_ld(&plan->entries);
             if (entry >= count) {
                 if (lane == 0) task.more = 0;
                 break;

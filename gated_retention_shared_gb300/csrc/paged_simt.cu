@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(D)
 paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ cuts, T *__restrict__ O, int G) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const PagedCut cut = cuts[blockIdx.x + 1];
+    const int *note = reinterpret_cast<const int *>(cuts + blockIdx.x + 1);
+    const PagedCut cut{paged_ld(note), paged_ld(note + 1), paged_ld(note + 2), paged_ld(note + 3)};
     if (cut.unit < 0) return;
     const int g = blockIdx.y, dd = threadIdx.x;
     float M = -INFINITY, L = 0.f, A = 0.f;
@@ -312,8 +313,8 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
     // (both loads at once: the list has room for every entry of the grid)
-    const int word = tid < 16 ? reinterpret_cast<const int *>(entries + entry)[tid] : 0;
-    if (entry >= plan->entries) return;
+    const int word = tid < 16 ? paged_ld(reinterpret_cast<const int *>(entries + entry) + tid) : 0;
+    if (entry >= paged_ld(&plan->entries)) return;
     if (tid < 16) reinterpret_cast<int *>(&blk)[tid] = word;
     __syncthreads();
     if (blk.nrow == 0) return;
@@ -485,11 +486,12 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
     int row0, nrow, pieces, slot, stride;
     auto look_up = [&](int64_t w) {
         const int *c = reinterpret_cast<const int *>(cuts + w / (D / kMergeCols) / sets / Hkv);
-        row0 = c[1], nrow = c[2], pieces = c[6], slot = c[7], stride = c[8];
+        row0 = paged_ld(c + 1), nrow = paged_ld(c + 2), pieces = paged_ld(c + 6), slot = paged_ld(c + 7);
+        stride = paged_ld(c + 8);
     };
     int64_t w = blockIdx.x;
     look_up(w);
-    const int64_t parts = (int64_t)plan->cut * Hkv * sets * (D / kMergeCols);
+    const int64_t parts = (int64_t)paged_ld(&plan->cut) * Hkv * sets * (D / kMergeCols);
     for (; w < parts; w += gridDim.x) {
         if (w != blockIdx.x) look_up(w);
         const int d0 = (int)(w % (D / kMergeCols)) * kMergeCols, unit = (int)(w / (D / kMergeCols));
