@@ -515,7 +515,7 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
             }
 #pragma unroll
             for (int k = 0; k < kMergePieces; ++k) {
-                if (s0 + k >= pieces) m[k] = -INFINITY;
+                if (s0 + k >= pieces) m[k] = -INFINITY, l[k] = 0.f;
                 top = fmaxf(top, m[k]);
             }
             const float ref = top == -INFINITY ? 0.f : top, old = exp2f(M - ref);
@@ -526,7 +526,9 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
 #pragma unroll
             for (int k = 0; k < kMergePieces; ++k) {
                 const float f = exp2f(m[k] - ref);
-                if (m[k] == -INFINITY) continue;  // no part of it, whatever it holds
+                // nothing seen in it, whatever it holds (where something was, it may be that every
+                // score is NaN, which no maximum shows: the sum is NaN then)
+                if (m[k] == -INFINITY && l[k] == 0.f) continue;
                 L = fmaf(l[k], f, L);
 #pragma unroll
                 for (int e = 0; e < kMergeCols; ++e) A[e] = fmaf(x[k][e], f, A[e]);

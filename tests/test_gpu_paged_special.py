@@ -1,0 +1,119 @@
+"""GPU checks of the paged calls where values or metadata are not the ordinary ones: NaN and
+infinities in queries and in slots that rows see, rows that see nothing, row bounds that fall
+back, sequences' rows in several calls' order.
+
+What a row gives is softmax's own answer: NaN where a score that it sees is NaN or +inf or where
+all of them are -inf, the rest of the keys' answer where some are -inf, and zeros for a row at a
+negative position, which sees nothing.  Finite answers are held to the bounds of
+test_gpu_paged.py (its S taken over the slots of finite score: the others' weights are 0 on both
+sides)."""
+import math
+
+import pytest
+import torch
+
+import test_gpu_paged as P
+
+pytestmark = pytest.mark.gpu
+Y = P.Y  # the fixture
+
+U, DT, TYPES = P.U, P.DT, P.TYPES
+
+
+def answer(pool, q, b, pos, scale):
+    """(o, bound, rows x heads that are NaN) in 64 bits of rows q [T, Hq, d] at positions pos."""
+    T, Hq, d = q.shape
+    out, tol = torch.zeros(T, Hq, d, dtype=torch.float64), torch.zeros(T, Hq, d, dtype=torch.float64)
+    nan = torch.zeros(T, Hq, dtype=torch.bool)
+    seen = torch.arange(pool.lens[b])[None] <= pos[:, None]
+    n = seen.sum(1, keepdim=True)
+    for h in range(Hq):
+        k, v = pool.rows(b, h // (Hq // pool.Hkv))
+        x = (q[:, h].double()[:, None, :] * k[None]).sum(-1) * scale if k.shape[0] <= 4096 else q[:, h].double() @ k.T * scale
+        size = (q[:, h].double().abs() @ torch.where(torch.isfinite(k), k, 0.0).abs().T * scale)
+        x = x.masked_fill(~seen, -math.inf)
+        p = torch.softmax(x, 1)
+        nan[:, h] = p.isnan().any(1) & (n[:, 0] > 0)
+        p = torch.nan_to_num(p)
+        S = torch.where(seen & torch.isfinite(x), size, 0.0).amax(1, keepdim=True)
+        e32 = U * (2 * (d + 4) * S + 2 * n + 16)
+        w, half = (2.0 ** -8 if d == 128 else 0.0, 2.0 ** -8) if q.dtype == torch.bfloat16 else (0.0, U)
+        o = p @ v
+        out[:, h], tol[:, h] = o, half * o.abs() + (e32 + w) * (p @ v.abs()) + 1e-30
+    return out, tol, nan
+
+
+def compare(got, pool, Q, cu, scale):
+    got = got.cpu().double()
+    some = False
+    for b in range(len(pool.lens)):
+        T = cu[b + 1] - cu[b]
+        ref, tol, nan = answer(pool, Q[cu[b]:cu[b + 1]].cpu(), b, torch.arange(T) + pool.lens[b] - T, scale)
+        mine = got[cu[b]:cu[b + 1]]
+        assert torch.equal(mine.isnan().any(-1), nan), (b, int(mine.isnan().any(-1).sum()), int(nan.sum()))
+        assert torch.equal(mine.isnan().all(-1), nan)
+        off = ((mine - ref).abs() / tol).masked_fill(nan[..., None], 0.0)
+        assert bool((off <= 1.0).all()), (b, float(off.max()))
+        some |= bool(nan.any())
+    return some
+
+
+def queries(rows, Hq, d, dtype, seed):
+    return (torch.randn(rows, Hq, d, generator=torch.Generator().manual_seed(seed)) * 2).to(DT[dtype])
+
+
+def prefill(Y, pool, Q, cu):
+    O = torch.full_like(Q, 7.0)
+    Y.yoco_paged_attn_prefill(Q, pool.dev, torch.tensor(cu, dtype=torch.int32, device="cuda"), O)
+    return O
+
+
+def slots(pool, b, at):
+    at = torch.as_tensor(at)
+    return pool.table[b].long()[at // pool.page], at % pool.page
+
+
+def put(pool, b, at, k, hk=slice(None), channel=slice(None)):
+    """k into slots `at` of sequence b, on both sides."""
+    pages, rows = slots(pool, b, at)
+    for p, r in zip(pages.tolist(), rows.tolist()):
+        pool.k[p, hk, r, channel] = k
+    pool.dev.k.copy_(pool.k)
+
+
+# few keys, and so many that the keys of these few rows are cut into pieces
+CONTEXTS = [90, 9000]
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("ctx", CONTEXTS)
+def test_prefill_of_a_nan_query_row(Y, dtype, d, ctx):
+    pool = P.Pool(Y, [ctx + 5, 40], 2, d, 64, dtype)
+    Q = queries(7, 6, d, dtype, 21)
+    Q[2, 4, 3] = math.nan
+    Q[6, 0] = math.nan
+    Q = Q.cuda()
+    assert compare(prefill(Y, pool, Q, [0, 5, 7]), pool, Q, [0, 5, 7], d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("ctx", CONTEXTS)
+@pytest.mark.parametrize("lo,hi", [(3, 4), (0, 700), (0, 768), (80, 93)])
+def test_prefill_over_nan_keys(Y, dtype, d, ctx, lo, hi):
+    """One NaN key, pieces of them (768 keys end where pieces of one, two or three tiles do), and
+    keys that only the later rows see."""
+    pool = P.Pool(Y, [ctx + 5, 40], 2, d, 64, dtype)
+    lo, hi = min(lo, ctx), min(hi, ctx + 3)
+    put(pool, 0, range(lo, hi), math.nan, hk=1)
+    Q = queries(7, 6, d, dtype, 22).cuda()
+    assert compare(prefill(Y, pool, Q, [0, 5, 7]), pool, Q, [0, 5, 7], d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_prefill_of_chunks_with_a_nan_key_among_the_new_rows(Y, dtype, d):
+    """Rows before the key's position are sound, those from it on are not."""
+    pool = P.Pool(Y, [300, 140], 2, d, 64, dtype)
+    put(pool, 0, [201], math.nan, hk=0)
+    put(pool, 1, [139], math.nan)
+    Q = queries(440, 6, d, dtype, 23).cuda()
+    assert compare(prefill(Y, pool, Q, [0, 300, 440]), pool, Q, [0, 300, 440], d ** -0.5)
