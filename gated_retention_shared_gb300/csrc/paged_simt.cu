@@ -133,15 +133,16 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                         s[x] = ok[x] ? d : -INFINITY;
                         top = fmaxf(top, s[x]);
                     }
-                    if (top == -INFINITY) continue;
-                    const float old = exp2f(m[i] - top);
+                    // (no score yet, or NaN alone, which no maximum shows: the weights are 0 or NaN)
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    const float old = exp2f(m[i] - ref);
                     m[i] = top;
                     l[i] *= old;
 #pragma unroll
                     for (int e = 0; e < EL; ++e) acc[i][e] *= old;
 #pragma unroll
                     for (int x = 0; x < kDecKeys; ++x) {
-                        const float pe = exp2f(s[x] - top);
+                        const float pe = exp2f(s[x] - ref);
                         l[i] += pe;
 #pragma unroll
                         for (int e = 0; e < EL; ++e) acc[i][e] = fmaf(pe, vx[x][e], acc[i][e]);

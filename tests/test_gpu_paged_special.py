@@ -117,3 +117,22 @@ def test_prefill_of_chunks_with_a_nan_key_among_the_new_rows(Y, dtype, d):
     put(pool, 1, [139], math.nan)
     Q = queries(440, 6, d, dtype, 23).cuda()
     assert compare(prefill(Y, pool, Q, [0, 300, 440]), pool, Q, [0, 300, 440], d ** -0.5)
+
+
+def decode(Y, pool, Q):
+    O = torch.full_like(Q, 7.0)
+    Y.yoco_paged_attn_decode(Q, pool.dev, O)
+    return O
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("G", [1, 3, 16])
+def test_decode_of_nan_queries_and_nan_keys(Y, dtype, d, G):
+    """A NaN query; one NaN key among 1, 20 and 700; the first 64; all; the last."""
+    pool = P.Pool(Y, [50, 1, 20, 700, 700, 130, 300, 70], 2, d, 16, dtype)
+    for b, at in ((1, [0]), (2, [7]), (3, [3]), (4, range(64)), (5, range(130)), (6, [299])):
+        put(pool, b, at, math.nan, hk=b % 2)
+    Q = queries(8, 2 * G, d, dtype, 24)
+    Q[0, G] = math.nan
+    Q = Q.cuda()
+    assert compare(decode(Y, pool, Q), pool, Q, list(range(9)), d ** -0.5)
