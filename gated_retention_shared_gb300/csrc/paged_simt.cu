@@ -221,7 +221,11 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
             a[x] = __ldcg(pp + dd);
             top = fmaxf(top, m[x]);
         }
-        if (top == -INFINITY) continue;
+        if (top == -INFINITY) {  // no score yet, or NaN alone, which no maximum shows: the sums are 0 or NaN
+#pragma unroll
+            for (int x = 0; x < kMergeBatch; ++x) L += l[x];
+            continue;
+        }
         const float old = exp2f(M - top);
         M = top;
         L *= old;

@@ -136,3 +136,24 @@ def test_decode_of_nan_queries_and_nan_keys(Y, dtype, d, G):
     Q[0, G] = math.nan
     Q = Q.cuda()
     assert compare(decode(Y, pool, Q), pool, Q, list(range(9)), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("at", [range(5), range(4096), range(6000), range(8192), range(40000, 60001)])
+def test_decode_of_a_long_sequence_with_nan_keys_is_nan(Y, dtype, d, at):
+    """The runs that the keys are cut into (two tiles, four on the tensor cores) are NaN in part,
+    from the first on, the first sixteen and no other, up to the last."""
+    pool = P.Pool(Y, [60001], 1, d, 64, dtype)
+    put(pool, 0, at, math.nan)
+    Q = queries(1, 2, d, dtype, 25).cuda()
+    assert bool(decode(Y, pool, Q).isnan().all())
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_decode_of_a_long_sequence_with_a_nan_query_is_nan(Y, dtype, d):
+    pool = P.Pool(Y, [60001], 1, d, 64, dtype)
+    Q = queries(1, 2, d, dtype, 26)
+    Q[0, 1, 5] = math.nan
+    Q = Q.cuda()
+    O = decode(Y, pool, Q)
+    assert bool(O[0, 1].isnan().all()) and bool(torch.isfinite(O[0, 0]).all())
