@@ -232,9 +232,10 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
         A *= old;
 #pragma unroll
         for (int x = 0; x < kMergeBatch; ++x) {
-            const float f = c0 + x <= cut.c_last ? exp2f(m[x] - top) : 0.f;
+            const bool there = c0 + x <= cut.c_last;
+            const float f = there ? exp2f(m[x] - top) : 0.f;
             L = fmaf(l[x], f, L);
-            A = fmaf(a[x], f, A);
+            A = fmaf(there ? a[x] : 0.f, f, A);  // (a value may be infinite)
         }
     }
     O[((size_t)cut.unit * G + g) * D + dd] = from_f32<T>(A / L);

@@ -157,3 +157,18 @@ def test_decode_of_a_long_sequence_with_a_nan_query_is_nan(Y, dtype, d):
     Q = Q.cuda()
     O = decode(Y, pool, Q)
     assert bool(O[0, 1].isnan().all()) and bool(torch.isfinite(O[0, 0]).all())
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("n", [95, 9003, 60001])
+def test_infinite_values_come_through(Y, dtype, d, n):
+    """A value of +inf that a row sees makes its channel +inf, whole or cut, and no other."""
+    pool = P.Pool(Y, [n], 1, d, 64, dtype)
+    for m in (3, n // 2, n - 4):
+        page, row = (int(x) for x in slots(pool, 0, m))
+        pool.dev.v[page, 0, row, 5] = math.inf
+    Q = queries(3, 2, d, dtype, 30).cuda() * 0.1
+    for O in (prefill(Y, pool, Q, [0, 3]), decode(Y, pool, Q[:1].contiguous())):
+        assert bool((O[..., 5] == math.inf).all())
+        O[..., 5] = 0
+        assert bool(torch.isfinite(O).all())
