@@ -647,6 +647,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         uint32_t ov[32];
                         tmem_ld32(o_t + cb * 32, ov);
                         tmem_wait_ld();
+                        if (__builtin_expect(pos < 0, 0)) {  // sees nothing: zero, though 0 times a value may be NaN
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ov[e] = 0;
+                        }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t w[4];

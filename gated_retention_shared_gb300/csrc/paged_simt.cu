@@ -464,12 +464,13 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
             }
         } else if (r < nr) {
             const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+            const bool none = blk.pos0 + r / G < 0;  // sees nothing: zero, though 0 times a value may be NaN
             T *op = O + (blk.row0 + r / G) * row_stride + (size_t)(hk * G + r % G) * D;
             if (!YOCO_DCHECK(blk.row0 + r / G < rows && hk * G + r % G < Hq, 0x65)) continue;
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) op[64 * n + 4 * tx + e] = from_f32<T>(acc[i][4 * n + e] * inv);
+                for (int e = 0; e < 4; ++e) op[64 * n + 4 * tx + e] = from_f32<T>(none ? 0.f : acc[i][4 * n + e] * inv);
         }
     }
 }

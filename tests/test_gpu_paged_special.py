@@ -172,3 +172,16 @@ def test_infinite_values_come_through(Y, dtype, d, n):
         assert bool((O[..., 5] == math.inf).all())
         O[..., 5] = 0
         assert bool(torch.isfinite(O).all())
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("length,rows", [(10, 25), (2900, 2917)])
+def test_rows_that_see_nothing_are_zeros_whatever_the_others_see(Y, dtype, d, length, rows):
+    """More new rows than the sequence holds, in one block with rows whose values are NaN."""
+    pool = P.Pool(Y, [length], 2, d, 16, dtype)
+    pages, at = slots(pool, 0, range(min(length, 40)))
+    for p, r in zip(pages.tolist(), at.tolist()):
+        pool.dev.v[p, :, r] = math.nan
+    Q = queries(rows, 6, d, dtype, 29).cuda()
+    O = prefill(Y, pool, Q, [0, rows])
+    assert bool((O[:rows - length] == 0).all()) and bool(O[rows - length:].isnan().all())
