@@ -641,7 +641,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     // o = O / l as bf16, staged in this set's Q tile (every S product is done), then rows
                     // of 256 bytes side by side
                     uint8_t *stg = sQ + x * kCTile;
-                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+                    // (a row whose scores are all -inf: 0 / 0, NaN as softmax has it)
+                    const float inv = pos < 0 ? 0.f : 1.f / l;
 #pragma unroll 1
                     for (int cb = 0; cb < 4; ++cb) {
                         uint32_t ov[32];

@@ -463,7 +463,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
                 pp[(D + 1) * kPreRows] = l[i];
             }
         } else if (r < nr) {
-            const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+            const float inv = 1.f / l[i];            // (0 / 0 where every score is -inf: NaN, as softmax has it)
             const bool none = blk.pos0 + r / G < 0;  // sees nothing: zero, though 0 times a value may be NaN
             T *op = O + (blk.row0 + r / G) * row_stride + (size_t)(hk * G + r % G) * D;
             if (!YOCO_DCHECK(blk.row0 + r / G < rows && hk * G + r % G < Hq, 0x65)) continue;
@@ -490,11 +490,11 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // (the first part's row block and how many there are, in one latency)
-    int row0, nrow, pieces, slot, stride;
+    int row0, nrow, pos0, pieces, slot, stride;
     auto look_up = [&](int64_t w) {
         const int *c = reinterpret_cast<const int *>(cuts + w / (D / kMergeCols) / sets / Hkv);
-        row0 = paged_ld(c + 1), nrow = paged_ld(c + 2), pieces = paged_ld(c + 6), slot = paged_ld(c + 7);
-        stride = paged_ld(c + 8);
+        row0 = paged_ld(c + 1), nrow = paged_ld(c + 2), pos0 = paged_ld(c + 3), pieces = paged_ld(c + 6);
+        slot = paged_ld(c + 7), stride = paged_ld(c + 8);
     };
     int64_t w = blockIdx.x;
     look_up(w);
@@ -541,7 +541,8 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
                 for (int e = 0; e < kMergeCols; ++e) A[e] = fmaf(x[k][e], f, A[e]);
             }
         }
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        // a row that sees nothing: zero; one whose scores are all -inf: 0 / 0, NaN as softmax has it
+        const float inv = pos0 + tok < 0 ? 0.f : 1.f / L;
         T *op = O + (size_t)(row0 + tok) * Hq * D + (size_t)(hk * G + r % G) * D + d0;
         if (!YOCO_DCHECK(row0 + tok < rows, 0x66)) continue;
 #pragma unroll

@@ -452,10 +452,12 @@ YOCO_API yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_h
  * may have been given back.  Query head h reads kv head h / (Hq / Hkv).
  *   Q, O [rows, Hq, d] cache dtype, dense; cu_rows as above, not NULL.
  * Rows at negative positions see nothing and come out as zeros; rows of O
- * behind the last sequence are not written.  Slots that no row of a sequence
- * sees may hold anything, NaN among it.  A row gives a slot that only other rows
- * of its sequence see the weight 0, so a v there that is not finite may make it
- * NaN.  O must not overlap Q.
+ * behind the last sequence are not written.  Where a score that a row sees is
+ * NaN or +inf, or all of them are -inf, softmax has no answer and the row is NaN.
+ * Slots that no row of a sequence sees may hold anything, NaN among it.  A row
+ * gives a slot that only other rows of its sequence see the weight 0, so a v
+ * there that is not finite may make it NaN (not a row at a negative position).
+ * O must not overlap Q.
  * Supported: Hq / Hkv <= 16; scale > 0.
  *   workspace  >= yoco_paged_attn_workspace_size(Hq, rows, cache) bytes,
  *              256-byte aligned.  Calls that share it must be ordered on one

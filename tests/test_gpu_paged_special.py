@@ -185,3 +185,32 @@ def test_rows_that_see_nothing_are_zeros_whatever_the_others_see(Y, dtype, d, le
     Q = queries(rows, 6, d, dtype, 29).cuda()
     O = prefill(Y, pool, Q, [0, rows])
     assert bool((O[:rows - length] == 0).all()) and bool(O[rows - length:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("ctx", CONTEXTS)
+@pytest.mark.parametrize("keys", ["all", "first", "last"])
+def test_scores_of_minus_infinity(Y, dtype, d, ctx, keys):
+    """Keys of score -inf have the weight 0; where a row sees no others there is no softmax."""
+    n = ctx + 3
+    pool = P.Pool(Y, [n, 10], 1, d, 64, dtype)
+    at = {"all": range(n), "first": range(n - 60), "last": range(n - 60, n)}[keys]
+    put(pool, 0, at, -math.inf, channel=2)
+    Q = queries(5, 3, d, dtype, 27)
+    Q[:, :, 2] = 1.0
+    Q = Q.cuda()
+    assert compare(prefill(Y, pool, Q, [0, 3, 5]), pool, Q, [0, 3, 5], d ** -0.5) == (keys == "all")
+    Q = Q[:2].contiguous()
+    assert compare(decode(Y, pool, Q), pool, Q, [0, 1, 2], d ** -0.5) == (keys == "all")
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+def test_scores_of_plus_infinity_are_nan(Y, dtype, d):
+    pool = P.Pool(Y, [95, 9003], 1, d, 64, dtype)
+    for b in range(2):
+        put(pool, b, [41], math.inf, channel=2)
+    Q = queries(4, 3, d, dtype, 28)
+    Q[:, :, 2] = 1.0
+    Q = Q.cuda()
+    assert bool(prefill(Y, pool, Q, [0, 2, 4]).isnan().all())
+    assert bool(decode(Y, pool, Q[:2].contiguous()).isnan().all())
