@@ -9,9 +9,10 @@
 // device.
 //
 // A warp takes one row (or, where there are few rows, a part of a row's heads, so that a
-// step of a few sequences still fills the GPU): it finds the row's sequence and page
-// once, holds the cosines and sines of its 16-byte chunk in registers, and copies head by
-// head with kUnroll loads in flight.  Bound by HBM: each value is read and written once.
+// step of a few sequences still fills the GPU): it finds the row's sequence, 32 bounds at a
+// time, and page once, holds the cosines and sines of its 16-byte chunk in registers, and
+// copies head by head with kUnroll loads in flight.  Bound by HBM: each value is read and
+// written once.
 #include <algorithm>
 #include <cmath>
 
@@ -50,79 +51,96 @@ paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const Ro
     const int64_t item = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int row = (int)(item / parts), part = (int)(item % parts);
     if (row >= a.rows) return;
-    // sequence b: as many cu[b + 1] <= row as come before it
-    int b = row, first = row, n = 1;
-    if (a.cu) {
-        b = 0;
-        for (int s = lane; s - lane < pv.B; s += 32)
-            b += __popc(__ballot_sync(0xffffffffu, s < pv.B && a.cu[min(s, pv.B - 1) + 1] <= row));
-        if (b >= pv.B) return;  // behind the last sequence
-        n = paged_rows(a.cu, a.rows, b, first, a.err);
-        if (row < first || row >= first + n) return;
-    }
-    const int pos = paged_len(pv, b, a.err) - n + (row - first);
-    if (pos < 0) return;
     const int ch = lane % CH;
-    float c[PC], s[PC];
-    if (a.turn) {
-#pragma unroll
-        for (int i = 0; i < PC; ++i) {
-            const uint64_t u = (uint64_t)pos * turns.f[ch * PC + i];
-            sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &s[i], &c[i]);
+    bool turn_q = a.q != nullptr;
+    // The sequences that have this row: cu[b] <= row < cu[b + 1] with bounds within [0, rows].  Bounds
+    // that do not decrease give it to one at most; where some fall back, two may have it, and the
+    // first one turns q.
+    int b = row, first = row, n = 1;
+    bool bad = false;
+    for (int from = 0, left = 1; left > 0; --left, from = b + 1) {
+        if (a.cu) {
+            int hits = 0, mine = pv.B;
+            const unsigned rows = (unsigned)a.rows;  // (as unsigned numbers, those below 0 are past every bound)
+#pragma unroll 8
+            for (int seq = from + lane; seq < pv.B; seq += 32) {
+                const unsigned c0 = (unsigned)a.cu[seq], c1 = (unsigned)a.cu[seq + 1];
+                const bool sound = c0 <= c1 && c1 <= rows, has = sound && (unsigned)row - c0 < c1 - c0;
+                bad |= !sound;
+                mine = min(mine, has ? seq : pv.B);
+                hits += has;
+            }
+            if (from == 0) left = __reduce_add_sync(0xffffffffu, hits);
+            if (bad && from == 0) paged_report(a.err, kErrPagedRows);
+            if (left == 0) return;  // between or behind the sequences
+            b = __reduce_min_sync(0xffffffffu, mine);
+            first = a.cu[b];
+            n = a.cu[b + 1] - first;
         }
-    }
-    // heads in the order k, v, q
-    const int nkv = a.k ? pv.Hkv : 0, heads = 2 * nkv + (a.q ? a.Hq : 0);
-    int64_t slot = -1;  // byte offset of the slot's kv head 0
-    const int64_t head_bytes = ((int64_t)D * sizeof(T)) << pv.shift;
-    if (nkv) {
-        const int page = paged_page(pv, b, pos >> pv.shift, a.err);
-        if (page >= 0)
-            slot = (int64_t)page * pv.Hkv * head_bytes + (int64_t)(pos & ((1 << pv.shift) - 1)) * D * sizeof(T);
-    }
-    for (int h0 = part * HS + lane / CH; h0 < heads; h0 += parts * HS * kUnroll) {
-        uint4 u[kUnroll];
+        const int pos = paged_len(pv, b, a.err) - n + (row - first);
+        if (pos < 0) continue;
+        float c[PC], s[PC];
+        if (a.turn) {
 #pragma unroll
-        for (int x = 0; x < kUnroll; ++x) {
-            const int h = h0 + x * parts * HS;
-            if (h >= heads) break;
-            const uint8_t *src = h < nkv       ? a.k + row * a.k_row + h * a.k_head
-                                 : h < 2 * nkv ? a.v + row * a.v_row + (h - nkv) * a.v_head
-                                               : a.q + row * a.q_row + (h - 2 * nkv) * a.q_head;
-            u[x] = *reinterpret_cast<const uint4 *>(src + ch * 16);
+            for (int i = 0; i < PC; ++i) {
+                const uint64_t u = (uint64_t)pos * turns.f[ch * PC + i];
+                sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &s[i], &c[i]);
+            }
         }
+        // heads in the order k, v, q
+        const int nkv = a.k ? pv.Hkv : 0, heads = 2 * nkv + (turn_q ? a.Hq : 0);
+        turn_q = false;
+        int64_t slot = -1;  // byte offset of the slot's kv head 0
+        const int64_t head_bytes = ((int64_t)D * sizeof(T)) << pv.shift;
+        if (nkv) {
+            const int page = paged_page(pv, b, pos >> pv.shift, a.err);
+            if (page >= 0)
+                slot = (int64_t)page * pv.Hkv * head_bytes + (int64_t)(pos & ((1 << pv.shift) - 1)) * D * sizeof(T);
+        }
+        for (int h0 = part * HS + lane / CH; h0 < heads; h0 += parts * HS * kUnroll) {
+            uint4 u[kUnroll];
 #pragma unroll
-        for (int x = 0; x < kUnroll; ++x) {
-            const int h = h0 + x * parts * HS;
-            if (h >= heads) break;
-            const bool is_v = h >= nkv && h < 2 * nkv;
-            if (a.turn && !is_v) {
-                uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+            for (int x = 0; x < kUnroll; ++x) {
+                const int h = h0 + x * parts * HS;
+                if (h >= heads) break;
+                const uint8_t *src = h < nkv       ? a.k + row * a.k_row + h * a.k_head
+                                     : h < 2 * nkv ? a.v + row * a.v_row + (h - nkv) * a.v_head
+                                                   : a.q + row * a.q_row + (h - 2 * nkv) * a.q_head;
+                u[x] = *reinterpret_cast<const uint4 *>(src + ch * 16);
+            }
 #pragma unroll
-                for (int i = 0; i < PC; ++i) {
-                    if constexpr (sizeof(T) == 2) {
-                        float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
-                        rope_turn(x0, x1, c[i], s[i]);
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
-                        w[i] = *reinterpret_cast<const uint32_t *>(&h2);
-                    } else {
-                        float x0 = __uint_as_float(w[2 * i]), x1 = __uint_as_float(w[2 * i + 1]);
-                        rope_turn(x0, x1, c[i], s[i]);
-                        w[2 * i] = __float_as_uint(x0);
-                        w[2 * i + 1] = __float_as_uint(x1);
+            for (int x = 0; x < kUnroll; ++x) {
+                const int h = h0 + x * parts * HS;
+                if (h >= heads) break;
+                const bool is_v = h >= nkv && h < 2 * nkv;
+                if (a.turn && !is_v) {
+                    uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+#pragma unroll
+                    for (int i = 0; i < PC; ++i) {
+                        if constexpr (sizeof(T) == 2) {
+                            float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
+                            rope_turn(x0, x1, c[i], s[i]);
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(x0, x1);
+                            w[i] = *reinterpret_cast<const uint32_t *>(&h2);
+                        } else {
+                            float x0 = __uint_as_float(w[2 * i]), x1 = __uint_as_float(w[2 * i + 1]);
+                            rope_turn(x0, x1, c[i], s[i]);
+                            w[2 * i] = __float_as_uint(x0);
+                            w[2 * i + 1] = __float_as_uint(x1);
+                        }
                     }
+                    u[x] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                u[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                uint8_t *dst;
+                if (h < 2 * nkv) {
+                    if (slot < 0) continue;
+                    if (!YOCO_DCHECK(b < pv.B && slot / head_bytes < (int64_t)pv.num_pages * pv.Hkv, 0x63)) continue;
+                    dst = (is_v ? a.vc : a.kc) + slot + (is_v ? h - nkv : h) * head_bytes;
+                } else {
+                    dst = a.q_out + ((int64_t)row * a.Hq + (h - 2 * nkv)) * (int64_t)(D * sizeof(T));
+                }
+                *reinterpret_cast<uint4 *>(dst + ch * 16) = u[x];
             }
-            uint8_t *dst;
-            if (h < 2 * nkv) {
-                if (slot < 0) continue;
-                if (!YOCO_DCHECK(b < pv.B && slot / head_bytes < (int64_t)pv.num_pages * pv.Hkv, 0x63)) continue;
-                dst = (is_v ? a.vc : a.kc) + slot + (is_v ? h - nkv : h) * head_bytes;
-            } else {
-                dst = a.q_out + ((int64_t)row * a.Hq + (h - 2 * nkv)) * (int64_t)(D * sizeof(T));
-            }
-            *reinterpret_cast<uint4 *>(dst + ch * 16) = u[x];
         }
     }
 }

@@ -400,7 +400,9 @@ YOCO_API size_t yoco_swa_workspace_size(int B, int Hq, const yoco_swa_ring *ring
  * above max_pages * page_size counts as 0, a page outside the pool as a page of
  * zeros that nothing is written to, a sequence whose cu_rows decrease or leave
  * [0, rows] as one without rows; each is recorded in the workspace and
- * yoco_workspace_status then returns YOCO_ERR_INVALID_ARG.
+ * yoco_workspace_status then returns YOCO_ERR_INVALID_ARG.  (Where bounds fall
+ * back, the sequences left may have a row in common: its k and v go to both, q
+ * is turned for the first that holds its position, and O has either's.)
  * B <= 4096, and B * Hkv * max_pages * page_size / 128 <= 2^30.  A call of
  * no rows does nothing; its tensors may be NULL.
  */

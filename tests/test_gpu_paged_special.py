@@ -214,3 +214,45 @@ def test_scores_of_plus_infinity_are_nan(Y, dtype, d):
     Q = Q.cuda()
     assert bool(prefill(Y, pool, Q, [0, 2, 4]).isnan().all())
     assert bool(decode(Y, pool, Q[:2].contiguous()).isnan().all())
+
+
+# ------------------------------------------------------- row bounds that fall back
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("more", [0, 37])
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 5, -1, 8], [0, 5, 3, 12], [0, 4, 100, 12], [2, 7, 7, 5], [-1, 3, 9, 12],
+                                [0, 2 ** 31 - 1, 4, 9], [4, 2, 0, 3]])
+def test_append_leaves_out_only_sequences_of_bad_bounds(Y, dtype, d, more, cu):
+    """A sequence whose bounds decrease or leave [0, rows] has no rows; every other one is written,
+    with a row that two of them claim in both caches and its q turned for the first."""
+    rows, Hkv, Hq, page = 12, 2, 4, 16
+    cu = cu + [cu[-1]] * more  # sequences without rows behind them: more than a warp looks up at once
+    B = len(cu) - 1
+    pool = P.Pool(Y, [60 + 3 * b for b in range(B)], Hkv, d, page, dtype, rope=1e4)
+    g = torch.Generator().manual_seed(31)
+    k, v, q = (torch.randn(rows, h, d, generator=g).to(DT[dtype]) for h in (Hkv, Hkv, Hq))
+    k0, v0 = pool.dev.k.cpu(), pool.dev.v.cpu()
+    out = torch.full((rows, Hq, d), 9.0, dtype=DT[dtype], device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    Y.yoco_paged_append(k.cuda(), v.cuda(), pool.dev, torch.tensor(cu, dtype=torch.int32, device="cuda"), q=q.cuda(),
+                        q_out=out, workspace=ws)
+    assert P.status(Y, ws) == Y.YOCO_ERR_INVALID_ARG
+    k1, v1, out = pool.dev.k.cpu(), pool.dev.v.cpu(), out.cpu()
+    owner = [-1] * rows
+    for b in range(B):
+        c0, c1 = cu[b], cu[b + 1]
+        if not 0 <= c0 <= c1 <= rows:
+            continue
+        for i in range(c0, c1):
+            pos = pool.lens[b] - (c1 - c0) + i - c0
+            pg, r = int(pool.table[b, pos // page]), pos % page
+            P.close_turn(k1[pg, :, r][None], k[i:i + 1], torch.tensor([pos]), 1e4, dtype)
+            assert torch.equal(v1[pg, :, r], v[i])
+            k0[pg, :, r], v0[pg, :, r] = k1[pg, :, r], v1[pg, :, r]
+            if owner[i] < 0:
+                owner[i] = b
+                P.close_turn(out[i:i + 1], q[i:i + 1], torch.tensor([pos]), 1e4, dtype)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(k0.view(bits), k1.view(bits)) and torch.equal(v0.view(bits), v1.view(bits))
+    for i in range(rows):
+        assert owner[i] >= 0 or bool((out[i] == 9.0).all())
