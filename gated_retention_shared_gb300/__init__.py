@@ -153,6 +153,18 @@ def _workspace(nbytes: int, device, workspace):
     return workspace
 
 
+def _scratch(nbytes: int, device, stream):
+    """A workspace of the binding's own from the pool of the stream that will use it.  What the
+    current stream's pool hands out may be memory that is free to that stream's later work only:
+    work queued there before may still write it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # another library's
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 # ------------------------------------------------------------------ gRet
 
 def yoco_gret_prefill_workspace_size(B, N, H, dk, dv, chunk, dtype) -> int:
@@ -444,11 +456,9 @@ def _paged_call(fn, name, cache, stream, *args):
 
 
 def _paged_workspace(nbytes, cache, workspace, stream):
-    """The caller's workspace, or a new one that is kept until `stream` is done with it, its pointer and bytes."""
+    """The caller's workspace, or a new one, its pointer and bytes."""
     if workspace is None:
-        workspace = torch.empty(nbytes() if callable(nbytes) else nbytes, dtype=torch.uint8, device=cache.k.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _scratch(nbytes() if callable(nbytes) else nbytes, cache.k.device, stream)
     elif workspace.get_device() != cache._dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     return workspace, workspace.data_ptr(), workspace.nbytes

@@ -256,3 +256,26 @@ def test_append_leaves_out_only_sequences_of_bad_bounds(Y, dtype, d, more, cu):
     assert torch.equal(k0.view(bits), k1.view(bits)) and torch.equal(v0.view(bits), v1.view(bits))
     for i in range(rows):
         assert owner[i] >= 0 or bool((out[i] == 9.0).all())
+
+
+# ------------------------------------------------------------------- streams
+
+def test_own_workspace_on_another_stream_waits_for_nothing_of_the_current_one(Y):
+    """Memory freed on the current stream, with the work that fills it still queued there, is not
+    what a call on another stream gets for its workspace."""
+    pool = P.Pool(Y, [6000, 40], 2, 128, 64, "bf16")
+    Q, cu = queries(12, 8, 128, "bf16", 33).cuda(), torch.tensor([0, 7, 12], dtype=torch.int32, device="cuda")
+    want, want_d, side = torch.empty_like(Q), torch.empty_like(Q[:2]), torch.cuda.Stream()
+    Y.yoco_paged_attn_prefill(Q, pool.dev, cu, want)
+    Y.yoco_paged_attn_decode(Q[:2], pool.dev, want_d)
+    n = Y.yoco_paged_attn_workspace_size(8, 12, pool.dev)
+    outs = [(torch.empty_like(Q), torch.empty_like(Q[:2])) for _ in range(4)]
+    torch.cuda.synchronize()
+    for o, od in outs:
+        torch.cuda._sleep(4_000_000)  # a few milliseconds
+        for _ in range(2):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+        Y.yoco_paged_attn_prefill(Q, pool.dev, cu, o, stream=side)
+        Y.yoco_paged_attn_decode(Q[:2], pool.dev, od, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) and torch.equal(od, want_d) for o, od in outs)
