@@ -145,11 +145,11 @@ def _need(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
-def _workspace(nbytes: int, device, workspace):
+def _workspace(nbytes: int, device, workspace, stream):
     if nbytes == 0:
         return workspace
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = _scratch(nbytes, device, stream)
     return workspace
 
 
@@ -179,7 +179,7 @@ def yoco_gret_prefill_chunkwise(q, k, v, gate_logits, tau, o, state, chunk=0, wo
     dv = v.shape[-1]
     dt = _dt(q)
     ws_n = lib.yoco_gret_prefill_workspace_size(B, N, H, dk, dv, chunk, dt)
-    ws = _workspace(ws_n, q.device, workspace)
+    ws = _workspace(ws_n, q.device, workspace, stream)
     st = lib.yoco_gret_prefill_chunkwise(_ptr(q), _ptr(k), _ptr(v), _ptr(gate_logits), float(tau), _ptr(o),
                                          _ptr(state), B, N, H, dk, dv, chunk, dt, _dt(o), _ptr(ws),
                                          0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
@@ -200,7 +200,7 @@ def yoco_gret_prefill_chunkwise_gn_gate(q, k, v, gate_logits, tau, gate, z, stat
         if t is not None and (t.dtype != torch.float32 or t.numel() != H * dv):
             raise ValueError(f"{n} must be fp32 with H * d elements")
     ws_n = lib.yoco_gret_prefill_workspace_size(B, N, H, dk, dv, 0, dt)
-    ws = _workspace(ws_n, q.device, workspace)
+    ws = _workspace(ws_n, q.device, workspace, stream)
     st = lib.yoco_gret_prefill_chunkwise_gn_gate(_ptr(q), _ptr(k), _ptr(v), _ptr(gate_logits), float(tau), _ptr(gate),
                                                  _ptr(gn_weight), _ptr(gn_bias), float(eps), _ptr(z), _ptr(state), B, N,
                                                  H, dk, dv, dt, _ptr(ws),
@@ -277,7 +277,7 @@ def yoco_shared_kv_project_append(M, Wk, Wv, cache: KVCache, eps=1e-6, rms_w=Non
         _need(t, n)
     B, T, dm = M.shape
     ws_n = lib.yoco_shared_kv_workspace_size(B, T, dm, ctypes.byref(cache.c))
-    ws = _workspace(ws_n, M.device, workspace)
+    ws = _workspace(ws_n, M.device, workspace, stream)
     st = lib.yoco_shared_kv_project_append(_ptr(M), _ptr(rms_w), float(eps), _ptr(Wk), _ptr(Wv), T, dm,
                                            ctypes.byref(cache.c), _ptr(ws),
                                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
@@ -310,7 +310,7 @@ def yoco_cross_attn_prefill(Q, cache: KVCache, p0, O, scale=None, workspace=None
     B, T, Hq, d = Q.shape
     scale = d ** -0.5 if scale is None else scale
     ws_n = lib.yoco_cross_attn_workspace_size(B, Hq, T, ctypes.byref(cache.c), 0)
-    ws = _workspace(ws_n, Q.device, workspace)
+    ws = _workspace(ws_n, Q.device, workspace, stream)
     st = lib.yoco_cross_attn_prefill(_ptr(Q), Hq, T, int(p0), ctypes.byref(cache.c), float(scale), _ptr(O), _ptr(ws),
                                      0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "yoco_cross_attn_prefill")
@@ -323,7 +323,7 @@ def yoco_cross_attn_decode(Q, cache: KVCache, O, scale=None, num_splits=0, works
     B, Hq, d = Q.shape
     scale = d ** -0.5 if scale is None else scale
     ws_n = lib.yoco_cross_attn_workspace_size(B, Hq, 1, ctypes.byref(cache.c), num_splits)
-    ws = _workspace(ws_n, Q.device, workspace)
+    ws = _workspace(ws_n, Q.device, workspace, stream)
     st = lib.yoco_cross_attn_decode(_ptr(Q), Hq, ctypes.byref(cache.c), float(scale), num_splits, _ptr(O), _ptr(ws),
                                     0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "yoco_cross_attn_decode")
@@ -352,7 +352,7 @@ def yoco_swa_prefill(q, k, v, ring: SwaRing, o, scale=None, workspace=None, stre
         _need(t, n)
     B, N, Hq, d = q.shape
     scale = d ** -0.5 if scale is None else scale
-    ws = _workspace(max(256, lib.yoco_swa_workspace_size(B, Hq, ctypes.byref(ring.c))), q.device, workspace)
+    ws = _workspace(max(256, lib.yoco_swa_workspace_size(B, Hq, ctypes.byref(ring.c))), q.device, workspace, stream)
     st = lib.yoco_swa_prefill(_ptr(q), _ptr(k), _ptr(v), Hq, N, float(scale), _ptr(o), ctypes.byref(ring.c),
                               _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "yoco_swa_prefill")
@@ -364,7 +364,7 @@ def yoco_swa_decode(q, k, v, ring: SwaRing, o, scale=None, workspace=None, strea
         _need(t, n)
     B, Hq, d = q.shape
     scale = d ** -0.5 if scale is None else scale
-    ws = _workspace(max(256, lib.yoco_swa_workspace_size(B, Hq, ctypes.byref(ring.c))), q.device, workspace)
+    ws = _workspace(max(256, lib.yoco_swa_workspace_size(B, Hq, ctypes.byref(ring.c))), q.device, workspace, stream)
     st = lib.yoco_swa_decode(_ptr(q), _ptr(k), _ptr(v), Hq, float(scale), _ptr(o), ctypes.byref(ring.c), _ptr(ws),
                              ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "yoco_swa_decode")
@@ -406,7 +406,7 @@ def yoco_gret_qkvg_project(X, W, H, q, k, v, gate_logits, rope_base=0.0, pos0=0,
     B, N, dm = X.shape
     d = q.shape[-1]
     ws_n = lib.yoco_gret_qkvg_workspace_size(B, N, H, d, float(rope_base))
-    ws = _workspace(ws_n, X.device, workspace)
+    ws = _workspace(ws_n, X.device, workspace, stream)
     st = lib.yoco_gret_qkvg_project(_ptr(X), _ptr(W), B, N, dm, H, d, int(pos0), float(rope_base), _ptr(q), _ptr(k),
                                     _ptr(v), _ptr(gate_logits), _ptr(ws), ws.numel() * ws.element_size(),
                                     _stream(stream))

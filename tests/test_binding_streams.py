@@ -56,3 +56,19 @@ CACHE = SimpleNamespace(k=SimpleNamespace(device="cuda:0"), _dev=0)
 def test_paged_workspace_belongs_to_the_stream_that_uses_it(Y, current, stream, pool, nbytes):
     ws, ptr, n = Y._paged_workspace(nbytes, CACHE, None, stream)
     assert (ws.pool, n) == (pool, 512) and current == [1]
+
+
+@pytest.mark.parametrize("stream,pool", [(None, 1), (Stream(7), 7), (SimpleNamespace(cuda_stream=9), 9)])
+def test_workspace_belongs_to_the_stream_that_uses_it(Y, current, stream, pool):
+    assert Y._workspace(512, "cuda:0", None, stream).pool == pool and current == [1]
+    assert Y._workspace(0, "cuda:0", None, stream) is None  # a call that needs none
+    assert Y._workspace(512, "cuda:0", "mine", stream) == "mine"
+
+
+def test_every_call_says_which_stream_its_workspace_is_for(Y):
+    """Each call's workspace is made for the stream that the call is given."""
+    import inspect
+    import re
+    source = inspect.getsource(Y)
+    made = re.findall(r"ws(?:, wp, wn)? = _(?:paged_)?workspace\(.*", source)
+    assert made and all(m.endswith("workspace, stream)") for m in made)
