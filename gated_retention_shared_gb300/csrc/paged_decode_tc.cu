@@ -298,7 +298,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         bool done_whole = false, alive = true;
         // acc = acc corr + O^T(i); corr belongs to tile i
         auto accumulate = [&](int i) {
-            alive &= mbar_wait(&sm.o_full[i & 1], (i / 2) & 1, abort_flag);
+            alive &= mbar_wait_warp(&sm.o_full[i & 1], (i / 2) & 1, abort_flag);
             __syncwarp();
             tc_fence_after();
             uint32_t o[16];
@@ -351,7 +351,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 l[n] = 0.f;
             }
             for (int t = w.t0; t < w.t1; ++t, ++i) {
-                alive &= mbar_wait(&sm.s_full[i & 1], (i / 2) & 1, abort_flag);
+                alive &= mbar_wait_warp(&sm.s_full[i & 1], (i / 2) & 1, abort_flag);
                 __syncwarp();
                 tc_fence_after();
                 uint32_t sv[16];
@@ -373,7 +373,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 // V rows out of sight: zero, once the tile has come (V(i - 3), the phase before, was used by
                 // a product that this warp has seen the end of)
                 if (range.edge(t, pv.sinks)) {
-                    alive &= mbar_wait(&sm.full_v[i % kPStages], (i / kPStages) & 1, abort_flag);
+                    alive &= mbar_wait_warp(&sm.full_v[i % kPStages], (i / kPStages) & 1, abort_flag);
                     if (alive && !seen) {
                         uint8_t *vr = tiles + (size_t)(i % kPStages) * 2 * kPTile + kPTile + r * 128;
 #pragma unroll

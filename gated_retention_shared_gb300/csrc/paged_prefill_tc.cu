@@ -485,10 +485,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         }
         float m_ref = -INFINITY, l = 0.f;  // base-2 units
         // One exit from the tile loop: a wait that gave up makes what follows garbage (the status word
-        // says so), but every barrier is still served.
+        // says so), but every barrier is still served.  A warp gives up as one: tcgen05.ld and the
+        // votes take whole warps.
         bool alive = true;
         for (int i = 0; i < ntiles && alive; ++i) {
-            alive = mbar_wait(&bar.s_full[x], i & 1, abort_flag);
+            alive = mbar_wait_warp(&bar.s_full[x], i & 1, abort_flag);
             tc_fence_after();
             const uint32_t s_t = tmem + colS + lane_base;
             uint32_t sv[128];
@@ -559,7 +560,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             l = fmaf(l, alpha, ls0 + ls1);
             // O_X holds tiles < i; rows whose reference moved rescale it before P V(i)
             if (__builtin_expect(i > 0 && __any_sync(0xffffffffu, move), 0)) {
-                alive &= mbar_wait(&bar.pv_done[p_slot(two, x, i - 1)][1], p_use(two, i - 1) & 1, abort_flag);
+                alive &= mbar_wait_warp(&bar.pv_done[p_slot(two, x, i - 1)][1], p_use(two, i - 1) & 1, abort_flag);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t o_t = tmem + colO + lane_base;
@@ -576,7 +577,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             }
             // V rows that no row of the block sees: zero, once the tile has come
             if (__builtin_expect(i < e_lo || i >= e_hi || !two, 0)) {
-                alive &= mbar_wait(&bar.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
+                alive &= mbar_wait_warp(&bar.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
                 if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
 #pragma unroll 1
@@ -596,7 +597,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             asm volatile("" : "+r"(swz));  // (eight addresses kept over the loop would spill)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-                alive &= mbar_wait(done + hh, par, abort_flag);
+                alive &= mbar_wait_warp(done + hh, par, abort_flag);
 #pragma unroll
                 for (int c8 = 0; c8 < 8; ++c8) {
                     const int ch = hh * 8 + c8;

@@ -1,7 +1,8 @@
 // selftest.cu -- checks the library's failure path on the device without faulting
 // it: one thread waits on an mbarrier that nothing ever completes, with the same
 // bounded wait the tensor-core kernels use, gives up after `limit_ns` and records
-// the status word in the workspace exactly as a stalled kernel would.
+// the status word in the workspace exactly as a stalled kernel would.  The word after
+// it holds the lanes that go on from a warp's wait of which half the lanes gave up: 0.
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -9,14 +10,24 @@
 namespace yoco {
 
 __global__ void selftest_wait_kernel(int *err, uint64_t limit_ns) {
-    __shared__ uint64_t bar;
+    __shared__ uint64_t bar, done;
     __shared__ int abort_flag;
-    if (threadIdx.x != 0) return;
-    abort_flag = 0;
-    tc::mbar_init(&bar, 1);
-    tc::fence_mbar_init();
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        abort_flag = 0;
+        tc::mbar_init(&bar, 1);
+        tc::mbar_init(&done, 1);
+        tc::fence_mbar_init();
+        tc::mbar_arrive(&done);
+    }
+    __syncwarp();
     // nothing arrives on `bar`: phase 0 never completes
-    if (!tc::mbar_wait(&bar, 0, &abort_flag, limit_ns)) atomicExch(err, (int)(kErrMagic | 0xEEu));
+    if (lane == 0 && !tc::mbar_wait(&bar, 0, &abort_flag, limit_ns)) atomicExch(err, (int)(kErrMagic | 0xEEu));
+    __syncwarp();
+    // half the lanes wait for a phase that is complete: they give up with the others all the same
+    const bool on = tc::mbar_wait_warp(lane < 16 ? &done : &bar, 0, &abort_flag, limit_ns);
+    const unsigned went_on = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) atomicExch(err + 1, (int)went_on);
 }
 
 // Occupies SMs for a while, to run the library's calls on a device shared with

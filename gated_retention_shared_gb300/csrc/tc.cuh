@@ -83,6 +83,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// The same for a whole warp: true where every lane has seen the phase, so that lanes of which some
+// gave up (the time limit, the abort flag) go on or leave together: what follows may be a
+// warp-wide instruction.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                               uint64_t limit_ns = 2000000000ull) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns));
+}
+
 // ------------------------------------------------------------------- fences
 
 __device__ __forceinline__ void fence_proxy_async_smem() {

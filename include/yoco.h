@@ -505,7 +505,9 @@ YOCO_API yoco_status yoco_workspace_status(void *workspace, int clear, void *str
  * tensor-core kernels; after limit_ns (<= 10 s) it gives up and records the
  * timeout in `workspace` (>= 256 bytes, 256-byte aligned).  A following
  * yoco_workspace_status returns YOCO_ERR_TIMEOUT and the CUDA context stays
- * usable.  Not part of the method; it exists so tests can exercise the
+ * usable.  Then a warp waits, half of its lanes on a barrier that is complete:
+ * the second 32-bit word of the workspace has the lanes that went on (0, since
+ * a warp goes on or gives up as one).  Not part of the method; it exists so tests can exercise the
  * timeout path without faulting or hanging a GPU.
  */
 YOCO_API yoco_status yoco_selftest_wait_timeout(void *workspace, uint64_t limit_ns, void *stream);

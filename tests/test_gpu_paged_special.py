@@ -279,3 +279,14 @@ def test_own_workspace_on_another_stream_waits_for_nothing_of_the_current_one(Y)
         Y.yoco_paged_attn_decode(Q[:2], pool.dev, od, stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) and torch.equal(od, want_d) for o, od in outs)
+
+
+def test_a_warp_gives_up_a_wait_as_one(Y):
+    """Half a warp waits for what is complete, half for what never is (50 ms): none goes on."""
+    ws = torch.full((64,), -1, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert Y.lib.yoco_selftest_wait_timeout(ws.data_ptr(), 50_000_000, stream) == Y.YOCO_OK
+    with pytest.raises(Y.YocoError) as e:
+        Y.yoco_workspace_status(ws)
+    assert e.value.status == Y.YOCO_ERR_TIMEOUT
+    assert ws[1].item() == 0
