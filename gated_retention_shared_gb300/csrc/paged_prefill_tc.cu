@@ -91,6 +91,7 @@ struct PagedPreTask {
 
 struct PagedPreSmem {
     PagedPreTask task[2];
+    uint64_t drain[2];
     int walive[2][4];
     uint32_t tmem_base;
     int abort_flag;
@@ -193,6 +194,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (tid == 0) {
         c_bars_init(sm.task[0].bar);
         c_bars_init(sm.task[1].bar);
+        for (int k = 0; k < 2; ++k) mbar_init(&sm.drain[k], 1);
+        fence_mbar_init();
         sm.abort_flag = 0;
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
@@ -294,6 +297,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     auto p_slot = [](bool two, int x, int i) { return two ? x : (i & 1); };
     auto p_use = [](bool two, int i) { return two ? i : (i >> 1); };
 
+    // where a wait gave up, products may still be running: none may be when tensor memory is given back
+    auto drain = [&](int k) {
+        if (lane == 0) {
+            volatile int no_abort = 0;
+            mma_commit(&sm.drain[k]);
+            mbar_wait(&sm.drain[k], 0, &no_abort, 200000000ull);
+        }
+        __syncwarp();
+    };
+
     if (warp == 0) {
         // -------------------------------------------------------------- TMA
         c_regs_dec();
@@ -390,7 +403,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 }
                 if (!ok) fail(52);
             }
-            if (!c_end(abort_flag) || !sm.task[(n + 1) & 1].more) break;
+            if (!c_end(abort_flag)) {
+                drain(0);
+                break;
+            }
+            if (!sm.task[(n + 1) & 1].more) break;
         }
     } else if (warp == 2) {
         // ------------------------------------------------------ MMA: O += P V
@@ -426,7 +443,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 }
                 if (!ok) fail(58);
             }
-            if (!c_end(abort_flag) || !sm.task[(n + 1) & 1].more) break;
+            if (!c_end(abort_flag)) {
+                drain(1);
+                break;
+            }
+            if (!sm.task[(n + 1) & 1].more) break;
         }
     } else if (warp == 3) {
         // -------------------------------------------- the next entry and its barriers
