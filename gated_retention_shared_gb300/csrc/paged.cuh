@@ -24,11 +24,21 @@ struct PagedView {
 
 constexpr int kPagedTile = 128;  // keys per tile
 
-// What one kernel of a call leaves for the next: that one may be running already when it is
-// written, which a load through the read-only path does not allow for.
+// These kernels are started while the one before them in the stream may still run, and wait for
+// its end (griddepcontrol.wait).  What that one may write -- a call's plan, notes and partial
+// results, and as well a caller's Q, K and V: the O of one call can be the Q of the next -- is not
+// read-only while they run, so it is not loaded through the read-only path, whose loads the
+// compiler may also move ahead of the wait.
 __device__ __forceinline__ int paged_ld(const int *p) {
     int v;
     asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// 16 bytes of a tensor (no clobber: nothing here writes what it reads, and it keeps its place
+// behind the wait, which is volatile too)
+__device__ __forceinline__ uint4 paged_ld16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 

@@ -264,7 +264,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int e = t + 64 * x;  // 16-byte chunk e % 16 of head e / 16
-                if (e < G * 16) v[x] = *reinterpret_cast<const uint4 *>(src + (size_t)e * 8);
+                if (e < G * 16) v[x] = paged_ld16(src + (size_t)e * 8);
             }
             if (unit >= 2 && !mbar_wait(&sm.q_empty[unit & 1], ((unit >> 1) - 1) & 1, abort_flag)) {
                 fail(43);

@@ -20,7 +20,7 @@ constexpr float kPagedLog2e = 1.4426950408889634f;
 
 // 4 or 8 consecutive elements (16 bytes) as floats
 template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16 / sizeof(T)]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 u = paged_ld16(p);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -82,8 +82,14 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
             const int nq = min(NQ, G - g0);
             const size_t qrow = (size_t)w.b * Hq + w.hk * G + g0;
             __syncthreads();
-            for (int e = tid; e < NQ * D; e += kDecThreads)
-                qs[e / D][e % D] = e < nq * D ? c2 * to_f32(Q[qrow * D + e]) : 0.f;
+            for (int e = tid * EV; e < NQ * D; e += kDecThreads * EV) {
+                float x[EV];
+#pragma unroll
+                for (int i = 0; i < EV; ++i) x[i] = 0.f;
+                if (e < nq * D) load16(Q + qrow * D + e, x);
+#pragma unroll
+                for (int i = 0; i < EV; ++i) qs[e / D][e % D + i] = c2 * x[i];
+            }
             __syncthreads();
             float m[NQ], l[NQ], acc[NQ][EL];
 #pragma unroll
@@ -273,7 +279,7 @@ template <typename T, int D, int PITCH> struct PreStage {
             const int64_t o = at[row];
             if constexpr (sizeof(T) == 2) {
                 r[n] = make_uint4(0, 0, 0, 0);
-                if (o >= 0) r[n] = __ldg(reinterpret_cast<const uint4 *>(src + o * D + ch * EV));
+                if (o >= 0) r[n] = paged_ld16(src + o * D + ch * EV);
             } else {
                 // 0 bytes are read and 16 zeros written where the slot is not to be read
                 const unsigned s = (unsigned)__cvta_generic_to_shared(dst + row * PITCH + ch * EV);

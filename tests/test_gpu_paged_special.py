@@ -7,6 +7,7 @@ all of them are -inf, the rest of the keys' answer where some are -inf, and zero
 negative position, which sees nothing.  Finite answers are held to the bounds of
 test_gpu_paged.py (its S taken over the slots of finite score: the others' weights are 0 on both
 sides)."""
+import itertools
 import math
 
 import pytest
@@ -290,3 +291,36 @@ def test_a_warp_gives_up_a_wait_as_one(Y):
         Y.yoco_workspace_status(ws)
     assert e.value.status == Y.YOCO_ERR_TIMEOUT
     assert ws[1].item() == 0
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("few", [True, False])
+def test_outputs_of_one_call_as_the_queries_of_the_next(Y, dtype, d, few):
+    """Calls one behind the other, each starting while the one before it ends: what they give is what
+    they give with the GPU waited for in between."""
+    new = [1, 1, 1] if few else [60, 3, 130]
+    lens = [700 + new[0], 3000 + new[1], 20 + new[2]]
+    pool = P.Pool(Y, lens, 2, d, 64, dtype)
+    cu = torch.tensor([0] + list(itertools.accumulate(new)), dtype=torch.int32, device="cuda")
+    Q = queries(sum(new), 6, d, dtype, 34).cuda()
+    ws = torch.empty(Y.yoco_paged_attn_workspace_size(6, sum(new), pool.dev), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        outs = [Q]
+        for i in range(12):
+            O = torch.full_like(Q, math.nan)
+            outs.append(O)
+        torch.cuda.synchronize()
+        for q, o in itertools.pairwise(outs):
+            if few:
+                Y.yoco_paged_attn_decode(q, pool.dev, o, scale=8.0, workspace=ws)
+            else:
+                Y.yoco_paged_attn_prefill(q, pool.dev, cu, o, scale=8.0, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        return torch.stack(outs[1:]).cpu()
+
+    want = chain(True)
+    assert bool(torch.isfinite(want).all())
+    for _ in range(3):
+        assert torch.equal(chain(False), want)
