@@ -31,7 +31,7 @@ __constant__ const float kPlanShare[kPlanTries] = {0.f,  3.f,  2.f,   1.5f, 1.2f
 constexpr int kPlanNoCut = 1 << 30;
 
 struct PlanSeq {
-    int first, n, pos, blocks, tiles;  // tiles: of the last row block
+    int first, n, pos, blocks, tiles;  // tiles: of the row block that sees most, give or take one
 };
 
 __device__ __forceinline__ PlanSeq plan_seq(const PagedView &pv, const int32_t *cu, int rows, int T_R, int b, int *err) {
@@ -41,7 +41,10 @@ __device__ __forceinline__ PlanSeq plan_seq(const PagedView &pv, const int32_t *
     if (s.n == 0) return s;
     s.blocks = (s.n + T_R - 1) / T_R;
     s.pos = len - s.n;
-    s.tiles = paged_range(pv, s.pos + (s.blocks - 1) * T_R, s.pos + s.n - 1).ntiles;
+    const int last = s.pos + (s.blocks - 1) * T_R;
+    s.tiles = paged_range(pv, last, s.pos + s.n - 1).ntiles;
+    // with a window a last row block of few rows sees less than the one before it
+    if (pv.window > 0 && s.blocks > 1) s.tiles = max(s.tiles, paged_range(pv, last - T_R, last - 1).ntiles);
     return s;
 }
 
@@ -122,7 +125,7 @@ __device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &p
     o.nrow = min(a.T_R, s.n - j * a.T_R);
     o.pos0 = s.pos + j * a.T_R;
     o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
-    // a block may see a tile more or less than the last one: the last piece takes what is left
+    // one may see a tile more than `tiles`, or many fewer: the last piece takes what is left
     o.pieces = min(pc, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
     o.i0 = min(piece * per, o.range.ntiles);
     o.i1 = piece == pc - 1 ? o.range.ntiles : min(o.i0 + per, o.range.ntiles);

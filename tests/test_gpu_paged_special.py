@@ -324,3 +324,36 @@ def test_outputs_of_one_call_as_the_queries_of_the_next(Y, dtype, d, few):
     assert bool(torch.isfinite(want).all())
     for _ in range(3):
         assert torch.equal(chain(False), want)
+
+
+# ---------------------------------------------------------------- the work list
+
+def work_list(ws):
+    """(sequence, rows, tiles) of every entry that a prefill's plan left in the workspace: a count
+    at byte 128, entries of 16 words (sequence, first row, rows, position, first and last tile)."""
+    words = ws.cpu().view(torch.int32)
+    n = int(words[32])
+    e = words[64:64 + 16 * n].reshape(n, 16).tolist()
+    return [(x[0], x[2], x[5] - x[4]) for x in e]
+
+
+@pytest.mark.parametrize("B", [3, 40])
+def test_window_plan_takes_the_longest_row_blocks_first(Y, B):
+    """One query head to a kv head, so blocks of 256 rows, and a window of 20: prompts of 1025 rows have
+    full blocks that see 275 slots and up to 15 of their first page, three tiles, and a last block
+    that sees one; the others have a block of two tiles."""
+    n = [1025 if b % 3 == 1 else 150 + b for b in range(B)]
+    pool = P.Pool(Y, [2000 + t for t in n], 1, 128, 16, "bf16")
+    cu = [0] + list(itertools.accumulate(n))
+    Q = queries(cu[-1], 1, 128, "bf16", 35).cuda()
+    O = torch.empty_like(Q)
+    ws = torch.zeros(Y.yoco_paged_attn_workspace_size(1, cu[-1], pool.dev), dtype=torch.uint8, device="cuda")
+    Y.yoco_paged_attn_prefill(Q, pool.dev, torch.tensor(cu, dtype=torch.int32, device="cuda"), O, window=20, workspace=ws)
+    Y.yoco_workspace_status(ws)
+    P.check(O, pool, Q, cu, 128 ** -0.5, 20, 0)
+    longest = {}  # of each sequence, in the order of the list
+    for b, rows, tiles in work_list(ws):
+        if rows:
+            longest[b] = max(longest.get(b, 0), tiles)
+    order = list(longest.values())
+    assert len(order) == B and order == sorted(order, reverse=True) and set(order) == {2, 3}
