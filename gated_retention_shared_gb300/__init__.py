@@ -521,12 +521,18 @@ def _paged_q(Q, O, cache):
     return shape[0], shape[1]
 
 
+def _reach(slots):
+    """A window or a number of sinks as the library's int: no sequence holds more than 2^30 slots, and
+    ctypes would cut a larger number to its low 32 bits."""
+    return max(-1, min(slots, 1 << 30))
+
+
 def yoco_paged_attn_prefill(Q, cache: PagedKV, cu_rows, O, scale=None, window=0, sinks=0, workspace=None, stream=None):
     """Q, O [rows, Hq, d]; rows cu_rows[b] .. cu_rows[b + 1] - 1 are sequence b's newest."""
     rows, Hq = _paged_q(Q, O, cache)
     ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
     _paged_call(lib.yoco_paged_attn_prefill, "yoco_paged_attn_prefill", cache, stream, Q.data_ptr(), Hq,
-                _paged_cu(cu_rows, cache), rows, cache.ref, cache._d ** -0.5 if scale is None else scale, window, sinks,
+                _paged_cu(cu_rows, cache), rows, cache.ref, cache._d ** -0.5 if scale is None else scale, _reach(window), _reach(sinks),
                 O.data_ptr(), wp, wn)
 
 
@@ -537,4 +543,4 @@ def yoco_paged_attn_decode(Q, cache: PagedKV, O, scale=None, window=0, sinks=0, 
         raise ValueError(f"Q has {rows} rows, the cache {cache._B} sequences")
     ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
     _paged_call(lib.yoco_paged_attn_decode, "yoco_paged_attn_decode", cache, stream, Q.data_ptr(), Hq, cache.ref,
-                cache._d ** -0.5 if scale is None else scale, window, sinks, O.data_ptr(), wp, wn)
+                cache._d ** -0.5 if scale is None else scale, _reach(window), _reach(sinks), O.data_ptr(), wp, wn)

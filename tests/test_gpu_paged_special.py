@@ -357,3 +357,21 @@ def test_window_plan_takes_the_longest_row_blocks_first(Y, B):
             longest[b] = max(longest.get(b, 0), tiles)
     order = list(longest.values())
     assert len(order) == B and order == sorted(order, reverse=True) and set(order) == {2, 3}
+
+
+def test_windows_and_sinks_past_32_bits(Y):
+    """A window that no sequence reaches the end of, as a number that does not fit an int; likewise
+    sinks, and numbers below any int."""
+    pool = P.Pool(Y, [300, 77], 2, 128, 64, "bf16")
+    Q, cu = queries(2, 4, 128, "bf16", 36).cuda(), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    for call in (lambda O, **kw: Y.yoco_paged_attn_decode(Q, pool.dev, O, **kw),
+                 lambda O, **kw: Y.yoco_paged_attn_prefill(Q, pool.dev, cu, O, **kw)):
+        want, got = torch.empty_like(Q), torch.empty_like(Q)
+        call(want)
+        for kw in (dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(window=20, sinks=2 ** 32 + 1)):
+            call(got.fill_(math.nan), **kw)
+            assert torch.equal(got, want)
+        for kw in (dict(window=-2 ** 32 + 5), dict(window=7, sinks=-2 ** 32)):
+            with pytest.raises(Y.YocoError) as e:
+                call(got, **kw)
+            assert e.value.status == Y.YOCO_ERR_INVALID_ARG
