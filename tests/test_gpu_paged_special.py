@@ -375,3 +375,19 @@ def test_windows_and_sinks_past_32_bits(Y):
             with pytest.raises(Y.YocoError) as e:
                 call(got, **kw)
             assert e.value.status == Y.YOCO_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype,d", TYPES)
+@pytest.mark.parametrize("B", [3, 300])
+def test_prefill_results_do_not_change_from_call_to_call(Y, dtype, d, B):
+    """Entries are taken from a counter and, of many sequences, ordered by atomics: what comes out is
+    the same bit for bit."""
+    new = [1 + (37 * b) % 90 for b in range(B)]
+    pool = P.Pool(Y, [t + (53 * b) % 400 + (9000 if b == 1 else 0) for b, t in enumerate(new)], 2, d, 16, dtype)
+    cu = torch.tensor([0] + list(itertools.accumulate(new)), dtype=torch.int32, device="cuda")
+    Q = queries(sum(new), 6, d, dtype, 37).cuda()
+    outs = []
+    for _ in range(5):
+        outs.append(torch.full_like(Q, math.nan))
+        Y.yoco_paged_attn_prefill(Q, pool.dev, cu, outs[-1])
+    assert bool(torch.isfinite(outs[0]).all()) and all(torch.equal(outs[0], o) for o in outs[1:])
