@@ -24,9 +24,11 @@
 // the rings never stand still between units.  The softmax warps meet once a tile; every
 // thread waits for what it reads itself, so no warp waits for another's wait as well.
 //
-// What bounds it: DRAM reads of K and V (32 sequences of 60 to 32000 keys 120 us, 6.3 TB/s;
-// one of 10^6 keys 602 us, 7.1 TB/s).  Short calls (700 keys: 8.8 us) are the launch, two
-// dependent tiles and the merge.  Four barriers a tile in place of one: 130 us for the 32.
+// What bounds it: DRAM reads of K and V (32 sequences of 60 to 32000 keys 122 us, 6.2 TB/s;
+// one of 10^6 keys 605 us, 7.1 TB/s).  With 16 query heads to a kv head the softmax shows: 32
+// sequences of 60 to 30000 keys over 8 kv heads take 287 us with 3 heads each (6.8 TB/s), 291
+// with 8 and 352 with 16 (5.6 TB/s).  Short calls (700 keys: 8.4 us) are the launch, two
+// dependent tiles and the merge.  Four barriers a tile in place of one: 130 us for the first 32.
 #include <cudaTypedefs.h>
 
 #include "common.cuh"

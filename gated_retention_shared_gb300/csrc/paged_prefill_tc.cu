@@ -32,8 +32,8 @@
 // A, 8-11 set B (thread = TMEM lane = row).  S and P V have issuers of their own so that
 // S_X(i + 1) goes as soon as S_X(i) has been read, whatever P the other issuer waits for.
 //
-// What bounds it (512 rows over 131072 keys: 590 us, 1.46 us a tile of 2 x 128 rows; the
-// products alone are 1.08): the softmax warps' own chain, about 2800 cycles a tile from S to P
+// What bounds it (512 rows over 131072 keys: 586-630 us with the card's power, 1.46 us a tile of
+// 2 x 128 rows at the least; the products alone are 1.08): the softmax warps' own chain, about 2800 cycles a tile from S to P
 // with no pipe above a third; and some 6 us an entry around its tiles (first Q, K, S; last P V;
 // rows out).  What counted, each timed as the kernel then was, on the long chunk if not said:
 //   - no register spilled in the tile loop: shared memory leaves next to no L1, so each reload
@@ -41,13 +41,13 @@
 //   - the exponentials in steps over 32 columns, not element by element (740 -> 690 us);
 //   - one copy of the tile loop's code for both sets (a copy for each: 2 x the time, the
 //     instruction cache);
-//   - waits that look at the abort flag and the clock between polls: a tight loop of polls
-//     takes issue slots from the softmax (663 -> 586 us);
+//   - the waits of the other kernels: one whose first 16384 polls were a loop of nothing else that
+//     fell through into what follows took 663 us against 586 (the cause was not shown);
 //   - S and P V issuers apart (757 -> 740 us);
 //   - little between a slot's release and its next copy (12 mixed sequences 63.4 -> 61.3 us);
 //   - blocks that stay instead of one per entry: 600 short sequences 218 -> 172 us, 3 windows 129
 //     -> 123, 16 prompts of 100 to 900 rows 67 -> 62; 12 mixed sequences, about one entry to a
-//     block, 61.3 -> 62.  The next kernel is let in when a block has found no further entry, not
+//     block, 61.3 -> 62 (59 today).  The next kernel is let in when a block has found no further entry, not
 //     at once (2 us).
 // Tried and slower: two warps to a row (half the columns each, 808 against 740 us), weights
 // before the maximum is known (752); S read twice by halves made no difference, nor did both

@@ -40,7 +40,9 @@ template <typename T> __device__ __forceinline__ void load16(const T *p, float (
 // the block: a key's score is summed over its lanes, and each group of eight lanes keeps a
 // running maximum, sum and weighted sum of its own, merged at the end of the unit.  K and V
 // go from global memory to registers once.  Groups with more than kDecQ heads take them
-// kDecQ at a time, reading K and V again (from L2).
+// kDecQ at a time, reading K and V again (from L2).  32 sequences of 60 to 30000 keys over 4 kv
+// heads: fp32 x 128 282 us with one head each (6.9 TB/s, the read rate), 427 with four, 468 with
+// eight; bf16 x 64 170, 223 and 440 us (2.9, 2.2 and 1.1 TB/s: the sums, not the reads).
 constexpr int kDecThreads = 256;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecQ = 8;      // query heads at a time
@@ -252,12 +254,13 @@ paged_merge_kernel(const float *__restrict__ part, const PagedCut *__restrict__ 
 // 64 rows (tokens x the G query heads of one kv head) against 64-key steps, 256 threads as
 // 16 x 16: thread (ty, tx) holds rows 4 ty .. and keys tx + 16 j of the scores, rows 4 ty ..
 // and dims 4 tx + 64 j .. of the output.  Everything the products read is in shared memory
-// as fp32, two blocks to an SM.  K and V have one buffer each: the next step's K comes in
+// as fp32: two blocks to an SM at head size 64, one at 128 (113 KB each).  K and V have one buffer each: the next step's K comes in
 // while this step's softmax and P V run, its V while the next scores do (asynchronous copies
 // for fp32, registers for bf16, which is widened on the way).  Bound by shared-memory reads and
 // the fp32 pipe, about half of its peak (4096 fp32 rows, 8 over 4 heads x 64: 475 us, 36 TFLOP/s;
-// 8 x 8 values to a thread and half the reads: 480 us).  Four chunks of 99 to 470 rows, 31 us: the
-// plan 3, two to four steps of 5 us each after 3 us of start, the merge 4.
+// x 128 998 us, 34; bf16, 16 over 4 heads x 64, 926 us, 37; 8 x 8 values to a thread and half the
+// reads: 480 us for the first).  Four chunks of 99 to 470 rows, 31 us: the plan 3, two to four steps
+// of 5 us each after 3 us of start, the merge 4.
 constexpr int kPreRows = 64, kPreKeys = 64, kPreThreads = 256;
 constexpr int kPreMinPiece = 1;       // tiles
 constexpr float kPreSplitCost = .002f;
@@ -583,7 +586,10 @@ constexpr int kMaxDecodeBlocks = (int)(kPagedCuts / sizeof(PagedCut));
 // the tensor-core kernels take what fits their tiles
 static bool paged_on_tc(const yoco_paged_kv *c) { return c->dtype == YOCO_BF16 && c->d == 128; }
 
-// resident blocks of the decode and prefill kernels: one per SM of the tensor-core ones
+// blocks that a decode's grid has and a prefill's plan counts on: one per SM of the tensor-core
+// kernels, two of the CUDA-core ones.  (Two are resident at head size 64 with up to four heads at a
+// time and at 128 with up to two; the decode with more of them, and the prefill at 128, have one:
+// the grid is then two rounds, and the plan's rounds are half as many as there are.)
 static int paged_slots(const yoco_paged_kv *c) { return (paged_on_tc(c) ? 1 : 2) * device_sm_count(); }
 static int paged_decode_blocks(const yoco_paged_kv *c) { return std::min(kMaxDecodeBlocks, paged_slots(c)); }
 
