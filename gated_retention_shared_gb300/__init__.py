@@ -51,6 +51,17 @@ class _PagedKVC(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("rope_base", ctypes.c_float)]
 
 
+class _RopeC(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_float), ("factor", ctypes.c_float), ("original", ctypes.c_float),
+                ("low", ctypes.c_float), ("high", ctypes.c_float), ("magnitude", ctypes.c_float)]
+
+
+class _PagedScoresC(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p),
+                ("doc_first", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libyoco.so not found at {LIB_PATH}; build it with "
@@ -60,6 +71,8 @@ def _load():
     cp = ctypes.POINTER(_KVCacheC)
     rp = ctypes.POINTER(_SwaRingC)
     pp = ctypes.POINTER(_PagedKVC)
+    op = ctypes.POINTER(_RopeC)
+    cs = ctypes.POINTER(_PagedScoresC)
     sigs = {
         "yoco_gret_prefill_chunkwise": (i, [vp, vp, vp, vp, f, vp, vp, i, i, i, i, i, i, i, i, vp, sz, vp]),
         "yoco_gret_prefill_workspace_size": (sz, [i, i, i, i, i, i, i]),
@@ -93,6 +106,15 @@ def _load():
         "yoco_paged_attn_prefill": (i, [vp, i, vp, i, pp, f, i, i, vp, vp, sz, vp]),
         "yoco_paged_attn_decode": (i, [vp, i, pp, f, i, i, vp, vp, sz, vp]),
         "yoco_paged_attn_workspace_size": (sz, [i, i, pp]),
+        "yoco_rope_apply_scaled": (i, [vp, i64, i64, vp, i64, i64, i, i, i, vp, i64, op, i, vp]),
+        "yoco_paged_append_rope": (i, [vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i, vp, i, pp, op, vp, sz, vp]),
+        "yoco_paged_attn_prefill_scored": (i, [vp, i, vp, i, pp, cs, f, i, i, vp, vp, sz, vp]),
+        "yoco_paged_attn_decode_scored": (i, [vp, i, pp, cs, f, i, i, vp, vp, sz, vp]),
+        "yoco_paged_resize": (i, [pp, vp, vp, vp, vp, sz, vp]),
+        "yoco_paged_fork": (i, [pp, vp, vp, vp, i, vp, sz, vp]),
+        "yoco_paged_compact": (i, [pp, vp, vp, vp, sz, vp]),
+        "yoco_paged_copy": (i, [pp, vp, i, vp]),
+        "yoco_paged_pool_workspace_size": (sz, [pp]),
         "yoco_debug_checks": (i, [i, ctypes.POINTER(ctypes.c_uint32)]),
     }
     for name, (res, args) in sigs.items():
@@ -112,7 +134,10 @@ EXPORTED = ("yoco_gret_prefill_chunkwise", "yoco_gret_prefill_workspace_size", "
             "yoco_rope_apply", "yoco_gret_qkvg_project", "yoco_gret_qkvg_workspace_size",
             "yoco_gret_decode_step_gn_gate", "yoco_cross_attn_decode_noalloc_status", "yoco_test_hook",
             "yoco_selftest_occupy_sms", "yoco_gret_prefill_chunkwise_gn_gate", "yoco_debug_checks", "yoco_paged_append",
-            "yoco_paged_attn_prefill", "yoco_paged_attn_decode", "yoco_paged_attn_workspace_size")
+            "yoco_paged_attn_prefill", "yoco_paged_attn_decode", "yoco_paged_attn_workspace_size",
+            "yoco_rope_apply_scaled", "yoco_paged_append_rope", "yoco_paged_attn_prefill_scored",
+            "yoco_paged_attn_decode_scored", "yoco_paged_resize", "yoco_paged_fork", "yoco_paged_compact",
+            "yoco_paged_copy", "yoco_paged_pool_workspace_size")
 YOCO_HOOK_FAIL_NEXT_CALLS, YOCO_HOOK_GRET_SEG0_DELAY_NS, YOCO_HOOK_GRET_SEGMENTS = 1, 2, 3
 
 
@@ -398,6 +423,50 @@ def yoco_rope_apply(x, base, pos0=0, stream=None):
     _check(st, "yoco_rope_apply")
 
 
+class Rope:
+    """A rotary encoding other than pairs of the whole head at one base: `rotary_dim` channels of each
+    head (None: all), in "pairs" (2i, 2i+1) or "halves" (i, i + r/2), frequencies unscaled ("none"),
+    "linear", "ntk" or "by_parts" (yoco.h has the formulas), turned channels times `magnitude`."""
+    LAYOUTS = {"pairs": 0, "halves": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+    def __init__(self, rotary_dim=None, layout="pairs", base=1e4, scaling="none", factor=1.0, original=8192.0, low=1.0,
+                 high=32.0, magnitude=1.0):
+        if layout not in self.LAYOUTS or scaling not in self.SCALINGS:
+            raise ValueError(f"layout is one of {list(self.LAYOUTS)}, scaling one of {list(self.SCALINGS)}")
+        if rotary_dim is not None and rotary_dim <= 0:
+            raise ValueError("rotary_dim must be positive")
+        self.c = _RopeC(rotary_dim or 0, self.LAYOUTS[layout], self.SCALINGS[scaling], base, factor, original, low, high,
+                        magnitude)
+        self.ref = ctypes.byref(self.c)
+
+
+def _rows_heads(t, name, like=None):
+    """Pointer and strides of a [rows, heads, d] tensor with adjacent channels."""
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda or len(shape) != 3 or (stride[2] != 1 and shape[2] != 1):
+        raise ValueError(f"{name} must be a CUDA tensor [rows, heads, d] with adjacent channels")
+    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have x's shape, dtype and device")
+    # (the stride of an axis of one element means nothing, and may be anything)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2], stride[1] if shape[1] > 1 else shape[2]
+
+
+def yoco_rope_apply_scaled(x, rope: Rope, out=None, positions=None, pos0=0, stream=None):
+    """x [rows, H, d] with any strides that are multiples of 16 bytes, turned into out (None: in
+    place), row i at positions[i] (int32 [rows]) or, without them, at pos0 + i."""
+    xp = _rows_heads(x, "x")
+    op = xp if out is None else _rows_heads(out, "out", x)
+    rows, H, d = x.shape
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (rows,) or
+                                  positions.device != x.device or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 [rows] on x's device")
+    if not -2**31 <= pos0 <= 2**31:
+        raise ValueError("pos0 is beyond 2^31")
+    _device_call(lib.yoco_rope_apply_scaled, "yoco_rope_apply_scaled", x.get_device(), stream, *xp, *op, rows, H, d,
+                 None if positions is None else positions.data_ptr(), pos0, rope.ref, _dt(x))
+
+
 def yoco_gret_qkvg_project(X, W, H, q, k, v, gate_logits, rope_base=0.0, pos0=0, workspace=None, stream=None):
     """X [B, N, dm] bf16; W [dm, 3 H d + H] bf16 (W_Q | W_K | W_V | W_gamma); writes q, k, v
     [B, N, H, d] bf16 and gate_logits [B, N, H] fp32."""
@@ -443,8 +512,7 @@ class PagedKV:
         self._dtype, self._dev, self._B, self._Hkv, self._d = k.dtype, k.get_device(), B, Hkv, d
 
 
-def _paged_call(fn, name, cache, stream, *args):
-    dev = cache._dev
+def _device_call(fn, name, dev, stream, *args):
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
         status = fn(*args, raw)
@@ -453,6 +521,10 @@ def _paged_call(fn, name, cache, stream, *args):
             status = fn(*args, raw)
     if status:
         _check(status, name)
+
+
+def _paged_call(fn, name, cache, stream, *args):
+    _device_call(fn, name, cache._dev, stream, *args)
 
 
 def _paged_workspace(nbytes, cache, workspace, stream):
@@ -486,10 +558,7 @@ def _paged_source(t, name, cache, heads, rows):
         stride[1] if shape[1] > 1 else shape[2]
 
 
-def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, workspace=None, stream=None):
-    """k, v [rows, Hkv, d] (or both None), q [rows, Hq, d] or None, each with any strides
-    that are multiples of 16 bytes; q_out [rows, Hq, d] (None: q in place).  cu_rows int32
-    [B + 1], or None for one row per sequence."""
+def _paged_append_args(k, v, cache, cu_rows, q, q_out):
     rows, Hq, qo = None, 0, None
     kp = vp = qp = (None, 0, 0)
     if k is not None:
@@ -507,9 +576,24 @@ def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, wo
     if rows is None:
         raise ValueError("neither k and v nor q given")
     cu = None if cu_rows is None else _paged_cu(cu_rows, cache)
+    return *kp, *vp, *qp, qo, Hq, cu, rows, cache.ref
+
+
+def yoco_paged_append(k, v, cache: PagedKV, cu_rows=None, q=None, q_out=None, workspace=None, stream=None):
+    """k, v [rows, Hkv, d] (or both None), q [rows, Hq, d] or None, each with any strides
+    that are multiples of 16 bytes; q_out [rows, Hq, d] (None: q in place).  cu_rows int32
+    [B + 1], or None for one row per sequence."""
+    args = _paged_append_args(k, v, cache, cu_rows, q, q_out)
     ws, wp, wn = _paged_workspace(256, cache, workspace, stream)
-    _paged_call(lib.yoco_paged_append, "yoco_paged_append", cache, stream, *kp, *vp, *qp, qo, Hq, cu, rows, cache.ref, wp,
-                wn)
+    _paged_call(lib.yoco_paged_append, "yoco_paged_append", cache, stream, *args, wp, wn)
+
+
+def yoco_paged_append_rope(k, v, cache: PagedKV, rope: Rope, cu_rows=None, q=None, q_out=None, workspace=None,
+                           stream=None):
+    """yoco_paged_append with k and q turned as `rope` says (the cache's rope_base must be 0)."""
+    args = _paged_append_args(k, v, cache, cu_rows, q, q_out)
+    ws, wp, wn = _paged_workspace(256, cache, workspace, stream)
+    _paged_call(lib.yoco_paged_append_rope, "yoco_paged_append_rope", cache, stream, *args, rope.ref, wp, wn)
 
 
 def _paged_q(Q, O, cache):
@@ -544,3 +628,104 @@ def yoco_paged_attn_decode(Q, cache: PagedKV, O, scale=None, window=0, sinks=0, 
     ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
     _paged_call(lib.yoco_paged_attn_decode, "yoco_paged_attn_decode", cache, stream, Q.data_ptr(), Hq, cache.ref,
                 cache._d ** -0.5 if scale is None else scale, _reach(window), _reach(sinks), O.data_ptr(), wp, wn)
+
+
+class PagedScores:
+    """Scores other than scale q.k and masks other than causal ones, for the scored paged calls:
+    a tanh cap, slopes fp32 [Hq] of a bias by distance, prefix int32 [B] (slots that every row of the
+    sequence sees), doc_first int32 [rows] (the first slot of each row's document)."""
+
+    def __init__(self, softcap=0.0, slopes=None, prefix=None, doc_first=None):
+        for t, n, dt in ((slopes, "slopes", torch.float32), (prefix, "prefix", torch.int32),
+                         (doc_first, "doc_first", torch.int32)):
+            if t is not None:
+                _need(t, n)
+                if t.dtype != dt or t.dim() != 1:
+                    raise ValueError(f"{n} must be a vector of {dt}")
+        self.softcap, self.slopes, self.prefix, self.doc_first = softcap, slopes, prefix, doc_first
+        self.c = _PagedScoresC(softcap, *(None if t is None else t.data_ptr() for t in (slopes, prefix, doc_first)))
+        self.ref = ctypes.byref(self.c)
+
+    def _check(self, cache, Hq, rows):
+        for t, n, size in ((self.slopes, "slopes", Hq), (self.prefix, "prefix", cache._B),
+                           (self.doc_first, "doc_first", rows)):
+            if t is not None and (t.shape[0] != size or t.get_device() != cache._dev):
+                raise ValueError(f"{n} must have {size} values on the cache's device")
+        return self.ref
+
+
+def yoco_paged_attn_prefill_scored(Q, cache: PagedKV, cu_rows, O, scores: PagedScores, scale=None, window=0, sinks=0,
+                                   workspace=None, stream=None):
+    """yoco_paged_attn_prefill with the scores and masks of `scores`."""
+    rows, Hq = _paged_q(Q, O, cache)
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
+    _paged_call(lib.yoco_paged_attn_prefill_scored, "yoco_paged_attn_prefill_scored", cache, stream, Q.data_ptr(), Hq,
+                _paged_cu(cu_rows, cache), rows, cache.ref, scores._check(cache, Hq, rows),
+                cache._d ** -0.5 if scale is None else scale, _reach(window), _reach(sinks), O.data_ptr(), wp, wn)
+
+
+def yoco_paged_attn_decode_scored(Q, cache: PagedKV, O, scores: PagedScores, scale=None, window=0, sinks=0,
+                                  workspace=None, stream=None):
+    """yoco_paged_attn_decode with the scores and masks of `scores` (doc_first int32 [B])."""
+    rows, Hq = _paged_q(Q, O, cache)
+    if rows != cache._B:
+        raise ValueError(f"Q has {rows} rows, the cache {cache._B} sequences")
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_attn_workspace_size(Hq, rows, cache), cache, workspace, stream)
+    _paged_call(lib.yoco_paged_attn_decode_scored, "yoco_paged_attn_decode_scored", cache, stream, Q.data_ptr(), Hq,
+                cache.ref, scores._check(cache, Hq, rows), cache._d ** -0.5 if scale is None else scale, _reach(window),
+                _reach(sinks), O.data_ptr(), wp, wn)
+
+
+# --------------------------------------------- the pages of a paged cache
+
+def yoco_paged_pool_workspace_size(cache: PagedKV) -> int:
+    return lib.yoco_paged_pool_workspace_size(cache.ref)
+
+
+def _pool_ints(t, name, cache, size):
+    if t.dtype != torch.int32 or t.get_device() != cache._dev or not t.is_contiguous() or t.dim() != 1 or \
+            (size is not None and t.shape[0] != size):
+        raise ValueError(f"{name} must be a contiguous int32 vector{'' if size is None else f' of {size}'} on the cache's device")
+    return t.data_ptr()
+
+
+def _pool_moves(moves, cache, most):
+    if moves is None:
+        return None
+    if moves.dtype != torch.int32 or moves.get_device() != cache._dev or not moves.is_contiguous() or \
+            moves.dim() != 2 or moves.shape[1] != 4 or moves.shape[0] < most + 1:
+        raise ValueError(f"moves must be a contiguous int32 [>= {most + 1}, 4] on the cache's device")
+    return moves.data_ptr()
+
+
+def yoco_paged_resize(cache: PagedKV, refs, new_lens, moves=None, workspace=None, stream=None):
+    """The sequences' lengths become new_lens (int32 [B], below 0: unchanged): cache.page_table,
+    cache.seq_lens and refs (int32 [num_pages]) are written, shared pages that are written next are
+    copied.  moves: int32 [>= B + 1, 4] for the list of copies, or None."""
+    r, n = _pool_ints(refs, "refs", cache, cache.k.shape[0]), _pool_ints(new_lens, "new_lens", cache, cache._B)
+    m = _pool_moves(moves, cache, cache._B)
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_pool_workspace_size(cache), cache, workspace, stream)
+    _paged_call(lib.yoco_paged_resize, "yoco_paged_resize", cache, stream, cache.ref, r, n, m, wp, wn)
+
+
+def yoco_paged_fork(cache: PagedKV, refs, src, dst, workspace=None, stream=None):
+    """Empty sequences dst (int32 [n]) become what sequences src are, on the same pages."""
+    r, s = _pool_ints(refs, "refs", cache, cache.k.shape[0]), _pool_ints(src, "src", cache, None)
+    d = _pool_ints(dst, "dst", cache, src.shape[0])
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_pool_workspace_size(cache), cache, workspace, stream)
+    _paged_call(lib.yoco_paged_fork, "yoco_paged_fork", cache, stream, cache.ref, r, s, d, src.shape[0], wp, wn)
+
+
+def yoco_paged_compact(cache: PagedKV, refs, moves=None, workspace=None, stream=None):
+    """The pages in use become the pool's first ones.  moves: int32 [>= num_pages // 2 + 1, 4], or None."""
+    r = _pool_ints(refs, "refs", cache, cache.k.shape[0])
+    m = _pool_moves(moves, cache, cache.k.shape[0] // 2)
+    ws, wp, wn = _paged_workspace(lambda: yoco_paged_pool_workspace_size(cache), cache, workspace, stream)
+    _paged_call(lib.yoco_paged_compact, "yoco_paged_compact", cache, stream, cache.ref, r, m, wp, wn)
+
+
+def yoco_paged_copy(cache: PagedKV, moves, stream=None):
+    """Makes the copies of a list (int32 [n, 4]) that a resize or a compact of another cache with the
+    same table wrote."""
+    m = _pool_moves(moves, cache, 0)
+    _paged_call(lib.yoco_paged_copy, "yoco_paged_copy", cache, stream, cache.ref, m, moves.shape[0] - 1)

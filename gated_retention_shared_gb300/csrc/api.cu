@@ -166,6 +166,12 @@ yoco_status yoco_workspace_status(void *workspace, int clear, void *stream) {
         return fail(YOCO_ERR_INVALID_ARG, "a paged call needed a page that the pool does not have");
     if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedRows)
         return fail(YOCO_ERR_INVALID_ARG, "a paged call met cu_rows that decrease or leave [0, rows]");
+    if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedRefs)
+        return fail(YOCO_ERR_INVALID_ARG, "more table entries name a page than refs says");
+    if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedSeq)
+        return fail(YOCO_ERR_INVALID_ARG, "a fork named a sequence that cannot be forked from or to");
+    if (hit && (word & 0xFFu) == (uint32_t)yoco::kErrPagedRoom)
+        return fail(YOCO_ERR_CAPACITY, "the pool has fewer free pages than the sequences need");
     if (hit) return fail(YOCO_ERR_TIMEOUT, "a bounded on-device wait gave up (site %u)", word & 0xFFu);
     g_last_error[0] = 0;
     return YOCO_OK;
@@ -481,6 +487,49 @@ yoco_status yoco_rope_apply(void *x, int B, int N, int H, int d, int64_t pos0, f
     return cuda_status(rope_apply(x, B, N, H, d, pos0, base, dt, (cudaStream_t)stream), "rope_apply");
 }
 
+static yoco_status check_rope(const yoco_rope *r, int d) {
+    if (!r) return fail(YOCO_ERR_INVALID_ARG, "rope is NULL");
+    if (r->rotary_dim < 0 || r->rotary_dim > d || r->rotary_dim % 16)
+        return fail(YOCO_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16 up to %d", r->rotary_dim, d);
+    if (r->layout != YOCO_ROPE_PAIRS && r->layout != YOCO_ROPE_HALVES) return fail(YOCO_ERR_INVALID_ARG, "rope layout invalid");
+    if (r->scaling < YOCO_ROPE_UNSCALED || r->scaling > YOCO_ROPE_BY_PARTS)
+        return fail(YOCO_ERR_INVALID_ARG, "rope scaling invalid");
+    if (!(r->base > 1.0f) || !isfinite(r->base)) return fail(YOCO_ERR_INVALID_ARG, "rope base must be finite and > 1");
+    if (!(r->magnitude > 0.0f) || !isfinite(r->magnitude))
+        return fail(YOCO_ERR_INVALID_ARG, "rope magnitude must be finite and > 0");
+    if (r->scaling != YOCO_ROPE_UNSCALED && (!(r->factor >= 1.0f) || !isfinite(r->factor)))
+        return fail(YOCO_ERR_INVALID_ARG, "rope factor must be finite and >= 1");
+    if (r->scaling == YOCO_ROPE_BY_PARTS &&
+        (!(r->original > 0.0f) || !isfinite(r->original) || !(r->low < r->high) || !isfinite(r->low) || !isfinite(r->high)))
+        return fail(YOCO_ERR_INVALID_ARG, "rope by parts needs original > 0 and low < high, all finite");
+    return YOCO_OK;
+}
+
+yoco_status yoco_rope_apply_scaled(const void *x, int64_t x_row, int64_t x_head, void *out, int64_t out_row,
+                                   int64_t out_head, int rows, int H, int d, const int32_t *positions, int64_t pos0,
+                                   const yoco_rope *rope, yoco_dtype dt, void *stream) {
+    if (!valid_dt(dt)) return fail(YOCO_ERR_INVALID_ARG, "dtype invalid");
+    if (d != 64 && d != 128) return fail(YOCO_ERR_UNSUPPORTED, "head size %d not in {64, 128}", d);
+    yoco_status s = check_rope(rope, d);
+    if (s != YOCO_OK) return s;
+    if (rows < 0 || H <= 0) return fail(YOCO_ERR_INVALID_ARG, "rows >= 0, H > 0");
+    if ((!x || !out) && rows != 0) return fail(YOCO_ERR_INVALID_ARG, "null tensor");
+    if ((int64_t)rows * H > INT32_MAX) return fail(YOCO_ERR_UNSUPPORTED, "rows * H above 2^31 - 1");
+    const int64_t far = (int64_t)1 << 31;
+    if (!positions && (pos0 < -far || pos0 > far || (pos0 < 0 ? -pos0 : pos0) + rows > far))
+        return fail(YOCO_ERR_INVALID_ARG, "|pos0| + rows above 2^31");
+    const int per16 = dt == YOCO_BF16 ? 8 : 4;
+    if (!aligned(x, 16) || !aligned(out, 16) || x_row % per16 || x_head % per16 || out_row % per16 || out_head % per16)
+        return fail(YOCO_ERR_INVALID_ARG, "x, out and their strides must be multiples of 16 bytes");
+    if (!aligned(positions, 4)) return fail(YOCO_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+    if (x == out && rows != 0 && (x_row != out_row || x_head != out_head))
+        return fail(YOCO_ERR_INVALID_ARG, "in place the strides must be the same");
+    if (rows == 0) return YOCO_OK;
+    YOCO_INJECTED_FAILURE("rope_apply_scaled");
+    const RopeArgs a{x, x_row, x_head, out, out_row, out_head, rows, H, d, positions, pos0, dt};
+    return cuda_status(rope_apply_scaled(a, *rope, (cudaStream_t)stream), "rope_apply_scaled");
+}
+
 // ------------------------------------------------ sliding-window self-decoder
 
 static yoco_status check_ring(const yoco_swa_ring *r, int Hq) {
@@ -597,12 +646,15 @@ size_t yoco_paged_attn_workspace_size(int Hq, int rows, const yoco_paged_kv *cac
     return paged_workspace(cache, Hq, rows);
 }
 
-yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
-                              int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out, int Hq,
-                              const int32_t *cu_rows, int rows, const yoco_paged_kv *cache, void *workspace,
-                              size_t ws_bytes, void *stream) {
+static yoco_status append_call(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                               int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out, int Hq,
+                               const int32_t *cu_rows, int rows, const yoco_paged_kv *cache, const yoco_rope *rope,
+                               void *workspace, size_t ws_bytes, void *stream, const char *name) {
     yoco_status s = check_paged(cache);
     if (s != YOCO_OK) return s;
+    if (rope && (s = check_rope(rope, cache->d)) != YOCO_OK) return s;
+    if (rope && cache->rope_base != 0.0f)
+        return fail(YOCO_ERR_INVALID_ARG, "rope takes the place of the cache's rope_base, which must be 0");
     if (rows < 0) return fail(YOCO_ERR_INVALID_ARG, "rows must be >= 0");
     if (!k != !v) return fail(YOCO_ERR_INVALID_ARG, "k and v come together");
     if (!q != !q_out) return fail(YOCO_ERR_INVALID_ARG, "q and q_out come together");
@@ -621,15 +673,87 @@ yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_head, cons
         return fail(YOCO_ERR_INVALID_ARG, "q may be turned in place only where it is dense");
     if ((s = check_ws(workspace, ws_bytes, 256)) != YOCO_OK) return s;
     if (rows == 0) return YOCO_OK;
-    YOCO_INJECTED_FAILURE("paged_append");
-    const PagedArgs a{q, q_out, cu_rows, rows, Hq, cache, 0.f, 0, 0, workspace, (int *)workspace};
+    YOCO_INJECTED_FAILURE(name);
+    const PagedArgs a{q, q_out, cu_rows, rows, Hq, cache, 0.f, 0, 0, workspace, (int *)workspace, nullptr};
     const PagedSource src{k, v, k_row, k_head, v_row, v_head, q_row, q_head};
-    return cuda_status(paged_append(a, src, (cudaStream_t)stream), "paged_append");
+    return cuda_status(paged_append(a, src, rope, (cudaStream_t)stream), name);
+}
+
+yoco_status yoco_paged_append(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                              int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out, int Hq,
+                              const int32_t *cu_rows, int rows, const yoco_paged_kv *cache, void *workspace,
+                              size_t ws_bytes, void *stream) {
+    return append_call(k, k_row, k_head, v, v_row, v_head, q, q_row, q_head, q_out, Hq, cu_rows, rows, cache, nullptr,
+                       workspace, ws_bytes, stream, "paged_append");
+}
+
+yoco_status yoco_paged_append_rope(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                                   int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out, int Hq,
+                                   const int32_t *cu_rows, int rows, const yoco_paged_kv *cache, const yoco_rope *rope,
+                                   void *workspace, size_t ws_bytes, void *stream) {
+    if (!rope) return fail(YOCO_ERR_INVALID_ARG, "rope is NULL");
+    return append_call(k, k_row, k_head, v, v_row, v_head, q, q_row, q_head, q_out, Hq, cu_rows, rows, cache, rope,
+                       workspace, ws_bytes, stream, "paged_append_rope");
+}
+
+// ------------------------------------------------------- the pages of a paged cache
+
+size_t yoco_paged_pool_workspace_size(const yoco_paged_kv *cache) {
+    return check_paged(cache) == YOCO_OK ? paged_pool_workspace(cache) : 0;
+}
+
+static yoco_status check_pool(const yoco_paged_kv *c, const int32_t *refs, const int32_t *moves, void *ws,
+                              size_t ws_bytes) {
+    yoco_status s = check_paged(c);
+    if (s != YOCO_OK) return s;
+    if (!refs || !aligned(refs, 4)) return fail(YOCO_ERR_INVALID_ARG, "refs must be set and 4-byte aligned");
+    if (!aligned(moves, 16)) return fail(YOCO_ERR_INVALID_ARG, "moves must be 16-byte aligned");
+    return check_ws(ws, ws_bytes, paged_pool_workspace(c));
+}
+
+yoco_status yoco_paged_resize(const yoco_paged_kv *cache, int32_t *refs, const int32_t *new_lens, int32_t *moves,
+                              void *workspace, size_t ws_bytes, void *stream) {
+    yoco_status s = check_pool(cache, refs, moves, workspace, ws_bytes);
+    if (s != YOCO_OK) return s;
+    if (!new_lens || !aligned(new_lens, 4)) return fail(YOCO_ERR_INVALID_ARG, "new_lens must be set and 4-byte aligned");
+    if (new_lens == cache->seq_lens) return fail(YOCO_ERR_INVALID_ARG, "new_lens must not be seq_lens");
+    YOCO_INJECTED_FAILURE("paged_resize");
+    return cuda_status(paged_resize(cache, refs, new_lens, moves, workspace, (cudaStream_t)stream), "paged_resize");
+}
+
+yoco_status yoco_paged_fork(const yoco_paged_kv *cache, int32_t *refs, const int32_t *src, const int32_t *dst, int n,
+                            void *workspace, size_t ws_bytes, void *stream) {
+    yoco_status s = check_pool(cache, refs, nullptr, workspace, ws_bytes);
+    if (s != YOCO_OK) return s;
+    if (n < 0 || n > cache->B) return fail(YOCO_ERR_INVALID_ARG, "n must be in [0, B]");
+    if (n == 0) return YOCO_OK;
+    if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4))
+        return fail(YOCO_ERR_INVALID_ARG, "src and dst must be set and 4-byte aligned");
+    YOCO_INJECTED_FAILURE("paged_fork");
+    return cuda_status(paged_fork(cache, refs, src, dst, n, workspace, (cudaStream_t)stream), "paged_fork");
+}
+
+yoco_status yoco_paged_compact(const yoco_paged_kv *cache, int32_t *refs, int32_t *moves, void *workspace,
+                               size_t ws_bytes, void *stream) {
+    yoco_status s = check_pool(cache, refs, moves, workspace, ws_bytes);
+    if (s != YOCO_OK) return s;
+    YOCO_INJECTED_FAILURE("paged_compact");
+    return cuda_status(paged_compact(cache, refs, moves, workspace, (cudaStream_t)stream), "paged_compact");
+}
+
+yoco_status yoco_paged_copy(const yoco_paged_kv *cache, const int32_t *moves, int most, void *stream) {
+    yoco_status s = check_paged(cache);
+    if (s != YOCO_OK) return s;
+    if (!moves || !aligned(moves, 16)) return fail(YOCO_ERR_INVALID_ARG, "moves must be set and 16-byte aligned");
+    if (most < 0) return fail(YOCO_ERR_INVALID_ARG, "most must be >= 0");
+    if (most == 0) return YOCO_OK;
+    YOCO_INJECTED_FAILURE("paged_copy");
+    return cuda_status(paged_copy(cache, moves, most, (cudaStream_t)stream), "paged_copy");
 }
 
 static yoco_status paged_attn(const void *Q, int Hq, const int32_t *cu_rows, int rows, const yoco_paged_kv *cache,
                               float scale, int window, int sinks, void *O, void *workspace, size_t ws_bytes,
-                              void *stream, bool one_row) {
+                              void *stream, bool one_row, const yoco_paged_scores *scores) {
     yoco_status s = check_paged(cache);
     if (s != YOCO_OK) return s;
     if (one_row) rows = cache->B;
@@ -644,21 +768,51 @@ static yoco_status paged_attn(const void *Q, int Hq, const int32_t *cu_rows, int
     if (sinks > (1 << 30)) sinks = 1 << 30;
     if ((s = check_ws(workspace, ws_bytes, paged_workspace(cache, Hq, rows))) != YOCO_OK) return s;
     if (rows == 0) return YOCO_OK;
-    const char *name = one_row ? "paged_attn_decode" : "paged_attn_prefill";
+    const char *name = scores ? (one_row ? "paged_attn_decode_scored" : "paged_attn_prefill_scored")
+                              : (one_row ? "paged_attn_decode" : "paged_attn_prefill");
     YOCO_INJECTED_FAILURE(name);
-    const PagedArgs a{Q, O, cu_rows, rows, Hq, cache, scale, window, sinks, workspace, (int *)workspace};
+    const PagedArgs a{Q, O, cu_rows, rows, Hq, cache, scale, window, sinks, workspace, (int *)workspace, scores};
     return cuda_status(one_row ? paged_decode(a, (cudaStream_t)stream) : paged_prefill(a, (cudaStream_t)stream), name);
 }
 
 yoco_status yoco_paged_attn_prefill(const void *Q, int Hq, const int32_t *cu_rows, int rows,
                                     const yoco_paged_kv *cache, float scale, int window, int sinks, void *O,
                                     void *workspace, size_t ws_bytes, void *stream) {
-    return paged_attn(Q, Hq, cu_rows, rows, cache, scale, window, sinks, O, workspace, ws_bytes, stream, false);
+    return paged_attn(Q, Hq, cu_rows, rows, cache, scale, window, sinks, O, workspace, ws_bytes, stream, false, nullptr);
 }
 
 yoco_status yoco_paged_attn_decode(const void *Q, int Hq, const yoco_paged_kv *cache, float scale, int window,
                                    int sinks, void *O, void *workspace, size_t ws_bytes, void *stream) {
-    return paged_attn(Q, Hq, nullptr, 0, cache, scale, window, sinks, O, workspace, ws_bytes, stream, true);
+    return paged_attn(Q, Hq, nullptr, 0, cache, scale, window, sinks, O, workspace, ws_bytes, stream, true, nullptr);
+}
+
+static yoco_status check_scores(const yoco_paged_scores *sc, float scale) {
+    if (!sc) return fail(YOCO_ERR_INVALID_ARG, "scores is NULL");
+    if (!aligned(sc->slopes, 4) || !aligned(sc->prefix, 4) || !aligned(sc->doc_first, 4))
+        return fail(YOCO_ERR_INVALID_ARG, "slopes, prefix and doc_first must be 4-byte aligned");
+    if (sc->softcap == 0.0f) return YOCO_OK;
+    if (!(scale > 0.0f) || !isfinite(scale)) return fail(YOCO_ERR_INVALID_ARG, "scale must be finite and > 0");
+    const float u = scale / sc->softcap;  // both stay far from what 32 bits cannot hold
+    if (!(sc->softcap >= 0x1p-64f && sc->softcap <= 0x1p64f && u >= 0x1p-64f && u <= 0x1p64f))
+        return fail(YOCO_ERR_INVALID_ARG, "softcap must be 0 (none), or it and scale / softcap within [2^-64, 2^64]");
+    return YOCO_OK;
+}
+
+yoco_status yoco_paged_attn_prefill_scored(const void *Q, int Hq, const int32_t *cu_rows, int rows,
+                                           const yoco_paged_kv *cache, const yoco_paged_scores *scores, float scale,
+                                           int window, int sinks, void *O, void *workspace, size_t ws_bytes,
+                                           void *stream) {
+    const yoco_status s = check_scores(scores, scale);
+    if (s != YOCO_OK) return s;
+    return paged_attn(Q, Hq, cu_rows, rows, cache, scale, window, sinks, O, workspace, ws_bytes, stream, false, scores);
+}
+
+yoco_status yoco_paged_attn_decode_scored(const void *Q, int Hq, const yoco_paged_kv *cache,
+                                          const yoco_paged_scores *scores, float scale, int window, int sinks, void *O,
+                                          void *workspace, size_t ws_bytes, void *stream) {
+    const yoco_status s = check_scores(scores, scale);
+    if (s != YOCO_OK) return s;
+    return paged_attn(Q, Hq, nullptr, 0, cache, scale, window, sinks, O, workspace, ws_bytes, stream, true, scores);
 }
 
 }  // extern "C"

@@ -54,6 +54,8 @@ __device__ __forceinline__ float log_gate(float logit, float inv_tau) {
 //   0x63 paged append: slot                                0x64 paged decode (CUDA cores): output / partial row
 //   0x65 paged prefill (CUDA cores): output row            0x66 paged prefill: merged row
 //   0x67 paged decode (tensor cores): output / partial row  0x68 paged prefill (tensor cores): output row
+//   0x69 scaled rotary encoding: row, head, channel        0x6A paged append with a rotation: slot
+//   0x6B paged resize: table entry                         0x6C paged compact: copy
 #ifdef YOCO_DEBUG_CHECKS
 static __device__ unsigned g_yoco_dbg_word;
 __device__ __forceinline__ bool dcheck(bool ok, unsigned site) {

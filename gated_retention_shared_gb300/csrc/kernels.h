@@ -116,6 +116,19 @@ cudaError_t rope_apply(void *x, int B, int N, int H, int d, int64_t pos0, float 
 // (cos, sin) of (pos0 + t) theta_i into tab [T][d/2] (float2)
 cudaError_t rope_table(float2 *tab, int64_t pos0, int T, int d, float base, cudaStream_t st);
 
+// rope_scaled.cu: strided rows at given positions
+struct RopeArgs {
+    const void *x;
+    int64_t x_row, x_head;  // strides in elements
+    void *out;
+    int64_t out_row, out_head;
+    int rows, H, d;
+    const int32_t *positions;
+    int64_t pos0;
+    yoco_dtype dt;
+};
+cudaError_t rope_apply_scaled(const RopeArgs &s, const yoco_rope &rope, cudaStream_t st);
+
 // qkvg_tc.cu: [q | k | v | logits] = X [W_Q | W_K | W_V | W_gamma], bf16, tensor cores
 cudaError_t qkvg_project(const void *X, const void *W, int B, int N, int dm, int H, int d, void *q, void *k, void *v,
                          float *logits, const float2 *rope_cs, int *err, cudaStream_t st);
@@ -131,12 +144,22 @@ struct PagedArgs {
     int window, sinks;
     void *ws;
     int *err;  // status word of ws
+    const yoco_paged_scores *scores;  // of a scored call, else NULL
 };
 struct PagedSource {  // new rows, strides in elements (Q of PagedArgs has q_row, q_head)
     const void *k, *v;
     int64_t k_row, k_head, v_row, v_head, q_row, q_head;
 };
-cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t st);
+// rope: in place of the cache's rope_base, or NULL
+cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, const yoco_rope *rope, cudaStream_t st);
+// paged_pool.cu: handing out pages
+size_t paged_pool_workspace(const yoco_paged_kv *c);
+cudaError_t paged_resize(const yoco_paged_kv *c, int32_t *refs, const int32_t *new_lens, int32_t *moves, void *ws,
+                         cudaStream_t st);
+cudaError_t paged_fork(const yoco_paged_kv *c, int32_t *refs, const int32_t *src, const int32_t *dst, int n, void *ws,
+                       cudaStream_t st);
+cudaError_t paged_compact(const yoco_paged_kv *c, int32_t *refs, int32_t *moves, void *ws, cudaStream_t st);
+cudaError_t paged_copy(const yoco_paged_kv *c, const int32_t *moves, int most, cudaStream_t st);
 size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows);
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st);
 cudaError_t paged_prefill(const PagedArgs &a, cudaStream_t st);
@@ -151,6 +174,7 @@ struct PagedGrid {
     float entry_cost;      // an entry's start and end, in tiles
     float split_cost;      // a piece's partial result, written and read, in tiles of one SM's time over all SMs
     void *plan, *entries, *cuts;
+    int *doc_lo;  // a scored call's: the least document start of each row block
     float *part;
 };
 cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st);
@@ -162,7 +186,8 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
 
 // debug builds: each kernel file's debug word (see YOCO_DEBUG_TU in common.cuh)
 #define YOCO_DEBUG_TUS(X) X(attn) X(attn_fa) X(attn_tc) X(gn_gate) X(gret_simt) X(gret_tc) X(kv_proj) \
-    X(kv_proj_tc) X(paged_append) X(paged_decode_tc) X(paged_plan) X(paged_prefill_tc) X(paged_simt) X(qkvg_tc) X(rope) X(swa)
+    X(kv_proj_tc) X(paged_append) X(paged_decode_tc) X(paged_plan) X(paged_pool) X(paged_prefill_tc) X(paged_simt) X(qkvg_tc) X(rope) \
+    X(rope_scaled) X(swa)
 #define YOCO_DECLARE_DEBUG_WORD(tu) cudaError_t debug_word_##tu(unsigned *w, int clear);
 YOCO_DEBUG_TUS(YOCO_DECLARE_DEBUG_WORD)
 

@@ -47,6 +47,9 @@ __device__ __forceinline__ uint4 paged_ld16(const void *p) {
 constexpr int kErrPagedLen = 0x60;   // a length below zero or past the table
 constexpr int kErrPagedPage = 0x61;  // a page number outside the pool
 constexpr int kErrPagedRows = 0x62;  // cu_rows decreases or leaves [0, rows]
+constexpr int kErrPagedRefs = 0x63;  // more table entries name a page than refs says
+constexpr int kErrPagedSeq = 0x64;   // a sequence that cannot be forked from or to
+constexpr int kErrPagedRoom = 0x65;  // not enough free pages: no sequence grew
 
 __device__ __forceinline__ void paged_report(int *err, int code) {
     if (err) atomicExch(err, (int)(kErrMagic | (uint32_t)code));
@@ -117,21 +120,107 @@ __device__ __forceinline__ PagedRange paged_range(const PagedView &pv, int p_lo,
     return r;
 }
 
+// ---------------------------------------------- scores and masks of the scored calls
+//
+// The row at position p >= 0 of a sequence of length L sees slot m < L when
+//     m >= doc[row]  and  ( m < prefix[b]  or  m <= p and (W == 0 or p - W < m or m < sinks) ).
+// Kernels are templates on MOD: false is the plain calls' code.
+struct PagedMod {
+    const float *slopes;        // [Hq], or nullptr
+    const int32_t *prefix;      // [B], or nullptr
+    const int32_t *doc;         // [rows], or nullptr
+    float cap2;                 // cap log2(e); 0: no cap
+    float qk;                   // what q.k is multiplied by: scale / cap with a cap, else scale log2(e)
+};
+
+// As PagedRange: the slots that some row of a block sees lie in `dlo <= m < hi` and (m >= lo or
+// m < see), dlo the least of its rows' document starts, `see` the end of the prefix or the sinks.
+// Whole chunks of the slots up to `see`, from slot `first` on, come before the window's.
+struct PagedRangeMod {
+    int lo, hi, base, sink_slots, places, ntiles;
+    int first, dlo, see, pre;  // pre: end of the prefix
+    __device__ __forceinline__ int slot(int v) const { return v < sink_slots ? v + first : v - sink_slots + base; }
+    __device__ __forceinline__ bool edge(int i, int) const {
+        const int v = i * kPagedTile;
+        if (v + kPagedTile > places) return true;
+        if (v >= sink_slots) return v - sink_slots + base < max(lo, dlo);
+        return v + kPagedTile > sink_slots || v + first < dlo || v + first + kPagedTile > see;
+    }
+    __device__ __forceinline__ bool seen(int m, int) const { return m < hi && m >= dlo && (m >= lo || m < see); }
+};
+
+__device__ __forceinline__ PagedRangeMod paged_range_mod(const PagedView &pv, int p_lo, int p_hi, int L, int prefix, int dlo) {
+    PagedRangeMod r;
+    const int cs = min(pv.shift, 7);
+    r.pre = p_hi < 0 ? 0 : max(0, min(prefix, L));
+    r.dlo = max(dlo, 0);
+    r.see = max(min(pv.sinks, max(p_hi + 1, 0)), r.pre);
+    r.hi = max(max(p_hi + 1, 0), r.pre);
+    r.lo = pv.window > 0 ? max(0, p_lo - pv.window + 1) : 0;
+    r.base = (max(r.lo, min(r.dlo, r.hi)) >> cs) << cs;
+    r.first = (min(r.dlo, r.see) >> cs) << cs;
+    r.sink_slots = r.dlo < r.see ? max(0, min(((r.see + (1 << cs) - 1) >> cs) << cs, r.base) - r.first) : 0;
+    r.places = r.dlo < r.hi ? r.sink_slots + r.hi - r.base : 0;
+    r.ntiles = (r.places + kPagedTile - 1) / kPagedTile;
+    return r;
+}
+
+// the row sees nothing at all
+__device__ __forceinline__ bool paged_blind(int pos, int doc, int pre) {
+    return pos < 0 || (doc > pos && max(doc, 0) >= pre);
+}
+
+// C tanh(u): in [-0.8, 0.8] u times the minimax polynomial of tanh(u) / u in u^2 (own fit by
+// reweighted least squares, relative error 6e-8), outside C - 2 C / (1 + e^2u), where nothing cancels.
+// The error stays relative to the result, so a cap far above the scores costs no precision.
+__device__ __forceinline__ float paged_cap(float u, float C) {
+    const float x = u * u;
+    float q = fmaf(x, -0.00435529966f, 0.019093302f);
+    q = fmaf(x, q, -0.0531143173f);
+    q = fmaf(x, q, 0.133210484f);
+    q = fmaf(x, q, -0.333326749f);
+    q = fmaf(x, q, 0.999999942f);
+    float e, i;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(u * 2.8853900817779268f));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(i) : "f"(1.f + e));
+    return fabsf(u) < 0.8f ? C * (u * q) : fmaf(-2.f * C, i, C);
+}
+
+constexpr float kPagedLog2E = 1.4426950408889634f;
+
 // ---------------------------------------------- chunks of rows (prefill)
 //
 // Rows of a sequence go to blocks of T_R; where that leaves SMs idle or one sequence much
 // longer than the rest, a sequence's tiles are cut into pieces.  paged_plan_kernel writes
 // the list of (row block, piece) from the lengths as they are on the device; the prefill
 // kernels take its entries, once for every kv head.
-struct alignas(16) PagedEntry {
+template <typename Range> struct alignas(16) PagedEntryOf {
     int b, row0, nrow, pos0;   // rows [row0, row0 + nrow) of the call, at positions pos0 ..
     int i0, i1;                // tiles of what they see
     int pieces, slot, stride;  // pieces > 1: this one's partial result is `slot`, piece 0's
                                // neighbour slot + stride (each times Hkv, plus the kv head)
-    PagedRange range;
+    Range range;
     int pad;
 };
-static_assert(sizeof(PagedEntry) == 64, "entries are read by 16 lanes");
+typedef PagedEntryOf<PagedRange> PagedEntry;
+typedef PagedEntryOf<PagedRangeMod> PagedEntryMod;
+static_assert(sizeof(PagedEntry) == 64 && sizeof(PagedEntryMod) == 80, "entries are read by as many lanes as they have words");
+
+template <bool MOD> struct PagedKind {
+    typedef PagedRange Range;
+    typedef PagedEntry Entry;
+};
+template <> struct PagedKind<true> {
+    typedef PagedRangeMod Range;
+    typedef PagedEntryMod Entry;
+};
+
+// what the newest row of sequence b, of length L, sees (the decode's rows)
+template <bool MOD>
+__device__ __forceinline__ typename PagedKind<MOD>::Range paged_newest(const PagedView &pv, const PagedMod &mod, int b, int L) {
+    if constexpr (MOD) return paged_range_mod(pv, L - 1, L - 1, L, mod.prefix ? mod.prefix[b] : 0, mod.doc ? mod.doc[b] : 0);
+    else return paged_range(pv, L - 1, L - 1);
+}
 
 struct PagedPlan {
     int entries;  // in the list
@@ -158,15 +247,15 @@ struct PagedCut {
 
 // tiles of all sequences before b into pre[b] (shared memory, B + 1 entries); all
 // THREADS threads; `sums` one int per warp
-template <int THREADS>
-__device__ __forceinline__ void paged_prefix(const PagedView &pv, int *pre, int *sums, int *err) {
+template <int THREADS, bool MOD>
+__device__ __forceinline__ void paged_prefix(const PagedView &pv, const PagedMod &mod, int *pre, int *sums, int *err) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (pv.B + THREADS - 1) / THREADS;
     const int b0 = min(pv.B, tid * each), b1 = min(pv.B, b0 + each);
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
         const int L = paged_len(pv, b, err);
-        const int n = paged_range(pv, L - 1, L - 1).ntiles;
+        const int n = paged_newest<MOD>(pv, mod, b, L).ntiles;
         pre[b] = n;
         mine += n;
     }
@@ -244,6 +333,7 @@ __device__ __forceinline__ PagedCut paged_cut(const PagedView &pv, const int *pr
 namespace yoco_host {
 struct PagedArgs;
 yoco::PagedView paged_view(const PagedArgs &a);
+yoco::PagedMod paged_mod(const PagedArgs &a);
 // bf16, 128-byte swizzle, what lies outside reads as zeros
 bool paged_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
                const uint32_t *box);

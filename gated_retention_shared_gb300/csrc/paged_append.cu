@@ -20,12 +20,9 @@
 #include "kernels.h"
 #include "paged.cuh"
 #include "rope.cuh"
+#include "rope_units.cuh"
 
 namespace yoco {
-
-struct RopeTurns {
-    uint64_t f[64];  // theta_i / 2 pi in 2^-64 turns; all 0: no rotary encoding
-};
 
 struct PagedAppend {
     const uint8_t *k, *v, *q;
@@ -40,18 +37,9 @@ struct PagedAppend {
 constexpr int kAppendWarps = 4;
 constexpr int kUnroll = 5;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32)
-paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const RopeTurns turns) {
-    constexpr int EV = 16 / (int)sizeof(T);  // elements per 16-byte chunk
-    constexpr int PC = EV / 2;               // pairs per chunk
-    constexpr int CH = D / EV;               // chunks per head
-    constexpr int HS = 32 / CH;              // heads a warp covers at a time
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-    const int row = (int)(item / parts), part = (int)(item % parts);
-    if (row >= a.rows) return;
-    const int ch = lane % CH;
+// Finds the sequences that have `row` and calls put(pos, b, turn_q) for each, all lanes together.
+template <typename Put>
+__device__ __forceinline__ void append_row(const PagedAppend &a, const PagedView &pv, int row, int lane, Put put) {
     bool turn_q = a.q != nullptr;
     // The sequences that have this row: cu[b] <= row < cu[b + 1] with bounds within [0, rows].  Bounds
     // that do not decrease give it to one at most; where some fall back, two may have it, and the
@@ -79,6 +67,34 @@ paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const Ro
         }
         const int pos = paged_len(pv, b, a.err) - n + (row - first);
         if (pos < 0) continue;
+        put(pos, b, turn_q);
+        turn_q = false;
+    }
+}
+
+// byte offset of the slot of position pos of sequence b for kv head 0, or -1
+template <typename T, int D>
+__device__ __forceinline__ int64_t append_slot(const PagedAppend &a, const PagedView &pv, int pos, int b, int nkv) {
+    if (!nkv) return -1;
+    const int64_t head_bytes = ((int64_t)D * sizeof(T)) << pv.shift;
+    const int page = paged_page(pv, b, pos >> pv.shift, a.err);
+    if (page < 0) return -1;
+    return (int64_t)page * pv.Hkv * head_bytes + (int64_t)(pos & ((1 << pv.shift) - 1)) * D * sizeof(T);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const RopeTurns turns) {
+    constexpr int EV = 16 / (int)sizeof(T);  // elements per 16-byte chunk
+    constexpr int PC = EV / 2;               // pairs per chunk
+    constexpr int CH = D / EV;               // chunks per head
+    constexpr int HS = 32 / CH;              // heads a warp covers at a time
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int row = (int)(item / parts), part = (int)(item % parts);
+    if (row >= a.rows) return;
+    const int ch = lane % CH;
+    append_row(a, pv, row, lane, [&](int pos, int b, bool turn_q) {
         float c[PC], s[PC];
         if (a.turn) {
 #pragma unroll
@@ -89,14 +105,8 @@ paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const Ro
         }
         // heads in the order k, v, q
         const int nkv = a.k ? pv.Hkv : 0, heads = 2 * nkv + (turn_q ? a.Hq : 0);
-        turn_q = false;
-        int64_t slot = -1;  // byte offset of the slot's kv head 0
+        const int64_t slot = append_slot<T, D>(a, pv, pos, b, nkv);
         const int64_t head_bytes = ((int64_t)D * sizeof(T)) << pv.shift;
-        if (nkv) {
-            const int page = paged_page(pv, b, pos >> pv.shift, a.err);
-            if (page >= 0)
-                slot = (int64_t)page * pv.Hkv * head_bytes + (int64_t)(pos & ((1 << pv.shift) - 1)) * D * sizeof(T);
-        }
         for (int h0 = part * HS + lane / CH; h0 < heads; h0 += parts * HS * kUnroll) {
             uint4 u[kUnroll];
 #pragma unroll
@@ -142,7 +152,52 @@ paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const Ro
                 *reinterpret_cast<uint4 *>(dst + ch * 16) = u[x];
             }
         }
-    }
+    });
+}
+
+// The same with a rotation as yoco_rope describes it: a lane has a unit of the head (rope_units.cuh).
+template <typename T, int D, bool HALVES>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+paged_append_rope_kernel(const PagedAppend a, const PagedView pv, int parts, const __grid_constant__ RopeScaled r) {
+    constexpr int U = HALVES ? 3 : 5;  // heads in flight
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int row = (int)(item / parts), part = (int)(item % parts);
+    if (row >= a.rows) return;
+    const int unit = lane & (r.lanes - 1), step = 32 / r.lanes;  // heads at a time
+    append_row(a, pv, row, lane, [&](int pos, int b, bool turn_q) {
+        const int nkv = a.k ? pv.Hkv : 0, heads = unit < r.units ? 2 * nkv + (turn_q ? a.Hq : 0) : 0;
+        RopeUnit<T, D, HALVES> u;
+        u.init(r, unit, pos, true);
+        const int64_t slot = append_slot<T, D>(a, pv, pos, b, nkv);
+        const int64_t head_bytes = ((int64_t)D * sizeof(T)) << pv.shift;
+        for (int h0 = part * step + lane / r.lanes; h0 < heads; h0 += parts * step * U) {
+            uint4 v[U], w[U];
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const int h = h0 + x * parts * step;
+                if (h >= heads) break;
+                u.load(h < nkv       ? a.k + row * a.k_row + h * a.k_head
+                       : h < 2 * nkv ? a.v + row * a.v_row + (h - nkv) * a.v_head
+                                     : a.q + row * a.q_row + (h - 2 * nkv) * a.q_head,
+                       v[x], w[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const int h = h0 + x * parts * step;
+                if (h >= heads) break;
+                const bool is_v = h >= nkv && h < 2 * nkv;
+                if (u.turns && !is_v) u.turn(v[x], w[x]);
+                if (h < 2 * nkv) {
+                    if (slot < 0) continue;
+                    if (!YOCO_DCHECK(b < pv.B && slot / head_bytes < (int64_t)pv.num_pages * pv.Hkv, 0x6A)) continue;
+                    u.store((is_v ? a.vc : a.kc) + slot + (is_v ? h - nkv : h) * head_bytes, v[x], w[x]);
+                } else {
+                    u.store(a.q_out + ((int64_t)row * a.Hq + (h - 2 * nkv)) * (int64_t)(D * sizeof(T)), v[x], w[x]);
+                }
+            }
+        }
+    });
 }
 
 }  // namespace yoco
@@ -165,18 +220,49 @@ PagedView paged_view(const PagedArgs &a) {
     return v;
 }
 
+PagedMod paged_mod(const PagedArgs &a) {
+    PagedMod m{};
+    const float cap = a.scores ? a.scores->softcap : 0.f;
+    m.qk = cap > 0.f ? a.scale / cap : a.scale * kPagedLog2E;
+    if (!a.scores) return m;
+    m.slopes = a.scores->slopes;
+    m.prefix = a.scores->prefix;
+    m.doc = a.scores->doc_first;
+    m.cap2 = cap * kPagedLog2E;
+    return m;
+}
+
+// warps to a row: one, or up to one per group of heads (hs of them) while that leaves the SMs
+// with fewer than 16 warps each; blocks: those that makes
+static int append_parts(const PagedAppend &p, const PagedView &pv, int hs, int64_t &blocks) {
+    const int heads = (p.k ? 2 * pv.Hkv : 0) + (p.q ? p.Hq : 0);
+    const int64_t want = (int64_t)device_sm_count() * 16;
+    const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((heads + hs - 1) / hs, want / p.rows));
+    blocks = ((int64_t)p.rows * parts + kAppendWarps - 1) / kAppendWarps;
+    return parts;
+}
+
 template <typename T, int D>
 static cudaError_t append_launch(const PagedAppend &p, const PagedView &pv, const RopeTurns &t, cudaStream_t st) {
-    constexpr int HS = 32 / (D * (int)sizeof(T) / 16);
-    const int heads = (p.k ? 2 * pv.Hkv : 0) + (p.q ? p.Hq : 0);
-    // a warp per row, or up to one per group of heads while that leaves the SMs with fewer
-    // than 16 warps each
-    const int64_t want = (int64_t)device_sm_count() * 16;
-    const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((heads + HS - 1) / HS, want / p.rows));
-    const int64_t blocks = ((int64_t)p.rows * parts + kAppendWarps - 1) / kAppendWarps;
+    int64_t blocks;
+    const int parts = append_parts(p, pv, 32 / (D * (int)sizeof(T) / 16), blocks);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     count_launches(1);
     paged_append_kernel<T, D><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, t);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+static cudaError_t append_rope_launch(const PagedAppend &p, const PagedView &pv, const yoco_rope &rope, cudaStream_t st) {
+    const RopeScaled &r = rope_scaled(rope, D, 16 / (int)sizeof(T));
+    int64_t blocks;
+    const int parts = append_parts(p, pv, 32 / r.lanes, blocks);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    count_launches(1);
+    if (rope.layout == YOCO_ROPE_HALVES)
+        paged_append_rope_kernel<T, D, true><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, r);
+    else
+        paged_append_rope_kernel<T, D, false><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, r);
     return cudaGetLastError();
 }
 
@@ -195,7 +281,7 @@ static const RopeTurns &rope_turns(float base, int d) {
     return t;
 }
 
-cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t st) {
+cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, const yoco_rope *rope, cudaStream_t st) {
     const int es = a.cache->dtype == YOCO_BF16 ? 2 : 4, d = a.cache->d;
     PagedAppend p{};
     p.k = (const uint8_t *)s.k;
@@ -214,9 +300,14 @@ cudaError_t paged_append(const PagedArgs &a, const PagedSource &s, cudaStream_t 
     p.rows = a.rows;
     p.Hq = a.Hq;
     p.err = a.err;
+    const PagedView pv = paged_view(a);
+    if (rope) {
+        if (es == 2)
+            return d == 64 ? append_rope_launch<bf16_t, 64>(p, pv, *rope, st) : append_rope_launch<bf16_t, 128>(p, pv, *rope, st);
+        return d == 64 ? append_rope_launch<float, 64>(p, pv, *rope, st) : append_rope_launch<float, 128>(p, pv, *rope, st);
+    }
     p.turn = a.cache->rope_base > 0.f;
     const RopeTurns &t = rope_turns(a.cache->rope_base, d);
-    const PagedView pv = paged_view(a);
     if (es == 2) return d == 64 ? append_launch<bf16_t, 64>(p, pv, t, st) : append_launch<bf16_t, 128>(p, pv, t, st);
     return d == 64 ? append_launch<float, 64>(p, pv, t, st) : append_launch<float, 128>(p, pv, t, st);
 }

@@ -48,7 +48,6 @@ constexpr int kPHalf = kPTile / 2;
 constexpr int kPThreads = 256;
 constexpr int kPQBytes = kPN * kPD * 2;
 constexpr uint32_t kPColS = 0, kPColO = 32;
-constexpr float kPLog2e = 1.4426950408889634f;
 
 struct PagedDecSmem {
     uint64_t full_k[kPStages], full_v[kPStages], empty_k[kPStages], empty_v[kPStages];
@@ -76,11 +75,12 @@ __device__ __forceinline__ float pex2(float x) {
     return y;
 }
 
-template <int NQ>
+template <int NQ, bool MOD>
 __global__ void __launch_bounds__(kPThreads, 1)
 paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const bf16_t *__restrict__ Q, bf16_t *__restrict__ O, float *__restrict__ part,
-                       PagedCut *__restrict__ cuts, int Hq, const PagedView pv, float c2, int keep_pages, int *err) {
+                       PagedCut *__restrict__ cuts, int Hq, const PagedView pv, const PagedMod mod, float c2, int keep_pages,
+                       int *err) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
@@ -123,7 +123,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     tc_fence_before();
-    paged_prefix<kPThreads>(pv, pre, sm.sums, err);
+    paged_prefix<kPThreads, MOD>(pv, mod, pre, sm.sums, err);
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     const int total = pre[pv.B] * pv.Hkv;
@@ -143,7 +143,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         const int psz = min(1 << pv.shift, kPagedTile);  // slots of a box
         const int boxes = 2 * (kPagedTile / psz);        // per tile: (page, 64-channel half)
         const uint64_t pol_keep = l2_policy_evict_normal(), pol_stream = l2_policy_evict_first();
-        PagedRange range{};
+        typename PagedKind<MOD>::Range range{};
         int t = 0, slot = 0, page = 0;
         // this lane's box of the tile at (w, t): its page, or the one past the pool
         auto look_up = [&]() {
@@ -156,8 +156,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
             if (page < 0) page = pv.num_pages;
         };
         auto enter = [&]() {
-            const int p = paged_len(pv, w.b, nullptr) - 1;
-            range = paged_range(pv, p, p);
+            range = paged_newest<MOD>(pv, mod, w.b, paged_len(pv, w.b, nullptr));
             t = w.t0;
         };
         if (more) {
@@ -345,12 +344,14 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         int i = 0;
         bool all = true;
         for (int unit = 0; more && all; ++unit, more = w.next(pv, pre)) {
-            const int p = paged_len(pv, w.b, nullptr) - 1;
-            const PagedRange range = paged_range(pv, p, p);
+            const int len = paged_len(pv, w.b, nullptr);
+            const typename PagedKind<MOD>::Range range = paged_newest<MOD>(pv, mod, w.b, len);
+            [[maybe_unused]] float slope[MOD ? NQ : 1];  // times log2(e)
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 m[n] = -INFINITY;
                 l[n] = 0.f;
+                if constexpr (MOD) slope[n] = mod.slopes && n < G ? mod.slopes[w.hk * G + n] * kPagedLog2E : 0.f;
             }
             for (int t = w.t0; t < w.t1; ++t, ++i) {
                 alive &= mbar_wait_warp(&sm.s_full[i & 1], (i / 2) & 1, abort_flag);
@@ -362,11 +363,17 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.s_free[i & 1]);
-                const bool seen = range.seen(range.slot(t * kPagedTile + r), pv.sinks);
+                const int key = range.slot(t * kPagedTile + r);
+                const bool seen = range.seen(key, pv.sinks);
                 float sc[NQ];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    sc[n] = seen && n < G ? c2 * __uint_as_float(sv[n]) : -INFINITY;
+                    float x2 = c2 * __uint_as_float(sv[n]);
+                    if constexpr (MOD) {
+                        if (mod.cap2 > 0.f) x2 = paged_cap(x2, mod.cap2);
+                        if (mod.slopes) x2 = fmaf(-slope[n], (float)(len - 1 - key), x2);
+                    }
+                    sc[n] = seen && n < G ? x2 : -INFINITY;
                     float x = sc[n];
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
@@ -469,11 +476,11 @@ bool paged_kv_map(CUtensorMap *m, const void *ptr, const yoco_paged_kv *c) {
     return paged_map(m, ptr, 4, dims, strides, box);
 }
 
-template <int NQ>
+template <int NQ, bool MOD>
 static cudaError_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const PagedArgs &a, const PagedView &pv,
                           PagedCut *cuts, float *part, int keep, int blocks, cudaStream_t st) {
     // the shared-memory opt-in is set on every launch (it belongs to the current device)
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_tc_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_tc_kernel<NQ, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)paged_dec_smem(kPagedMaxB));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -487,8 +494,18 @@ static cudaError_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Pa
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<NQ>, mk, mv, (const bf16_t *)a.Q, (bf16_t *)a.O, part, cuts,
-                              a.Hq, pv, a.scale * kPLog2e, keep, a.err);
+    const PagedMod mod = paged_mod(a);
+    return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<NQ, MOD>, mk, mv, (const bf16_t *)a.Q, (bf16_t *)a.O, part, cuts,
+                              a.Hq, pv, mod, mod.qk, keep, a.err);
+}
+
+template <bool MOD>
+static cudaError_t launch_heads(const CUtensorMap &mk, const CUtensorMap &mv, const PagedArgs &a, const PagedView &pv,
+                                PagedCut *cuts, float *part, int keep, int blocks, cudaStream_t st) {
+    const int G = a.Hq / pv.Hkv;
+    return G <= 4   ? launch<4, MOD>(mk, mv, a, pv, cuts, part, keep, blocks, st)
+           : G <= 8 ? launch<8, MOD>(mk, mv, a, pv, cuts, part, keep, blocks, st)
+                    : launch<16, MOD>(mk, mv, a, pv, cuts, part, keep, blocks, st);
 }
 
 cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blocks, cudaStream_t st) {
@@ -500,11 +517,9 @@ cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blo
     const int64_t l2 = device_l2_bytes();
     const int64_t page_bytes = (int64_t)a.cache->page_size * a.cache->Hkv * kPD * 2 * 2;
     const int keep = (int)(l2 / 2 / page_bytes);
-    const int G = a.Hq / pv.Hkv;
     PagedCut *pc = (PagedCut *)cuts;
-    return G <= 4   ? launch<4>(mk, mv, a, pv, pc, part, keep, blocks, st)
-           : G <= 8 ? launch<8>(mk, mv, a, pv, pc, part, keep, blocks, st)
-                    : launch<16>(mk, mv, a, pv, pc, part, keep, blocks, st);
+    return a.scores ? launch_heads<true>(mk, mv, a, pv, pc, part, keep, blocks, st)
+                    : launch_heads<false>(mk, mv, a, pv, pc, part, keep, blocks, st);
 }
 
 }  // namespace yoco_host

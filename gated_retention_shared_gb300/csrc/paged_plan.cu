@@ -62,7 +62,8 @@ struct PlanArgs {
     float entry_cost, split_cost;
     int cap;
     PagedPlan *plan;
-    PagedEntry *entries, *cuts;
+    void *entries, *cuts;  // PagedKind<MOD>::Entry
+    int *doc_lo;           // a scored call's
     int *err;
 };
 
@@ -112,19 +113,32 @@ __device__ __forceinline__ float plan_cost(const PlanArgs &a, int B, int Hkv, in
     return split <= a.max_split ? cost : 3e38f;
 }
 
+// what row block j of sequence b sees, number g of the call's (row bounds that overlap may pass the
+// list's end: such a block is taken to see everything)
+__device__ __forceinline__ PagedRangeMod plan_range(const PlanArgs &a, const PagedView &pv, const PagedMod &mod,
+                                                    const PlanSeq &s, int b, int j, int g) {
+    const int pos0 = s.pos + j * a.T_R, n = min(a.T_R, s.n - j * a.T_R);
+    return paged_range_mod(pv, pos0, pos0 + n - 1, s.pos + s.n, mod.prefix ? mod.prefix[b] : 0,
+                           mod.doc && g < a.cap ? a.doc_lo[g] : 0);
+}
+
 // entry e: number idx of sequence b's, whose partial results and cut row blocks start at slot0, cut0
-__device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &pv, const PlanSeq &s, int b, int pc, int idx,
-                                           int e, int slot0, int cut0) {
+// (block0: a scored call's first row block of the sequence, numbered over the call)
+template <bool MOD>
+__device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &pv, const PagedMod &mod, const PlanSeq &s, int b,
+                                           int pc, int idx, int e, int slot0, int cut0, int block0) {
     const int per = (s.tiles + pc - 1) / pc;
     // the row blocks that see most come first; a cut sequence's row blocks of one piece are
     // neighbours (they read the same keys)
     const int piece = idx / s.blocks, j = s.blocks - 1 - (idx - piece * s.blocks);
-    PagedEntry o;
+    typedef typename PagedKind<MOD>::Entry Entry;
+    Entry o;
     o.b = b;
     o.row0 = s.first + j * a.T_R;
     o.nrow = min(a.T_R, s.n - j * a.T_R);
     o.pos0 = s.pos + j * a.T_R;
-    o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
+    if constexpr (MOD) o.range = plan_range(a, pv, mod, s, b, j, block0 + j);
+    else o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
     // one may see a tile more than `tiles`, or many fewer: the last piece takes what is left
     o.pieces = min(pc, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
     o.i0 = min(piece * per, o.range.ntiles);
@@ -134,11 +148,12 @@ __device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &p
     o.stride = s.blocks;
     o.pad = 0;
     const int4 *from = reinterpret_cast<const int4 *>(&o);
+    constexpr int kQuads = sizeof(Entry) / 16;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(a.entries + e)[x] = from[x];
+    for (int x = 0; x < kQuads; ++x) reinterpret_cast<int4 *>((Entry *)a.entries + e)[x] = from[x];
     if (pc > 1 && piece == 0) {  // for the merge
 #pragma unroll
-        for (int x = 0; x < 4; ++x) reinterpret_cast<int4 *>(a.cuts + cut0 + idx)[x] = from[x];
+        for (int x = 0; x < kQuads; ++x) reinterpret_cast<int4 *>((Entry *)a.cuts + cut0 + idx)[x] = from[x];
     }
 }
 
@@ -209,15 +224,19 @@ paged_plan_small_kernel(const PagedView pv, const PlanArgs a) {
         const int t_slot = __shfl_sync(0xffffffffu, slot, k), t_cut = __shfl_sync(0xffffffffu, cut, k);
         const int n = (int)min((long long)t.blocks * t_pc, (long long)(a.cap - t_first));
         for (int idx = (warp % share) * 32 + lane; idx < n; idx += 32 * share)
-            plan_entry(a, pv, t, k, t_pc, idx, t_first + idx, t_slot, t_cut);
+            plan_entry<false>(a, pv, PagedMod{}, t, k, t_pc, idx, t_first + idx, t_slot, t_cut, 0);
     }
 }
 
+// A scored call's row blocks see what their masks leave: each is looked at (a warp reads a block's
+// document starts), a sequence's `tiles` is its longest block's.
+template <bool MOD>
 __global__ void __launch_bounds__(kPlanThreads)
-paged_plan_kernel(const PagedView pv, const PlanArgs a) {
+paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
     extern __shared__ int sh[];
     int *tiles = sh, *blocks = tiles + pv.B, *order = blocks + pv.B;
     int *start = order + pv.B, *slot0 = start + pv.B + 1, *cut0 = slot0 + pv.B + 1;
+    [[maybe_unused]] int *block0 = cut0 + pv.B + 1;  // [B + 1] row blocks before the sequence's
     __shared__ float r_W[kPlanThreads / 32], c_cost[kPlanTries];
     __shared__ long long r_sum[3][kPlanThreads / 32];
     __shared__ int r_longest[kPlanThreads / 32], c_q[kPlanTries];
@@ -232,11 +251,62 @@ paged_plan_kernel(const PagedView pv, const PlanArgs a) {
 #pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) {
         const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
-        tiles[b] = s.tiles;
+        tiles[b] = MOD ? 0 : s.tiles;
         blocks[b] = s.blocks;
-        W += (float)s.blocks * (float)s.tiles;
         nblocks += s.blocks;
-        longest = max(longest, s.tiles);
+        if constexpr (!MOD) {
+            W += (float)s.blocks * (float)s.tiles;
+            longest = max(longest, s.tiles);
+        }
+    }
+    const int each = (B + kPlanThreads - 1) / kPlanThreads;
+    const int p0 = min(B, tid * each), p1 = min(B, p0 + each);
+    if constexpr (MOD) {
+        __syncthreads();
+        long long mine = 0, sum;
+        for (int b = p0; b < p1; ++b) mine += blocks[b];
+        sum = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += v;
+        }
+        if (lane == 31) r_sum[1][warp] = sum;
+        __syncthreads();
+        long long run = sum - mine;
+        for (int w = 0; w < warp; ++w) run += r_sum[1][w];
+        for (int b = p0; b < p1; ++b) {
+            block0[b] = (int)min(run, 0x7fffffffll);
+            run += blocks[b];
+        }
+        if (p0 < B && p1 == B) block0[B] = (int)min(run, 0x7fffffffll);
+        __syncthreads();
+        const int step = mod.doc ? kPlanThreads / 32 : kPlanThreads;
+        for (int g = mod.doc ? warp : tid; g < min(block0[B], a.cap); g += step) {
+            int lo = 0, hi = B;  // the sequence: block0[lo] <= g < block0[lo + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (block0[mid] <= g) lo = mid;
+                else hi = mid;
+            }
+            const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, lo, nullptr);
+            const int j = g - block0[lo];
+            if (mod.doc) {
+                int least = 0x7fffffff;
+#pragma unroll 4
+                for (int r = j * a.T_R + lane; r < min(s.n, (j + 1) * a.T_R); r += 32) least = min(least, mod.doc[s.first + r]);
+                least = __reduce_min_sync(0xffffffffu, least);
+                if (lane == 0) a.doc_lo[g] = least;
+                __syncwarp();
+            }
+            if (!mod.doc || lane == 0) {
+                const int n = plan_range(a, pv, mod, s, lo, j, g).ntiles;
+                atomicMax(&tiles[lo], n);
+                W += (float)n;
+                longest = max(longest, n);
+            }
+        }
+        __syncthreads();  // (r_sum is written again)
     }
     W = plan_sum(W);
     nblocks = plan_sum(nblocks);
@@ -314,8 +384,6 @@ paged_plan_kernel(const PagedView pv, const PlanArgs a) {
     }
     __syncthreads();
     // where each sequence's entries, partial results and cut row blocks start
-    const int each = (B + kPlanThreads - 1) / kPlanThreads;
-    const int p0 = min(B, tid * each), p1 = min(B, p0 + each);
     long long sum[3] = {0, 0, 0}, inc[3];
     for (int p = p0; p < p1; ++p) {
         const int b = order[p], pc = plan_pieces(tiles[b], Q);
@@ -369,8 +437,9 @@ paged_plan_kernel(const PagedView pv, const PlanArgs a) {
             else hi = mid;
         }
         const int b = order[lo], idx = e - start[lo];
-        const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
-        plan_entry(a, pv, s, b, plan_pieces(s.tiles, Q), idx, e, slot0[lo], cut0[lo]);
+        PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
+        if constexpr (MOD) s.tiles = tiles[b];
+        plan_entry<MOD>(a, pv, mod, s, b, plan_pieces(s.tiles, Q), idx, e, slot0[lo], cut0[lo], MOD ? block0[b] : 0);
     }
 }
 
@@ -380,15 +449,20 @@ namespace yoco_host {
 using namespace yoco;
 
 cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
-    const bool small = a.cache->B <= 32;
-    cudaError_t e = small ? cudaSuccess
-                          : cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)((6 * (size_t)kPagedMaxB + 3) * sizeof(int)));
+    const bool small = a.cache->B <= 32 && !a.scores;
+    const size_t words = a.scores ? 7 * (size_t)a.cache->B + 4 : 6 * (size_t)a.cache->B + 3;
+    cudaError_t e = cudaSuccess;
+    if (a.scores)
+        e = cudaFuncSetAttribute(paged_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)((7 * (size_t)kPagedMaxB + 4) * sizeof(int)));
+    else if (!small)
+        e = cudaFuncSetAttribute(paged_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)((6 * (size_t)kPagedMaxB + 3) * sizeof(int)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = small ? 0 : (6 * (size_t)a.cache->B + 3) * sizeof(int);
+    cfg.dynamicSmemBytes = small ? 0 : words * sizeof(int);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -397,8 +471,10 @@ cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) 
     cfg.numAttrs = 1;
     count_launches(1);
     const PlanArgs p{a.cu, a.rows, g.rows, g.slots, g.max_split, g.min_piece, g.entry_cost, g.split_cost, g.cap,
-                     (PagedPlan *)g.plan, (PagedEntry *)g.entries, (PagedEntry *)g.cuts, a.err};
-    return cudaLaunchKernelEx(&cfg, small ? paged_plan_small_kernel : paged_plan_kernel, paged_view(a), p);
+                     (PagedPlan *)g.plan, g.entries, g.cuts, g.doc_lo, a.err};
+    if (small) return cudaLaunchKernelEx(&cfg, paged_plan_small_kernel, paged_view(a), p);
+    if (a.scores) return cudaLaunchKernelEx(&cfg, paged_plan_kernel<true>, paged_view(a), paged_mod(a), p);
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel<false>, paged_view(a), paged_mod(a), p);
 }
 
 }  // namespace yoco_host

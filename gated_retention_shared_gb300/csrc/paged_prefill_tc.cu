@@ -71,8 +71,7 @@ constexpr int kCStages = 2;
 constexpr int kCTile = kPagedTile * kCD * 2;   // 32 KB
 constexpr int kCHalf = kCTile / 2;             // 64 channels (or keys) of 128 rows
 constexpr int kCThreads = 384;
-constexpr float kCLog2e = 1.4426950408889634f;
-constexpr float kCGap = 8.f * kCLog2e;
+constexpr float kCGap = 8.f * kPagedLog2E;
 
 struct PagedPreBars {
     uint64_t q_full;
@@ -82,15 +81,15 @@ struct PagedPreBars {
 };
 
 // what an entry needs; the next entry's is filled while this one's runs
-struct PagedPreTask {
+template <bool MOD> struct PagedPreTask {
     PagedPreBars bar;
-    PagedEntry blk;
+    typename PagedKind<MOD>::Entry blk;
     int hk;
     int more;  // there is such an entry
 };
 
-struct PagedPreSmem {
-    PagedPreTask task[2];
+template <bool MOD> struct PagedPreSmem {
+    PagedPreTask<MOD> task[2];
     uint64_t drain[2];
     int walive[2][4];
     uint32_t tmem_base;
@@ -99,8 +98,11 @@ struct PagedPreSmem {
 };
 
 constexpr size_t kCTileBytes = (size_t)3 * kCTile + (size_t)kCStages * 2 * kCTile;  // Q_A, Q_B, P, K/V rings
-constexpr size_t kCSmem = kCTileBytes + sizeof(PagedPreSmem) + 1024;
-static_assert(kCSmem <= 232448, "paged prefill tiles must fit shared memory");
+template <bool MOD> constexpr size_t kCSmem = kCTileBytes + sizeof(PagedPreSmem<MOD>) + 1024;
+static_assert(kCSmem<true> <= 232448, "paged prefill tiles must fit shared memory");
+
+// what a kernel's rows do to their scores before the softmax, beyond the masks of the plain calls
+constexpr int kModMask = 1, kModCap = 2, kModBias = 4;
 
 __device__ __forceinline__ void cbar(int id) {  // the four warps of a set
     __syncwarp();
@@ -176,18 +178,102 @@ __device__ __forceinline__ uint32_t c_below(int n) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
+// The scores of a row over a tile, in place: cap tanh(q.k scale / cap) - slope |p - m|, times log2(e).
+// Place c of the tile is slot v0 + first + c before the first run's end, v0 + delta + c from there on.
+// Where no score of the warp leaves [-0.8, 0.8] caps (with caps of some tens that is the rule), the
+// tanh is u times a polynomial of degree 4 in u^2 (own minimax fit by reweighted least squares,
+// relative error 1e-6, a 2000th of the rounding of the weights that follows), two scores to an
+// instruction and no further trip to the special-function unit, which the exponentials fill.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void c_scores(uint32_t (&sv)[128], const PagedMod &mod, float c2, float slope, bool used, int pos,
+                                         int pre, int v0, int sink_slots, int first, int delta) {
+    if constexpr (CAP) {
+        const float C = mod.cap2;
+        float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kPagedTile; c += 2)
+            top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], fabsf(__uint_as_float(sv[c])), fabsf(__uint_as_float(sv[c + 1])));
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
+        if (__builtin_expect(__any_sync(0xffffffffu, used && most > 0.8f), 0)) {
+#pragma unroll
+            for (int c = 0; c < kPagedTile; ++c) sv[c] = __float_as_uint(paged_cap(__uint_as_float(sv[c]) * c2, C));
+        } else {
+            const uint64_t cc = f2_pack(c2, c2);
+            const uint64_t a0 = f2_pack(C * 0.999998994f, C * 0.999998994f), a1 = f2_pack(C * -0.333253721f, C * -0.333253721f);
+            const uint64_t a2 = f2_pack(C * 0.132305659f, C * 0.132305659f), a3 = f2_pack(C * -0.049180146f, C * -0.049180146f);
+            const uint64_t a4 = f2_pack(C * 0.0121001389f, C * 0.0121001389f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint64_t u[8], x[8], t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = 16 * q + 2 * e;
+                    u[e] = f2_mul(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cc);
+                    x[e] = f2_mul(u[e], u[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], a4, a3);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], t[e], a2);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], t[e], a1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], t[e], a0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float y0, y1;
+                    f2_unpack(f2_mul(u[e], t[e]), y0, y1);
+                    sv[16 * q + 2 * e] = __float_as_uint(y0);
+                    sv[16 * q + 2 * e + 1] = __float_as_uint(y1);
+                }
+            }
+        }
+    }
+    if constexpr (BIAS) {
+        const bool head = v0 + kPagedTile <= sink_slots;
+        const int k0 = v0 + (head ? first : delta);
+        // no slot past the row's position is one that it sees, and all places are of one run
+        const bool behind = (head || v0 >= sink_slots) && (k0 + kPagedTile - 1 <= pos || pre <= max(k0, pos + 1));
+        if (__builtin_expect(__all_sync(0xffffffffu, behind || !used), 1)) {
+            const float at = slope * (float)(k0 - pos);
+            const uint64_t at2 = f2_pack(at, at), cc = f2_pack(c2, c2);
+#pragma unroll
+            for (int c = 0; c < kPagedTile; c += 2) {
+                float y0, y1;
+                const uint64_t s2 = f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                f2_unpack(CAP ? f2_add(s2, at2) : f2_fma(s2, cc, at2), y0, y1);
+                sv[c] = __float_as_uint(fmaf(slope, (float)c, y0));
+                sv[c + 1] = __float_as_uint(fmaf(slope, (float)(c + 1), y1));
+            }
+        } else {
+            const float o1 = (float)(v0 + first - pos), o2 = (float)(v0 + delta - pos);
+            const int split = sink_slots - v0;  // places before it are the first run's
+#pragma unroll
+            for (int c = 0; c < kPagedTile; ++c) {
+                const float far = fabsf((float)c + (c < split ? o1 : o2)), y = __uint_as_float(sv[c]);
+                sv[c] = __float_as_uint(fmaf(-slope, far, CAP ? y : y * c2));
+            }
+        }
+    }
+}
+
+template <int MODE>
 __global__ void __launch_bounds__(kCThreads, 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
-                        PagedPlan *plan, const PagedEntry *__restrict__ entries, int cap, int rows, int Hq, const PagedView pv,
-                        float c2, int *err) {
+                        PagedPlan *plan, const typename PagedKind<(MODE > 0)>::Entry *__restrict__ entries, int cap, int rows,
+                        int Hq, const PagedView pv, const PagedMod mod, float c2, int *err) {
+    constexpr bool MOD = MODE > 0, CAP = MODE & kModCap, BIAS = MODE & kModBias;
+    typedef typename PagedKind<MOD>::Entry Entry;
+    typedef PagedPreTask<MOD> Task;
+    constexpr int kWords = sizeof(Entry) / 4;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
     uint8_t *sQ = tiles;                 // Q_A, Q_B
     uint8_t *sP = tiles + 2 * kCTile;
     uint8_t *ring = tiles + 3 * kCTile;  // stage s: K at ring + 2 s kCTile, V after it
-    PagedPreSmem &sm = *reinterpret_cast<PagedPreSmem *>(tiles + kCTileBytes);
+    PagedPreSmem<MOD> &sm = *reinterpret_cast<PagedPreSmem<MOD> *>(tiles + kCTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = Hq / pv.Hkv, TS = kCRows / G;
 
@@ -209,16 +295,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         paged_report(err, code);
     };
     // warp 3: the first entry with rows from `item` on, item by item of all blocks' common counter
-    auto fetch = [&](int item, int entry, PagedPreTask &task) {
+    auto fetch = [&](int item, int entry, Task &task) {
         for (;;) {
             // (both loads at once: the list has room for `cap` entries)
-            const int word = lane < 16 ? paged_ld(reinterpret_cast<const int *>(entries + min(entry, cap - 1)) + lane) : 0;
+            const int word = lane < kWords ? paged_ld(reinterpret_cast<const int *>(entries + min(entry, cap - 1)) + lane) : 0;
             const int count = paged_ld(&plan->entries);
             if (entry >= count) {
                 if (lane == 0) task.more = 0;
                 break;
             }
-            if (lane < 16) reinterpret_cast<int *>(&task.blk)[lane] = word;
+            if (lane < kWords) reinterpret_cast<int *>(&task.blk)[lane] = word;
             if (lane == 0) {
                 task.hk = item - entry * pv.Hkv;
                 task.more = 1;
@@ -238,22 +324,22 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     const int mine = (lane >> 1) * psz;
     // what the table says of this lane's box of tile i (fetched ahead of use, so not yet looked
     // at); -1 past the last place
-    auto look_up = [&](const PagedEntry &blk, int i) -> int {
+    auto look_up = [&](const Entry &blk, int i) -> int {
         const int v = (blk.i0 + i) * kPagedTile + mine, e = blk.range.slot(v) >> pv.shift;
         const bool there = lane < boxes && v < blk.range.places && e < pv.max_pages;
         return there ? pv.table[(size_t)blk.b * pv.max_pages + e] : -1;
     };
     // that page, or the one past the pool
-    auto page_of = [&](const PagedEntry &blk, int i, int entry_of_table) -> int {
+    auto page_of = [&](const Entry &blk, int i, int entry_of_table) -> int {
         if ((unsigned)entry_of_table < (unsigned)pv.num_pages) return entry_of_table;
         if (lane < boxes && (blk.i0 + i) * kPagedTile + mine < blk.range.places) paged_report(err, kErrPagedPage);
         return pv.num_pages;
     };
     const int half = lane & 1;
-    auto row_of = [&](const PagedEntry &blk, int i) -> int {  // of tile i's box in its page
+    auto row_of = [&](const Entry &blk, int i) -> int {  // of tile i's box in its page
         return blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
     };
-    auto copy = [&](PagedPreTask &task, int hk, int i, bool is_v, int page, int row) {  // K or V tile i into its (free) slot
+    auto copy = [&](Task &task, int hk, int i, bool is_v, int page, int row) {  // K or V tile i into its (free) slot
         const int s = i % kCStages;
         uint8_t *st = ring + (size_t)s * 2 * kCTile + (is_v ? kCTile : 0);
         uint64_t *full = is_v ? &task.bar.vfull[s] : &task.bar.kfull[s];
@@ -262,7 +348,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         if (lane < boxes)
             tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
     };
-    auto copy_q = [&](PagedPreTask &task) {
+    auto copy_q = [&](Task &task) {
         if (lane == 0) {
             const int sets = task.blk.nrow > TS ? 2 : 1;
             mbar_arrive_expect_tx(&task.bar.q_full, (uint32_t)(sets * 2 * TS * G * 128));
@@ -275,7 +361,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     };
     int pg0 = -1, pg1 = -1;
     // the entry's first pages and K tile
-    auto first_k = [&](PagedPreTask &task) {
+    auto first_k = [&](Task &task) {
         if (task.blk.i1 == task.blk.i0) return;
         pg0 = look_up(task.blk, 0);
         pg1 = task.blk.i1 - task.blk.i0 > 1 ? look_up(task.blk, 1) : -1;
@@ -311,8 +397,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // -------------------------------------------------------------- TMA
         c_regs_dec();
         for (int n = 0;; ++n) {
-            PagedPreTask &task = sm.task[n & 1], &next = sm.task[(n + 1) & 1];
-            const PagedEntry &blk = task.blk;
+            Task &task = sm.task[n & 1], &next = sm.task[(n + 1) & 1];
+            const Entry &blk = task.blk;
             const int ntiles = blk.i1 - blk.i0;
             volatile int no_abort = 0;
             bool told = false;  // warp 3 takes the next entry late: who is done first takes the longest
@@ -324,10 +410,12 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (n > 0) copy_q(task);
                 int nk = 1, nv = 0;  // tiles whose K / V copy was issued
                 const int c_i0 = blk.i0, c_sink = blk.range.sink_slots, c_delta = blk.range.base - c_sink, c_hk = task.hk;
+                int c_first = 0;
+                if constexpr (MOD) c_first = blk.range.first;
                 bool ok = true;
                 auto load = [&](int i, bool is_v, int page) {
                     const int s = i % kCStages, v = (c_i0 + i) * kPagedTile + mine;
-                    const int row = (v < c_sink ? v : v + c_delta) & ((1 << pv.shift) - 1);
+                    const int row = (v < c_sink ? v + c_first : v + c_delta) & ((1 << pv.shift) - 1);
                     if (i >= kCStages)
                         ok = mbar_wait(is_v ? &task.bar.vempty[s] : &task.bar.kempty[s], ((i / kCStages) + 1) & 1, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
@@ -377,7 +465,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         c_regs_dec();
         for (int n = 0;; ++n) {
             PagedPreBars &bar = sm.task[n & 1].bar;
-            const PagedEntry &blk = sm.task[n & 1].blk;
+            const Entry &blk = sm.task[n & 1].blk;
             const int ntiles = blk.i1 - blk.i0;
             const bool two = blk.nrow > TS;
             if (lane == 0 && ntiles > 0) {
@@ -414,7 +502,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         c_regs_dec();
         for (int n = 0;; ++n) {
             PagedPreBars &bar = sm.task[n & 1].bar;
-            const PagedEntry &blk = sm.task[n & 1].blk;
+            const Entry &blk = sm.task[n & 1].blk;
             const int ntiles = blk.i1 - blk.i0;
             const bool two = blk.nrow > TS;
             if (lane == 0) {
@@ -453,7 +541,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // -------------------------------------------- the next entry and its barriers
         c_regs_dec();
         for (int n = 0;; ++n) {
-            PagedPreTask &next = sm.task[(n + 1) & 1];
+            Task &next = sm.task[(n + 1) & 1];
             asm volatile("bar.sync 11, 64;\n" ::: "memory");
             int item = 0;
             if (lane == 0) item = (int)gridDim.x + atomicAdd(&plan->next, 1);
@@ -481,7 +569,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const uint32_t colS = 256 * x, colO = 256 * x + 128;
         for (int n = 0;; ++n) {
         PagedPreBars &bar = sm.task[n & 1].bar;
-        const PagedEntry &blk = sm.task[n & 1].blk;
+        const Entry &blk = sm.task[n & 1].blk;
         const int hk = sm.task[n & 1].hk, ntiles = blk.i1 - blk.i0;
         const bool two = *(const volatile int *)&blk.nrow > TS;
         if (ntiles == 0) {  // nothing to see: zeros
@@ -498,11 +586,22 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // their V rows.  (A parity can only tell a phase from the one before: with two sets P(i - 1)
         // waited for P_B V(i - 2), so V(i - 2) has come; with one set every tile waits for V)
         int e_lo = 0, e_hi = 0x7fffffff;
-        if (x == 0) {
-            const PagedRange &rg = blk.range;
+        if (!MOD && x == 0) {
+            const auto &rg = blk.range;
             const int from = rg.sink_slots + rg.lo - rg.base;  // the first place that is seen for being in the window
             e_lo = (from + kPagedTile - 1) / kPagedTile - blk.i0;
             e_hi = rg.places / kPagedTile - blk.i0;
+        }
+        // a scored call's row: its document's start, the prefix that it sees, its head's slope
+        [[maybe_unused]] int doc = 0, pre = 0, first = 0;
+        [[maybe_unused]] float slope = 0.f;
+        bool blind = pos < 0;  // sees nothing
+        if constexpr (MOD) {
+            if (used && mod.doc) doc = max(0, mod.doc[blk.row0 + x * TS + r / G]);
+            pre = pos < 0 ? 0 : blk.range.pre;
+            first = blk.range.first;
+            blind = paged_blind(pos, doc, pre);
+            if (BIAS && used) slope = mod.slopes[hk * G + r % G] * kPagedLog2E;
         }
         float m_ref = -INFINITY, l = 0.f;  // base-2 units
         // One exit from the tile loop: a wait that gave up makes what follows garbage (the status word
@@ -523,9 +622,19 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (lane == 0) mbar_arrive(&bar.s_free[x]);
             // place 0 of the tile, and what its slot is where it lies past the sinks' chunks
             const int v0 = (blk.i0 + i) * kPagedTile, key0 = v0 + delta;
-            // every row of the set sees every slot of the tile
-            const bool full = v0 >= sink_slots && key0 + kPagedTile - 1 <= set_lo &&
-                              (pv.window <= 0 || key0 > set_hi - pv.window || key0 + kPagedTile <= pv.sinks);
+            // every row of the set (a scored call: of the warp) sees every slot of the tile
+            bool full;
+            if constexpr (MOD) {
+                const int k0 = v0 + kPagedTile <= sink_slots ? v0 + first : key0;  // (no two runs in the tile)
+                const bool mine = doc <= k0 && ((k0 + kPagedTile - 1 <= pos &&
+                                                 (pv.window <= 0 || k0 > pos - pv.window || k0 + kPagedTile <= pv.sinks)) ||
+                                                k0 + kPagedTile <= pre);
+                full = (v0 >= sink_slots || v0 + kPagedTile <= sink_slots) && __all_sync(0xffffffffu, mine || !used);
+                c_scores<CAP, BIAS>(sv, mod, c2, slope, used, pos, pre, v0, sink_slots, first, delta);
+            } else {
+                full = v0 >= sink_slots && key0 + kPagedTile - 1 <= set_lo &&
+                       (pv.window <= 0 || key0 > set_hi - pv.window || key0 + kPagedTile <= pv.sinks);
+            }
             if (__builtin_expect(!full, 0)) {
                 // the places this row sees of the tile: sinks in the sinks' chunks, then a run up to its
                 // own position from the window's first slot on, and sinks that lie in those chunks
@@ -534,6 +643,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 const int sk_c = min(pv.sinks - key0, hi_c);
                 const int ch_c = sink_slots - v0, sc_c = min(ch_c, min(pv.sinks, pos + 1) - v0);
                 uint32_t bits[4];
+                if constexpr (MOD) {
+                    const int f_c = v0 + first;  // slot of place 0 if it lies in the first run
+                    const int pre_c = pre - key0, doc_c = doc - key0;
+                    const int sc_1 = max(min(pv.sinks, pos + 1), pre) - f_c, doc_1 = doc - f_c;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(max(sk_c, pre_c) - 32 * w)) &
+                                   ~c_below(ch_c - 32 * w) & ~c_below(doc_c - 32 * w)) |
+                                  (c_below(sc_1 - 32 * w) & ~c_below(doc_1 - 32 * w) & c_below(ch_c - 32 * w));
+                } else
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
                     bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w)) &
@@ -548,7 +667,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
             // rows past the set's tokens hold whatever shared memory held: they never move the
             // reference (no rescaling for their sake) and are never stored
-            const float mt = used ? fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * c2 : -INFINITY;
+            const float mt = used ? fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * (CAP || BIAS ? 1.f : c2) : -INFINITY;
             const bool move = (mt > m_ref + kCGap) || (m_ref == -INFINITY && mt > -INFINITY);
             const float m_old = m_ref;
             m_ref = move ? mt : m_ref;
@@ -563,7 +682,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 #pragma unroll
                 for (int c = 16 * q; c < 16 * q + 16; ++c) {
                     float x0, x1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), c2x2, nmu2), x0, x1);
+                    const uint64_t s2 = f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
+                    f2_unpack(CAP || BIAS ? f2_add(s2, nmu2) : f2_fma(s2, c2x2, nmu2), x0, x1);
                     sv[2 * c] = __float_as_uint(x0);
                     sv[2 * c + 1] = __float_as_uint(x1);
                 }
@@ -597,7 +717,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tmem_wait_st();
             }
             // V rows that no row of the block sees: zero, once the tile has come
-            if (__builtin_expect(i < e_lo || i >= e_hi || !two, 0)) {
+            bool edge;
+            if constexpr (MOD) edge = x == 0 && blk.range.edge(blk.i0 + i, 0);
+            else edge = i < e_lo || i >= e_hi;
+            if (__builtin_expect(edge || !two, 0)) {
                 alive &= mbar_wait_warp(&bar.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
                 if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
@@ -664,13 +787,13 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     // of 256 bytes side by side
                     uint8_t *stg = sQ + x * kCTile;
                     // (a row whose scores are all -inf: 0 / 0, NaN as softmax has it)
-                    const float inv = pos < 0 ? 0.f : 1.f / l;
+                    const float inv = blind ? 0.f : 1.f / l;
 #pragma unroll 1
                     for (int cb = 0; cb < 4; ++cb) {
                         uint32_t ov[32];
                         tmem_ld32(o_t + cb * 32, ov);
                         tmem_wait_ld();
-                        if (__builtin_expect(pos < 0, 0)) {  // sees nothing: zero, though 0 times a value may be NaN
+                        if (__builtin_expect(blind, 0)) {  // sees nothing: zero, though 0 times a value may be NaN
 #pragma unroll
                             for (int e = 0; e < 32; ++e) ov[e] = 0;
                         }
@@ -716,6 +839,32 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 namespace yoco_host {
 using namespace yoco;
 
+template <int MODE>
+static cudaError_t launch(const PagedArgs &a, const PagedGrid &g, const CUtensorMap &mq, const CUtensorMap &mk,
+                          const CUtensorMap &mv, cudaStream_t st) {
+    // the shared-memory opt-in is set on every launch (it belongs to the current device)
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kCSmem<(MODE > 0)>);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    const int64_t items = (int64_t)g.cap * a.cache->Hkv;
+    if (items > 0x7fffffff) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, g.slots));
+    cfg.blockDim = dim3(kCThreads);
+    cfg.dynamicSmemBytes = kCSmem<(MODE > 0)>;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    const PagedMod mod = paged_mod(a);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel<MODE>, mq, mk, mv, (bf16_t *)a.O, g.part, (PagedPlan *)g.plan,
+                              (const typename PagedKind<(MODE > 0)>::Entry *)g.entries, g.cap, a.rows, a.Hq, paged_view(a), mod,
+                              mod.qk, a.err);
+}
+
 cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
     const int G = a.Hq / a.cache->Hkv, TS = kCRows / G;
     CUtensorMap mq, mk, mv;
@@ -726,24 +875,10 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
     if (!paged_map(&mq, a.Q, 3, dims, strides, box) || !paged_kv_map(&mk, a.cache->k, a.cache) ||
         !paged_kv_map(&mv, a.cache->v, a.cache))
         return cudaErrorInvalidValue;
-    // the shared-memory opt-in is set on every launch (it belongs to the current device)
-    cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    const int64_t items = (int64_t)g.cap * a.cache->Hkv;
-    if (items > 0x7fffffff) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, g.slots));
-    cfg.blockDim = dim3(kCThreads);
-    cfg.dynamicSmemBytes = kCSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel, mq, mk, mv, (bf16_t *)a.O, g.part, (PagedPlan *)g.plan,
-                              (const PagedEntry *)g.entries, g.cap, a.rows, a.Hq, paged_view(a), a.scale * kCLog2e, a.err);
+    if (!a.scores) return launch<0>(a, g, mq, mk, mv, st);
+    const bool cap = a.scores->softcap > 0.f, bias = a.scores->slopes != nullptr;
+    if (cap) return bias ? launch<kModMask + kModCap + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask + kModCap>(a, g, mq, mk, mv, st);
+    return bias ? launch<kModMask + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask>(a, g, mq, mk, mv, st);
 }
 
 }  // namespace yoco_host

@@ -16,8 +16,6 @@
 
 namespace yoco {
 
-constexpr float kPagedLog2e = 1.4426950408889634f;
-
 // 4 or 8 consecutive elements (16 bytes) as floats
 template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16 / sizeof(T)]) {
     const uint4 u = paged_ld16(p);
@@ -48,11 +46,11 @@ constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecQ = 8;      // query heads at a time
 constexpr int kDecKeys = 2;   // keys of a lane group in flight
 
-template <typename T, int D, int NQ>
+template <typename T, int D, int NQ, bool MOD>
 __global__ void __launch_bounds__(kDecThreads)
 paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
-                         float *__restrict__ part, PagedCut *__restrict__ cuts, int Hq, const PagedView pv, float c2,
-                         int *err) {
+                         float *__restrict__ part, PagedCut *__restrict__ cuts, int Hq, const PagedView pv,
+                         const PagedMod mod, float c2, int *err) {
     constexpr int EV = 16 / (int)sizeof(T);
     constexpr int NC = D / EV / 8;  // chunks of a key per lane
     constexpr int EL = NC * EV;     // elements of a key per lane
@@ -65,7 +63,7 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
     const int G = Hq / pv.Hkv, c = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    paged_prefix<kDecThreads>(pv, pre, sums, err);
+    paged_prefix<kDecThreads, MOD>(pv, mod, pre, sums, err);
     const int total = pre[pv.B] * pv.Hkv;
     const int each = (total + (int)gridDim.x - 1) / (int)gridDim.x;
     // sequences without a key: zeros
@@ -78,8 +76,8 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
     if (more && w.t0 > 0) cut = paged_cut(pv, pre, w, c, each);
     if (tid == 0) cuts[c] = cut;
     for (int seg = 0; more; ++seg, more = w.next(pv, pre)) {
-        const int p = paged_len(pv, w.b, err) - 1;
-        const PagedRange range = paged_range(pv, p, p);
+        const int len = paged_len(pv, w.b, err);
+        const typename PagedKind<MOD>::Range range = paged_newest<MOD>(pv, mod, w.b, len);
         for (int g0 = 0; g0 < G; g0 += NQ) {
             const int nq = min(NQ, G - g0);
             const size_t qrow = (size_t)w.b * Hq + w.hk * G + g0;
@@ -94,8 +92,10 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
             }
             __syncthreads();
             float m[NQ], l[NQ], acc[NQ][EL];
+            [[maybe_unused]] float slope[MOD ? NQ : 1];  // times log2(e)
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
+                if constexpr (MOD) slope[i] = mod.slopes && i < nq ? mod.slopes[w.hk * G + g0 + i] * kPagedLog2E : 0.f;
                 m[i] = -INFINITY;
                 l[i] = 0.f;
 #pragma unroll
@@ -106,9 +106,11 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
             for (int st = 0; st < steps; st += kDecKeys) {
                 float kx[kDecKeys][EL], vx[kDecKeys][EL];
                 bool ok[kDecKeys];
+                [[maybe_unused]] float far[kDecKeys];  // from the row
 #pragma unroll
                 for (int x = 0; x < kDecKeys; ++x) {
                     const int key = range.slot(w.t0 * kPagedTile + (st + x) * 32 + grp);
+                    if constexpr (MOD) far[x] = (float)(len - 1 - key);
                     ok[x] = range.seen(key, pv.sinks);
                     const int page = ok[x] ? paged_page(pv, w.b, key >> pv.shift, err) : -1;
                     const size_t at = (((size_t)max(page, 0) * pv.Hkv + w.hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
@@ -138,6 +140,10 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                         for (int e = 0; e < EL; ++e) d = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d);
 #pragma unroll
                         for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                        if constexpr (MOD) {
+                            if (mod.cap2 > 0.f) d = mod.cap2 * tanhf(d);
+                            if (mod.slopes) d = fmaf(-slope[i], far[x], d);
+                        }
                         s[x] = ok[x] ? d : -INFINITY;
                         top = fmaxf(top, s[x]);
                     }
@@ -311,16 +317,18 @@ template <typename T, int D, int PITCH> struct PreStage {
     }
 };
 
-template <typename T, int D>
+template <typename T, int D, bool MOD>
 __global__ void __launch_bounds__(kPreThreads, 2)
 paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
                           float *__restrict__ part, const PagedPlan *__restrict__ plan,
-                          const PagedEntry *__restrict__ entries, int rows, int Hq, const PagedView pv, float c2, int *err) {
+                          const typename PagedKind<MOD>::Entry *__restrict__ entries, int rows, int Hq, const PagedView pv,
+                          const PagedMod mod, float c2, int *err) {
     constexpr int EV = 16 / (int)sizeof(T), NJ = D / 64;
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4);
     float *sk = sq + kPreRows * D, *sv = sk + kPreKeys * (D + 4), *sp = sv + kPreKeys * D;
-    __shared__ PagedEntry blk;
+    __shared__ typename PagedKind<MOD>::Entry blk;
+    constexpr int kWords = sizeof(blk) / 4;
     __shared__ int64_t at[2][kPreKeys];
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int G = Hq / pv.Hkv, TS = kPreRows / G;
@@ -328,9 +336,9 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int hk = blockIdx.x % pv.Hkv, entry = blockIdx.x / pv.Hkv;
     // (both loads at once: the list has room for every entry of the grid)
-    const int word = tid < 16 ? paged_ld(reinterpret_cast<const int *>(entries + entry) + tid) : 0;
+    const int word = tid < kWords ? paged_ld(reinterpret_cast<const int *>(entries + entry) + tid) : 0;
     if (entry >= paged_ld(&plan->entries)) return;
-    if (tid < 16) reinterpret_cast<int *>(&blk)[tid] = word;
+    if (tid < kWords) reinterpret_cast<int *>(&blk)[tid] = word;
     __syncthreads();
     if (blk.nrow == 0) return;
     const int nr = blk.nrow * G;  // rows in use: (token, head) = (r / G, r % G)
@@ -366,8 +374,15 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         for (int i = 0; i < EV; ++i) sq[r * D + ch * EV + i] = c2 * x[i];
     }
     float m[4], l[4], acc[4][4 * NJ];
+    [[maybe_unused]] int doc[MOD ? 4 : 1];
+    [[maybe_unused]] float slope[MOD ? 4 : 1];  // times log2(e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if constexpr (MOD) {
+            const int r = 4 * ty + i;
+            doc[i] = mod.doc && r < nr ? mod.doc[blk.row0 + r / G] : 0;
+            slope[i] = mod.slopes && r < nr ? mod.slopes[hk * G + r % G] * kPagedLog2E : 0.f;
+        }
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -404,7 +419,12 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int key = blk.range.slot(v0 + tx + 16 * x);
-                const bool seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
+                bool seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
+                if constexpr (MOD) {
+                    seen = (seen || key < blk.range.pre) && key >= doc[i] && pos >= 0;
+                    if (mod.cap2 > 0.f) s[i][x] = mod.cap2 * tanhf(s[i][x]);
+                    if (mod.slopes) s[i][x] = fmaf(-slope[i], fabsf((float)(pos - key)), s[i][x]);
+                }
                 if (!seen) s[i][x] = -INFINITY;
                 top = fmaxf(top, s[i][x]);
             }
@@ -473,7 +493,8 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
             }
         } else if (r < nr) {
             const float inv = 1.f / l[i];            // (0 / 0 where every score is -inf: NaN, as softmax has it)
-            const bool none = blk.pos0 + r / G < 0;  // sees nothing: zero, though 0 times a value may be NaN
+            bool none = blk.pos0 + r / G < 0;  // sees nothing: zero, though 0 times a value may be NaN
+            if constexpr (MOD) none = paged_blind(blk.pos0 + r / G, doc[i], blk.range.pre);
             T *op = O + (blk.row0 + r / G) * row_stride + (size_t)(hk * G + r % G) * D;
             if (!YOCO_DCHECK(blk.row0 + r / G < rows && hk * G + r % G < Hq, 0x65)) continue;
 #pragma unroll
@@ -491,19 +512,22 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 // nothing does not launch thousands of blocks to find that out.
 constexpr int kMergeCols = 8, kMergePieces = 4, kMergeBlocks = 12;
 
-template <typename T, int D, int R>
+template <typename T, int D, int R, bool MOD>
 __global__ void __launch_bounds__(R)
 paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const PagedPlan *__restrict__ plan,
-                        const PagedEntry *__restrict__ cuts, int rows, int Hq, int Hkv, int sets) {
+                        const typename PagedKind<MOD>::Entry *__restrict__ cuts, const PagedMod mod, int rows, int Hq,
+                        int Hkv, int sets) {
     const int r = threadIdx.x, G = Hq / Hkv, TS = R / G;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // (the first part's row block and how many there are, in one latency)
     int row0, nrow, pos0, pieces, slot, stride;
+    [[maybe_unused]] int pre = 0;
     auto look_up = [&](int64_t w) {
         const int *c = reinterpret_cast<const int *>(cuts + w / (D / kMergeCols) / sets / Hkv);
         row0 = paged_ld(c + 1), nrow = paged_ld(c + 2), pos0 = paged_ld(c + 3), pieces = paged_ld(c + 6);
         slot = paged_ld(c + 7), stride = paged_ld(c + 8);
+        if constexpr (MOD) pre = paged_ld(c + (offsetof(PagedEntryMod, range) + offsetof(PagedRangeMod, pre)) / 4);
     };
     int64_t w = blockIdx.x;
     look_up(w);
@@ -551,7 +575,9 @@ paged_merge_rows_kernel(const float *__restrict__ part, T *__restrict__ O, const
             }
         }
         // a row that sees nothing: zero; one whose scores are all -inf: 0 / 0, NaN as softmax has it
-        const float inv = pos0 + tok < 0 ? 0.f : 1.f / L;
+        bool none = pos0 + tok < 0;
+        if constexpr (MOD) none = paged_blind(pos0 + tok, mod.doc ? mod.doc[row0 + tok] : 0, pre);
+        const float inv = none ? 0.f : 1.f / L;
         T *op = O + (size_t)(row0 + tok) * Hq * D + (size_t)(hk * G + r % G) * D + d0;
         if (!YOCO_DCHECK(row0 + tok < rows, 0x66)) continue;
 #pragma unroll
@@ -616,9 +642,11 @@ static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &
     size_t at = kPagedHead;
     g.plan = ws + kPagedPlanAt;
     g.entries = ws + at;
-    at += align256((size_t)g.cap * sizeof(PagedEntry));
+    at += align256((size_t)g.cap * sizeof(PagedEntryMod));  // (one size for the plain and the scored calls)
     g.cuts = ws + at;
-    at += align256((size_t)(split / 2) * sizeof(PagedEntry));
+    at += align256((size_t)(split / 2) * sizeof(PagedEntryMod));
+    g.doc_lo = (int *)(ws + at);
+    at += align256((size_t)g.cap * sizeof(int));
     g.part = (float *)(ws + at);
     return at + (size_t)split * c->Hkv * (tc ? 256 : kPreRows) * (c->d + 2) * sizeof(float);
 }
@@ -642,19 +670,30 @@ static void pdl_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 
     cfg.numAttrs = 1;
 }
 
-template <typename T, int D, int NQ>
+template <typename T, int D, int NQ, bool MOD>
 static cudaError_t decode_simt(const PagedArgs &a, const PagedView &pv, PagedCut *cuts, float *part, int blocks,
                                cudaStream_t st) {
     const size_t smem = ((size_t)pv.B + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D, NQ>,
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt_kernel<T, D, NQ, MOD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (kPagedMaxB + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     pdl_config(cfg, attr, dim3(blocks), kDecThreads, smem, st);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_decode_simt_kernel<T, D, NQ>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
-                              (const T *)a.cache->v, part, cuts, a.Hq, pv, a.scale * kPagedLog2e, a.err);
+    const PagedMod mod = paged_mod(a);
+    return cudaLaunchKernelEx(&cfg, paged_decode_simt_kernel<T, D, NQ, MOD>, (const T *)a.Q, (T *)a.O,
+                              (const T *)a.cache->k, (const T *)a.cache->v, part, cuts, a.Hq, pv, mod, mod.qk, a.err);
+}
+
+template <typename T, int D, bool MOD>
+static cudaError_t decode_heads(const PagedArgs &a, const PagedView &pv, PagedCut *cuts, float *part, int blocks,
+                                cudaStream_t st) {
+    const int G = a.Hq / pv.Hkv;
+    return G <= 1   ? decode_simt<T, D, 1, MOD>(a, pv, cuts, part, blocks, st)
+           : G <= 2 ? decode_simt<T, D, 2, MOD>(a, pv, cuts, part, blocks, st)
+           : G <= 4 ? decode_simt<T, D, 4, MOD>(a, pv, cuts, part, blocks, st)
+                    : decode_simt<T, D, kDecQ, MOD>(a, pv, cuts, part, blocks, st);
 }
 
 template <typename T, int D>
@@ -667,10 +706,8 @@ static cudaError_t decode(const PagedArgs &a, cudaStream_t st) {
     if constexpr (sizeof(T) == 2 && D == 128)
         e = paged_decode_tc(a, cuts, part, blocks, st);
     else
-        e = G <= 1   ? decode_simt<T, D, 1>(a, pv, cuts, part, blocks, st)
-            : G <= 2 ? decode_simt<T, D, 2>(a, pv, cuts, part, blocks, st)
-            : G <= 4 ? decode_simt<T, D, 4>(a, pv, cuts, part, blocks, st)
-                     : decode_simt<T, D, kDecQ>(a, pv, cuts, part, blocks, st);
+        e = a.scores ? decode_heads<T, D, true>(a, pv, cuts, part, blocks, st)
+                     : decode_heads<T, D, false>(a, pv, cuts, part, blocks, st);
     if (e != cudaSuccess || blocks < 2) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
@@ -679,9 +716,9 @@ static cudaError_t decode(const PagedArgs &a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, (const float *)part, (const PagedCut *)cuts, (T *)a.O, G);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MOD>
 static cudaError_t prefill_simt(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(paged_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_simt_kernel<T, D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)pre_smem<D>());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
@@ -690,13 +727,15 @@ static cudaError_t prefill_simt(const PagedArgs &a, const PagedGrid &g, cudaStre
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     pdl_config(cfg, attr, dim3((unsigned)blocks), kPreThreads, pre_smem<D>(), st);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_prefill_simt_kernel<T, D>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
-                              (const T *)a.cache->v, g.part, (const PagedPlan *)g.plan, (const PagedEntry *)g.entries,
-                              a.rows, a.Hq, paged_view(a), a.scale * kPagedLog2e, a.err);
+    const PagedMod mod = paged_mod(a);
+    return cudaLaunchKernelEx(&cfg, paged_prefill_simt_kernel<T, D, MOD>, (const T *)a.Q, (T *)a.O, (const T *)a.cache->k,
+                              (const T *)a.cache->v, g.part, (const PagedPlan *)g.plan,
+                              (const typename PagedKind<MOD>::Entry *)g.entries, a.rows, a.Hq, paged_view(a), mod, mod.qk,
+                              a.err);
 }
 
-template <typename T, int D>
-static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
+template <typename T, int D, bool MOD>
+static cudaError_t prefill_call(const PagedArgs &a, cudaStream_t st) {
     constexpr bool tc = sizeof(T) == 2 && D == 128;
     constexpr int R = tc ? 128 : kPreRows, sets = tc ? 2 : 1;
     PagedGrid g{};
@@ -704,15 +743,20 @@ static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
     cudaError_t e = paged_plan(a, g, st);
     if (e != cudaSuccess) return e;
     if constexpr (tc) e = paged_prefill_tc(a, g, st);
-    else e = prefill_simt<T, D>(a, g, st);
+    else e = prefill_simt<T, D, MOD>(a, g, st);
     const int64_t cut = g.max_split / a.cache->Hkv / 2;  // what is cut has two pieces or more
     if (e != cudaSuccess || cut == 0) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     pdl_config(cfg, attr, dim3((unsigned)std::min<int64_t>(cut * a.cache->Hkv * sets * (D / kMergeCols), kMergeBlocks * g.slots)), R, 0, st);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R>, (const float *)g.part, (T *)a.O,
-                              (const PagedPlan *)g.plan, (const PagedEntry *)g.cuts, a.rows, a.Hq, a.cache->Hkv, sets);
+    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, D, R, MOD>, (const float *)g.part, (T *)a.O,
+                              (const PagedPlan *)g.plan, (const typename PagedKind<MOD>::Entry *)g.cuts, paged_mod(a), a.rows,
+                              a.Hq, a.cache->Hkv, sets);
+}
+
+template <typename T, int D> static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
+    return a.scores ? prefill_call<T, D, true>(a, st) : prefill_call<T, D, false>(a, st);
 }
 
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st) {

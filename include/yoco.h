@@ -333,6 +333,55 @@ YOCO_API size_t yoco_gret_qkvg_workspace_size(int B, int N, int H, int d, float 
 YOCO_API yoco_status yoco_rope_apply(void *x, int B, int N, int H, int d, int64_t pos0, float base, yoco_dtype dt,
                                      void *stream);
 
+/*
+ * Rotary encoding in the forms that models outside the paper use, for rows at any positions:
+ *   rotary_dim  channels r of each head that turn, from its first; a multiple of 16,
+ *               0: the whole head.  The others are copied.
+ *   layout      YOCO_ROPE_PAIRS: pair i is channels (2i, 2i+1);
+ *               YOCO_ROPE_HALVES: channels (i, i + r/2)
+ *   scaling     of the frequencies theta_i = base^(-2i/r), i < r/2, for contexts that are longer
+ *               than the trained one:
+ *       YOCO_ROPE_UNSCALED  theta_i (factor, original, low and high are not looked at)
+ *       YOCO_ROPE_LINEAR    theta_i / factor (position interpolation)
+ *       YOCO_ROPE_NTK       those of base * factor^(r / (r - 2))
+ *       YOCO_ROPE_BY_PARTS  theta_i (w + (1 - w) / factor), w = min(1, max(0, (n_i - low) /
+ *                           (high - low))), n_i = original theta_i / 2 pi the turns of pair i over
+ *                           the original length ("NTK-by-parts", arXiv:2309.00071 Section 3.2)
+ *   factor      finite, >= 1;   original > 0, low < high, all finite
+ *   magnitude   > 0, finite: the turned channels are multiplied by it (1: not)
+ * Pair (x0, x1) of a row at position p becomes magnitude (x0 cos a - x1 sin a, x0 sin a + x1 cos a)
+ * with a = p theta_i, which is kept modulo one turn to 2^-32 turns whatever the position; rounded
+ * once.
+ */
+#define YOCO_ROPE_PAIRS 0
+#define YOCO_ROPE_HALVES 1
+#define YOCO_ROPE_UNSCALED 0
+#define YOCO_ROPE_LINEAR 1
+#define YOCO_ROPE_NTK 2
+#define YOCO_ROPE_BY_PARTS 3
+typedef struct {
+    int32_t rotary_dim;
+    int32_t layout;
+    int32_t scaling;
+    float base;       /* finite, > 1 */
+    float factor;
+    float original;
+    float low, high;
+    float magnitude;
+} yoco_rope;
+
+/*
+ * x [rows, H, d] with the given strides, in elements, between rows and between heads (channels
+ * adjacent) to out [rows, H, d] with strides of its own: for instance q and k, as Hq + Hkv heads,
+ * out of a fused projection.  Row i is at positions[i] (device int32 [rows], any value), or at
+ * pos0 + i where positions is NULL (pos0 is not looked at otherwise); |pos0| + rows <= 2^31.
+ * out may be x itself with the same strides, and must not overlap it otherwise.
+ *   d in {64, 128}; pointers and strides multiples of 16 bytes; rows * H < 2^31.
+ */
+YOCO_API yoco_status yoco_rope_apply_scaled(const void *x, int64_t x_row, int64_t x_head, void *out, int64_t out_row,
+                                            int64_t out_head, int rows, int H, int d, const int32_t *positions,
+                                            int64_t pos0, const yoco_rope *rope, yoco_dtype dt, void *stream);
+
 /* ------------------------------------------- sliding-window self-decoder */
 
 /*
@@ -390,7 +439,7 @@ YOCO_API size_t yoco_swa_workspace_size(int B, int Hq, const yoco_swa_ring *ring
  *               anything.  Two sequences may name the same page (a shared
  *               prefix) as long as neither appends to it.
  *   seq_lens    device int32 [B]: each sequence's length, the call's own new
- *               rows included.  No call changes it.
+ *               rows included.  No call but yoco_paged_resize and yoco_paged_fork changes it.
  *   page_size   a power of two in [16, 1024]; max_pages * page_size <= 2^30
  *   rope_base   0, or > 1: yoco_paged_append turns k and q.  The attention
  *               calls take queries as they are (a query turned at its append is
@@ -480,6 +529,109 @@ YOCO_API yoco_status yoco_paged_attn_decode(const void *Q, int Hq, const yoco_pa
 
 /* Workspace bytes for any paged call with up to `rows` rows (0 for a cache or head count the calls refuse). */
 YOCO_API size_t yoco_paged_attn_workspace_size(int Hq, int rows, const yoco_paged_kv *cache);
+
+/*
+ * yoco_paged_append with the rotation that `rope` describes in place of the cache's rope_base,
+ * which has to be 0.
+ */
+YOCO_API yoco_status yoco_paged_append_rope(const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                                            int64_t v_head, const void *q, int64_t q_row, int64_t q_head, void *q_out,
+                                            int Hq, const int32_t *cu_rows, int rows, const yoco_paged_kv *cache,
+                                            const yoco_rope *rope, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Scores other than scale q.k, and masks other than causal ones:
+ *   softcap    0: none.  > 0: the score is softcap * tanh(scale q.k / softcap)
+ *   slopes     device fp32 [Hq], finite, or NULL: slopes[h] * |p - m| is then taken off the score
+ *              (after the cap) of the row at position p for slot m
+ *   prefix     device int32 [B], or NULL: slots m < prefix[b] of sequence b are seen by all its
+ *              rows, those before them too, whatever the window (values below 0 count as 0, and
+ *              the sequence's end bounds them)
+ *   doc_first  device int32 [rows] ([B] for the decode), or NULL: the row sees only slots
+ *              m >= doc_first[row], its document's first (values below 0 count as 0)
+ * So the row at position p >= 0 sees m < seq_lens[b] when
+ *     m >= doc_first[row]  and  ( m < prefix[b]  or
+ *                                 m <= p and (window == 0 or p - window < m or m < sinks) ).
+ * The values are read on the device when the call runs.
+ */
+typedef struct {
+    float softcap;
+    const float *slopes;
+    const int32_t *prefix;
+    const int32_t *doc_first;
+} yoco_paged_scores;
+
+/*
+ * yoco_paged_attn_prefill and yoco_paged_attn_decode with such scores (and the same workspace).
+ * Rows that see nothing (a negative position, or a doc_first past all that they would see) come out
+ * as zeros.  What the plain calls say of NaN and infinite scores holds for the scores after cap and
+ * bias; the cap makes infinite products finite.  Slots before every document of a sequence's rows
+ * and past every row (and prefix) may hold anything; between them each page in the table is read,
+ * and values there that are not finite may make rows NaN that do not see them.
+ *   softcap    finite, >= 0, and where it is not 0: softcap and scale / softcap within
+ *              [2^-64, 2^64]
+ */
+YOCO_API yoco_status yoco_paged_attn_prefill_scored(const void *Q, int Hq, const int32_t *cu_rows, int rows,
+                                                    const yoco_paged_kv *cache, const yoco_paged_scores *scores,
+                                                    float scale, int window, int sinks, void *O, void *workspace,
+                                                    size_t ws_bytes, void *stream);
+YOCO_API yoco_status yoco_paged_attn_decode_scored(const void *Q, int Hq, const yoco_paged_kv *cache,
+                                                   const yoco_paged_scores *scores, float scale, int window, int sinks,
+                                                   void *O, void *workspace, size_t ws_bytes, void *stream);
+
+/* --------------------------------------------- the pages of a paged cache */
+
+/*
+ * Handing out the pages of a yoco_paged_kv, on the device and in the stream's order:
+ *   refs   device int32 [num_pages], the caller's: how many of the sequences' table entries name the
+ *          page (entries that hold a slot: the first ceil(seq_lens[b] / page_size) of sequence b).
+ *          0: the page is free.  A new pool: refs and seq_lens all 0.
+ * These calls, and no others, write the cache's page_table and seq_lens (the memory that these
+ * members of the struct point to has to be writable) and refs.  Nothing is read back and nothing
+ * waits, so they are captured like the rest; what they decide goes by the device's values alone and
+ * is the same every time.
+ *   workspace  >= yoco_paged_pool_workspace_size(cache) bytes, 256-byte aligned; calls that share it
+ *              are ordered on one stream.  Its status word (yoco_workspace_status) gets
+ *              YOCO_ERR_CAPACITY where pages ran out, and YOCO_ERR_INVALID_ARG for a length that the
+ *              table cannot hold, an entry outside the pool, a count of refs that is below what the
+ *              table says, or an index of a sequence that cannot be used.
+ *   moves      NULL, or a list of the page copies that the call made, device int32, 16-byte
+ *              aligned: {count, n, 0, 0}, then for each {from, to, slots, 0}: the first `slots` slots
+ *              of page `from` went to `to`, in k and v of `cache`.  Where other caches (layers) share
+ *              the table, yoco_paged_copy does the same there.
+ *
+ * yoco_paged_resize: sequence b gets length new_lens[b] (device int32 [B]; below 0: it stays as it
+ * is).
+ *   - Pages behind a shorter sequence's end go back (their entries become -1); 0 frees it all.
+ *   - Then a longer one gets the pages it lacks.  A page in which it will write its next slot and
+ *     that other sequences have as well (refs > 1) is replaced by a copy of the slots it holds; but
+ *     where every sequence that has the page grows in this call, the one of lowest index keeps it.
+ *   - New pages are the lowest free ones (those that this call gave back among them), handed out in
+ *     the order of the sequences and of their slots.
+ *   - If there are not enough, no sequence grows: none gets a page or a copy, and their lengths stay.
+ *   moves: up to B copies, 4 (B + 1) ints; n is the number of free pages after the call.
+ *
+ * yoco_paged_fork: sequence dst[i] becomes what sequence src[i] is, on the same pages (device int32
+ * [n], n <= B).  dst[i] has to be empty.  A pair is left out, and recorded, where an index is outside
+ * [0, B), dst[i] is not empty or named by an earlier pair, or src[i] is some pair's dst.
+ *
+ * yoco_paged_compact: the pages in use become pages 0 .. n - 1: the used pages from n on, in order,
+ * go to the free ones before n, in order, whole; the tables name the new ones.
+ *   moves: up to num_pages / 2 copies, 4 (num_pages / 2 + 1) ints; n is the number of pages in use.
+ *
+ * yoco_paged_copy: applies such a list to `cache` (pages from and to of one list must not overlap;
+ * `most`: copies there is room for in it; entries that name no page of the pool are left out).
+ */
+YOCO_API yoco_status yoco_paged_resize(const yoco_paged_kv *cache, int32_t *refs, const int32_t *new_lens,
+                                       int32_t *moves, void *workspace, size_t ws_bytes, void *stream);
+YOCO_API yoco_status yoco_paged_fork(const yoco_paged_kv *cache, int32_t *refs, const int32_t *src, const int32_t *dst,
+                                     int n, void *workspace, size_t ws_bytes, void *stream);
+YOCO_API yoco_status yoco_paged_compact(const yoco_paged_kv *cache, int32_t *refs, int32_t *moves, void *workspace,
+                                        size_t ws_bytes, void *stream);
+YOCO_API yoco_status yoco_paged_copy(const yoco_paged_kv *cache, const int32_t *moves, int most, void *stream);
+
+/* Workspace bytes for the calls above (0 for a cache that they refuse). */
+YOCO_API size_t yoco_paged_pool_workspace_size(const yoco_paged_kv *cache);
 
 /* ------------------------------------------------------------ utilities */
 
