@@ -3,16 +3,23 @@
 //
 // refs[p] is how many table entries name page p; the free pages are those with 0.  Which pages a
 // call hands out goes by their numbers alone (the lowest free ones, in the order of the sequences
-// and slots), so nothing depends on the order of threads.  With chunks of kPoolChunk pages counted
-// first, a page's rank among the free (or used) ones is what lies in the chunks before its own
-// plus its rank in the chunk; entry number r of those that are wanted is found in the prefix sums
-// of what the sequences need.
+// and slots), so nothing depends on the order of threads: each warp of a cluster counts the free
+// (or used) pages of a run of its own, and a page's rank is what lies in the runs before plus its
+// rank in the run; number r of those that are wanted is found in the prefix sums of what the
+// sequences need.
+//
+// A resize and a compact are one cluster of eight blocks, its phases divided by cluster barriers,
+// and one grid that copies: these calls are latencies one after the other, and a launch for each
+// phase cost more than what eight SMs lack in bandwidth (a search round of 8 x 4 sequences, two
+// resizes and a fork, 38 -> 27 us; a serving round of two resizes of 1024 sequences over 200000
+// pages 44 -> 38; with two blocks 64, with four 43).  A compact's grid copies at 6.9 TB/s (1.16 GB
+// moved: 168 us), the copy rate.
 //
 // A resize: 1. sequences that shrink give pages back; 2. one block decides, per growing sequence,
-// whether the page it writes next has to be copied, and sums up what is needed; 3. free pages are
-// counted; 4. handed out; 5. copies are made.  Of the sequences that share a page and all grow the
-// first keeps it: each takes its count off refs; where that leaves 0, all of them grow, and the
-// least b - B, written to refs itself, says which is first.
+// whether the page it writes next has to be copied, and sums up what is needed, while the others
+// count free pages; 3. pages are handed out; 4. the second grid copies.  Of the sequences that
+// share a page and all grow the first keeps it: a table in shared memory, keyed by the page, has
+// how many they are and which is first.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,24 +28,25 @@
 
 namespace yoco {
 
-constexpr int kPoolChunk = 4096;      // pages counted by a block
 constexpr int kPoolThreads = 256;
-constexpr int kPoolEach = kPoolChunk / kPoolThreads;
-constexpr int kShareThreads = 1024;   // the deciding block
-constexpr int kShareEach = kPagedMaxB / kShareThreads;
+constexpr int kClusterBlocks = 8, kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterBlocks * kClusterThreads / 32;
+constexpr int kShareEach = kPagedMaxB / kClusterThreads;
+constexpr int kPoolUnroll = 4, kPoolStep = kPoolUnroll * kClusterBlocks * kClusterThreads;  // table entries of a thread at a time
+constexpr int kShareSlots = 2 * kPagedMaxB;  // of the table of shared pages
 
 struct PoolView {
     int32_t *table, *lens, *refs;
-    int32_t B, max_pages, num_pages, shift, chunks;
+    int32_t B, max_pages, num_pages, shift;
     int4 *moves;
     // scratch
-    int *start;   // [B + 1] pages needed by the sequences before b
-    int *first;   // [B] table entry that the first of them goes to
+    // pages needed by the sequences before b are start[b], the first of its own goes to table entry
+    // first[b] (both in every block's shared memory)
     int *old;     // [B] page that it copies, or -1
     int *fill;    // [B] slots of it in use
     int *copies;  // [B + 1] copies made by the sequences before b
-    int *count;   // [chunks] free (used) pages
-    int *rank;    // [num_pages] of a page that moves, among those
+    int *rank;    // [num_pages] a compact's: of a page that moves, among those; a resize's: the pages
+                  // that are handed out, in order
     int *err;
 };
 
@@ -69,20 +77,6 @@ __device__ __forceinline__ int pool_page(const PoolView &v, int b, int e) {
     return -1;
 }
 
-__global__ void __launch_bounds__(kPoolThreads) pool_release_kernel(const PoolView v, const int32_t *new_lens) {
-    const int b = blockIdx.x;
-    int L, N;
-    pool_lens(v, new_lens, b, L, N, threadIdx.x == 0);
-    for (int e = pool_pages(v, N) + threadIdx.x, e1 = pool_pages(v, L); e < e1; e += kPoolThreads) {
-        const int p = pool_page(v, b, e);
-        v.table[(size_t)b * v.max_pages + e] = -1;
-        if (p >= 0 && atomicSub(v.refs + p, 1) <= 0) {  // more entries name it than it was counted
-            atomicAdd(v.refs + p, 1);
-            paged_report(v.err, kErrPagedRefs);
-        }
-    }
-}
-
 // exclusive prefix sums of x over the block's threads; `sums` one per warp; total: of all
 template <int THREADS, typename N> __device__ __forceinline__ N pool_scan(N x, N *sums, N &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -104,146 +98,283 @@ template <int THREADS, typename N> __device__ __forceinline__ N pool_scan(N x, N
     return before + inc - x;
 }
 
-__global__ void __launch_bounds__(kShareThreads) pool_share_kernel(const PoolView v, const int32_t *new_lens) {
-    __shared__ long long sums[kShareThreads / 32];  // (what all sequences ask for may pass 32 bits)
-    const int each = (v.B + kShareThreads - 1) / kShareThreads, b0 = threadIdx.x * each;
-    int page[kShareEach], need[kShareEach], at[kShareEach], fill[kShareEach];
-    bool copy[kShareEach], last[kShareEach];  // last: all who have the page grow
-#pragma unroll
-    for (int k = 0; k < kShareEach; ++k) {
-        page[k] = -1;
-        need[k] = at[k] = fill[k] = 0;
-        copy[k] = false;
-        if (k >= each || b0 + k >= v.B) continue;
-        int L, N;
-        pool_lens(v, new_lens, b0 + k, L, N, false);
-        if (N <= L) continue;
-        at[k] = pool_pages(v, L);
-        need[k] = pool_pages(v, N) - at[k];
-        fill[k] = L & ((1 << v.shift) - 1);
-        if (fill[k] == 0) continue;
-        page[k] = pool_page(v, b0 + k, at[k] - 1);
-        if (page[k] >= 0) copy[k] = __ldcg(v.refs + page[k]) > 1;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// x into the same place of block `rank`'s shared memory
+__device__ __forceinline__ void cluster_put(int *at, int rank, int x) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
+    asm volatile("st.shared::cluster.s32 [%0], %1;\n" ::"r"(to), "r"(x) : "memory");
+}
+
+struct PoolSmem {
+    long long sums[kClusterThreads / 32];
+    int before[kPagedMaxB + 1];  // entries that go back of the sequences before b
+    int from[kPagedMaxB];        // first of them in the table
+    int count[kClusterWarps];    // free (used) pages of each warp's run
+    int start[kPagedMaxB + 1];   // as in PoolView
+    int first[kPagedMaxB];
+};
+struct PoolShared {  // the deciding block's table of shared pages
+    int page[kShareSlots], grow[kShareSlots], first[kShareSlots];
+};
+constexpr size_t kResizeSmem = sizeof(PoolSmem) + sizeof(PoolShared);
+
+// the place of `page` in the table, taken if it is not there yet (at most half of the table is)
+__device__ __forceinline__ int pool_slot(PoolShared &t, int page) {
+    int at = (int)((unsigned)page * 2654435761u >> 19) & (kShareSlots - 1);
+    for (;;) {
+        const int was = atomicCAS(&t.page[at], -1, page);
+        if (was == -1 || was == page) return at;
+        at = (at + 1) & (kShareSlots - 1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kShareEach; ++k)
-        if (copy[k]) atomicSub(v.refs + page[k], 1);
-    __threadfence();
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kShareEach; ++k) {
-        const int left = copy[k] ? __ldcg(v.refs + page[k]) : 1;
-        last[k] = left <= 0;
-        if (left < 0) paged_report(v.err, kErrPagedRefs);
+}
+
+// b with before[b] <= i < before[b + 1]
+__device__ __forceinline__ int pool_owner(const int *before, int B, int i) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= i) lo = mid;
+        else hi = mid;
     }
-    __syncthreads();
+    return lo;
+}
+
+// A warp's run of pages: [p0, p1), the same for every pass; `w` of `warps`
+__device__ __forceinline__ void pool_run(const PoolView &v, int w, int warps, int &p0, int &p1) {
+    const int per = ((v.num_pages + warps - 1) / warps + 31) / 32 * 32;
+    p0 = (int)min((long long)w * per, (long long)v.num_pages);
+    p1 = (int)min((long long)p0 + per, (long long)v.num_pages);
+}
+
+// how many pages of a run are used (or free), eight loads of a lane in flight
+template <bool USED> __device__ __forceinline__ int pool_count(const PoolView &v, int p0, int p1) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int p = p0 + lane; p < p1; p += 256) {
+        int r[8];
 #pragma unroll
-    for (int k = 0; k < kShareEach; ++k)
-        if (last[k]) atomicMin(v.refs + page[k], b0 + k - v.B);
-    __threadfence();
-    __syncthreads();
+        for (int k = 0; k < 8; ++k) r[k] = p + 32 * k < p1 ? __ldcg(v.refs + p + 32 * k) : (USED ? 0 : 1);
 #pragma unroll
-    for (int k = 0; k < kShareEach; ++k)
-        if (last[k] && __ldcg(v.refs + page[k]) == b0 + k - v.B) copy[k] = false;
+        for (int k = 0; k < 8; ++k) n += (r[k] > 0) == USED;
+    }
+    return __reduce_add_sync(0xffffffffu, n);
+}
+
+// counts of the runs before run w (w may be their number), and of all; all threads of the block
+__device__ __forceinline__ void pool_before(PoolSmem &sm, int w, int warps, int &before, int &all) {
+    const int tid = threadIdx.x;
+    int total;
+    const int mine = tid < warps ? sm.count[tid] : 0;
+    const int at = pool_scan<kClusterThreads>(mine, reinterpret_cast<int *>(sm.sums), total);
+    sm.from[tid] = at;
     __syncthreads();
-    long long sum = 0, made = 0;
+    before = w < warps ? sm.from[w] : total;
+    all = total;
+    __syncthreads();
+}
+
+// a warp's count, told to every block
+__device__ __forceinline__ void pool_tell(PoolSmem &sm, int w, int count) {
+    if ((threadIdx.x & 31) < kClusterBlocks) cluster_put(&sm.count[w], threadIdx.x & 31, count);
+}
+
+// Of the sequences that grow: what they need and which pages have to be copied, into v's scratch and
+// every block's start and first; one block.  page[k]: the page that holds the last slot of its sequence b0 + k, where that is not full.
+__device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kShareEach], const int (&N)[kShareEach],
+                                           const int (&page)[kShareEach], int each, PoolSmem &sm, PoolShared &t) {
+    const int b0 = threadIdx.x * each;
+    int refs[kShareEach], slot[kShareEach];
+    bool any = false;
 #pragma unroll
     for (int k = 0; k < kShareEach; ++k) {
-        if (last[k] && !copy[k]) v.refs[page[k]] = 1;
-        if (copy[k]) {
-            ++need[k];
-            --at[k];
+        refs[k] = page[k] >= 0 ? __ldcg(v.refs + page[k]) : 0;
+        slot[k] = -1;
+        any |= refs[k] > 1;
+    }
+    if (__syncthreads_or(any)) {
+        for (int i = threadIdx.x; i < kShareSlots; i += kClusterThreads) {
+            t.page[i] = -1;
+            t.grow[i] = 0;
+            t.first[i] = kPagedMaxB;
         }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kShareEach; ++k) {
+            if (refs[k] <= 1) continue;
+            slot[k] = pool_slot(t, page[k]);
+            atomicAdd(&t.grow[slot[k]], 1);
+            atomicMin(&t.first[slot[k]], b0 + k);
+        }
+        __syncthreads();
+    }
+    long long sum = 0, made = 0;  // (what all sequences ask for may pass 32 bits)
+    int need[kShareEach];
+    bool copy[kShareEach];
+#pragma unroll
+    for (int k = 0; k < kShareEach; ++k) {
+        copy[k] = slot[k] >= 0;
+        if (copy[k] && t.grow[slot[k]] > refs[k]) paged_report(v.err, kErrPagedRefs);
+        if (copy[k] && t.grow[slot[k]] >= refs[k] && t.first[slot[k]] == b0 + k) copy[k] = false;
+        if (copy[k]) atomicSub(v.refs + page[k], 1);
+        need[k] = N[k] > L[k] ? pool_pages(v, N[k]) - pool_pages(v, L[k]) + copy[k] : 0;
         sum += need[k];
         made += copy[k];
     }
     long long all, all_made;
-    long long before = pool_scan<kShareThreads>(sum, sums, all);
-    long long made_before = pool_scan<kShareThreads>(made, sums, all_made);
+    long long before = pool_scan<kClusterThreads>(sum, sm.sums, all);
+    long long made_before = pool_scan<kClusterThreads>(made, sm.sums, all_made);
     const long long top = 0x7fffffff;
 #pragma unroll
     for (int k = 0; k < kShareEach; ++k) {
         const int b = b0 + k;
         if (k >= each || b >= v.B) break;
-        v.start[b] = (int)min(before, top);
-        v.first[b] = at[k];
+#pragma unroll
+        for (int c = 0; c < kClusterBlocks; ++c) {
+            cluster_put(&sm.start[b], c, (int)min(before, top));
+            cluster_put(&sm.first[b], c, pool_pages(v, L[k]) - copy[k]);
+        }
         v.old[b] = copy[k] ? page[k] : -1;
-        v.fill[b] = fill[k];
+        v.fill[b] = L[k] & ((1 << v.shift) - 1);
         v.copies[b] = (int)made_before;
         before += need[k];
         made_before += copy[k];
     }
-    if (threadIdx.x == 0) {
-        v.start[v.B] = (int)min(all, top);
-        v.copies[v.B] = (int)all_made;
-    }
+    if (threadIdx.x < kClusterBlocks) cluster_put(&sm.start[v.B], threadIdx.x, (int)min(all, top));
+    if (threadIdx.x == 0) v.copies[v.B] = (int)all_made;
 }
 
-// pages of the chunk that are free (or used)
-template <bool USED> __global__ void __launch_bounds__(kPoolThreads) pool_count_kernel(const PoolView v) {
-    __shared__ int sums[kPoolThreads / 32];
-    int n = 0;
-    for (int k = 0; k < kPoolEach; ++k) {
-        const int p = blockIdx.x * kPoolChunk + k * kPoolThreads + threadIdx.x;
-        if (p < v.num_pages) n += (v.refs[p] > 0) == USED;
+__global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads)
+pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
+    extern __shared__ long long smem8[];
+    PoolSmem &sm = *reinterpret_cast<PoolSmem *>(smem8);
+    PoolShared &shared = *reinterpret_cast<PoolShared *>(&sm + 1);
+    const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x;
+    cluster_arrive();  // (waited for before another block's memory is written)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    // 1. entries behind the ends of shorter sequences, numbered over all of them
+    const int each = (v.B + kClusterThreads - 1) / kClusterThreads, b0 = tid * each;
+    int L[kShareEach], N[kShareEach], page[kShareEach];
+    long long mine = 0, drops;
+#pragma unroll
+    for (int k = 0; k < kShareEach; ++k) {
+        L[k] = N[k] = 0;
+        page[k] = -1;
+        if (k < each && b0 + k < v.B) pool_lens(v, new_lens, b0 + k, L[k], N[k], rank == 0);
     }
-    int all;
-    (void)pool_scan<kPoolThreads>(n, sums, all);
-    if (threadIdx.x == 0) v.count[blockIdx.x] = all;
-}
-
-// of all chunks, and of those before this block's
-__device__ __forceinline__ void pool_counts(const PoolView &v, int *sums, int chunk, int &before, int &all) {
-    int n = 0, m = 0;
-    for (int c = threadIdx.x; c < v.chunks; c += kPoolThreads) {
-        const int x = v.count[c];
-        n += x;
-        m += c < chunk ? x : 0;
+#pragma unroll
+    for (int k = 0; k < kShareEach; ++k) {
+        if (k >= each || b0 + k >= v.B) break;
+        sm.from[b0 + k] = pool_pages(v, N[k]);
+        sm.before[b0 + k] = max(0, pool_pages(v, L[k]) - pool_pages(v, N[k]));
+        mine += sm.before[b0 + k];
+        if (rank == 0 && N[k] > L[k] && (L[k] & ((1 << v.shift) - 1))) page[k] = pool_page(v, b0 + k, pool_pages(v, L[k]) - 1);
     }
-    (void)pool_scan<kPoolThreads>(n, sums, all);
-    (void)pool_scan<kPoolThreads>(m, sums, before);
-}
-
-__global__ void __launch_bounds__(kPoolThreads) pool_assign_kernel(const PoolView v, const int32_t *new_lens) {
-    __shared__ int sums[kPoolThreads / 32];
-    int before, all;
-    pool_counts(v, sums, blockIdx.x, before, all);
-    const int total = v.start[v.B];
+    long long run = pool_scan<kClusterThreads>(mine, sm.sums, drops);
+    cluster_wait();
+    if (drops > 0) {  // (the same for every block)
+#pragma unroll
+        for (int k = 0; k < kShareEach; ++k) {
+            if (k >= each || b0 + k >= v.B) break;
+            const int n = sm.before[b0 + k];
+            sm.before[b0 + k] = (int)min(run, 0x7fffffffll);
+            run += n;
+        }
+        __syncthreads();
+        // (each entry is held by a sequence; more than 2^31 of them are not in any memory)
+        const int top = (int)min(drops, 0x7fffffffll - kPoolStep);
+        for (int i0 = rank * kClusterThreads + tid; i0 < top; i0 += kPoolStep) {
+            int32_t *at[kPoolUnroll];
+            int p[kPoolUnroll], was[kPoolUnroll];
+#pragma unroll
+            for (int u = 0; u < kPoolUnroll; ++u) {
+                const int i = i0 + u * kClusterBlocks * kClusterThreads;
+                at[u] = nullptr;
+                if (i >= top) continue;
+                const int b = pool_owner(sm.before, v.B, i), e = sm.from[b] + i - sm.before[b];
+                if (YOCO_DCHECK(e < v.max_pages, 0x6B)) at[u] = v.table + (size_t)b * v.max_pages + e;
+            }
+#pragma unroll
+            for (int u = 0; u < kPoolUnroll; ++u) p[u] = at[u] ? *at[u] : -1;
+#pragma unroll
+            for (int u = 0; u < kPoolUnroll; ++u) {
+                was[u] = 1;
+                if (!at[u]) continue;
+                *at[u] = -1;
+                if ((unsigned)p[u] < (unsigned)v.num_pages) was[u] = atomicSub(v.refs + p[u], 1);
+                else paged_report(v.err, kErrPagedPage);
+            }
+#pragma unroll
+            for (int u = 0; u < kPoolUnroll; ++u) {
+                if (was[u] > 0) continue;  // (else more entries name it than it was counted)
+                atomicAdd(v.refs + p[u], 1);
+                paged_report(v.err, kErrPagedRefs);
+            }
+        }
+        cluster_sync();
+    }
+    // 2. the first block decides, the others count
+    const int warps = kClusterWarps - kClusterThreads / 32, w = (rank - 1) * (kClusterThreads / 32) + (tid >> 5);
+    int p0 = 0, p1 = 0;
+    if (rank == 0) {
+        pool_share(v, L, N, page, each, sm, shared);
+    } else {
+        pool_run(v, w, warps, p0, p1);
+        pool_tell(sm, w, pool_count<false>(v, p0, p1));
+    }
+    cluster_sync();
+    // 3. the free pages that are taken, in order
+    const int total = sm.start[v.B];
+    int r, all;
+    pool_before(sm, rank == 0 ? warps : w, warps, r, all);
     const bool room = total <= all;
-    if (blockIdx.x == 0) {
-        for (int b = threadIdx.x; b < v.B; b += kPoolThreads) {
-            int L, N;
-            pool_lens(v, new_lens, b, L, N, false);
-            if (N < L || (N > L && room)) v.lens[b] = N;
+    if (rank == 0) {
+#pragma unroll
+        for (int k = 0; k < kShareEach; ++k) {
+            const int b = b0 + k;
+            if (k >= each || b >= v.B) break;
+            if (N[k] < L[k] || (N[k] > L[k] && room)) v.lens[b] = N[k];
             if (!room && v.old[b] >= 0) atomicAdd(v.refs + v.old[b], 1);
         }
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             v.moves[0] = make_int4(room ? v.copies[v.B] : 0, room ? all - total : all, 0, 0);
             if (!room) paged_report(v.err, kErrPagedRoom);
         }
     }
-    if (!room || before >= total) return;
-    // each thread's pages side by side, so that ranks go by page number
-    const int p0 = blockIdx.x * kPoolChunk + threadIdx.x * kPoolEach;
-    unsigned free = 0;
-    for (int k = 0; k < kPoolEach; ++k)
-        if (p0 + k < v.num_pages && v.refs[p0 + k] <= 0) free |= 1u << k;
-    int in_chunk;
-    int r = before + pool_scan<kPoolThreads>(__popc(free), sums, in_chunk);
-    for (; free && r < total; free &= free - 1, ++r) {
-        const int p = p0 + __ffs(free) - 1;
-        int lo = 0, hi = v.B;  // the sequence: start[lo] <= r < start[lo + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (v.start[mid] <= r) lo = mid;
-            else hi = mid;
+    if (!room || total == 0) return;
+    for (int q = p0 + lane; q - lane < p1 && r < total; q += 256) {
+        int refs[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool free = refs[k] <= 0;
+            const unsigned who = __ballot_sync(0xffffffffu, free);
+            const int i = r + __popc(who & ((1u << lane) - 1));
+            r += __popc(who);
+            if (free && i < total) {
+                v.rank[i] = q + 32 * k;
+                v.refs[q + 32 * k] = 1;
+            }
         }
-        const int idx = r - v.start[lo], e = v.first[lo] + idx;
-        if (!YOCO_DCHECK(lo < v.B && e < v.max_pages, 0x6B)) continue;
-        v.table[(size_t)lo * v.max_pages + e] = p;
-        v.refs[p] = 1;
-        if (idx == 0 && v.old[lo] >= 0) v.moves[1 + v.copies[lo]] = make_int4(v.old[lo], p, v.fill[lo], 0);
+    }
+    cluster_sync();
+    // 4. to whom they go
+#pragma unroll 4
+    for (int i = rank * kClusterThreads + tid; i < total; i += kClusterBlocks * kClusterThreads) {
+        const int p = __ldcg(v.rank + i);
+        const int b = pool_owner(sm.start, v.B, i), idx = i - sm.start[b], e = sm.first[b] + idx;
+        if (!YOCO_DCHECK(b < v.B && e < v.max_pages, 0x6B)) continue;
+        v.table[(size_t)b * v.max_pages + e] = p;
+        if (idx == 0) {
+            const int old = __ldcg(v.old + b);
+            if (old >= 0) v.moves[1 + __ldcg(v.copies + b)] = make_int4(old, p, __ldcg(v.fill + b), 0);
+        }
     }
 }
 
@@ -284,68 +415,92 @@ pool_fork_kernel(const PoolView v, const int32_t *src, const int32_t *dst, int n
 }
 
 // who moves where
-__global__ void __launch_bounds__(kPoolThreads) pool_moves_kernel(const PoolView v) {
-    __shared__ int sums[kPoolThreads / 32];
-    int before, live;
-    pool_counts(v, sums, blockIdx.x, before, live);
-    // used pages below page `live`: those of the chunks before its own, and a part of that one
-    int in_front = 0, all;
+__global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads) pool_moves_kernel(const PoolView v) {
+    extern __shared__ long long smem8[];
+    PoolSmem &sm = *reinterpret_cast<PoolSmem *>(smem8);
+    const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x;
+    cluster_arrive();  // (waited for before another block's memory is written)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int w = rank * (kClusterThreads / 32) + (tid >> 5);
+    int p0, p1;
+    pool_run(v, w, kClusterWarps, p0, p1);
+    const int count = pool_count<true>(v, p0, p1);
+    cluster_wait();
+    pool_tell(sm, w, count);
+    cluster_sync();
+    int at, live;
+    pool_before(sm, w, kClusterWarps, at, live);
+    // used pages below page `live`: those of the runs before its own, and a part of that one
+    int in_front, edge0, edge1;
     {
-        const int edge = live / kPoolChunk;  // (past the last chunk where every page is used)
+        int e = 0;
+        pool_run(v, 0, kClusterWarps, edge0, edge1);
+        if (edge1 > 0) e = min(live / edge1, kClusterWarps);  // (runs are as long as the first one)
+        int before, all;
+        pool_before(sm, e, kClusterWarps, before, all);
         int n = 0;
-        for (int c = threadIdx.x; c < min(edge, v.chunks); c += kPoolThreads) n += v.count[c];
-        for (int p = edge * kPoolChunk + threadIdx.x; p < live; p += kPoolThreads) n += v.refs[p] > 0;
-        (void)pool_scan<kPoolThreads>(n, sums, in_front);
+        for (int p = e * edge1 + tid; p < live; p += kClusterThreads) n += __ldcg(v.refs + p) > 0;
+        in_front = before;
+        int part;
+        (void)pool_scan<kClusterThreads>(n, reinterpret_cast<int *>(sm.sums), part);
+        in_front += part;
     }
-    const int p0 = blockIdx.x * kPoolChunk + threadIdx.x * kPoolEach;
-    unsigned used = 0;
-    for (int k = 0; k < kPoolEach; ++k)
-        if (p0 + k < v.num_pages && v.refs[p0 + k] > 0) used |= 1u << k;
-    int at = before + pool_scan<kPoolThreads>(__popc(used), sums, all);  // used pages before p0
+    if (tid == 0 && rank == 0) v.moves[0] = make_int4(live - in_front, live, 0, 0);
+    if (live == in_front) return;
     int *moves = reinterpret_cast<int *>(v.moves + 1);
-    for (int k = 0; k < kPoolEach && p0 + k < v.num_pages; ++k) {
-        const int p = p0 + k;
-        const bool is = used >> k & 1;
-        if (is && p >= live) {
-            const int r = at - in_front;
-            if (!YOCO_DCHECK(r >= 0 && r < v.num_pages / 2, 0x6C)) continue;
-            v.rank[p] = r;
-            moves[4 * r] = p;
-            moves[4 * r + 2] = 1 << v.shift;
-            moves[4 * r + 3] = 0;
-        } else if (!is && p < live) {
-            moves[4 * (p - at) + 1] = p;
+    // (a run before page `live` has holes, one behind it pages that move)
+    for (int q = p0 + lane; q - lane < p1; q += 256) {
+        int refs[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int p = q + 32 * k;
+            const bool is = refs[k] > 0;
+            const unsigned who = __ballot_sync(0xffffffffu, is);
+            const int used = at + __popc(who & ((1u << lane) - 1));  // used pages before p
+            at += __popc(who);
+            if (p >= p1) continue;
+            if (is && p >= live) {
+                const int r = used - in_front;
+                if (!YOCO_DCHECK(r >= 0 && r < v.num_pages / 2, 0x6C)) continue;
+                v.rank[p] = r;
+                moves[4 * r] = p;
+                moves[4 * r + 2] = 1 << v.shift;
+                moves[4 * r + 3] = 0;
+            } else if (!is && p < live) {
+                moves[4 * (p - used) + 1] = p;
+            }
         }
-        at += is;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) v.moves[0] = make_int4(live - in_front, live, 0, 0);
 }
 
-// tables and counts follow the moves
-__global__ void __launch_bounds__(kPoolThreads) pool_follow_kernel(const PoolView v) {
-    const int4 head = v.moves[0];
+// tables and counts follow the moves; the blocks of the copying grid, before they copy
+__device__ __forceinline__ void pool_follow(const PoolView &v) {
+    const int4 head = __ldcg(v.moves);
     const int count = head.x, live = head.y;
     for (int i = blockIdx.x * kPoolThreads + threadIdx.x; i < count; i += gridDim.x * kPoolThreads) {
-        const int4 m = v.moves[1 + i];
+        const int4 m = __ldcg(v.moves + 1 + i);
         v.refs[m.y] = v.refs[m.x];
         v.refs[m.x] = 0;
     }
     for (int b = blockIdx.x; b < v.B; b += gridDim.x) {
-        const int L = v.lens[b];
+        const int L = paged_ld(v.lens + b);
         if (!pool_len_ok(v, L)) {
             if (threadIdx.x == 0) paged_report(v.err, kErrPagedLen);
             continue;
         }
         for (int e = threadIdx.x, held = pool_pages(v, L); e < held; e += kPoolThreads) {
             int32_t *at = v.table + (size_t)b * v.max_pages + e;
-            const int p = *at;
+            const int p = paged_ld(at);
             if (p < live && p >= 0) continue;
             if ((unsigned)p >= (unsigned)v.num_pages) {
                 paged_report(v.err, kErrPagedPage);
                 continue;
             }
-            const int r = v.rank[p];  // (of a page that was not counted as used: anything)
-            if ((unsigned)r < (unsigned)count && v.moves[1 + r].x == p) *at = v.moves[1 + r].y;
+            const int r = paged_ld(v.rank + p);  // (of a page that was not counted as used: anything)
+            const int4 m = (unsigned)r < (unsigned)count ? __ldcg(v.moves + 1 + r) : make_int4(-1, 0, 0, 0);
+            if (m.x == p) *at = m.y;
             else paged_report(v.err, kErrPagedRefs);
         }
     }
@@ -354,12 +509,16 @@ __global__ void __launch_bounds__(kPoolThreads) pool_follow_kernel(const PoolVie
 // The copies of a list: block by block a (move, k or v, kv head), whose slots lie side by side.
 constexpr int kCopyUnroll = 4;
 
+template <bool FOLLOW>
 __global__ void __launch_bounds__(kPoolThreads)
-pool_copy_kernel(uint4 *k, uint4 *v, const int4 *moves, int most, int Hkv, int num_pages, int shift, int row16) {
-    const int64_t items = (int64_t)min(max(moves[0].x, 0), most) * 2 * Hkv;
+pool_copy_kernel(uint4 *k, uint4 *v, const int4 *moves, int most, int Hkv, int num_pages, int shift, int row16,
+                 const PoolView view) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (the list, where the call made it)
+    if constexpr (FOLLOW) pool_follow(view);
+    const int64_t items = (int64_t)min(max(__ldcg(moves).x, 0), most) * 2 * Hkv;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int head = (int)(it % Hkv), which = (int)(it / Hkv) & 1;
-        const int4 m = moves[1 + it / (2 * Hkv)];
+        const int4 m = __ldcg(moves + 1 + it / (2 * Hkv));
         if ((unsigned)m.x >= (unsigned)num_pages || (unsigned)m.y >= (unsigned)num_pages || m.z < 0 || m.z > 1 << shift) continue;
         const int n = m.z * row16;
         const int64_t head16 = (int64_t)row16 << shift;
@@ -396,7 +555,6 @@ static size_t pool_view(const yoco_paged_kv *c, int32_t *refs, int32_t *moves, c
     v.max_pages = c->max_pages;
     v.num_pages = c->num_pages;
     while ((1 << v.shift) < c->page_size) ++v.shift;
-    v.chunks = (c->num_pages + kPoolChunk - 1) / kPoolChunk;
     v.err = (int *)ws;
     size_t at = 256;
     auto take = [&](size_t ints) {
@@ -404,12 +562,9 @@ static size_t pool_view(const yoco_paged_kv *c, int32_t *refs, int32_t *moves, c
         at += up256(ints * sizeof(int));
         return p;
     };
-    v.start = take((size_t)c->B + 1);
-    v.first = take(c->B);
     v.old = take(c->B);
     v.fill = take(c->B);
     v.copies = take((size_t)c->B + 1);
-    v.count = take(v.chunks);
     v.rank = take(c->num_pages);
     v.moves = (int4 *)take(4 * ((size_t)std::max(c->B, c->num_pages / 2) + 1));
     if (moves) v.moves = (int4 *)moves;
@@ -421,30 +576,40 @@ size_t paged_pool_workspace(const yoco_paged_kv *c) {
     return pool_view(c, nullptr, nullptr, nullptr, v);
 }
 
-static cudaError_t pool_copy(const yoco_paged_kv *c, const int4 *moves, int most, cudaStream_t st) {
+// `follow`: the call is a compact, its tables and counts are brought in line as well
+static cudaError_t pool_copy(const yoco_paged_kv *c, const int4 *moves, int most, const PoolView *follow, bool early,
+                             cudaStream_t st) {
     if (most <= 0) return cudaSuccess;
     int shift = 0;
     while ((1 << shift) < c->page_size) ++shift;
     const int64_t items = (int64_t)most * 2 * c->Hkv;
-    const int blocks = (int)std::min<int64_t>(items, (int64_t)device_sm_count() * 8);
     const int row16 = c->d * (c->dtype == YOCO_BF16 ? 2 : 4) / 16;
+    cudaLaunchConfig_t cfg = {};
+    // a resize copies little or nothing: a grid that starts fast
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, (int64_t)device_sm_count() * (early && !follow ? 2 : 8)));
+    cfg.blockDim = dim3(kPoolThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
     count_launches(1);
-    pool_copy_kernel<<<blocks, kPoolThreads, 0, st>>>((uint4 *)c->k, (uint4 *)c->v, moves, most, c->Hkv, c->num_pages, shift,
-                                                      row16);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, follow ? pool_copy_kernel<true> : pool_copy_kernel<false>, (uint4 *)c->k, (uint4 *)c->v,
+                              moves, most, c->Hkv, c->num_pages, shift, row16, follow ? *follow : PoolView{});
 }
 
 cudaError_t paged_resize(const yoco_paged_kv *c, int32_t *refs, const int32_t *new_lens, int32_t *moves, void *ws,
                          cudaStream_t st) {
     PoolView v;
     (void)pool_view(c, refs, moves, (char *)ws, v);
-    count_launches(4);
-    pool_release_kernel<<<v.B, kPoolThreads, 0, st>>>(v, new_lens);
-    pool_share_kernel<<<1, kShareThreads, 0, st>>>(v, new_lens);
-    pool_count_kernel<false><<<v.chunks, kPoolThreads, 0, st>>>(v);
-    pool_assign_kernel<<<v.chunks, kPoolThreads, 0, st>>>(v, new_lens);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : pool_copy(c, v.moves, c->B, st);
+    // the shared-memory opt-in is set on every launch (it belongs to the current device)
+    cudaError_t e = cudaFuncSetAttribute(pool_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kResizeSmem);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    pool_resize_kernel<<<kClusterBlocks, kClusterThreads, kResizeSmem, st>>>(v, new_lens);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : pool_copy(c, v.moves, c->B, nullptr, true, st);
 }
 
 cudaError_t paged_fork(const yoco_paged_kv *c, int32_t *refs, const int32_t *src, const int32_t *dst, int n, void *ws,
@@ -459,16 +624,16 @@ cudaError_t paged_fork(const yoco_paged_kv *c, int32_t *refs, const int32_t *src
 cudaError_t paged_compact(const yoco_paged_kv *c, int32_t *refs, int32_t *moves, void *ws, cudaStream_t st) {
     PoolView v;
     (void)pool_view(c, refs, moves, (char *)ws, v);
-    count_launches(3);
-    pool_count_kernel<true><<<v.chunks, kPoolThreads, 0, st>>>(v);
-    pool_moves_kernel<<<v.chunks, kPoolThreads, 0, st>>>(v);
-    pool_follow_kernel<<<std::max(v.B, 64), kPoolThreads, 0, st>>>(v);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : pool_copy(c, v.moves, c->num_pages / 2, st);
+    cudaError_t e = cudaFuncSetAttribute(pool_moves_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PoolSmem));
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    pool_moves_kernel<<<kClusterBlocks, kClusterThreads, sizeof(PoolSmem), st>>>(v);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : pool_copy(c, v.moves, c->num_pages / 2, &v, true, st);
 }
 
 cudaError_t paged_copy(const yoco_paged_kv *c, const int32_t *moves, int most, cudaStream_t st) {
-    return pool_copy(c, (const int4 *)moves, most, st);
+    return pool_copy(c, (const int4 *)moves, most, nullptr, false, st);
 }
 
 }  // namespace yoco_host
