@@ -131,6 +131,9 @@ struct PagedMod {
     const int32_t *doc;         // [rows], or nullptr
     float cap2;                 // cap log2(e); 0: no cap
     float qk;                   // what q.k is multiplied by: scale / cap with a cap, else scale log2(e)
+    // with a cap, for |q.k| <= quick: cap2 tanh(qk s) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6)
+    float a0, a1, a2, a3, quick;
+    float hidden;  // a product whose weight comes out as 0 that way
 };
 
 // As PagedRange: the slots that some row of a block sees lie in `dlo <= m < hi` and (m >= lo or
@@ -187,6 +190,8 @@ __device__ __forceinline__ float paged_cap(float u, float C) {
 }
 
 constexpr float kPagedLog2E = 1.4426950408889634f;
+// the tensor-core prefill's quick way (paged_prefill_tc.cu): how large scores and slopes may be, times log2(e)
+constexpr float kQuickSlack = 22.f, kQuickSlope = 44.f / 31.f;
 
 // ---------------------------------------------- chunks of rows (prefill)
 //

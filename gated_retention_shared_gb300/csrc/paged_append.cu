@@ -229,6 +229,21 @@ PagedMod paged_mod(const PagedArgs &a) {
     m.prefix = a.scores->prefix;
     m.doc = a.scores->doc_first;
     m.cap2 = cap * kPagedLog2E;
+    if (cap > 0.f) {
+        const double k = m.qk, c = m.cap2;
+        const double a[4] = {c * k * 0.999999456, -c * std::pow(k, 3) * 0.33326318, c * std::pow(k, 5) * 0.131902967,
+                             -c * std::pow(k, 7) * 0.0444022262};
+        m.a0 = (float)a[0];
+        m.a1 = (float)a[1];
+        m.a2 = (float)a[2];
+        m.a3 = (float)a[3];
+        m.quick = (float)std::min(0.5 / k, (double)kQuickSlack / (c * k));
+        m.hidden = (float)(32768.0 / k);  // (a3 < 0: the polynomial falls with s^7, here to some -2^100 C)
+        // (caps that 32 bits cannot follow that way go the exact way)
+        for (double x : a)
+            if (!(std::fabs(x) > 1e-36 && std::fabs(x) < 1e36)) m.quick = -1.f;
+        if (!(m.quick < 1e18f)) m.quick = -1.f;
+    }
     return m;
 }
 

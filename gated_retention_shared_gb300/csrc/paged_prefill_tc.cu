@@ -178,83 +178,42 @@ __device__ __forceinline__ uint32_t c_below(int n) {
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-// The scores of a row over a tile, in place: cap tanh(q.k scale / cap) - slope |p - m|, times log2(e).
-// Place c of the tile is slot v0 + first + c before the first run's end, v0 + delta + c from there on.
-// Where no score of the warp leaves [-0.8, 0.8] caps (with caps of some tens that is the rule), the
-// tanh is u times a polynomial of degree 4 in u^2 (own minimax fit by reweighted least squares,
-// relative error 1e-6, a 2000th of the rounding of the weights that follows), two scores to an
-// instruction and no further trip to the special-function unit, which the exponentials fill.
+// How a scored tile goes.  The reference of a row's exponentials need not be its maximum, only no
+// less and not far above, so it comes from the raw products: with a cap (which is monotone) from their largest
+// magnitude, with a bias from the largest of each 32 columns and the bias at their end.  The cap
+// and the bias are then part of the exponentials' argument,
+//     2^(s Q(s^2) + (slope (m - p) - reference)),
+// Q the polynomial of C tanh(k s) / s of degree 3 in s^2 (own minimax fit by reweighted least squares,
+// relative error 5.4e-7 up to |k s| = 0.5, a 2000th of the rounding of the weights that follows), the bracket
+// advanced by additions from every eighth column on: two scores to an instruction, 4 + 1 more
+// for two scores than without, and nothing more for the special-function unit.  That is where the
+// products of all rows of a warp are within kQuickSlack of 0 (and half the cap's bend), slopes
+// below kQuickSlope and all that is seen behind the row, so that a reference is at most 2 x 22 + 44 above the
+// maximum: weights 2^-38 below it still are normal numbers.  Other tiles take the exact way, score by
+// score, in small steps over tensor memory: unrolled over the row's registers its code cost the quick
+// tiles their place in the instruction cache (4096 rows, cap 30, 3 % of the tiles exact: 256 us).
+// 16 places of the tile from place c0 on, in place: cap tanh(q.k scale / cap) - slope |p - m|, times
+// log2(e), and -inf where `seen` has no bit.  Place c is slot v0 + first + c before the first run's end,
+// v0 + delta + c from there on.
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ void c_scores(uint32_t (&sv)[128], const PagedMod &mod, float c2, float slope, bool used, int pos,
-                                         int pre, int v0, int sink_slots, int first, int delta) {
-    if constexpr (CAP) {
-        const float C = mod.cap2;
-        float top[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void c_scores(uint32_t (&sv)[16], int c0, uint32_t seen, const PagedMod &mod, float c2, float slope,
+                                         int pos, int v0, int sink_slots, int first, int delta) {
 #pragma unroll
-        for (int c = 0; c < kPagedTile; c += 2)
-            top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], fabsf(__uint_as_float(sv[c])), fabsf(__uint_as_float(sv[c + 1])));
-        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
-        if (__builtin_expect(__any_sync(0xffffffffu, used && most > 0.8f), 0)) {
-#pragma unroll
-            for (int c = 0; c < kPagedTile; ++c) sv[c] = __float_as_uint(paged_cap(__uint_as_float(sv[c]) * c2, C));
-        } else {
-            const uint64_t cc = f2_pack(c2, c2);
-            const uint64_t a0 = f2_pack(C * 0.999998994f, C * 0.999998994f), a1 = f2_pack(C * -0.333253721f, C * -0.333253721f);
-            const uint64_t a2 = f2_pack(C * 0.132305659f, C * 0.132305659f), a3 = f2_pack(C * -0.049180146f, C * -0.049180146f);
-            const uint64_t a4 = f2_pack(C * 0.0121001389f, C * 0.0121001389f);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint64_t u[8], x[8], t[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int c = 16 * q + 2 * e;
-                    u[e] = f2_mul(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), cc);
-                    x[e] = f2_mul(u[e], u[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], a4, a3);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], t[e], a2);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], t[e], a1);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = f2_fma(x[e], t[e], a0);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float y0, y1;
-                    f2_unpack(f2_mul(u[e], t[e]), y0, y1);
-                    sv[16 * q + 2 * e] = __float_as_uint(y0);
-                    sv[16 * q + 2 * e + 1] = __float_as_uint(y1);
-                }
-            }
+    for (int c = 0; c < 16; ++c) {
+        float y = __uint_as_float(sv[c]) * c2;
+        if constexpr (CAP) y = paged_cap(y, mod.cap2);
+        if constexpr (BIAS) {
+            const int v = v0 + c0 + c, m = v + (v < sink_slots ? first : delta);
+            y = fmaf(-slope, fabsf((float)(m - pos)), y);
         }
+        sv[c] = seen & (1u << c) ? __float_as_uint(y) : 0xff800000u;
     }
-    if constexpr (BIAS) {
-        const bool head = v0 + kPagedTile <= sink_slots;
-        const int k0 = v0 + (head ? first : delta);
-        // no slot past the row's position is one that it sees, and all places are of one run
-        const bool behind = (head || v0 >= sink_slots) && (k0 + kPagedTile - 1 <= pos || pre <= max(k0, pos + 1));
-        if (__builtin_expect(__all_sync(0xffffffffu, behind || !used), 1)) {
-            const float at = slope * (float)(k0 - pos);
-            const uint64_t at2 = f2_pack(at, at), cc = f2_pack(c2, c2);
-#pragma unroll
-            for (int c = 0; c < kPagedTile; c += 2) {
-                float y0, y1;
-                const uint64_t s2 = f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-                f2_unpack(CAP ? f2_add(s2, at2) : f2_fma(s2, cc, at2), y0, y1);
-                sv[c] = __float_as_uint(fmaf(slope, (float)c, y0));
-                sv[c + 1] = __float_as_uint(fmaf(slope, (float)(c + 1), y1));
-            }
-        } else {
-            const float o1 = (float)(v0 + first - pos), o2 = (float)(v0 + delta - pos);
-            const int split = sink_slots - v0;  // places before it are the first run's
-#pragma unroll
-            for (int c = 0; c < kPagedTile; ++c) {
-                const float far = fabsf((float)c + (c < split ? o1 : o2)), y = __uint_as_float(sv[c]);
-                sv[c] = __float_as_uint(fmaf(-slope, far, CAP ? y : y * c2));
-            }
-        }
-    }
+}
+
+__device__ __forceinline__ float c_max_nan(float a, float b) {  // NaN where one is NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 template <int MODE>
@@ -263,7 +222,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
                         PagedPlan *plan, const typename PagedKind<(MODE > 0)>::Entry *__restrict__ entries, int cap, int rows,
                         int Hq, const PagedView pv, const PagedMod mod, float c2, int *err) {
-    constexpr bool MOD = MODE > 0, CAP = MODE & kModCap, BIAS = MODE & kModBias;
+    constexpr bool MOD = MODE > 0, CAP = MODE & kModCap, BIAS = MODE & kModBias, SCORED = CAP || BIAS;
     typedef typename PagedKind<MOD>::Entry Entry;
     typedef PagedPreTask<MOD> Task;
     constexpr int kWords = sizeof(Entry) / 4;
@@ -324,20 +283,23 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     const int mine = (lane >> 1) * psz;
     // what the table says of this lane's box of tile i (fetched ahead of use, so not yet looked
     // at); -1 past the last place
+    // the entry's i-th tile.  A bias takes the nearest first: from the farthest on, each tile's scores
+    // would pass the reference and the sums would be rescaled every time (4096 rows, slopes 2^(-i/3): 135 us)
+    auto tile_of = [&](const Entry &blk, int i) { return BIAS ? blk.i1 - 1 - i : blk.i0 + i; };
     auto look_up = [&](const Entry &blk, int i) -> int {
-        const int v = (blk.i0 + i) * kPagedTile + mine, e = blk.range.slot(v) >> pv.shift;
+        const int v = tile_of(blk, i) * kPagedTile + mine, e = blk.range.slot(v) >> pv.shift;
         const bool there = lane < boxes && v < blk.range.places && e < pv.max_pages;
         return there ? pv.table[(size_t)blk.b * pv.max_pages + e] : -1;
     };
     // that page, or the one past the pool
     auto page_of = [&](const Entry &blk, int i, int entry_of_table) -> int {
         if ((unsigned)entry_of_table < (unsigned)pv.num_pages) return entry_of_table;
-        if (lane < boxes && (blk.i0 + i) * kPagedTile + mine < blk.range.places) paged_report(err, kErrPagedPage);
+        if (lane < boxes && tile_of(blk, i) * kPagedTile + mine < blk.range.places) paged_report(err, kErrPagedPage);
         return pv.num_pages;
     };
     const int half = lane & 1;
     auto row_of = [&](const Entry &blk, int i) -> int {  // of tile i's box in its page
-        return blk.range.slot((blk.i0 + i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
+        return blk.range.slot(tile_of(blk, i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
     };
     auto copy = [&](Task &task, int hk, int i, bool is_v, int page, int row) {  // K or V tile i into its (free) slot
         const int s = i % kCStages;
@@ -409,13 +371,15 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (ntiles > 0) {
                 if (n > 0) copy_q(task);
                 int nk = 1, nv = 0;  // tiles whose K / V copy was issued
-                const int c_i0 = blk.i0, c_sink = blk.range.sink_slots, c_delta = blk.range.base - c_sink, c_hk = task.hk;
-                int c_first = 0;
-                if constexpr (MOD) c_first = blk.range.first;
+                const int c_i0 = BIAS ? blk.i1 - 1 : blk.i0, c_sink = blk.range.sink_slots, c_delta = blk.range.base - c_sink, c_hk = task.hk;
                 bool ok = true;
                 auto load = [&](int i, bool is_v, int page) {
-                    const int s = i % kCStages, v = (c_i0 + i) * kPagedTile + mine;
-                    const int row = (v < c_sink ? v + c_first : v + c_delta) & ((1 << pv.shift) - 1);
+                    const int s = i % kCStages, v = (BIAS ? c_i0 - i : c_i0 + i) * kPagedTile + mine;
+                    int to = v < c_sink ? 0 : c_delta;
+                    if constexpr (MOD) {
+                        if (v < c_sink) to = blk.range.first;  // (from shared memory: a register more would spill)
+                    }
+                    const int row = (v + to) & ((1 << pv.shift) - 1);
                     if (i >= kCStages)
                         ok = mbar_wait(is_v ? &task.bar.vempty[s] : &task.bar.kempty[s], ((i / kCStages) + 1) & 1, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
@@ -592,15 +556,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             e_lo = (from + kPagedTile - 1) / kPagedTile - blk.i0;
             e_hi = rg.places / kPagedTile - blk.i0;
         }
-        // a scored call's row: its document's start, the prefix that it sees, its head's slope
-        [[maybe_unused]] int doc = 0, pre = 0, first = 0;
+        // a scored call's row sees the slots [lo, pos] and [doc, head): its window from its document's
+        // start on, and of the document's slots the prefix and the sinks
+        [[maybe_unused]] int lo = 0, doc = 0, head = 0;
         [[maybe_unused]] float slope = 0.f;
-        bool blind = pos < 0;  // sees nothing
         if constexpr (MOD) {
             if (used && mod.doc) doc = max(0, mod.doc[blk.row0 + x * TS + r / G]);
-            pre = pos < 0 ? 0 : blk.range.pre;
-            first = blk.range.first;
-            blind = paged_blind(pos, doc, pre);
+            lo = max(doc, pv.window > 0 ? pos + 1 - pv.window : 0);
+            head = pos < 0 ? 0 : max(blk.range.pre, min(pv.sinks, pos + 1));
             if (BIAS && used) slope = mod.slopes[hk * G + r % G] * kPagedLog2E;
         }
         float m_ref = -INFINITY, l = 0.f;  // base-2 units
@@ -609,6 +572,21 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // votes take whole warps.
         bool alive = true;
         for (int i = 0; i < ntiles && alive; ++i) {
+            // place 0 of the tile, and what its slot is where it lies past the sinks' chunks
+            const int v0 = tile_of(blk, i) * kPagedTile, key0 = v0 + delta;
+            // every row of the set (a scored call: of the warp) sees every slot of the tile
+            bool full, edge = false;
+            [[maybe_unused]] int first = 0, k0 = 0;  // of the first run's slots; of the tile's where it has one run
+            [[maybe_unused]] bool behind = true;     // no slot past the row's position is one that it sees
+            if constexpr (MOD) {
+                first = blk.range.first;
+                const bool one = v0 + kPagedTile <= sink_slots, run = one || v0 >= sink_slots;
+                k0 = v0 + (one ? first : delta);
+                const bool mine = (lo <= k0 && k0 + kPagedTile - 1 <= pos) || (doc <= k0 && k0 + kPagedTile <= head);
+                full = run && __all_sync(0xffffffffu, mine || !used);
+                edge = x == 0 && blk.range.edge(tile_of(blk, i), 0);
+                behind = run && (k0 + kPagedTile - 1 <= pos || head <= max(k0, pos + 1));
+            }
             alive = mbar_wait_warp(&bar.s_full[x], i & 1, abort_flag);
             tc_fence_after();
             const uint32_t s_t = tmem + colS + lane_base;
@@ -616,76 +594,182 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) tmem_ld32(s_t + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * cb));
             tmem_wait_ld();
-            // S is in registers: the MMA may write S(i + 1) over it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.s_free[x]);
-            // place 0 of the tile, and what its slot is where it lies past the sinks' chunks
-            const int v0 = (blk.i0 + i) * kPagedTile, key0 = v0 + delta;
-            // every row of the set (a scored call: of the warp) sees every slot of the tile
-            bool full;
-            if constexpr (MOD) {
-                const int k0 = v0 + kPagedTile <= sink_slots ? v0 + first : key0;  // (no two runs in the tile)
-                const bool mine = doc <= k0 && ((k0 + kPagedTile - 1 <= pos &&
-                                                 (pv.window <= 0 || k0 > pos - pv.window || k0 + kPagedTile <= pv.sinks)) ||
-                                                k0 + kPagedTile <= pre);
-                full = (v0 >= sink_slots || v0 + kPagedTile <= sink_slots) && __all_sync(0xffffffffu, mine || !used);
-                c_scores<CAP, BIAS>(sv, mod, c2, slope, used, pos, pre, v0, sink_slots, first, delta);
-            } else {
+            if constexpr (!SCORED) {
+                // S is in registers: the MMA may write S(i + 1) over it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.s_free[x]);
+            }
+            if constexpr (!MOD)
                 full = v0 >= sink_slots && key0 + kPagedTile - 1 <= set_lo &&
                        (pv.window <= 0 || key0 > set_hi - pv.window || key0 + kPagedTile <= pv.sinks);
-            }
+            [[maybe_unused]] uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
             if (__builtin_expect(!full, 0)) {
-                // the places this row sees of the tile: sinks in the sinks' chunks, then a run up to its
-                // own position from the window's first slot on, and sinks that lie in those chunks
-                const int hi_c = pos + 1 - key0;
-                const int lo_c = pv.window > 0 ? pos + 1 - pv.window - key0 : -1;
-                const int sk_c = min(pv.sinks - key0, hi_c);
-                const int ch_c = sink_slots - v0, sc_c = min(ch_c, min(pv.sinks, pos + 1) - v0);
-                uint32_t bits[4];
                 if constexpr (MOD) {
-                    const int f_c = v0 + first;  // slot of place 0 if it lies in the first run
-                    const int pre_c = pre - key0, doc_c = doc - key0;
-                    const int sc_1 = max(min(pv.sinks, pos + 1), pre) - f_c, doc_1 = doc - f_c;
+                    // [lo, pos] and [doc, head) of the second run's places, [doc, head) of the first run's
+                    const int ch_c = sink_slots - v0, f_c = v0 + first;
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(max(sk_c, pre_c) - 32 * w)) &
-                                   ~c_below(ch_c - 32 * w) & ~c_below(doc_c - 32 * w)) |
-                                  (c_below(sc_1 - 32 * w) & ~c_below(doc_1 - 32 * w) & c_below(ch_c - 32 * w));
-                } else
+                        bits[w] = (((c_below(pos + 1 - key0 - 32 * w) & ~c_below(lo - key0 - 32 * w)) |
+                                    (c_below(head - key0 - 32 * w) & ~c_below(doc - key0 - 32 * w))) & ~c_below(ch_c - 32 * w)) |
+                                  (c_below(head - f_c - 32 * w) & ~c_below(doc - f_c - 32 * w) & c_below(ch_c - 32 * w));
+                } else {
+                    // the places this row sees of the tile: sinks in the sinks' chunks, then a run up to its
+                    // own position from the window's first slot on, and sinks that lie in those chunks
+                    const int hi_c = pos + 1 - key0;
+                    const int lo_c = pv.window > 0 ? pos + 1 - pv.window - key0 : -1;
+                    const int sk_c = min(pv.sinks - key0, hi_c);
+                    const int ch_c = sink_slots - v0, sc_c = min(ch_c, min(pv.sinks, pos + 1) - v0);
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w)) &
-                               ~c_below(ch_c - 32 * w)) | c_below(sc_c - 32 * w);
+                    for (int w = 0; w < 4; ++w)
+                        bits[w] = (((c_below(hi_c - 32 * w) & ~c_below(lo_c - 32 * w)) | c_below(sk_c - 32 * w)) &
+                                   ~c_below(ch_c - 32 * w)) | c_below(sc_c - 32 * w);
+                }
+                if constexpr (!SCORED) {
 #pragma unroll
-                for (int c = 0; c < kPagedTile; ++c)
-                    sv[c] = (bits[c >> 5] & (1u << (c & 31))) ? sv[c] : 0xff800000u;  // -inf
+                    for (int c = 0; c < kPagedTile; ++c)
+                        sv[c] = (bits[c >> 5] & (1u << (c & 31))) ? sv[c] : 0xff800000u;  // -inf
+                }
             }
-            float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mt;
+            [[maybe_unused]] bool quick = true;
+            if constexpr (SCORED) {
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // of 32 columns, of those that the row sees
+                if (__builtin_expect(full, 1)) {
 #pragma unroll
-            for (int c = 0; c < kPagedTile; c += 2)
-                mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                    for (int c = 0; c < kPagedTile; c += 2) {
+                        const float s0 = __uint_as_float(sv[c]), s1 = __uint_as_float(sv[c + 1]);
+                        top[c >> 5] = CAP ? fmax3(top[c >> 5], fabsf(s0), fabsf(s1)) : fmax3(top[c >> 5], s0, s1);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kPagedTile; ++c) {
+                        const bool seen = bits[c >> 5] & (1u << (c & 31));
+                        const float s0 = __uint_as_float(sv[c]);
+                        top[c >> 5] = fmaxf(top[c >> 5], seen ? (CAP ? fabsf(s0) : s0) : -INFINITY);
+                        sv[c] = seen ? sv[c] : __float_as_uint(CAP ? mod.hidden : -INFINITY);  // (weight 0)
+                    }
+                }
+                bool ok = true;
+                if constexpr (CAP) ok = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), 0.f) <= mod.quick;
+                if constexpr (BIAS) ok = ok && fabsf(slope) <= kQuickSlope && behind;
+                quick = __all_sync(0xffffffffu, ok || !used);
+                mt = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float y = top[q] * c2;
+                    if constexpr (CAP) {
+                        const float x2 = top[q] * top[q];
+                        y = top[q] * fmaf(x2, fmaf(x2, fmaf(x2, mod.a3, mod.a2), mod.a1), mod.a0);
+                        if (top[q] == -INFINITY) y = -INFINITY;
+                    }
+                    if constexpr (BIAS) y = fmaf(slope, (float)(k0 - pos + 32 * q), y) + fmaxf(31.f * slope, 0.f);
+                    mt = fmaxf(mt, y);
+                }
+                if (__builtin_expect(!quick, 0)) {
+                    mt = -INFINITY;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kPagedTile; c0 += 16) {
+                        const uint32_t seen = (c0 < 64 ? (c0 < 32 ? bits[0] : bits[1]) : (c0 < 96 ? bits[2] : bits[3])) >> (c0 & 31);
+                        uint32_t y[16];
+                        tmem_ld16(s_t + c0, y);
+                        tmem_wait_ld();
+                        c_scores<CAP, BIAS>(y, c0, seen, mod, c2, slope, pos, v0, sink_slots, first, delta);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) mt = fmaxf(mt, __uint_as_float(y[c]));
+                        tmem_st16(s_t + c0, y);
+                    }
+                    tmem_wait_st();
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) tmem_ld32(s_t + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * cb));
+                    tmem_wait_ld();
+                }
+                // S is in registers: the MMA may write S(i + 1) over it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.s_free[x]);
+            } else {
+                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kPagedTile; c += 2)
+                    mq[(c >> 1) & 3] = fmax3(mq[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * c2;
+            }
             // rows past the set's tokens hold whatever shared memory held: they never move the
             // reference (no rescaling for their sake) and are never stored
-            const float mt = used ? fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * (CAP || BIAS ? 1.f : c2) : -INFINITY;
+            mt = used ? mt : -INFINITY;
             const bool move = (mt > m_ref + kCGap) || (m_ref == -INFINITY && mt > -INFINITY);
             const float m_old = m_ref;
             m_ref = move ? mt : m_ref;
             const float alpha = move ? (m_old == -INFINITY ? 0.f : c_ex2(m_old - mt)) : 1.f;
             const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
             const uint64_t c2x2 = f2_pack(c2, c2), nmu2 = f2_pack(-mu, -mu);
+            // the argument's terms: (a0 + a1 s^2 + a2 s^4 + a3 s^6) s + b0 + step c; a tile that went the
+            // exact way holds arguments already
+            [[maybe_unused]] float a0 = c2, a1 = 0.f, a2 = 0.f, a3 = 0.f, b0 = -mu, step = 0.f;
+            if constexpr (SCORED) {
+                if constexpr (CAP) a0 = mod.a0, a1 = mod.a1, a2 = mod.a2, a3 = mod.a3;
+                if constexpr (BIAS) {
+                    step = slope;
+                    b0 = fmaf(slope, (float)(k0 - pos), -mu);
+                }
+                if (__builtin_expect(!quick, 0)) {
+                    a0 = 1.f, a1 = a2 = a3 = b0 = step = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kPagedTile; ++c)  // (s^2 stays finite)
+                        sv[c] = __float_as_uint(c_max_nan(__uint_as_float(sv[c]) - mu, -1e18f));
+                }
+            }
             uint64_t acc2[4] = {0, 0, 0, 0};  // packed zeros
             uint32_t pk[kPagedTile / 2];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // 32 columns at a time, each step for all of them: element by element
                                            // they come out as chains of latencies
+                if constexpr (SCORED) {
+                    const uint64_t a0x2 = f2_pack(a0, a0), a1x2 = f2_pack(a1, a1), a2x2 = f2_pack(a2, a2), a3x2 = f2_pack(a3, a3);
+                    const uint64_t b0x2 = f2_pack(b0, b0), step2 = f2_pack(2.f * step, 2.f * step);
 #pragma unroll
-                for (int c = 16 * q; c < 16 * q + 16; ++c) {
-                    float x0, x1;
-                    const uint64_t s2 = f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
-                    f2_unpack(CAP || BIAS ? f2_add(s2, nmu2) : f2_fma(s2, c2x2, nmu2), x0, x1);
-                    sv[2 * c] = __float_as_uint(x0);
-                    sv[2 * c + 1] = __float_as_uint(x1);
+                    for (int g = 0; g < 2; ++g) {  // 16 columns at a time
+                        uint64_t s2[8], f2[8], run[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int c = 32 * q + 16 * g + 2 * e;
+                            s2[e] = f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                            run[e] = b0x2;
+                            if constexpr (BIAS) {
+                                const float at = fmaf(step, (float)c, b0);
+                                run[e] = e & 3 ? f2_add(run[e - 1], step2) : f2_pack(at, at + step);
+                            }
+                            f2[e] = a0x2;
+                        }
+                        if constexpr (CAP) {
+                            uint64_t x2[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x2[e] = f2_mul(s2[e], s2[e]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], a3x2, a2x2);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], f2[e], a1x2);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], f2[e], a0x2);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int c = 32 * q + 16 * g + 2 * e;
+                            float x0, x1;
+                            f2_unpack(f2_fma(s2[e], f2[e], run[e]), x0, x1);
+                            sv[c] = __float_as_uint(x0);
+                            sv[c + 1] = __float_as_uint(x1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 16 * q; c < 16 * q + 16; ++c) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), c2x2, nmu2), x0, x1);
+                        sv[2 * c] = __float_as_uint(x0);
+                        sv[2 * c + 1] = __float_as_uint(x1);
+                    }
                 }
 #pragma unroll
                 for (int c = 32 * q; c < 32 * q + 32; ++c) sv[c] = __float_as_uint(c_ex2(__uint_as_float(sv[c])));
@@ -717,9 +801,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tmem_wait_st();
             }
             // V rows that no row of the block sees: zero, once the tile has come
-            bool edge;
-            if constexpr (MOD) edge = x == 0 && blk.range.edge(blk.i0 + i, 0);
-            else edge = i < e_lo || i >= e_hi;
+            if constexpr (!MOD) edge = i < e_lo || i >= e_hi;
             if (__builtin_expect(edge || !two, 0)) {
                 alive &= mbar_wait_warp(&bar.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
                 if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
@@ -787,6 +869,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     // of 256 bytes side by side
                     uint8_t *stg = sQ + x * kCTile;
                     // (a row whose scores are all -inf: 0 / 0, NaN as softmax has it)
+                    bool blind = pos < 0;  // sees nothing
+                    if constexpr (MOD) blind = lo > pos && doc >= head;
                     const float inv = blind ? 0.f : 1.f / l;
 #pragma unroll 1
                     for (int cb = 0; cb < 4; ++cb) {
