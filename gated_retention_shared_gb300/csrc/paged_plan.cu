@@ -34,17 +34,26 @@ struct PlanSeq {
     int first, n, pos, blocks, tiles;  // tiles: of the row block that sees most, give or take one
 };
 
-__device__ __forceinline__ PlanSeq plan_seq(const PagedView &pv, const int32_t *cu, int rows, int T_R, int b, int *err) {
+// (documents shorten row blocks one by one: plan_range)
+template <bool MOD>
+__device__ __forceinline__ PlanSeq plan_seq(const PagedView &pv, const PagedMod &mod, const int32_t *cu, int rows, int T_R, int b,
+                                            int *err) {
     PlanSeq s{0, 0, 0, 0, 0};
+    int prefix = 0;
+    if constexpr (MOD) prefix = mod.prefix ? mod.prefix[b] : 0;
     const int len = paged_len(pv, b, err);  // (asked for before the rows are known: one latency, not two)
     s.n = paged_rows(cu, rows, b, s.first, err);
     if (s.n == 0) return s;
     s.blocks = (s.n + T_R - 1) / T_R;
     s.pos = len - s.n;
     const int last = s.pos + (s.blocks - 1) * T_R;
-    s.tiles = paged_range(pv, last, s.pos + s.n - 1).ntiles;
+    auto tiles = [&](int p0, int p1) {
+        if constexpr (MOD) return paged_range_mod(pv, p0, p1, len, prefix, 0).ntiles;
+        else return paged_range(pv, p0, p1).ntiles;
+    };
+    s.tiles = tiles(last, s.pos + s.n - 1);
     // with a window a last row block of few rows sees less than the one before it
-    if (pv.window > 0 && s.blocks > 1) s.tiles = max(s.tiles, paged_range(pv, last - T_R, last - 1).ntiles);
+    if (pv.window > 0 && s.blocks > 1) s.tiles = max(s.tiles, tiles(last - T_R, last - 1));
     return s;
 }
 
@@ -64,6 +73,7 @@ struct PlanArgs {
     PagedPlan *plan;
     void *entries, *cuts;  // PagedKind<MOD>::Entry
     int *doc_lo;           // a scored call's
+    int units;             // with documents: row blocks that are planned one by one; 0: more than there is room for
     int *err;
 };
 
@@ -122,30 +132,27 @@ __device__ __forceinline__ PagedRangeMod plan_range(const PlanArgs &a, const Pag
                            mod.doc && g < a.cap ? a.doc_lo[g] : 0);
 }
 
-// entry e: number idx of sequence b's, whose partial results and cut row blocks start at slot0, cut0
-// (block0: a scored call's first row block of the sequence, numbered over the call)
+// entry e: piece `piece` of row block j of sequence b, one of pc of at most `per` tiles; its partial
+// result is `slot`, the next piece's slot + stride; cut: where the merge finds its row block
 template <bool MOD>
 __device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &pv, const PagedMod &mod, const PlanSeq &s, int b,
-                                           int pc, int idx, int e, int slot0, int cut0, int block0) {
-    const int per = (s.tiles + pc - 1) / pc;
-    // the row blocks that see most come first; a cut sequence's row blocks of one piece are
-    // neighbours (they read the same keys)
-    const int piece = idx / s.blocks, j = s.blocks - 1 - (idx - piece * s.blocks);
+                                           int j, int g, int piece, int pc, int e, int slot, int stride, int cut) {
     typedef typename PagedKind<MOD>::Entry Entry;
+    const int per = (s.tiles + pc - 1) / pc;
     Entry o;
     o.b = b;
     o.row0 = s.first + j * a.T_R;
     o.nrow = min(a.T_R, s.n - j * a.T_R);
     o.pos0 = s.pos + j * a.T_R;
-    if constexpr (MOD) o.range = plan_range(a, pv, mod, s, b, j, block0 + j);
+    if constexpr (MOD) o.range = plan_range(a, pv, mod, s, b, j, g);
     else o.range = paged_range(pv, o.pos0, o.pos0 + o.nrow - 1);
     // one may see a tile more than `tiles`, or many fewer: the last piece takes what is left
     o.pieces = min(pc, max(1, per > 0 ? (o.range.ntiles + per - 1) / per : 1));
     o.i0 = min(piece * per, o.range.ntiles);
     o.i1 = piece == pc - 1 ? o.range.ntiles : min(o.i0 + per, o.range.ntiles);
     if (piece >= o.pieces) o.nrow = 0;
-    o.slot = slot0 + idx;
-    o.stride = s.blocks;
+    o.slot = slot;
+    o.stride = stride;
     o.pad = 0;
     const int4 *from = reinterpret_cast<const int4 *>(&o);
     constexpr int kQuads = sizeof(Entry) / 16;
@@ -153,13 +160,24 @@ __device__ __forceinline__ void plan_entry(const PlanArgs &a, const PagedView &p
     for (int x = 0; x < kQuads; ++x) reinterpret_cast<int4 *>((Entry *)a.entries + e)[x] = from[x];
     if (pc > 1 && piece == 0) {  // for the merge
 #pragma unroll
-        for (int x = 0; x < kQuads; ++x) reinterpret_cast<int4 *>((Entry *)a.cuts + cut0 + idx)[x] = from[x];
+        for (int x = 0; x < kQuads; ++x) reinterpret_cast<int4 *>((Entry *)a.cuts + cut)[x] = from[x];
     }
 }
 
+// The same for number idx of sequence b's entries: the row blocks that see most come first; a cut
+// sequence's row blocks of one piece are neighbours (they read the same keys).  block0: the number
+// of its first row block.
+template <bool MOD>
+__device__ __forceinline__ void plan_seq_entry(const PlanArgs &a, const PagedView &pv, const PagedMod &mod, const PlanSeq &s,
+                                               int b, int pc, int idx, int e, int slot0, int cut0, int block0) {
+    const int piece = idx / s.blocks, j = s.blocks - 1 - (idx - piece * s.blocks);
+    plan_entry<MOD>(a, pv, mod, s, b, j, block0 + j, piece, pc, e, slot0 + idx, s.blocks, cut0 + idx);
+}
+
 // Up to 32 sequences: lane b of every warp has sequence b in registers, one barrier (for the tries).
+template <bool MOD>
 __global__ void __launch_bounds__(kPlanThreads)
-paged_plan_small_kernel(const PagedView pv, const PlanArgs a) {
+paged_plan_small_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
     __shared__ float c_cost[kPlanTries];
     __shared__ int c_q[kPlanTries];
     static_assert(kPlanTries <= kPlanThreads / 32 && kPlanTries <= 32, "a warp for each try, a lane for each cost");
@@ -168,7 +186,7 @@ paged_plan_small_kernel(const PagedView pv, const PlanArgs a) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     PlanSeq s{0, 0, 0, 0, 0};
-    if (lane < B) s = plan_seq(pv, a.cu, a.rows, a.T_R, lane, warp == 0 ? a.err : nullptr);
+    if (lane < B) s = plan_seq<MOD>(pv, mod, a.cu, a.rows, a.T_R, lane, warp == 0 ? a.err : nullptr);
     const float W = plan_sum((float)s.blocks * (float)s.tiles) * (float)pv.Hkv;
     const long long nblocks = plan_sum((long long)s.blocks);
     const int longest = __reduce_max_sync(0xffffffffu, s.tiles);
@@ -224,45 +242,51 @@ paged_plan_small_kernel(const PagedView pv, const PlanArgs a) {
         const int t_slot = __shfl_sync(0xffffffffu, slot, k), t_cut = __shfl_sync(0xffffffffu, cut, k);
         const int n = (int)min((long long)t.blocks * t_pc, (long long)(a.cap - t_first));
         for (int idx = (warp % share) * 32 + lane; idx < n; idx += 32 * share)
-            plan_entry<false>(a, pv, PagedMod{}, t, k, t_pc, idx, t_first + idx, t_slot, t_cut, 0);
+            plan_seq_entry<MOD>(a, pv, mod, t, k, t_pc, idx, t_first + idx, t_slot, t_cut, 0);
     }
 }
 
-// A scored call's row blocks see what their masks leave: each is looked at (a warp reads a block's
-// document starts), a sequence's `tiles` is its longest block's.
+// With documents each row block is looked at (eight lanes read its rows' document starts) and, where
+// there is room for them, planned by itself as if it were a sequence: what they see may differ by
+// much.  (As one sequence with the longest block's tiles 8192 rows of documents of 700 with a
+// question of 100 rows that sees all of them were not cut: 157 us.)
 template <bool MOD>
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
     extern __shared__ int sh[];
-    int *tiles = sh, *blocks = tiles + pv.B, *order = blocks + pv.B;
-    int *start = order + pv.B, *slot0 = start + pv.B + 1, *cut0 = slot0 + pv.B + 1;
-    [[maybe_unused]] int *block0 = cut0 + pv.B + 1;  // [B + 1] row blocks before the sequence's
+    const int room = max(pv.B, MOD ? a.units : 0);
+    int *tiles = sh, *blocks = tiles + room, *order = blocks + room;
+    int *start = order + room, *slot0 = start + room + 1, *cut0 = slot0 + room + 1;
+    [[maybe_unused]] int *block0 = cut0 + room + 1;  // [B + 1] row blocks before the sequence's
     __shared__ float r_W[kPlanThreads / 32], c_cost[kPlanTries];
     __shared__ long long r_sum[3][kPlanThreads / 32];
     __shared__ int r_longest[kPlanThreads / 32], c_q[kPlanTries];
     static_assert(kPlanTries <= kPlanThreads / 32, "a warp for each");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = pv.B;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int B = pv.B;  // sequences, or row blocks that are planned one by one
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
     float W = 0.f;
     long long nblocks = 0;
     int longest = 0;
+    const bool docs = MOD && mod.doc;
+    bool single = false;  // row blocks are planned one by one
 #pragma unroll 1
     for (int b = tid; b < B; b += kPlanThreads) {
-        const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
-        tiles[b] = MOD ? 0 : s.tiles;
+        const PlanSeq s = plan_seq<MOD>(pv, mod, a.cu, a.rows, a.T_R, b, a.err);
+        tiles[b] = docs ? 0 : s.tiles;
         blocks[b] = s.blocks;
         nblocks += s.blocks;
-        if constexpr (!MOD) {
+        if (!docs) {
             W += (float)s.blocks * (float)s.tiles;
             longest = max(longest, s.tiles);
         }
     }
-    const int each = (B + kPlanThreads - 1) / kPlanThreads;
-    const int p0 = min(B, tid * each), p1 = min(B, p0 + each);
-    if constexpr (MOD) {
+    if (docs) {
         __syncthreads();
+        const int each = (B + kPlanThreads - 1) / kPlanThreads;
+        const int p0 = min(B, tid * each), p1 = min(B, p0 + each);
         long long mine = 0, sum;
         for (int b = p0; b < p1; ++b) mine += blocks[b];
         sum = mine;
@@ -281,32 +305,40 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
         }
         if (p0 < B && p1 == B) block0[B] = (int)min(run, 0x7fffffffll);
         __syncthreads();
-        const int step = mod.doc ? kPlanThreads / 32 : kPlanThreads;
-        for (int g = mod.doc ? warp : tid; g < min(block0[B], a.cap); g += step) {
+        // (row bounds that overlap may pass what there is room for)
+        single = block0[B] <= a.units;
+        const int all = min(block0[B], a.cap);
+        for (int g0 = tid / 8; g0 - (tid & 31) / 8 < all; g0 += kPlanThreads / 8) {
+            const int g = min(g0, all - 1);
             int lo = 0, hi = B;  // the sequence: block0[lo] <= g < block0[lo + 1]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (block0[mid] <= g) lo = mid;
                 else hi = mid;
             }
-            const PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, lo, nullptr);
-            const int j = g - block0[lo];
-            if (mod.doc) {
-                int least = 0x7fffffff;
-#pragma unroll 4
-                for (int r = j * a.T_R + lane; r < min(s.n, (j + 1) * a.T_R); r += 32) least = min(least, mod.doc[s.first + r]);
-                least = __reduce_min_sync(0xffffffffu, least);
-                if (lane == 0) a.doc_lo[g] = least;
-                __syncwarp();
-            }
-            if (!mod.doc || lane == 0) {
+            const PlanSeq s = plan_seq<MOD>(pv, mod, a.cu, a.rows, a.T_R, lo, nullptr);
+            const int j = g - block0[lo], r1 = min(s.n, (j + 1) * a.T_R);
+            int least = 0x7fffffff;
+#pragma unroll 8
+            for (int r = j * a.T_R + (lane & 7); r < r1; r += 8) least = min(least, mod.doc[s.first + r]);
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, off));
+            if ((lane & 7) == 0 && g0 < all) {
+                a.doc_lo[g] = least;
                 const int n = plan_range(a, pv, mod, s, lo, j, g).ntiles;
-                atomicMax(&tiles[lo], n);
+                if (single) {
+                    tiles[g] = n;
+                    blocks[g] = 1;
+                } else {
+                    atomicMax(&tiles[lo], n);
+                }
                 W += (float)n;
                 longest = max(longest, n);
             }
+            __syncwarp();
         }
         __syncthreads();  // (r_sum is written again)
+        if (single) B = all;
     }
     W = plan_sum(W);
     nblocks = plan_sum(nblocks);
@@ -384,6 +416,8 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
     }
     __syncthreads();
     // where each sequence's entries, partial results and cut row blocks start
+    const int each = (B + kPlanThreads - 1) / kPlanThreads;
+    const int p0 = min(B, tid * each), p1 = min(B, p0 + each);
     long long sum[3] = {0, 0, 0}, inc[3];
     for (int p = p0; p < p1; ++p) {
         const int b = order[p], pc = plan_pieces(tiles[b], Q);
@@ -436,10 +470,22 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
             if (start[mid] <= e) lo = mid;
             else hi = mid;
         }
-        const int b = order[lo], idx = e - start[lo];
-        PlanSeq s = plan_seq(pv, a.cu, a.rows, a.T_R, b, a.err);
-        if constexpr (MOD) s.tiles = tiles[b];
-        plan_entry<MOD>(a, pv, mod, s, b, plan_pieces(s.tiles, Q), idx, e, slot0[lo], cut0[lo], MOD ? block0[b] : 0);
+        const int b = order[lo], idx = e - start[lo], pc = plan_pieces(tiles[b], Q);
+        if (single) {
+            int seq = 0, end = pv.B;  // row block b's sequence
+            while (end - seq > 1) {
+                const int mid = (seq + end) >> 1;
+                if (block0[mid] <= b) seq = mid;
+                else end = mid;
+            }
+            PlanSeq s = plan_seq<MOD>(pv, mod, a.cu, a.rows, a.T_R, seq, nullptr);
+            s.tiles = tiles[b];
+            plan_entry<MOD>(a, pv, mod, s, seq, b - block0[seq], b, idx, pc, e, slot0[lo] + idx, 1, cut0[lo]);
+        } else {
+            PlanSeq s = plan_seq<MOD>(pv, mod, a.cu, a.rows, a.T_R, b, nullptr);
+            s.tiles = tiles[b];
+            plan_seq_entry<MOD>(a, pv, mod, s, b, pc, idx, e, slot0[lo], cut0[lo], docs ? block0[b] : 0);
+        }
     }
 }
 
@@ -448,21 +494,21 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
 namespace yoco_host {
 using namespace yoco;
 
-cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
-    const bool small = a.cache->B <= 32 && !a.scores;
-    const size_t words = a.scores ? 7 * (size_t)a.cache->B + 4 : 6 * (size_t)a.cache->B + 3;
+template <bool MOD> static cudaError_t plan_launch(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
+    const bool docs = a.scores && a.scores->doc_first, small = a.cache->B <= 32 && !docs;
+    // row blocks of any bounds that do not overlap: as many as the list has entries for them
+    const int64_t most = (int64_t)a.rows / g.rows + std::min(a.cache->B, a.rows);
+    const int units = docs && most <= kPagedMaxB ? (int)most : 0;
+    const size_t n = (size_t)std::max(a.cache->B, units);
     cudaError_t e = cudaSuccess;
-    if (a.scores)
-        e = cudaFuncSetAttribute(paged_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (!small)
+        e = cudaFuncSetAttribute(paged_plan_kernel<MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)((7 * (size_t)kPagedMaxB + 4) * sizeof(int)));
-    else if (!small)
-        e = cudaFuncSetAttribute(paged_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)((6 * (size_t)kPagedMaxB + 3) * sizeof(int)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = small ? 0 : words * sizeof(int);
+    cfg.dynamicSmemBytes = small ? 0 : (6 * n + 3 + (docs ? (size_t)a.cache->B + 1 : 0)) * sizeof(int);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -471,10 +517,12 @@ cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) 
     cfg.numAttrs = 1;
     count_launches(1);
     const PlanArgs p{a.cu, a.rows, g.rows, g.slots, g.max_split, g.min_piece, g.entry_cost, g.split_cost, g.cap,
-                     (PagedPlan *)g.plan, g.entries, g.cuts, g.doc_lo, a.err};
-    if (small) return cudaLaunchKernelEx(&cfg, paged_plan_small_kernel, paged_view(a), p);
-    if (a.scores) return cudaLaunchKernelEx(&cfg, paged_plan_kernel<true>, paged_view(a), paged_mod(a), p);
-    return cudaLaunchKernelEx(&cfg, paged_plan_kernel<false>, paged_view(a), paged_mod(a), p);
+                     (PagedPlan *)g.plan, g.entries, g.cuts, g.doc_lo, units, a.err};
+    return cudaLaunchKernelEx(&cfg, small ? paged_plan_small_kernel<MOD> : paged_plan_kernel<MOD>, paged_view(a), paged_mod(a), p);
+}
+
+cudaError_t paged_plan(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
+    return a.scores ? plan_launch<true>(a, g, st) : plan_launch<false>(a, g, st);
 }
 
 }  // namespace yoco_host
