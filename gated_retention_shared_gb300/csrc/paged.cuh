@@ -189,6 +189,9 @@ __device__ __forceinline__ float paged_cap(float u, float C) {
     return fabsf(u) < 0.8f ? C * (u * q) : fmaf(-2.f * C, i, C);
 }
 
+// what a tensor-core kernel's rows do to their scores before the softmax, beyond the plain calls'
+constexpr int kModMask = 1, kModCap = 2, kModBias = 4;
+
 constexpr float kPagedLog2E = 1.4426950408889634f;
 // the tensor-core prefill's quick way (paged_prefill_tc.cu): how large scores and slopes may be, times log2(e)
 constexpr float kQuickSlack = 22.f, kQuickSlope = 44.f / 31.f;

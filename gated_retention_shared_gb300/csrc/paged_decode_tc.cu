@@ -75,12 +75,14 @@ __device__ __forceinline__ float pex2(float x) {
     return y;
 }
 
-template <int NQ, bool MOD>
+// MODE as in paged_prefill_tc.cu: kModMask, with kModCap and kModBias where scores are capped or biased
+template <int NQ, int MODE>
 __global__ void __launch_bounds__(kPThreads, 1)
 paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const bf16_t *__restrict__ Q, bf16_t *__restrict__ O, float *__restrict__ part,
                        PagedCut *__restrict__ cuts, int Hq, const PagedView pv, const PagedMod mod, float c2, int keep_pages,
                        int *err) {
+    constexpr bool MOD = MODE > 0, CAP = MODE & kModCap, BIAS = MODE & kModBias;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
@@ -346,12 +348,12 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         for (int unit = 0; more && all; ++unit, more = w.next(pv, pre)) {
             const int len = paged_len(pv, w.b, nullptr);
             const typename PagedKind<MOD>::Range range = paged_newest<MOD>(pv, mod, w.b, len);
-            [[maybe_unused]] float slope[MOD ? NQ : 1];  // times log2(e)
+            [[maybe_unused]] float slope[BIAS ? NQ : 1];  // times log2(e)
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 m[n] = -INFINITY;
                 l[n] = 0.f;
-                if constexpr (MOD) slope[n] = mod.slopes && n < G ? mod.slopes[w.hk * G + n] * kPagedLog2E : 0.f;
+                if constexpr (BIAS) slope[n] = n < G ? mod.slopes[w.hk * G + n] * kPagedLog2E : 0.f;
             }
             for (int t = w.t0; t < w.t1; ++t, ++i) {
                 alive &= mbar_wait_warp(&sm.s_full[i & 1], (i / 2) & 1, abort_flag);
@@ -366,14 +368,33 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 const int key = range.slot(t * kPagedTile + r);
                 const bool seen = range.seen(key, pv.sinks);
                 float sc[NQ];
+                if constexpr (CAP) {
+                    // a polynomial where no score of the warp is past half the cap (paged_prefill_tc.cu)
+                    float most = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) most = fmaxf(most, fabsf(__uint_as_float(sv[n])));
+                    if (__all_sync(0xffffffffu, most <= mod.quick || !seen)) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const float s0 = __uint_as_float(sv[n]), x2 = s0 * s0;
+                            sc[n] = s0 * fmaf(x2, fmaf(x2, fmaf(x2, mod.a3, mod.a2), mod.a1), mod.a0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) sc[n] = paged_cap(c2 * __uint_as_float(sv[n]), mod.cap2);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) sc[n] = c2 * __uint_as_float(sv[n]);
+                }
+                if constexpr (BIAS) {
+                    const float far = (float)(len - 1 - key);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) sc[n] = fmaf(-slope[n], far, sc[n]);
+                }
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    float x2 = c2 * __uint_as_float(sv[n]);
-                    if constexpr (MOD) {
-                        if (mod.cap2 > 0.f) x2 = paged_cap(x2, mod.cap2);
-                        if (mod.slopes) x2 = fmaf(-slope[n], (float)(len - 1 - key), x2);
-                    }
-                    sc[n] = seen && n < G ? x2 : -INFINITY;
+                    sc[n] = seen && n < G ? sc[n] : -INFINITY;
                     float x = sc[n];
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
@@ -476,11 +497,11 @@ bool paged_kv_map(CUtensorMap *m, const void *ptr, const yoco_paged_kv *c) {
     return paged_map(m, ptr, 4, dims, strides, box);
 }
 
-template <int NQ, bool MOD>
+template <int NQ, int MODE>
 static cudaError_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const PagedArgs &a, const PagedView &pv,
                           PagedCut *cuts, float *part, int keep, int blocks, cudaStream_t st) {
     // the shared-memory opt-in is set on every launch (it belongs to the current device)
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_tc_kernel<NQ, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_tc_kernel<NQ, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)paged_dec_smem(kPagedMaxB));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -495,17 +516,17 @@ static cudaError_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Pa
     cfg.numAttrs = 1;
     count_launches(1);
     const PagedMod mod = paged_mod(a);
-    return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<NQ, MOD>, mk, mv, (const bf16_t *)a.Q, (bf16_t *)a.O, part, cuts,
+    return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<NQ, MODE>, mk, mv, (const bf16_t *)a.Q, (bf16_t *)a.O, part, cuts,
                               a.Hq, pv, mod, mod.qk, keep, a.err);
 }
 
-template <bool MOD>
+template <int MODE>
 static cudaError_t launch_heads(const CUtensorMap &mk, const CUtensorMap &mv, const PagedArgs &a, const PagedView &pv,
                                 PagedCut *cuts, float *part, int keep, int blocks, cudaStream_t st) {
     const int G = a.Hq / pv.Hkv;
-    return G <= 4   ? launch<4, MOD>(mk, mv, a, pv, cuts, part, keep, blocks, st)
-           : G <= 8 ? launch<8, MOD>(mk, mv, a, pv, cuts, part, keep, blocks, st)
-                    : launch<16, MOD>(mk, mv, a, pv, cuts, part, keep, blocks, st);
+    return G <= 4   ? launch<4, MODE>(mk, mv, a, pv, cuts, part, keep, blocks, st)
+           : G <= 8 ? launch<8, MODE>(mk, mv, a, pv, cuts, part, keep, blocks, st)
+                    : launch<16, MODE>(mk, mv, a, pv, cuts, part, keep, blocks, st);
 }
 
 cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blocks, cudaStream_t st) {
@@ -518,8 +539,12 @@ cudaError_t paged_decode_tc(const PagedArgs &a, void *cuts, float *part, int blo
     const int64_t page_bytes = (int64_t)a.cache->page_size * a.cache->Hkv * kPD * 2 * 2;
     const int keep = (int)(l2 / 2 / page_bytes);
     PagedCut *pc = (PagedCut *)cuts;
-    return a.scores ? launch_heads<true>(mk, mv, a, pv, pc, part, keep, blocks, st)
-                    : launch_heads<false>(mk, mv, a, pv, pc, part, keep, blocks, st);
+    if (!a.scores) return launch_heads<0>(mk, mv, a, pv, pc, part, keep, blocks, st);
+    const bool cap = a.scores->softcap > 0.f, bias = a.scores->slopes != nullptr;
+    if (cap && bias) return launch_heads<kModMask + kModCap + kModBias>(mk, mv, a, pv, pc, part, keep, blocks, st);
+    return cap    ? launch_heads<kModMask + kModCap>(mk, mv, a, pv, pc, part, keep, blocks, st)
+           : bias ? launch_heads<kModMask + kModBias>(mk, mv, a, pv, pc, part, keep, blocks, st)
+                  : launch_heads<kModMask>(mk, mv, a, pv, pc, part, keep, blocks, st);
 }
 
 }  // namespace yoco_host

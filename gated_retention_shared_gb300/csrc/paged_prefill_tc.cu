@@ -101,9 +101,6 @@ constexpr size_t kCTileBytes = (size_t)3 * kCTile + (size_t)kCStages * 2 * kCTil
 template <bool MOD> constexpr size_t kCSmem = kCTileBytes + sizeof(PagedPreSmem<MOD>) + 1024;
 static_assert(kCSmem<true> <= 232448, "paged prefill tiles must fit shared memory");
 
-// what a kernel's rows do to their scores before the softmax, beyond the masks of the plain calls
-constexpr int kModMask = 1, kModCap = 2, kModBias = 4;
-
 __device__ __forceinline__ void cbar(int id) {  // the four warps of a set
     __syncwarp();
     asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory");

@@ -141,7 +141,7 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
 #pragma unroll
                         for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
                         if constexpr (MOD) {
-                            if (mod.cap2 > 0.f) d = mod.cap2 * tanhf(d);
+                            if (mod.cap2 > 0.f) d = paged_cap(d, mod.cap2);
                             if (mod.slopes) d = fmaf(-slope[i], far[x], d);
                         }
                         s[x] = ok[x] ? d : -INFINITY;
@@ -422,7 +422,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
                 bool seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
                 if constexpr (MOD) {
                     seen = (seen || key < blk.range.pre) && key >= doc[i] && pos >= 0;
-                    if (mod.cap2 > 0.f) s[i][x] = mod.cap2 * tanhf(s[i][x]);
+                    if (mod.cap2 > 0.f) s[i][x] = paged_cap(s[i][x], mod.cap2);
                     if (mod.slopes) s[i][x] = fmaf(-slope[i], fabsf((float)(pos - key)), s[i][x]);
                 }
                 if (!seen) s[i][x] = -INFINITY;

@@ -6,8 +6,8 @@ each weight by that and a few u, the sums by n u, all twice for numerator and de
 rounded to bf16 for the tensor cores by 2^-8 at most) with, for what comes after q.k, with Y the
 largest |cap tanh(x / cap)| and B the largest slope * distance of the slots that the row sees,
   cap    eta Y: eta = 1.5e-6 in bf16 at head size 128 (a polynomial of relative error 1.01e-6 or
-         exponential and reciprocal of 2^-22 each, and six roundings), else 16 u (a tanh of 2 ulp and
-         as many).  (It does not enlarge the error of its argument: its slope is at most 1.)
+         exponential and reciprocal of 2^-22 each, and six roundings), else 16 u (a polynomial of 6e-8
+         or exponential and reciprocal of 4 u and 2 u, of which at most 0.76 come through, and as many).  (It does not enlarge the error of its argument: its slope is at most 1.)
   bias   8 u (Y + B): the slope times log2(e), the product, and the sum, in two steps
 each twice as well.
 """
