@@ -173,20 +173,24 @@ __device__ __forceinline__ bool paged_blind(int pos, int doc, int pre) {
     return pos < 0 || (doc > pos && max(doc, 0) >= pre);
 }
 
-// C tanh(u): in [-0.8, 0.8] u times the minimax polynomial of tanh(u) / u in u^2 (own fit by
-// reweighted least squares, relative error 6e-8), outside C - 2 C / (1 + e^2u), where nothing cancels.
+// C tanh(u): in [-0.8, 0.8] (paged_cap_near) u times the minimax polynomial of tanh(u) / u in u^2 (own fit
+// by reweighted least squares, relative error 6e-8), outside C - 2 C / (1 + e^2u), where nothing cancels.
 // The error stays relative to the result, so a cap far above the scores costs no precision.
-__device__ __forceinline__ float paged_cap(float u, float C) {
+constexpr float kCapNear = 0.8f;
+__device__ __forceinline__ float paged_cap_near(float u, float C) {
     const float x = u * u;
     float q = fmaf(x, -0.00435529966f, 0.019093302f);
     q = fmaf(x, q, -0.0531143173f);
     q = fmaf(x, q, 0.133210484f);
     q = fmaf(x, q, -0.333326749f);
     q = fmaf(x, q, 0.999999942f);
+    return C * (u * q);
+}
+__device__ __forceinline__ float paged_cap(float u, float C) {
     float e, i;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(u * 2.8853900817779268f));
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(i) : "f"(1.f + e));
-    return fabsf(u) < 0.8f ? C * (u * q) : fmaf(-2.f * C, i, C);
+    return fabsf(u) < kCapNear ? paged_cap_near(u, C) : fmaf(-2.f * C, i, C);
 }
 
 // what a tensor-core kernel's rows do to their scores before the softmax, beyond the plain calls'

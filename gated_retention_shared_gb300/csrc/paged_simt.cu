@@ -374,13 +374,19 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         for (int i = 0; i < EV; ++i) sq[r * D + ch * EV + i] = c2 * x[i];
     }
     float m[4], l[4], acc[4][4 * NJ];
-    [[maybe_unused]] int doc[MOD ? 4 : 1];
+    // a scored call's row sees `run` slots from lo on (its window, from its document's start) and
+    // `head` from doc on (of the document's the prefix and the sinks)
+    [[maybe_unused]] int lo[MOD ? 4 : 1], run[MOD ? 4 : 1], doc[MOD ? 4 : 1], head[MOD ? 4 : 1];
     [[maybe_unused]] float slope[MOD ? 4 : 1];  // times log2(e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (MOD) {
             const int r = 4 * ty + i;
-            doc[i] = mod.doc && r < nr ? mod.doc[blk.row0 + r / G] : 0;
+            const int pos = blk.pos0 + r / G;
+            doc[i] = mod.doc && r < nr ? max(0, mod.doc[blk.row0 + r / G]) : 0;
+            lo[i] = max(doc[i], pv.window > 0 ? pos + 1 - pv.window : 0);
+            run[i] = max(0, pos + 1 - lo[i]);
+            head[i] = pos < 0 ? 0 : max(0, max(blk.range.pre, min(pv.sinks, pos + 1)) - doc[i]);
             slope[i] = mod.slopes && r < nr ? mod.slopes[hk * G + r % G] * kPagedLog2E : 0.f;
         }
         m[i] = -INFINITY;
@@ -412,6 +418,40 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         }
         __syncthreads();  // K read by everyone
         stage_k.issue(K, sk, at[(t + 1) & 1]);
+        // distances are taken from the step's first slot (fewer conversions)
+        [[maybe_unused]] int k0 = 0;
+        [[maybe_unused]] float to[4];
+        if constexpr (MOD) {
+            k0 = blk.range.slot(v0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) to[x] = (float)(blk.range.slot(v0 + tx + 16 * x) - k0);
+            if (mod.cap2 > 0.f) {
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) most = fmaxf(most, fabsf(s[i][x]));
+                if (__all_sync(0xffffffffu, most < kCapNear)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[i][x] = paged_cap_near(s[i][x], mod.cap2);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[i][x] = paged_cap(s[i][x], mod.cap2);
+                }
+            }
+            if (mod.slopes) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float from = (float)(blk.pos0 + (4 * ty + i) / G - k0);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[i][x] = fmaf(-slope[i], fabsf(from - to[x]), s[i][x]);
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pos = blk.pos0 + (4 * ty + i) / G;
@@ -419,12 +459,9 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int key = blk.range.slot(v0 + tx + 16 * x);
-                bool seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
-                if constexpr (MOD) {
-                    seen = (seen || key < blk.range.pre) && key >= doc[i] && pos >= 0;
-                    if (mod.cap2 > 0.f) s[i][x] = paged_cap(s[i][x], mod.cap2);
-                    if (mod.slopes) s[i][x] = fmaf(-slope[i], fabsf((float)(pos - key)), s[i][x]);
-                }
+                bool seen;
+                if constexpr (MOD) seen = (unsigned)(key - lo[i]) < (unsigned)run[i] || (unsigned)(key - doc[i]) < (unsigned)head[i];
+                else seen = key <= pos && (pv.window <= 0 || key > pos - pv.window || key < pv.sinks);
                 if (!seen) s[i][x] = -INFINITY;
                 top = fmaxf(top, s[i][x]);
             }
@@ -494,7 +531,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         } else if (r < nr) {
             const float inv = 1.f / l[i];            // (0 / 0 where every score is -inf: NaN, as softmax has it)
             bool none = blk.pos0 + r / G < 0;  // sees nothing: zero, though 0 times a value may be NaN
-            if constexpr (MOD) none = paged_blind(blk.pos0 + r / G, doc[i], blk.range.pre);
+            if constexpr (MOD) none = run[i] == 0 && head[i] == 0;
             T *op = O + (blk.row0 + r / G) * row_stride + (size_t)(hk * G + r % G) * D;
             if (!YOCO_DCHECK(blk.row0 + r / G < rows && hk * G + r % G < Hq, 0x65)) continue;
 #pragma unroll
