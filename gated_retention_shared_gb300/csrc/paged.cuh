@@ -187,10 +187,11 @@ __device__ __forceinline__ float paged_cap_near(float u, float C) {
     return C * (u * q);
 }
 __device__ __forceinline__ float paged_cap(float u, float C) {
+    const float near = paged_cap_near(u, C);
     float e, i;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(u * 2.8853900817779268f));
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(i) : "f"(1.f + e));
-    return fabsf(u) < kCapNear ? paged_cap_near(u, C) : fmaf(-2.f * C, i, C);
+    return fabsf(u) < kCapNear ? near : fmaf(-2.f * C, i, C);
 }
 
 // what a tensor-core kernel's rows do to their scores before the softmax, beyond the plain calls'
