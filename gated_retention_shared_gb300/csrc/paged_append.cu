@@ -35,7 +35,7 @@ struct PagedAppend {
 };
 
 constexpr int kAppendWarps = 4;
-constexpr int kUnroll = 5;
+constexpr int kUnroll = 5, kRopeHalvesUnroll = 4;
 
 // Finds the sequences that have `row` and calls put(pos, b, turn_q) for each, all lanes together.
 template <typename Put>
@@ -159,29 +159,38 @@ paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const Ro
 template <typename T, int D, bool HALVES>
 __global__ void __launch_bounds__(kAppendWarps * 32)
 paged_append_rope_kernel(const PagedAppend a, const PagedView pv, int parts, const __grid_constant__ RopeScaled r) {
-    constexpr int U = HALVES ? 3 : 5;  // heads in flight
+    constexpr int U = HALVES ? kRopeHalvesUnroll : kUnroll;  // heads in flight
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int row = (int)(item / parts), part = (int)(item % parts);
     if (row >= a.rows) return;
-    const int unit = lane & (r.lanes - 1), step = 32 / r.lanes;  // heads at a time
+    RopeUnit<T, D, HALVES> u;
+    constexpr int step = 32 / u.N;  // heads at a time
+    const int unit = lane % u.N, h_first = part * step + lane / u.N;
+    const int nkv = a.k ? pv.Hkv : 0, all = 2 * nkv + (a.q ? a.Hq : 0);
+    u.place(r, unit);
+    uint4 v[U], w[U];
+    auto load = [&](int h0, int heads) {  // heads h0, h0 + parts step .. in the order k, v, q
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+            const int h = h0 + x * parts * step;
+            if (h >= heads) break;
+            u.load(h < nkv       ? a.k + row * a.k_row + h * a.k_head
+                   : h < 2 * nkv ? a.v + row * a.v_row + (h - nkv) * a.v_head
+                                 : a.q + row * a.q_row + (h - 2 * nkv) * a.q_head,
+                   v[x], w[x]);
+        }
+    };
+    load(h_first, all);  // on its way while the row's place is looked up
+    bool there = true;
     append_row(a, pv, row, lane, [&](int pos, int b, bool turn_q) {
-        const int nkv = a.k ? pv.Hkv : 0, heads = unit < r.units ? 2 * nkv + (turn_q ? a.Hq : 0) : 0;
-        RopeUnit<T, D, HALVES> u;
-        u.init(r, unit, pos, true);
+        const int heads = turn_q ? all : min(all, 2 * nkv);
+        u.turn_by(r, unit, pos);
         const int64_t slot = append_slot<T, D>(a, pv, pos, b, nkv);
         const int64_t head_bytes = ((int64_t)D * sizeof(T)) << pv.shift;
-        for (int h0 = part * step + lane / r.lanes; h0 < heads; h0 += parts * step * U) {
-            uint4 v[U], w[U];
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-                const int h = h0 + x * parts * step;
-                if (h >= heads) break;
-                u.load(h < nkv       ? a.k + row * a.k_row + h * a.k_head
-                       : h < 2 * nkv ? a.v + row * a.v_row + (h - nkv) * a.v_head
-                                     : a.q + row * a.q_row + (h - 2 * nkv) * a.q_head,
-                       v[x], w[x]);
-            }
+        for (int h0 = h_first; h0 < heads; h0 += parts * step * U) {
+            if (!there) load(h0, heads);
+            there = false;
 #pragma unroll
             for (int x = 0; x < U; ++x) {
                 const int h = h0 + x * parts * step;
@@ -197,6 +206,7 @@ paged_append_rope_kernel(const PagedAppend a, const PagedView pv, int parts, con
                 }
             }
         }
+        there = false;
     });
 }
 
@@ -270,14 +280,13 @@ static cudaError_t append_launch(const PagedAppend &p, const PagedView &pv, cons
 template <typename T, int D>
 static cudaError_t append_rope_launch(const PagedAppend &p, const PagedView &pv, const yoco_rope &rope, cudaStream_t st) {
     const RopeScaled &r = rope_scaled(rope, D, 16 / (int)sizeof(T));
+    const bool halves = rope.layout == YOCO_ROPE_HALVES;
     int64_t blocks;
-    const int parts = append_parts(p, pv, 32 / r.lanes, blocks);
+    const int parts = append_parts(p, pv, 32 / (halves ? RopeUnit<T, D, true>::N : RopeUnit<T, D, false>::N), blocks);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     count_launches(1);
-    if (rope.layout == YOCO_ROPE_HALVES)
-        paged_append_rope_kernel<T, D, true><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, r);
-    else
-        paged_append_rope_kernel<T, D, false><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, r);
+    if (halves) paged_append_rope_kernel<T, D, true><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, r);
+    else paged_append_rope_kernel<T, D, false><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(p, pv, parts, r);
     return cudaGetLastError();
 }
 

@@ -34,19 +34,24 @@ rope_scaled_kernel(const RopeRows a, int parts, const __grid_constant__ RopeScal
     const int64_t item = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     const int row = (int)(item / parts), part = (int)(item % parts);
     if (row >= a.rows) return;
-    const int unit = lane & (r.lanes - 1), step = 32 / r.lanes;  // heads at a time
-    if (unit >= r.units) return;
     RopeUnit<T, D, HALVES> u;
-    u.init(r, unit, a.positions ? a.positions[row] : a.pos0 + row, true);
+    constexpr int step = 32 / u.N;  // heads at a time
+    const int unit = lane % u.N;
+    u.place(r, unit);
     const uint8_t *x = a.x + row * a.x_row;
     uint8_t *out = a.out + row * a.out_row;
-    for (int h0 = part * step + lane / r.lanes; h0 < a.H; h0 += parts * step * U) {
-        uint4 v[U], w[U];
+    uint4 v[U], w[U];
+    auto load = [&](int h0) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int h = h0 + k * parts * step;
             if (h < a.H) u.load(x + h * a.x_head, v[k], w[k]);
         }
+    };
+    int h0 = part * step + lane / u.N;
+    load(h0);  // on its way while the angles are formed
+    u.turn_by(r, unit, a.positions ? a.positions[row] : a.pos0 + row);
+    for (;;) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int h = h0 + k * parts * step;
@@ -55,6 +60,9 @@ rope_scaled_kernel(const RopeRows a, int parts, const __grid_constant__ RopeScal
             if (!YOCO_DCHECK(h < a.H && row < a.rows && u.far < D, 0x69)) continue;
             u.store(out + h * a.out_head, v[k], w[k]);
         }
+        h0 += parts * step * U;
+        if (h0 >= a.H) break;
+        load(h0);
     }
 }
 
@@ -84,11 +92,7 @@ const RopeScaled &rope_scaled(const yoco_rope &rope, int d, int per16) {
         t.turns.f[i] = (uint64_t)std::ldexp(theta / kRopeTwoPi, 64);
     }
     t.magnitude = rope.magnitude;
-    const int chunks = d / per16, turning = r / per16;
-    t.paired = rope.layout == YOCO_ROPE_HALVES ? turning / 2 : turning;
-    t.units = t.paired + chunks - turning;
-    t.lanes = 1;
-    while (t.lanes < t.units) t.lanes *= 2;
+    t.paired = r / per16 / (rope.layout == YOCO_ROPE_HALVES ? 2 : 1);
     of = rope;
     of_d = d;
     of_per = per16;
@@ -99,7 +103,7 @@ template <typename T, int D, bool HALVES>
 static cudaError_t rope_launch(const RopeRows &a, const RopeScaled &r, cudaStream_t st) {
     // a warp per row, or up to one per group of heads while that leaves the SMs with fewer than
     // 16 warps each
-    const int step = 32 / r.lanes;
+    constexpr int step = 32 / RopeUnit<T, D, HALVES>::N;
     const int64_t want = (int64_t)device_sm_count() * 16;
     const int parts = (int)std::max<int64_t>(1, std::min<int64_t>((a.H + step - 1) / step, want / a.rows));
     const int64_t blocks = ((int64_t)a.rows * parts + kRopeWarps - 1) / kRopeWarps;

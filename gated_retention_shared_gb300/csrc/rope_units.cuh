@@ -4,9 +4,10 @@
 //
 // A head is cut into units that one lane turns alone: with pairs (2i, 2i+1) one 16-byte chunk of
 // the channels, with halves (i, i + r/2) the two chunks whose channels turn together, so no lane
-// needs another's values and a row may be turned in place.  Chunks past the r channels are units
-// that are copied.  A lane keeps its unit from head to head, so the cosines and sines of a row
-// are formed once.
+// needs another's values and a row may be turned in place.  Past the r channels a unit is as many
+// chunks, which are copied: all lanes have the same to move (with units of one chunk there, half a
+// head turned took 46 us in place of 32, 12000 rows of 32 heads).  A lane keeps its unit from head to
+// head, so the cosines and sines of a row are formed once.
 //
 // The angle p theta_i is kept in turns as 64-bit fixed point: theta_i / 2 pi is a fraction F_i of
 // 2^64 (formed on the host in fp64), p F_i wraps modulo one turn by itself, and its top 32 bits,
@@ -25,26 +26,27 @@ struct RopeTurns {
 struct RopeScaled {
     RopeTurns turns;
     float magnitude;
-    int units;   // of a head
-    int paired;  // of them, those that turn: the first ones
-    int lanes;   // a head's lanes: a power of two, >= units
+    int paired;  // of a head's units, those that turn: the first ones
 };
 
 template <typename T, int D, bool HALVES> struct RopeUnit {
     static constexpr int EV = 16 / (int)sizeof(T);     // channels of a chunk
     static constexpr int R = HALVES ? EV : EV / 2;     // pairs of a unit
+    static constexpr int N = D / EV / (HALVES ? 2 : 1);  // units of a head, a lane each
     float c[R], s[R];
-    int at, far;  // first channel of the chunk, and of its partner (halves; else at)
+    int at, far;  // first channel of the chunk, and of the other one (halves; else at)
     bool turns;
-    __device__ __forceinline__ void init(const RopeScaled &r, int unit, int64_t pos, bool on) {
+    __device__ __forceinline__ void place(const RopeScaled &r, int unit) {
         turns = unit < r.paired;
-        at = EV * (HALVES && !turns ? unit + r.paired : unit);
-        far = HALVES && turns ? at + EV * r.paired : at;
+        at = EV * (HALVES && !turns ? 2 * unit : unit);
+        far = !HALVES ? at : at + EV * (turns ? r.paired : 1);
+    }
+    __device__ __forceinline__ void turn_by(const RopeScaled &r, int unit, int64_t pos) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             c[i] = 1.f;
             s[i] = 0.f;
-            if (turns && on) {
+            if (turns) {
                 const uint64_t u = (uint64_t)pos * r.turns.f[min(unit * R + i, 63)];
                 sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &s[i], &c[i]);
                 c[i] *= r.magnitude;
@@ -54,7 +56,7 @@ template <typename T, int D, bool HALVES> struct RopeUnit {
     }
     __device__ __forceinline__ void load(const uint8_t *head, uint4 &a, uint4 &b) const {
         a = *reinterpret_cast<const uint4 *>(head + at * sizeof(T));
-        if (HALVES && turns) b = *reinterpret_cast<const uint4 *>(head + far * sizeof(T));
+        if constexpr (HALVES) b = *reinterpret_cast<const uint4 *>(head + far * sizeof(T));
     }
     __device__ __forceinline__ void turn(uint4 &a, uint4 &b) const {
         uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -97,7 +99,7 @@ template <typename T, int D, bool HALVES> struct RopeUnit {
     }
     __device__ __forceinline__ void store(uint8_t *head, const uint4 &a, const uint4 &b) const {
         *reinterpret_cast<uint4 *>(head + at * sizeof(T)) = a;
-        if (HALVES && turns) *reinterpret_cast<uint4 *>(head + far * sizeof(T)) = b;
+        if constexpr (HALVES) *reinterpret_cast<uint4 *>(head + far * sizeof(T)) = b;
     }
 };
 
