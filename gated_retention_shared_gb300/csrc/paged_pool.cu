@@ -32,6 +32,7 @@ constexpr int kPoolThreads = 256;
 constexpr int kClusterBlocks = 8, kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterBlocks * kClusterThreads / 32;
 constexpr int kShareEach = kPagedMaxB / kClusterThreads;
+constexpr int kPoolLoads = 16;  // of refs, of a lane at a time
 constexpr int kPoolUnroll = 4, kPoolStep = kPoolUnroll * kClusterBlocks * kClusterThreads;  // table entries of a thread at a time
 constexpr int kShareSlots = 2 * kPagedMaxB;  // of the table of shared pages
 
@@ -69,12 +70,10 @@ __device__ __forceinline__ void pool_lens(const PoolView &v, const int32_t *new_
     }
 }
 
-// page e of sequence b, or -1
-__device__ __forceinline__ int pool_page(const PoolView &v, int b, int e) {
-    const int p = v.table[(size_t)b * v.max_pages + e];
-    if ((unsigned)p < (unsigned)v.num_pages) return p;
-    paged_report(v.err, kErrPagedPage);
-    return -1;
+// whether a table entry names a page; below 0 it says that there is none (a window has left it)
+__device__ __forceinline__ bool pool_names(const PoolView &v, int p) {
+    if (p >= v.num_pages) paged_report(v.err, kErrPagedPage);
+    return (unsigned)p < (unsigned)v.num_pages;
 }
 
 // exclusive prefix sums of x over the block's threads; `sums` one per warp; total: of all
@@ -152,16 +151,16 @@ __device__ __forceinline__ void pool_run(const PoolView &v, int w, int warps, in
     p1 = (int)min((long long)p0 + per, (long long)v.num_pages);
 }
 
-// how many pages of a run are used (or free), eight loads of a lane in flight
+// how many pages of a run are used (or free), kPoolLoads loads of a lane in flight
 template <bool USED> __device__ __forceinline__ int pool_count(const PoolView &v, int p0, int p1) {
     const int lane = threadIdx.x & 31;
     int n = 0;
-    for (int p = p0 + lane; p < p1; p += 256) {
-        int r[8];
+    for (int p = p0 + lane; p < p1; p += 32 * kPoolLoads) {
+        int r[kPoolLoads];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] = p + 32 * k < p1 ? __ldcg(v.refs + p + 32 * k) : (USED ? 0 : 1);
+        for (int k = 0; k < kPoolLoads; ++k) r[k] = p + 32 * k < p1 ? __ldcg(v.refs + p + 32 * k) : (USED ? 0 : 1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) n += (r[k] > 0) == USED;
+        for (int k = 0; k < kPoolLoads; ++k) n += (r[k] > 0) == USED;
     }
     return __reduce_add_sync(0xffffffffu, n);
 }
@@ -273,7 +272,11 @@ pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
         sm.from[b0 + k] = pool_pages(v, N[k]);
         sm.before[b0 + k] = max(0, pool_pages(v, L[k]) - pool_pages(v, N[k]));
         mine += sm.before[b0 + k];
-        if (rank == 0 && N[k] > L[k] && (L[k] & ((1 << v.shift) - 1))) page[k] = pool_page(v, b0 + k, pool_pages(v, L[k]) - 1);
+        if (rank == 0 && N[k] > L[k] && (L[k] & ((1 << v.shift) - 1))) {
+            const int p = v.table[(size_t)(b0 + k) * v.max_pages + pool_pages(v, L[k]) - 1];
+            if ((unsigned)p < (unsigned)v.num_pages) page[k] = p;
+            else paged_report(v.err, kErrPagedPage);  // (the page that is written next has to be there)
+        }
     }
     long long run = pool_scan<kClusterThreads>(mine, sm.sums, drops);
     cluster_wait();
@@ -306,8 +309,7 @@ pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
                 was[u] = 1;
                 if (!at[u]) continue;
                 *at[u] = -1;
-                if ((unsigned)p[u] < (unsigned)v.num_pages) was[u] = atomicSub(v.refs + p[u], 1);
-                else paged_report(v.err, kErrPagedPage);
+                if (pool_names(v, p[u])) was[u] = atomicSub(v.refs + p[u], 1);
             }
 #pragma unroll
             for (int u = 0; u < kPoolUnroll; ++u) {
@@ -347,12 +349,12 @@ pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
         }
     }
     if (!room || total == 0) return;
-    for (int q = p0 + lane; q - lane < p1 && r < total; q += 256) {
-        int refs[8];
+    for (int q = p0 + lane; q - lane < p1 && r < total; q += 32 * kPoolLoads) {
+        int refs[kPoolLoads];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 1;
+        for (int k = 0; k < kPoolLoads; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 1;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kPoolLoads; ++k) {
             const bool free = refs[k] <= 0;
             const unsigned who = __ballot_sync(0xffffffffu, free);
             const int i = r + __popc(who & ((1u << lane) - 1));
@@ -407,9 +409,9 @@ pool_fork_kernel(const PoolView v, const int32_t *src, const int32_t *dst, int n
     }
     __syncthreads();
     for (int e = threadIdx.x, held = pool_pages(v, L); e < held; e += kPoolThreads) {
-        const int p = pool_page(v, a, e);
+        const int p = v.table[(size_t)a * v.max_pages + e];
         v.table[(size_t)b * v.max_pages + e] = p;
-        if (p >= 0) atomicAdd(v.refs + p, 1);
+        if (pool_names(v, p)) atomicAdd(v.refs + p, 1);
     }
     if (threadIdx.x == 0) v.lens[b] = L;
 }
@@ -449,12 +451,12 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
     if (live == in_front) return;
     int *moves = reinterpret_cast<int *>(v.moves + 1);
     // (a run before page `live` has holes, one behind it pages that move)
-    for (int q = p0 + lane; q - lane < p1; q += 256) {
-        int refs[8];
+    for (int q = p0 + lane; q - lane < p1; q += 32 * kPoolLoads) {
+        int refs[kPoolLoads];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 0;
+        for (int k = 0; k < kPoolLoads; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kPoolLoads; ++k) {
             const int p = q + 32 * k;
             const bool is = refs[k] > 0;
             const unsigned who = __ballot_sync(0xffffffffu, is);
@@ -493,11 +495,7 @@ __device__ __forceinline__ void pool_follow(const PoolView &v) {
         for (int e = threadIdx.x, held = pool_pages(v, L); e < held; e += kPoolThreads) {
             int32_t *at = v.table + (size_t)b * v.max_pages + e;
             const int p = paged_ld(at);
-            if (p < live && p >= 0) continue;
-            if ((unsigned)p >= (unsigned)v.num_pages) {
-                paged_report(v.err, kErrPagedPage);
-                continue;
-            }
+            if (p < live || !pool_names(v, p)) continue;
             const int r = paged_ld(v.rank + p);  // (of a page that was not counted as used: anything)
             const int4 m = (unsigned)r < (unsigned)count ? __ldcg(v.moves + 1 + r) : make_int4(-1, 0, 0, 0);
             if (m.x == p) *at = m.y;

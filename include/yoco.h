@@ -585,7 +585,9 @@ YOCO_API yoco_status yoco_paged_attn_decode_scored(const void *Q, int Hq, const 
  * Handing out the pages of a yoco_paged_kv, on the device and in the stream's order:
  *   refs   device int32 [num_pages], the caller's: how many of the sequences' table entries name the
  *          page (entries that hold a slot: the first ceil(seq_lens[b] / page_size) of sequence b).
- *          0: the page is free.  A new pool: refs and seq_lens all 0.
+ *          0: the page is free.  A new pool: refs and seq_lens all 0.  An entry below 0 names no
+ *          page: a caller that gives back a page that no row sees any more (a window has passed it)
+ *          takes 1 off its refs and writes -1 there.
  * These calls, and no others, write the cache's page_table and seq_lens (the memory that these
  * members of the struct point to has to be writable) and refs.  Nothing is read back and nothing
  * waits, so they are captured like the rest; what they decide goes by the device's values alone and
@@ -600,8 +602,8 @@ YOCO_API yoco_status yoco_paged_attn_decode_scored(const void *Q, int Hq, const 
  *              of page `from` went to `to`, in k and v of `cache`.  Where other caches (layers) share
  *              the table, yoco_paged_copy does the same there.
  *
- * yoco_paged_resize: sequence b gets length new_lens[b] (device int32 [B]; below 0: it stays as it
- * is).
+ * yoco_paged_resize: sequence b gets length new_lens[b] (device int32 [B], memory of its own; below
+ * 0: it stays as it is).
  *   - Pages behind a shorter sequence's end go back (their entries become -1); 0 frees it all.
  *   - Then a longer one gets the pages it lacks.  A page in which it will write its next slot and
  *     that other sequences have as well (refs > 1) is replaced by a copy of the slots it holds; but

@@ -271,6 +271,58 @@ def test_bad_lengths_entries_and_counts_are_recorded(Y):
     bad(fork_bad_len)
 
 
+def test_pages_that_a_window_has_left(Y):
+    """Entries of -1 in front are passed over by every call, and stay -1."""
+    def ints(*x):
+        return torch.tensor(x, dtype=torch.int32).cuda()
+    s = Pair(Y, 4, 30, 16, 8)
+    s.resize([60, 100, 0, 0])
+    for e in (0, 1, 2):  # given back by the caller
+        s.refs[s.m.table[1][e]] -= 1
+    s.cache.page_table[1, :3] = -1
+    Y.yoco_paged_fork(s.cache, s.refs, ints(1), ints(2), workspace=s.ws)
+    Y.yoco_paged_resize(s.cache, s.refs, ints(0, 101, 110, 20), workspace=s.ws)
+    Y.yoco_paged_compact(s.cache, s.refs, workspace=s.ws)
+    Y.yoco_workspace_status(s.ws)
+    table = s.cache.page_table.cpu()
+    assert table[1, :3].tolist() == table[2, :3].tolist() == [-1] * 3
+    pages = [p for row in table.tolist() for p in row if p >= 0]
+    # 4 pages of sequence 1, of which 3 are sequence 2's too; its copy of the fourth; 2 of sequence 3
+    assert sorted(set(pages)) == list(range(7)) and int((s.refs > 0).sum()) == 7
+    assert s.refs.tolist() == [pages.count(p) for p in range(30)]
+    Y.yoco_paged_resize(s.cache, s.refs, ints(0, 0, 0, 0), workspace=s.ws)
+    Y.yoco_workspace_status(s.ws)
+    assert int(s.refs.abs().sum()) == 0
+
+
+def test_large_pool(Y):
+    """More pages than a pass of the warps' runs takes at once, handed out and moved across all of them."""
+    pages, page, most = 400000, 16, 5000
+    k = torch.zeros(pages, 1, page, 64, dtype=torch.bfloat16, device="cuda")
+    k[:, 0, 0, 0] = torch.arange(pages, device="cuda").remainder(256).to(torch.bfloat16)
+    cache = Y.PagedKV(k, k.clone(), torch.full((100, most), -1, dtype=torch.int32).cuda(), torch.zeros(100, dtype=torch.int32).cuda())
+    refs = torch.zeros(pages, dtype=torch.int32).cuda()
+    ws = torch.zeros(Y.yoco_paged_pool_workspace_size(cache), dtype=torch.uint8).cuda()
+    Y.yoco_paged_resize(cache, refs, torch.full((100,), 4000 * page - 3, dtype=torch.int32).cuda(), workspace=ws)
+    assert torch.equal(cache.page_table[:, :4000].reshape(-1), torch.arange(pages, dtype=torch.int32, device="cuda"))
+    low = torch.where(torch.arange(100) % 3 == 1, 0, -1).to(torch.int32).cuda()
+    Y.yoco_paged_resize(cache, refs, low, workspace=ws)
+    kept = (torch.arange(100, device="cuda") % 3 != 1).nonzero()[:, 0]
+    marks = cache.page_table[kept, :4000].long().remainder(256)
+    Y.yoco_paged_compact(cache, refs, workspace=ws)
+    Y.yoco_workspace_status(ws)
+    n = len(kept) * 4000
+    now = cache.page_table[kept, :4000].long()
+    assert torch.equal(now.reshape(-1).sort()[0], torch.arange(n, device="cuda"))
+    assert bool((refs[:n] == 1).all()) and bool((refs[n:] == 0).all())
+    for t in (cache.k, cache.v):
+        assert torch.equal(t[now, 0, 0, 0].long(), marks)
+    Y.yoco_paged_resize(cache, refs, torch.full((100,), 4000 * page, dtype=torch.int32).cuda(), workspace=ws)
+    Y.yoco_workspace_status(ws)
+    assert bool((refs == 1).all())
+    assert torch.equal(cache.page_table[:, :4000].reshape(-1).sort()[0], torch.arange(pages, dtype=torch.int32, device="cuda"))
+
+
 def test_copy_leaves_out_what_names_no_page(Y):
     k = torch.randn(6, 2, 16, 64, device="cuda")
     v = torch.randn(6, 2, 16, 64, device="cuda")
