@@ -3,16 +3,16 @@
 //
 // refs[p] is how many table entries name page p; the free pages are those with 0.  Which pages a
 // call hands out goes by their numbers alone (the lowest free ones, in the order of the sequences
-// and slots), so nothing depends on the order of threads: each warp of a cluster counts the free
-// (or used) pages of a run of its own, and a page's rank is what lies in the runs before plus its
-// rank in the run; number r of those that are wanted is found in the prefix sums of what the
-// sequences need.
+// and slots), so nothing depends on the order of threads: the warps of a cluster count the free
+// (or used) pages of runs of kPoolRun, taken in turn (the lowest pages, which are handed out, are
+// then every warp's work), and a page's rank is what lies in the runs before plus its rank in the
+// run; number r of those that are wanted is found in the prefix sums of what the sequences need.
 //
 // A resize and a compact are one cluster of eight blocks, its phases divided by cluster barriers,
 // and one grid that copies: these calls are latencies one after the other, and a launch for each
 // phase cost more than what eight SMs lack in bandwidth (a search round of 8 x 4 sequences, two
-// resizes and a fork, 38 -> 27 us; a serving round of two resizes of 1024 sequences over 200000
-// pages 44 -> 38; with two blocks 64, with four 43).  A compact's grid copies at 6.9 TB/s (1.16 GB
+// resizes and a fork, 38 -> 21 us; a serving round of two resizes of 1024 sequences over 200000
+// pages 44 -> 26).  A compact's grid copies at 6.9 TB/s (1.16 GB
 // moved: 168 us), the copy rate.
 //
 // A resize: 1. sequences that shrink give pages back; 2. one block decides, per growing sequence,
@@ -33,6 +33,7 @@ constexpr int kClusterBlocks = 8, kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterBlocks * kClusterThreads / 32;
 constexpr int kShareEach = kPagedMaxB / kClusterThreads;
 constexpr int kPoolLoads = 16;  // of refs, of a lane at a time
+constexpr int kPoolRun = 32 * kPoolLoads, kPoolRuns = 8192;  // pages to a run, or more where the runs would not be enough
 constexpr int kPoolUnroll = 4, kPoolStep = kPoolUnroll * kClusterBlocks * kClusterThreads;  // table entries of a thread at a time
 constexpr int kShareSlots = 2 * kPagedMaxB;  // of the table of shared pages
 
@@ -76,25 +77,27 @@ __device__ __forceinline__ bool pool_names(const PoolView &v, int p) {
     return (unsigned)p < (unsigned)v.num_pages;
 }
 
-// exclusive prefix sums of x over the block's threads; `sums` one per warp; total: of all
-template <int THREADS, typename N> __device__ __forceinline__ N pool_scan(N x, N *sums, N &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    N inc = x;
+// exclusive prefix sums of x over the block's threads; `sums` one per warp; total: of all.  (Every
+// warp scans the warps' sums by itself: a loop over them in every thread took 3000 cycles.)
+template <typename N> __device__ __forceinline__ N pool_scan_warp(N x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const N y = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += y;
+        const N y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
     }
+    return x;
+}
+template <int THREADS, typename N> __device__ __forceinline__ N pool_scan(N x, N *sums, N &total) {
+    static_assert(THREADS == 1024, "a lane for each warp's sum");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const N inc = pool_scan_warp(x);
     __syncthreads();  // `sums` may still be read
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    N before = 0;
-    total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        before += w < warp ? sums[w] : 0;
-        total += sums[w];
-    }
-    return before + inc - x;
+    const N mine = sums[lane], all = pool_scan_warp(mine);
+    total = __shfl_sync(0xffffffffu, all, 31);
+    return inc - x + __shfl_sync(0xffffffffu, all - mine, warp);
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory"); }
@@ -103,18 +106,26 @@ __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();
 }
-// x into the same place of block `rank`'s shared memory
-__device__ __forceinline__ void cluster_put(int *at, int rank, int x) {
+// the same place in block `rank`'s shared memory
+__device__ __forceinline__ uint32_t cluster_at(const int *at, int rank) {
     uint32_t to;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
-    asm volatile("st.shared::cluster.s32 [%0], %1;\n" ::"r"(to), "r"(x) : "memory");
+    return to;
+}
+__device__ __forceinline__ void cluster_put(int *at, int rank, int x) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;\n" ::"r"(cluster_at(at, rank)), "r"(x) : "memory");
+}
+__device__ __forceinline__ int cluster_get(const int *at, int rank) {
+    int x;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(x) : "r"(cluster_at(at, rank)) : "memory");
+    return x;
 }
 
 struct PoolSmem {
     long long sums[kClusterThreads / 32];
     int before[kPagedMaxB + 1];  // entries that go back of the sequences before b
     int from[kPagedMaxB];        // first of them in the table
-    int count[kClusterWarps];    // free (used) pages of each warp's run
+    int count[kPoolRuns];        // free (used) pages of each run, then of those before it
     int start[kPagedMaxB + 1];   // as in PoolView
     int first[kPagedMaxB];
 };
@@ -144,14 +155,13 @@ __device__ __forceinline__ int pool_owner(const int *before, int B, int i) {
     return lo;
 }
 
-// A warp's run of pages: [p0, p1), the same for every pass; `w` of `warps`
-__device__ __forceinline__ void pool_run(const PoolView &v, int w, int warps, int &p0, int &p1) {
-    const int per = ((v.num_pages + warps - 1) / warps + 31) / 32 * 32;
-    p0 = (int)min((long long)w * per, (long long)v.num_pages);
-    p1 = (int)min((long long)p0 + per, (long long)v.num_pages);
+// pages to a run
+__device__ __forceinline__ int pool_per(const PoolView &v) {
+    const int least = (int)(((long long)v.num_pages + kPoolRuns - 1) / kPoolRuns);
+    return max(kPoolRun, (least + 31) / 32 * 32);
 }
 
-// how many pages of a run are used (or free), kPoolLoads loads of a lane in flight
+// how many pages of [p0, p1) are used (or free), kPoolLoads loads of a lane in flight
 template <bool USED> __device__ __forceinline__ int pool_count(const PoolView &v, int p0, int p1) {
     const int lane = threadIdx.x & 31;
     int n = 0;
@@ -165,26 +175,33 @@ template <bool USED> __device__ __forceinline__ int pool_count(const PoolView &v
     return __reduce_add_sync(0xffffffffu, n);
 }
 
-// counts of the runs before run w (w may be their number), and of all; all threads of the block
-__device__ __forceinline__ void pool_before(PoolSmem &sm, int w, int warps, int &before, int &all) {
-    const int tid = threadIdx.x;
-    int total;
-    const int mine = tid < warps ? sm.count[tid] : 0;
-    const int at = pool_scan<kClusterThreads>(mine, reinterpret_cast<int *>(sm.sums), total);
-    sm.from[tid] = at;
-    __syncthreads();
-    before = w < warps ? sm.from[w] : total;
-    all = total;
-    __syncthreads();
+// counts the runs of warp w of `warps` and tells every block
+template <bool USED> __device__ __forceinline__ void pool_tell(const PoolView &v, PoolSmem &sm, int w, int warps, int per) {
+    const int lane = threadIdx.x & 31;
+    for (int run = w; (long long)run * per < v.num_pages; run += warps) {
+        const int p0 = run * per, n = pool_count<USED>(v, p0, min(p0 + per, v.num_pages));
+        if (lane < kClusterBlocks) cluster_put(&sm.count[run], lane, n);
+    }
 }
 
-// a warp's count, told to every block
-__device__ __forceinline__ void pool_tell(PoolSmem &sm, int w, int count) {
-    if ((threadIdx.x & 31) < kClusterBlocks) cluster_put(&sm.count[w], threadIdx.x & 31, count);
+// the counts become those of the runs before each; their sum; all threads of the block
+__device__ __forceinline__ int pool_before(const PoolView &v, PoolSmem &sm, int per) {
+    const int runs = (v.num_pages + per - 1) / per, each = (runs + kClusterThreads - 1) / kClusterThreads;
+    const int r0 = min(runs, (int)threadIdx.x * each), r1 = min(runs, r0 + each);
+    int mine = 0, total;
+    for (int k = r0; k < r1; ++k) mine += sm.count[k];
+    int before = pool_scan<kClusterThreads>(mine, reinterpret_cast<int *>(sm.sums), total);
+    for (int k = r0; k < r1; ++k) {
+        const int n = sm.count[k];
+        sm.count[k] = before;
+        before += n;
+    }
+    __syncthreads();
+    return total;
 }
 
 // Of the sequences that grow: what they need and which pages have to be copied, into v's scratch and
-// every block's start and first; one block.  page[k]: the page that holds the last slot of its sequence b0 + k, where that is not full.
+// the block's start and first; one block.  page[k]: the page that holds the last slot of its sequence b0 + k, where that is not full.
 __device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kShareEach], const int (&N)[kShareEach],
                                            const int (&page)[kShareEach], int each, PoolSmem &sm, PoolShared &t) {
     const int b0 = threadIdx.x * each;
@@ -212,7 +229,10 @@ __device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kSh
         }
         __syncthreads();
     }
-    long long sum = 0, made = 0;  // (what all sequences ask for may pass 32 bits)
+    // what is needed and, in the low 13 bits, how many copies that makes (all that sequences ask for may
+    // pass 32 bits: 4096 times 2^26 pages)
+    static_assert(kPagedMaxB < 1 << 13, "the copies of all sequences are counted in 13 bits");
+    long long sum = 0, all;
     int need[kShareEach];
     bool copy[kShareEach];
 #pragma unroll
@@ -222,30 +242,23 @@ __device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kSh
         if (copy[k] && t.grow[slot[k]] >= refs[k] && t.first[slot[k]] == b0 + k) copy[k] = false;
         if (copy[k]) atomicSub(v.refs + page[k], 1);
         need[k] = N[k] > L[k] ? pool_pages(v, N[k]) - pool_pages(v, L[k]) + copy[k] : 0;
-        sum += need[k];
-        made += copy[k];
+        sum += ((long long)need[k] << 13) + copy[k];
     }
-    long long all, all_made;
     long long before = pool_scan<kClusterThreads>(sum, sm.sums, all);
-    long long made_before = pool_scan<kClusterThreads>(made, sm.sums, all_made);
     const long long top = 0x7fffffff;
 #pragma unroll
     for (int k = 0; k < kShareEach; ++k) {
         const int b = b0 + k;
         if (k >= each || b >= v.B) break;
-#pragma unroll
-        for (int c = 0; c < kClusterBlocks; ++c) {
-            cluster_put(&sm.start[b], c, (int)min(before, top));
-            cluster_put(&sm.first[b], c, pool_pages(v, L[k]) - copy[k]);
-        }
+        sm.start[b] = (int)min(before >> 13, top);
+        sm.first[b] = pool_pages(v, L[k]) - copy[k];
         v.old[b] = copy[k] ? page[k] : -1;
         v.fill[b] = L[k] & ((1 << v.shift) - 1);
-        v.copies[b] = (int)made_before;
-        before += need[k];
-        made_before += copy[k];
+        v.copies[b] = (int)(before & 8191);
+        before += ((long long)need[k] << 13) + copy[k];
     }
-    if (threadIdx.x < kClusterBlocks) cluster_put(&sm.start[v.B], threadIdx.x, (int)min(all, top));
-    if (threadIdx.x == 0) v.copies[v.B] = (int)all_made;
+    if (threadIdx.x < kClusterBlocks) cluster_put(&sm.start[v.B], threadIdx.x, (int)min(all >> 13, top));
+    if (threadIdx.x == 0) v.copies[v.B] = (int)(all & 8191);
 }
 
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads)
@@ -321,19 +334,12 @@ pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
         cluster_sync();
     }
     // 2. the first block decides, the others count
-    const int warps = kClusterWarps - kClusterThreads / 32, w = (rank - 1) * (kClusterThreads / 32) + (tid >> 5);
-    int p0 = 0, p1 = 0;
-    if (rank == 0) {
-        pool_share(v, L, N, page, each, sm, shared);
-    } else {
-        pool_run(v, w, warps, p0, p1);
-        pool_tell(sm, w, pool_count<false>(v, p0, p1));
-    }
+    const int warps = kClusterWarps - kClusterThreads / 32, w = (rank - 1) * (kClusterThreads / 32) + (tid >> 5), per = pool_per(v);
+    if (rank == 0) pool_share(v, L, N, page, each, sm, shared);
+    else pool_tell<false>(v, sm, w, warps, per);
     cluster_sync();
     // 3. the free pages that are taken, in order
-    const int total = sm.start[v.B];
-    int r, all;
-    pool_before(sm, rank == 0 ? warps : w, warps, r, all);
+    const int total = sm.start[v.B], all = pool_before(v, sm, per);
     const bool room = total <= all;
     if (rank == 0) {
 #pragma unroll
@@ -349,33 +355,53 @@ pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
         }
     }
     if (!room || total == 0) return;
-    for (int q = p0 + lane; q - lane < p1 && r < total; q += 32 * kPoolLoads) {
-        int refs[kPoolLoads];
+    if (rank != 0) {
+        for (int b = tid; b < v.B; b += kClusterThreads) {
+            sm.start[b] = cluster_get(&sm.start[b], 0);
+            sm.first[b] = cluster_get(&sm.first[b], 0);
+        }
+        for (int run = w; (long long)run * per < v.num_pages; run += warps) {
+            int r = sm.count[run];
+            if (r >= total) break;
+            for (int q = run * per + lane, p1 = min(run * per + per, v.num_pages); q - lane < p1 && r < total; q += 32 * kPoolLoads) {
+                int refs[kPoolLoads];
 #pragma unroll
-        for (int k = 0; k < kPoolLoads; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 1;
+                for (int k = 0; k < kPoolLoads; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 1;
 #pragma unroll
-        for (int k = 0; k < kPoolLoads; ++k) {
-            const bool free = refs[k] <= 0;
-            const unsigned who = __ballot_sync(0xffffffffu, free);
-            const int i = r + __popc(who & ((1u << lane) - 1));
-            r += __popc(who);
-            if (free && i < total) {
-                v.rank[i] = q + 32 * k;
-                v.refs[q + 32 * k] = 1;
+                for (int k = 0; k < kPoolLoads; ++k) {
+                    const bool free = refs[k] <= 0;
+                    const unsigned who = __ballot_sync(0xffffffffu, free);
+                    const int i = r + __popc(who & ((1u << lane) - 1));
+                    r += __popc(who);
+                    if (free && i < total) {
+                        v.rank[i] = q + 32 * k;
+                        v.refs[q + 32 * k] = 1;
+                    }
+                }
             }
         }
     }
     cluster_sync();
-    // 4. to whom they go
-#pragma unroll 4
-    for (int i = rank * kClusterThreads + tid; i < total; i += kClusterBlocks * kClusterThreads) {
-        const int p = __ldcg(v.rank + i);
-        const int b = pool_owner(sm.start, v.B, i), idx = i - sm.start[b], e = sm.first[b] + idx;
-        if (!YOCO_DCHECK(b < v.B && e < v.max_pages, 0x6B)) continue;
-        v.table[(size_t)b * v.max_pages + e] = p;
-        if (idx == 0) {
-            const int old = __ldcg(v.old + b);
-            if (old >= 0) v.moves[1 + __ldcg(v.copies + b)] = make_int4(old, p, __ldcg(v.fill + b), 0);
+    // 4. to whom they go, shared out anew (given out by the runs' own warps, a run of free pages is one
+    // warp's search after search: 34 us for the round of 1024 sequences)
+    for (int i0 = rank * kClusterThreads + tid; i0 < total; i0 += kPoolStep) {
+        int p[kPoolUnroll];
+#pragma unroll
+        for (int u = 0; u < kPoolUnroll; ++u) {
+            const int i = i0 + u * kClusterBlocks * kClusterThreads;
+            if (i < total) p[u] = __ldcg(v.rank + i);
+        }
+#pragma unroll
+        for (int u = 0; u < kPoolUnroll; ++u) {
+            const int i = i0 + u * kClusterBlocks * kClusterThreads;
+            if (i >= total) break;
+            const int b = pool_owner(sm.start, v.B, i), idx = i - sm.start[b], e = sm.first[b] + idx;
+            if (!YOCO_DCHECK(b < v.B && e < v.max_pages, 0x6B)) continue;
+            v.table[(size_t)b * v.max_pages + e] = p[u];
+            if (idx == 0) {
+                const int old = __ldcg(v.old + b);
+                if (old >= 0) v.moves[1 + __ldcg(v.copies + b)] = make_int4(old, p[u], __ldcg(v.fill + b), 0);
+            }
         }
     }
 }
@@ -423,55 +449,45 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
     const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x;
     cluster_arrive();  // (waited for before another block's memory is written)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const int w = rank * (kClusterThreads / 32) + (tid >> 5);
-    int p0, p1;
-    pool_run(v, w, kClusterWarps, p0, p1);
-    const int count = pool_count<true>(v, p0, p1);
+    const int w = rank * (kClusterThreads / 32) + (tid >> 5), per = pool_per(v);
     cluster_wait();
-    pool_tell(sm, w, count);
+    pool_tell<true>(v, sm, w, kClusterWarps, per);
     cluster_sync();
-    int at, live;
-    pool_before(sm, w, kClusterWarps, at, live);
+    const int live = pool_before(v, sm, per);
     // used pages below page `live`: those of the runs before its own, and a part of that one
-    int in_front, edge0, edge1;
-    {
-        int e = 0;
-        pool_run(v, 0, kClusterWarps, edge0, edge1);
-        if (edge1 > 0) e = min(live / edge1, kClusterWarps);  // (runs are as long as the first one)
-        int before, all;
-        pool_before(sm, e, kClusterWarps, before, all);
-        int n = 0;
-        for (int p = e * edge1 + tid; p < live; p += kClusterThreads) n += __ldcg(v.refs + p) > 0;
-        in_front = before;
-        int part;
-        (void)pool_scan<kClusterThreads>(n, reinterpret_cast<int *>(sm.sums), part);
-        in_front += part;
-    }
+    int in_front, part, n = 0;
+    const int edge = live / per;
+    for (int p = edge * per + tid; p < live; p += kClusterThreads) n += __ldcg(v.refs + p) > 0;
+    (void)pool_scan<kClusterThreads>(n, reinterpret_cast<int *>(sm.sums), part);
+    in_front = part + (edge * per < v.num_pages ? sm.count[edge] : live);
     if (tid == 0 && rank == 0) v.moves[0] = make_int4(live - in_front, live, 0, 0);
     if (live == in_front) return;
     int *moves = reinterpret_cast<int *>(v.moves + 1);
     // (a run before page `live` has holes, one behind it pages that move)
-    for (int q = p0 + lane; q - lane < p1; q += 32 * kPoolLoads) {
-        int refs[kPoolLoads];
+    for (int run = w; (long long)run * per < v.num_pages; run += kClusterWarps) {
+        int at = sm.count[run];
+        for (int q = run * per + lane, p1 = min(run * per + per, v.num_pages); q - lane < p1; q += 32 * kPoolLoads) {
+            int refs[kPoolLoads];
 #pragma unroll
-        for (int k = 0; k < kPoolLoads; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 0;
+            for (int k = 0; k < kPoolLoads; ++k) refs[k] = q + 32 * k < p1 ? __ldcg(v.refs + q + 32 * k) : 0;
 #pragma unroll
-        for (int k = 0; k < kPoolLoads; ++k) {
-            const int p = q + 32 * k;
-            const bool is = refs[k] > 0;
-            const unsigned who = __ballot_sync(0xffffffffu, is);
-            const int used = at + __popc(who & ((1u << lane) - 1));  // used pages before p
-            at += __popc(who);
-            if (p >= p1) continue;
-            if (is && p >= live) {
-                const int r = used - in_front;
-                if (!YOCO_DCHECK(r >= 0 && r < v.num_pages / 2, 0x6C)) continue;
-                v.rank[p] = r;
-                moves[4 * r] = p;
-                moves[4 * r + 2] = 1 << v.shift;
-                moves[4 * r + 3] = 0;
-            } else if (!is && p < live) {
-                moves[4 * (p - used) + 1] = p;
+            for (int k = 0; k < kPoolLoads; ++k) {
+                const int p = q + 32 * k;
+                const bool is = refs[k] > 0;
+                const unsigned who = __ballot_sync(0xffffffffu, is);
+                const int used = at + __popc(who & ((1u << lane) - 1));  // used pages before p
+                at += __popc(who);
+                if (p >= p1) continue;
+                if (is && p >= live) {
+                    const int r = used - in_front;
+                    if (!YOCO_DCHECK(r >= 0 && r < v.num_pages / 2, 0x6C)) continue;
+                    v.rank[p] = r;
+                    moves[4 * r] = p;
+                    moves[4 * r + 2] = 1 << v.shift;
+                    moves[4 * r + 3] = 0;
+                } else if (!is && p < live) {
+                    moves[4 * (p - used) + 1] = p;
+                }
             }
         }
     }
