@@ -150,7 +150,8 @@ class Pair:
 @pytest.mark.parametrize("seed", range(6))
 @pytest.mark.parametrize("B,pages,page,most,Hkv,d,dtype", [
     (1, 5, 16, 8, 1, 64, torch.float32), (7, 40, 16, 20, 2, 64, torch.bfloat16), (60, 300, 32, 30, 1, 128, torch.bfloat16),
-    (1100, 5000, 16, 12, 1, 64, torch.bfloat16), (20, 9000, 16, 300, 1, 64, torch.bfloat16)])
+    (1100, 5000, 16, 12, 1, 64, torch.bfloat16), (20, 9000, 16, 300, 1, 64, torch.bfloat16),
+    (12, 25, 1024, 6, 1, 64, torch.float32)])
 def test_random_rounds(Y, B, pages, page, most, Hkv, d, dtype, seed):
     rng = random.Random(seed)
     s = Pair(Y, B, pages, page, most, Hkv, d, dtype)

@@ -338,6 +338,30 @@ def test_many_sequences(Y, B):
     run(Y, [1] * B, ctx, 4, 2, 128, 16, "bf16", cap=20.0, docs=100, decode=True)
 
 
+def test_more_row_blocks_than_are_planned_one_by_one(Y):
+    """4096 sequences with documents: planned by sequences, as they would be by row blocks."""
+    g = np.random.RandomState(7)
+    new, ctx = [int(x) for x in g.randint(0, 3, 4096)], [int(x) for x in g.randint(0, 60, 4096)]
+    run(Y, new, ctx, 1, 1, 64, 16, "f32", docs=20)
+
+
+def test_overlapping_row_bounds_with_documents(Y):
+    """Bounds that fall back give two sequences the same rows: all of them are planned and written."""
+    pool = P.Pool(Y, [1000] * 5, 1, 64, 16, "f32")
+    Q = torch.randn(1000, 1, 64, device="cuda")
+    O = torch.full_like(Q, 7.0)
+    s = Y.PagedScores(doc_first=cuda_ints([0] * 1000))
+    ws = torch.zeros(Y.yoco_paged_attn_workspace_size(1, 1000, pool.dev), dtype=torch.uint8, device="cuda")
+    Y.yoco_paged_attn_prefill_scored(Q, pool.dev, cuda_ints([0, 1000, 0, 1000, 0, 1000]), O, s, workspace=ws)
+    with pytest.raises(Y.YocoError) as e:
+        Y.yoco_workspace_status(ws)
+    assert e.value.status == Y.YOCO_ERR_INVALID_ARG
+    pos = torch.arange(1000)
+    refs = [reference(pool, Q.cpu(), b, pos, torch.zeros(1000, dtype=torch.int64), 0, 0.0, None, 0, 0, 0.125) for b in (0, 2, 4)]
+    ok = torch.stack([((O.cpu().double() - r).abs() <= t).all(-1).all(-1) for r, t in refs]).any(0)
+    assert bool(ok.all())  # each row is one of the three sequences'
+
+
 def test_bad_metadata_is_recorded_and_reads_nothing_outside(Y):
     """Row bounds that decrease and lengths past the table: recorded, the sound sequences' rows are right."""
     pool = P.Pool(Y, [100, 80], 2, 128, 16, "bf16")
