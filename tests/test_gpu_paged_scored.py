@@ -358,8 +358,9 @@ def test_overlapping_row_bounds_with_documents(Y):
     assert e.value.status == Y.YOCO_ERR_INVALID_ARG
     pos = torch.arange(1000)
     refs = [reference(pool, Q.cpu(), b, pos, torch.zeros(1000, dtype=torch.int64), 0, 0.0, None, 0, 0, 0.125) for b in (0, 2, 4)]
-    ok = torch.stack([((O.cpu().double() - r).abs() <= t).all(-1).all(-1) for r, t in refs]).any(0)
-    assert bool(ok.all())  # each row is one of the three sequences'
+    # blocks of the three sequences write the same rows, a few channels to a thread, in any order
+    ok = torch.stack([(O.cpu().double() - r).abs() <= t for r, t in refs]).any(0)
+    assert bool(ok.all())
 
 
 def test_bad_metadata_is_recorded_and_reads_nothing_outside(Y):
