@@ -91,16 +91,23 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                 for (int i = 0; i < EV; ++i) qs[e / D][e % D + i] = c2 * x[i];
             }
             __syncthreads();
-            float m[NQ], l[NQ], acc[NQ][EL];
-            [[maybe_unused]] float slope[MOD ? NQ : 1];  // times log2(e)
+            // with four heads or more a lane keeps the maximum and sum of one of them (see below)
+            constexpr bool kOwn = NQ >= 4;
+            constexpr int kMine = kOwn ? 1 : NQ;
+            const int own = NQ == 8 ? j8 : j8 >> 1;
+            float m[kMine], l[kMine], acc[NQ][EL];
+            [[maybe_unused]] float slope[MOD ? kMine : 1];  // times log2(e)
 #pragma unroll
-            for (int i = 0; i < NQ; ++i) {
-                if constexpr (MOD) slope[i] = mod.slopes && i < nq ? mod.slopes[w.hk * G + g0 + i] * kPagedLog2E : 0.f;
+            for (int i = 0; i < kMine; ++i) {
+                const int head = kOwn ? own : i;
+                if constexpr (MOD) slope[i] = mod.slopes && head < nq ? mod.slopes[w.hk * G + g0 + head] * kPagedLog2E : 0.f;
                 m[i] = -INFINITY;
                 l[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
 #pragma unroll
                 for (int e = 0; e < EL; ++e) acc[i][e] = 0.f;
-            }
             // this group's keys of the run: 4 of each 128-key tile
             const int steps = (w.t1 - w.t0) * (kPagedTile / 32);
             for (int st = 0; st < steps; st += kDecKeys) {
@@ -130,46 +137,112 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                         }
                     }
                 }
+                if constexpr (kOwn) {
+                    // The 8 or 16 scores of the lane group's two keys: halved three times over, each lane
+                    // ends with the one or two of its own head (the sums are those of a butterfly, with
+                    // less than a third of its shuffles), takes their cap, bias and exponentials alone
+                    // and hands the weights round.
+                    static_assert(kDecKeys == 2, "scores are ordered by head, then by key");
+                    float d[2 * NQ];
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    float s[kDecKeys], top = m[i];
+                    for (int i = 0; i < NQ; ++i)
 #pragma unroll
-                    for (int x = 0; x < kDecKeys; ++x) {
-                        float d = 0.f;
+                        for (int x = 0; x < 2; ++x) {
+                            d[2 * i + x] = 0.f;
 #pragma unroll
-                        for (int e = 0; e < EL; ++e) d = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d);
-#pragma unroll
-                        for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-                        if constexpr (MOD) {
-                            if (mod.cap2 > 0.f) d = paged_cap(d, mod.cap2);
-                            if (mod.slopes) d = fmaf(-slope[i], far[x], d);
+                            for (int e = 0; e < EL; ++e)
+                                d[2 * i + x] = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d[2 * i + x]);
                         }
-                        s[x] = ok[x] ? d : -INFINITY;
-                        top = fmaxf(top, s[x]);
+#pragma unroll
+                    for (int half = 0; half < 3; ++half) {
+                        const int off = 4 >> half, n = NQ >> half;
+                        const bool up = j8 & off;
+#pragma unroll
+                        for (int v = 0; v < n; ++v) {
+                            const float give = up ? d[v] : d[v + n], keep = up ? d[v + n] : d[v];
+                            d[v] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                        }
                     }
+                    constexpr int kScores = NQ / 4;  // of a lane: keys 0 and 1 of head j8, or key j8 % 2 of head j8 / 2
+                    float top = m[0];
+#pragma unroll
+                    for (int v = 0; v < kScores; ++v) {
+                        const int x = kScores == 2 ? v : j8 & 1;
+                        if constexpr (MOD) {
+                            if (mod.cap2 > 0.f) d[v] = paged_cap(d[v], mod.cap2);
+                            if (mod.slopes) d[v] = fmaf(-slope[0], x ? far[1] : far[0], d[v]);
+                        }
+                        d[v] = (x ? ok[1] : ok[0]) ? d[v] : -INFINITY;
+                        top = fmaxf(top, d[v]);
+                    }
+                    if constexpr (kScores == 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     // (no score yet, or NaN alone, which no maximum shows: the weights are 0 or NaN)
                     const float ref = top == -INFINITY ? 0.f : top;
-                    const float old = exp2f(m[i] - ref);
-                    m[i] = top;
-                    l[i] *= old;
+                    const float old = exp2f(m[0] - ref);
+                    m[0] = top;
 #pragma unroll
-                    for (int e = 0; e < EL; ++e) acc[i][e] *= old;
+                    for (int v = 0; v < kScores; ++v) d[v] = exp2f(d[v] - ref);
+                    const float other = kScores == 2 ? d[1] : __shfl_xor_sync(0xffffffffu, d[0], 1);
+                    const bool odd = kScores == 1 && (j8 & 1);
+                    l[0] = l[0] * old + (odd ? other : d[0]) + (odd ? d[0] : other);
 #pragma unroll
-                    for (int x = 0; x < kDecKeys; ++x) {
-                        const float pe = exp2f(s[x] - ref);
-                        l[i] += pe;
+                    for (int i = 0; i < NQ; ++i) {
+                        const int from = kScores == 2 ? i : 2 * i;
+                        const float fall = __shfl_sync(0xffffffffu, old, from, 8);
+                        const float p0 = __shfl_sync(0xffffffffu, d[0], from, 8);
+                        const float p1 = kScores == 2 ? __shfl_sync(0xffffffffu, d[1], from, 8) : __shfl_sync(0xffffffffu, d[0], from + 1, 8);
 #pragma unroll
-                        for (int e = 0; e < EL; ++e) acc[i][e] = fmaf(pe, vx[x][e], acc[i][e]);
+                        for (int e = 0; e < EL; ++e) {
+                            acc[i][e] *= fall;
+                            acc[i][e] = fmaf(p0, vx[0][e], acc[i][e]);
+                            acc[i][e] = fmaf(p1, vx[1][e], acc[i][e]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) {
+                        float s[kDecKeys], top = m[i];
+#pragma unroll
+                        for (int x = 0; x < kDecKeys; ++x) {
+                            float d = 0.f;
+#pragma unroll
+                            for (int e = 0; e < EL; ++e) d = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d);
+#pragma unroll
+                            for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                            if constexpr (MOD) {
+                                if (mod.cap2 > 0.f) d = paged_cap(d, mod.cap2);
+                                if (mod.slopes) d = fmaf(-slope[i], far[x], d);
+                            }
+                            s[x] = ok[x] ? d : -INFINITY;
+                            top = fmaxf(top, s[x]);
+                        }
+                        // (no score yet, or NaN alone, which no maximum shows: the weights are 0 or NaN)
+                        const float ref = top == -INFINITY ? 0.f : top;
+                        const float old = exp2f(m[i] - ref);
+                        m[i] = top;
+                        l[i] *= old;
+#pragma unroll
+                        for (int e = 0; e < EL; ++e) acc[i][e] *= old;
+#pragma unroll
+                        for (int x = 0; x < kDecKeys; ++x) {
+                            const float pe = exp2f(s[x] - ref);
+                            l[i] += pe;
+#pragma unroll
+                            for (int e = 0; e < EL; ++e) acc[i][e] = fmaf(pe, vx[x][e], acc[i][e]);
+                        }
                     }
                 }
             }
             // the warp's four groups, then the eight warps
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                float M = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
+                const int from = NQ == 8 ? i : 2 * i;  // the lane that has head i's maximum and sum
+                const float mi = kOwn ? __shfl_sync(0xffffffffu, m[0], from, 8) : m[kOwn ? 0 : i];
+                const float li = kOwn ? __shfl_sync(0xffffffffu, l[0], from, 8) : l[kOwn ? 0 : i];
+                float M = fmaxf(mi, __shfl_xor_sync(0xffffffffu, mi, 8));
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-                const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - M);
-                float L = l[i] * f;
+                const float f = mi == -INFINITY ? 0.f : exp2f(mi - M);
+                float L = li * f;
                 L += __shfl_xor_sync(0xffffffffu, L, 8);
                 L += __shfl_xor_sync(0xffffffffu, L, 16);
                 if (lane == 0) {
