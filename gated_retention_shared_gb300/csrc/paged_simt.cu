@@ -17,8 +17,7 @@
 namespace yoco {
 
 // 4 or 8 consecutive elements (16 bytes) as floats
-template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16 / sizeof(T)]) {
-    const uint4 u = paged_ld16(p);
+template <typename T> __device__ __forceinline__ void widen(const uint4 &u, float (&x)[16 / sizeof(T)]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -30,6 +29,9 @@ template <typename T> __device__ __forceinline__ void load16(const T *p, float (
         }
     }
 }
+template <typename T> __device__ __forceinline__ void load16(const T *p, float (&x)[16 / sizeof(T)]) {
+    widen<T>(paged_ld16(p), x);
+}
 
 // ----------------------------------------------------------------- decode
 //
@@ -39,15 +41,19 @@ template <typename T> __device__ __forceinline__ void load16(const T *p, float (
 // running maximum, sum and weighted sum of its own, merged at the end of the unit.  K and V
 // go from global memory to registers once.  Groups with more than kDecQ heads take them
 // kDecQ at a time, reading K and V again (from L2).  32 sequences of 60 to 30000 keys over 4 kv
-// heads: fp32 x 128 282 us with one head each (6.9 TB/s, the read rate), 427 with four, 468 with
-// eight; bf16 x 64 170, 223 and 440 us (2.9, 2.2 and 1.1 TB/s: the sums, not the reads).
+// heads: fp32 x 128 284 us with one or two heads each (6.9 TB/s, the read rate), 301 with four, 426
+// with eight; bf16 x 64 110, 127 (four) and 220 us (eight: 2.2 TB/s, the sums, not the reads).  What
+// counted, with a cap the same to a tenth: a step's keys on their way under the step before (four
+// heads, fp32 x 64, 209 -> 162 us; eight, bf16 x 64, 445 -> 237, of it 80 us the query's four
+// elements of all lanes side by side in shared memory), each lane one head's scores (eight capped fp32
+// heads x 64 128 -> 89 us for half the keys), two blocks to an SM (one bf16 head x 64 129 -> 110).
 constexpr int kDecThreads = 256;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecQ = 8;      // query heads at a time
 constexpr int kDecKeys = 2;   // keys of a lane group in flight
 
 template <typename T, int D, int NQ, bool MOD>
-__global__ void __launch_bounds__(kDecThreads)
+__global__ void __launch_bounds__(kDecThreads, NQ * D <= 256 ? 2 : 1)
 paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__restrict__ K, const T *__restrict__ V,
                          float *__restrict__ part, PagedCut *__restrict__ cuts, int Hq, const PagedView pv,
                          const PagedMod mod, float c2, int *err) {
@@ -61,6 +67,8 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
     __shared__ float wm[kDecWarps][NQ], wl[kDecWarps][NQ], wo[kDecWarps][NQ][D];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, j8 = lane & 7, grp = warp * 4 + (lane >> 3);
     const int G = Hq / pv.Hkv, c = blockIdx.x;
+    // where element i of a row's chunk lies: the eight lanes' four elements side by side
+    auto q_at = [](int chunk, int i) { return ((chunk / 8 * (EV / 4) + i / 4) * 8 + chunk % 8) * 4 + i % 4; };
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     paged_prefix<kDecThreads, MOD>(pv, mod, pre, sums, err);
@@ -88,7 +96,7 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                 for (int i = 0; i < EV; ++i) x[i] = 0.f;
                 if (e < nq * D) load16(Q + qrow * D + e, x);
 #pragma unroll
-                for (int i = 0; i < EV; ++i) qs[e / D][e % D + i] = c2 * x[i];
+                for (int i = 0; i < EV; ++i) qs[e / D][q_at(e % D / EV, i)] = c2 * x[i];
             }
             __syncthreads();
             // with four heads or more a lane keeps the maximum and sum of one of them (see below)
@@ -110,32 +118,54 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                 for (int e = 0; e < EL; ++e) acc[i][e] = 0.f;
             // this group's keys of the run: 4 of each 128-key tile
             const int steps = (w.t1 - w.t0) * (kPagedTile / 32);
-            for (int st = 0; st < steps; st += kDecKeys) {
-                float kx[kDecKeys][EL], vx[kDecKeys][EL];
-                bool ok[kDecKeys];
-                [[maybe_unused]] float far[kDecKeys];  // from the row
+            uint4 kr[kDecKeys][NC], vr[kDecKeys][NC];
+            bool there[kDecKeys];
+            [[maybe_unused]] float apart[kDecKeys];  // from the row
+            auto fetch = [&](int st) {  // the keys of step st, on their way
 #pragma unroll
                 for (int x = 0; x < kDecKeys; ++x) {
                     const int key = range.slot(w.t0 * kPagedTile + (st + x) * 32 + grp);
-                    if constexpr (MOD) far[x] = (float)(len - 1 - key);
-                    ok[x] = range.seen(key, pv.sinks);
-                    const int page = ok[x] ? paged_page(pv, w.b, key >> pv.shift, err) : -1;
+                    if constexpr (MOD) apart[x] = (float)(len - 1 - key);
+                    there[x] = range.seen(key, pv.sinks);
+                    const int page = there[x] ? paged_page(pv, w.b, key >> pv.shift, err) : -1;
                     const size_t at = (((size_t)max(page, 0) * pv.Hkv + w.hk) << pv.shift) + (key & ((1 << pv.shift) - 1));
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
-                        float t[EV], u[EV];
-#pragma unroll
-                        for (int e = 0; e < EV; ++e) t[e] = u[e] = 0.f;
+                        kr[x][n] = vr[x][n] = make_uint4(0, 0, 0, 0);
                         if (page >= 0) {
-                            load16(K + at * D + (n * 8 + j8) * EV, t);
-                            load16(V + at * D + (n * 8 + j8) * EV, u);
+                            kr[x][n] = paged_ld16(K + at * D + (n * 8 + j8) * EV);
+                            vr[x][n] = paged_ld16(V + at * D + (n * 8 + j8) * EV);
                         }
+                    }
+                }
+            };
+            // a step's keys come in under the one before (not with one or two heads, whose reads are at HBM's
+            // rate without, nor with eight of 128, for want of registers)
+            constexpr bool kAhead = NQ >= 4 && NQ * D <= 512;
+            if constexpr (kAhead) fetch(0);
+            for (int st = 0; st < steps; st += kDecKeys) {
+                float kx[kDecKeys][EL], vx[kDecKeys][EL];
+                bool ok[kDecKeys];
+                [[maybe_unused]] float far[kDecKeys];
+                if constexpr (!kAhead) fetch(st);
+#pragma unroll
+                for (int x = 0; x < kDecKeys; ++x) {
+                    ok[x] = there[x];
+                    if constexpr (MOD) far[x] = apart[x];
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) {
+                        float t[EV], u[EV];
+                        widen<T>(kr[x][n], t);
+                        widen<T>(vr[x][n], u);
 #pragma unroll
                         for (int e = 0; e < EV; ++e) {
                             kx[x][n * EV + e] = t[e];
                             vx[x][n * EV + e] = u[e];
                         }
                     }
+                }
+                if constexpr (kAhead) {
+                    if (st + kDecKeys < steps) fetch(st + kDecKeys);
                 }
                 if constexpr (kOwn) {
                     // The 8 or 16 scores of the lane group's two keys: halved three times over, each lane
@@ -151,7 +181,7 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                             d[2 * i + x] = 0.f;
 #pragma unroll
                             for (int e = 0; e < EL; ++e)
-                                d[2 * i + x] = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d[2 * i + x]);
+                                d[2 * i + x] = fmaf(qs[i][q_at(e / EV * 8 + j8, e % EV)], kx[x][e], d[2 * i + x]);
                         }
 #pragma unroll
                     for (int half = 0; half < 3; ++half) {
@@ -206,7 +236,7 @@ paged_decode_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *__
                         for (int x = 0; x < kDecKeys; ++x) {
                             float d = 0.f;
 #pragma unroll
-                            for (int e = 0; e < EL; ++e) d = fmaf(qs[i][(e / EV * 8 + j8) * EV + e % EV], kx[x][e], d);
+                            for (int e = 0; e < EL; ++e) d = fmaf(qs[i][q_at(e / EV * 8 + j8, e % EV)], kx[x][e], d);
 #pragma unroll
                             for (int off = 4; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
                             if constexpr (MOD) {
