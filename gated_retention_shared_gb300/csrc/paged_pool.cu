@@ -123,7 +123,7 @@ __device__ __forceinline__ int cluster_get(const int *at, int rank) {
 
 struct PoolSmem {
     long long sums[kClusterThreads / 32];
-    int before[kPagedMaxB + 1];  // entries that go back of the sequences before b
+    long long before[kPagedMaxB];  // entries that go back of the sequences before b
     int from[kPagedMaxB];        // first of them in the table
     int count[kPoolRuns];        // free (used) pages of each run, then of those before it
     int start[kPagedMaxB + 1];   // as in PoolView
@@ -145,7 +145,7 @@ __device__ __forceinline__ int pool_slot(PoolShared &t, int page) {
 }
 
 // b with before[b] <= i < before[b + 1]
-__device__ __forceinline__ int pool_owner(const int *before, int B, int i) {
+template <typename N> __device__ __forceinline__ int pool_owner(const N *before, int B, N i) {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -201,7 +201,8 @@ __device__ __forceinline__ int pool_before(const PoolView &v, PoolSmem &sm, int 
 }
 
 // Of the sequences that grow: what they need and which pages have to be copied, into v's scratch and
-// the block's start and first; one block.  page[k]: the page that holds the last slot of its sequence b0 + k, where that is not full.
+// the block's start and first; one block.  page[k]: the page that holds the last slot of its
+// sequence b0 + k, where that is not full.
 __device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kShareEach], const int (&N)[kShareEach],
                                            const int (&page)[kShareEach], int each, PoolSmem &sm, PoolShared &t) {
     const int b0 = threadIdx.x * each;
@@ -297,22 +298,20 @@ pool_resize_kernel(const PoolView v, const int32_t *new_lens) {
 #pragma unroll
         for (int k = 0; k < kShareEach; ++k) {
             if (k >= each || b0 + k >= v.B) break;
-            const int n = sm.before[b0 + k];
-            sm.before[b0 + k] = (int)min(run, 0x7fffffffll);
+            const long long n = sm.before[b0 + k];
+            sm.before[b0 + k] = run;
             run += n;
         }
         __syncthreads();
-        // (each entry is held by a sequence; more than 2^31 of them are not in any memory)
-        const int top = (int)min(drops, 0x7fffffffll - kPoolStep);
-        for (int i0 = rank * kClusterThreads + tid; i0 < top; i0 += kPoolStep) {
+        for (long long i0 = rank * kClusterThreads + tid; i0 < drops; i0 += kPoolStep) {
             int32_t *at[kPoolUnroll];
             int p[kPoolUnroll], was[kPoolUnroll];
 #pragma unroll
             for (int u = 0; u < kPoolUnroll; ++u) {
-                const int i = i0 + u * kClusterBlocks * kClusterThreads;
+                const long long i = i0 + u * kClusterBlocks * kClusterThreads;
                 at[u] = nullptr;
-                if (i >= top) continue;
-                const int b = pool_owner(sm.before, v.B, i), e = sm.from[b] + i - sm.before[b];
+                if (i >= drops) continue;
+                const int b = pool_owner(sm.before, v.B, i), e = sm.from[b] + (int)(i - sm.before[b]);
                 if (YOCO_DCHECK(e < v.max_pages, 0x6B)) at[u] = v.table + (size_t)b * v.max_pages + e;
             }
 #pragma unroll

@@ -212,6 +212,28 @@ def test_needs_past_32_bits_are_no_room(Y):
     assert int(refs.abs().sum()) == 0 and int(cache.seq_lens.sum()) == 0
 
 
+def test_entries_past_32_bits_go_back(Y):
+    """2100 forks of a sequence of 2^20 pages: 2^31 and more table entries are given back in one call."""
+    B, n = 2100, 1 << 20
+    k = torch.zeros(n + 5, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    cache = Y.PagedKV(k, k, torch.full((B, n), -1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda"))
+    refs = torch.zeros(n + 5, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(Y.yoco_paged_pool_workspace_size(cache), dtype=torch.uint8, device="cuda")
+    lens = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    lens[7] = 16 * n
+    Y.yoco_paged_resize(cache, refs, lens, workspace=ws)
+    dst = torch.tensor([b for b in range(B) if b != 7], dtype=torch.int32, device="cuda")
+    Y.yoco_paged_fork(cache, refs, torch.full_like(dst, 7), dst, workspace=ws)
+    Y.yoco_workspace_status(ws)
+    assert bool((refs[:n] == B).all()) and bool((refs[n:] == 0).all())
+    lens.fill_(0)
+    lens[B - 1] = 16 * n - 16  # all but the last page of the last one
+    Y.yoco_paged_resize(cache, refs, lens, workspace=ws)
+    Y.yoco_workspace_status(ws)
+    assert bool((refs[:n - 1] == 1).all()) and bool((refs[n - 1:] == 0).all())
+    assert bool((cache.page_table[:B - 1] == -1).all()) and int(cache.page_table[B - 1, n - 1]) == -1
+
+
 def test_bad_forks_are_left_out(Y):
     s = Pair(Y, 8, 40, 16, 8)
     s.resize([20, 30, 40, 0, 0, 0, 0, 0])
