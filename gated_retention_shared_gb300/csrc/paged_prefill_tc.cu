@@ -547,21 +547,33 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // their V rows.  (A parity can only tell a phase from the one before: with two sets P(i - 1)
         // waited for P_B V(i - 2), so V(i - 2) has come; with one set every tile waits for V)
         int e_lo = 0, e_hi = 0x7fffffff;
-        if (!MOD && x == 0) {
+        if (x == 0) {
             const auto &rg = blk.range;
-            const int from = rg.sink_slots + rg.lo - rg.base;  // the first place that is seen for being in the window
+            int lo = rg.lo;
+            if constexpr (MOD) lo = max(lo, rg.dlo);
+            const int from = rg.sink_slots + lo - rg.base;  // the first place that is seen for being in the window
             e_lo = (from + kPagedTile - 1) / kPagedTile - blk.i0;
             e_hi = rg.places / kPagedTile - blk.i0;
         }
         // a scored call's row sees the slots [lo, pos] and [doc, head): its window from its document's
-        // start on, and of the document's slots the prefix and the sinks
-        [[maybe_unused]] int lo = 0, doc = 0, head = 0;
+        // start on, and of the document's slots the prefix and the sinks; all rows of the warp see
+        // [all_lo, all_hi) and [all_doc, all_head)
+        [[maybe_unused]] int lo = 0, doc = 0, head = 0, all_lo = 0, all_hi = 0, all_doc = 0, all_head = 0;
         [[maybe_unused]] float slope = 0.f;
+        [[maybe_unused]] bool gentle = true, back = true;  // slopes for the quick way; no row sees past itself
         if constexpr (MOD) {
             if (used && mod.doc) doc = max(0, mod.doc[blk.row0 + x * TS + r / G]);
             lo = max(doc, pv.window > 0 ? pos + 1 - pv.window : 0);
             head = pos < 0 ? 0 : max(blk.range.pre, min(pv.sinks, pos + 1));
-            if (BIAS && used) slope = mod.slopes[hk * G + r % G] * kPagedLog2E;
+            all_lo = __reduce_max_sync(0xffffffffu, used ? lo : 0);
+            all_hi = __reduce_min_sync(0xffffffffu, used ? pos + 1 : 0x7fffffff);
+            all_doc = __reduce_max_sync(0xffffffffu, used ? doc : 0);
+            all_head = __reduce_min_sync(0xffffffffu, used ? head : 0x7fffffff);
+            if constexpr (BIAS) {
+                if (used) slope = mod.slopes[hk * G + r % G] * kPagedLog2E;
+                gentle = __all_sync(0xffffffffu, fabsf(slope) <= kQuickSlope);
+                back = __all_sync(0xffffffffu, head <= pos + 1 || !used);
+            }
         }
         float m_ref = -INFINITY, l = 0.f;  // base-2 units
         // One exit from the tile loop: a wait that gave up makes what follows garbage (the status word
@@ -572,17 +584,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             // place 0 of the tile, and what its slot is where it lies past the sinks' chunks
             const int v0 = tile_of(blk, i) * kPagedTile, key0 = v0 + delta;
             // every row of the set (a scored call: of the warp) sees every slot of the tile
-            bool full, edge = false;
-            [[maybe_unused]] int first = 0, k0 = 0;  // of the first run's slots; of the tile's where it has one run
-            [[maybe_unused]] bool behind = true;     // no slot past the row's position is one that it sees
+            bool full;
+            [[maybe_unused]] int first = 0, k0 = key0;  // of the first run's slots; of the tile's where it has one run
+            [[maybe_unused]] bool run = true;
             if constexpr (MOD) {
-                first = blk.range.first;
-                const bool one = v0 + kPagedTile <= sink_slots, run = one || v0 >= sink_slots;
-                k0 = v0 + (one ? first : delta);
-                const bool mine = (lo <= k0 && k0 + kPagedTile - 1 <= pos) || (doc <= k0 && k0 + kPagedTile <= head);
-                full = run && __all_sync(0xffffffffu, mine || !used);
-                edge = x == 0 && blk.range.edge(tile_of(blk, i), 0);
-                behind = run && (k0 + kPagedTile - 1 <= pos || head <= max(k0, pos + 1));
+                if (__builtin_expect(v0 < sink_slots, 0)) {
+                    first = blk.range.first;
+                    run = v0 + kPagedTile <= sink_slots;
+                    k0 = v0 + first;
+                }
+                full = run && ((all_lo <= k0 && k0 + kPagedTile <= all_hi) || (all_doc <= k0 && k0 + kPagedTile <= all_head));
             }
             alive = mbar_wait_warp(&bar.s_full[x], i & 1, abort_flag);
             tc_fence_after();
@@ -649,8 +660,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 }
                 bool ok = true;
                 if constexpr (CAP) ok = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), 0.f) <= mod.quick;
-                if constexpr (BIAS) ok = ok && fabsf(slope) <= kQuickSlope && behind;
-                quick = __all_sync(0xffffffffu, ok || !used);
+                if constexpr (CAP) quick = __all_sync(0xffffffffu, ok || !used);
+                // (no slot past a row's position is one that it sees)
+                if constexpr (BIAS) quick = quick && gentle && run && (back || k0 + kPagedTile <= all_hi);
                 mt = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -798,8 +810,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tmem_wait_st();
             }
             // V rows that no row of the block sees: zero, once the tile has come
-            if constexpr (!MOD) edge = i < e_lo || i >= e_hi;
-            if (__builtin_expect(edge || !two, 0)) {
+            const int at = BIAS ? ntiles - 1 - i : i;
+            if (__builtin_expect(at < e_lo || at >= e_hi || !two, 0)) {
                 alive &= mbar_wait_warp(&bar.vfull[i % kCStages], (i / kCStages) & 1, abort_flag);
                 if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
