@@ -156,6 +156,8 @@ paged_append_kernel(const PagedAppend a, const PagedView pv, int parts, const Ro
 }
 
 // The same with a rotation as yoco_rope describes it: a lane has a unit of the head (rope_units.cuh).
+// The first heads' loads go before the row's place is looked up, which takes three latencies (11924
+// rows of 8 sequences, half of each head turned, 55 -> 43 us with that and units of one size, 5.7 TB/s).
 template <typename T, int D, bool HALVES>
 __global__ void __launch_bounds__(kAppendWarps * 32)
 paged_append_rope_kernel(const PagedAppend a, const PagedView pv, int parts, const __grid_constant__ RopeScaled r) {

@@ -29,6 +29,9 @@
 // sequences of 60 to 30000 keys over 8 kv heads take 287 us with 3 heads each (6.8 TB/s), 291
 // with 8 and 352 with 16 (5.6 TB/s).  Short calls (700 keys: 8.4 us) are the launch, two
 // dependent tiles and the merge.  Four barriers a tile in place of one: 130 us for the first 32.
+// Scored calls have kernels of their own for each of cap and bias: the first 32 sequences 124 us with
+// a cap, 123 with a bias, 122 with masks alone (looked up at run time in one kernel 148, 138 and 137;
+// with 16 heads to a kv head 342 in place of 222).
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
