@@ -199,7 +199,7 @@ constexpr int kModMask = 1, kModCap = 2, kModBias = 4;
 
 constexpr float kPagedLog2E = 1.4426950408889634f;
 // the tensor-core prefill's quick way (paged_prefill_tc.cu): how large scores and slopes may be, times log2(e)
-constexpr float kQuickSlack = 22.f, kQuickSlope = 44.f / 31.f;
+constexpr float kQuickScore = 22.f, kQuickSlope = 22.f / 15.f;
 
 // ---------------------------------------------- chunks of rows (prefill)
 //

@@ -249,7 +249,7 @@ PagedMod paged_mod(const PagedArgs &a) {
         m.a1 = (float)a[1];
         m.a2 = (float)a[2];
         m.a3 = (float)a[3];
-        m.quick = (float)std::min(0.5 / k, (double)kQuickSlack / (c * k));
+        m.quick = (float)std::min(0.5 / k, kQuickScore / (c * k));
         m.hidden = (float)(32768.0 / k);  // (a3 < 0: the polynomial falls with s^7, here to some -2^100 C)
         // (caps that 32 bits cannot follow that way go the exact way)
         for (double x : a)

@@ -20,7 +20,7 @@
 //
 // The kernel is a template: MODE 0 is the plain call's, the others are those of the scored calls
 // (masks; a cap; a bias by distance; both), whose softmax is described at c_scores.  4096 fresh rows
-// take 87 us plain, 90 with masks, 102 biased, 115 capped, 133 with both: in the tile loop the fp32 pipe
+// take 87 us plain, 90 with masks, 103 biased, 115 capped, 138 with both: in the tile loop the fp32 pipe
 // (37 % with a cap) and the chain from S to P; the products are 54.
 //
 // Pages, rows out of sight and pages that are not there: as in paged_decode_tc.cu; set A's
@@ -181,19 +181,22 @@ __device__ __forceinline__ uint32_t c_below(int n) {
 }
 
 // How a scored tile goes.  The reference of a row's exponentials need not be its maximum, only no
-// less and not far above, so it comes from the raw products: with a cap (which is monotone) from their largest
-// magnitude, with a bias from the largest of each 32 columns and the bias at their end.  The cap
-// and the bias are then part of the exponentials' argument,
+// less and not far above, so it is found from the raw products: with a cap (which is monotone) from
+// their largest magnitude, with a bias from the largest of each 16 columns and the bias at their end.
+// The cap and the bias are then part of the exponentials' argument,
 //     2^(s Q(s^2) + (slope (m - p) - reference)),
 // Q the polynomial of C tanh(k s) / s of degree 3 in s^2 (own minimax fit by reweighted least squares,
-// relative error 5.4e-7 up to |k s| = 0.5, a 2000th of the rounding of the weights that follows), the bracket
-// advanced by additions from every eighth column on: two scores to an instruction, 4 + 1 more
-// for two scores than without, and nothing more for the special-function unit.  That is where the
-// products of all rows of a warp are within kQuickSlack of 0 (and half the cap's bend), slopes
-// below kQuickSlope and all that is seen behind the row, so that a reference is at most 2 x 22 + 44 above the
-// maximum: weights 2^-38 below it still are normal numbers.  Other tiles take the exact way, score by
-// score, in small steps over tensor memory: unrolled over the row's registers its code cost the quick
-// tiles their place in the instruction cache (4096 rows, cap 30, 3 % of the tiles exact: 256 us).
+// relative error 5.4e-7 up to |k s| = 0.5, a 2000th of the rounding of the weights that follows), the
+// bracket advanced by additions from every eighth column on: two scores to an instruction, 4 + 1 more
+// for two scores than without, and nothing more for the special-function unit.  That is where all
+// products of the warp's rows are within half the cap and scores within kQuickScore of 0, slopes
+// below kQuickSlope and all that is seen lies behind the row: a reference is then at most 2 x 22 (cap) and
+// 22 (bias) powers of two above the maximum, and what is 2^-60 of the largest weight still is a normal
+// number (the smallest products as well took 122 us in place of 115 for 4096 rows).
+// Other tiles take the exact way, score by score, in small steps over tensor memory: unrolled over the
+// row's registers its code cost the quick tiles their place in the instruction cache (4096 rows, cap 30,
+// 3 % of the tiles exact: 256 us).
+
 // 16 places of the tile from place c0 on, in place: cap tanh(q.k scale / cap) - slope |p - m|, times
 // log2(e), and -inf where `seen` has no bit.  Place c is slot v0 + first + c before the first run's end,
 // v0 + delta + c from there on.
@@ -648,38 +651,46 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             float mt;
             [[maybe_unused]] bool quick = true;
             if constexpr (SCORED) {
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // of 32 columns, of those that the row sees
+                // the largest products (with a cap in magnitude), with a bias of each 16 columns: of those
+                // that the row sees
+                constexpr int kGroups = BIAS ? 8 : 4;
+                auto size = [](uint32_t w) { return CAP ? fabsf(__uint_as_float(w)) : __uint_as_float(w); };
+                float top[kGroups];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) top[g] = -INFINITY;
                 if (__builtin_expect(full, 1)) {
 #pragma unroll
-                    for (int c = 0; c < kPagedTile; c += 2) {
-                        const float s0 = __uint_as_float(sv[c]), s1 = __uint_as_float(sv[c + 1]);
-                        top[c >> 5] = CAP ? fmax3(top[c >> 5], fabsf(s0), fabsf(s1)) : fmax3(top[c >> 5], s0, s1);
+                    for (int j = 0; j < kPagedTile / 2; ++j) {  // (chain by chain in turn)
+                        const int g = j % kGroups, c = kPagedTile / kGroups * g + 2 * (j / kGroups);
+                        top[g] = fmax3(top[g], size(sv[c]), size(sv[c + 1]));
                     }
                 } else {
 #pragma unroll
                     for (int c = 0; c < kPagedTile; ++c) {
                         const bool seen = bits[c >> 5] & (1u << (c & 31));
-                        const float s0 = __uint_as_float(sv[c]);
-                        top[c >> 5] = fmaxf(top[c >> 5], seen ? (CAP ? fabsf(s0) : s0) : -INFINITY);
+                        float &t = top[c / (kPagedTile / kGroups)];
+                        t = fmaxf(t, seen ? size(sv[c]) : -INFINITY);
                         sv[c] = seen ? sv[c] : __float_as_uint(CAP ? mod.hidden : -INFINITY);  // (weight 0)
                     }
                 }
-                bool ok = true;
-                if constexpr (CAP) ok = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), 0.f) <= mod.quick;
-                if constexpr (CAP) quick = __all_sync(0xffffffffu, ok || !used);
+                auto scored = [&](float s0) {  // cap tanh(s0 scale / cap), times log2(e)
+                    if constexpr (!CAP) return s0 * c2;
+                    const float x2 = s0 * s0;
+                    return s0 == -INFINITY ? s0 : s0 * fmaf(x2, fmaf(x2, fmaf(x2, mod.a3, mod.a2), mod.a1), mod.a0);
+                };
+                float most = 0.f;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) most = fmaxf(most, top[g]);
+                if constexpr (CAP) quick = __all_sync(0xffffffffu, most <= mod.quick || !used);
                 // (no slot past a row's position is one that it sees)
                 if constexpr (BIAS) quick = quick && gentle && run && (back || k0 + kPagedTile <= all_hi);
                 mt = -INFINITY;
+                if constexpr (BIAS) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float y = top[q] * c2;
-                    if constexpr (CAP) {
-                        const float x2 = top[q] * top[q];
-                        y = top[q] * fmaf(x2, fmaf(x2, fmaf(x2, mod.a3, mod.a2), mod.a1), mod.a0);
-                        if (top[q] == -INFINITY) y = -INFINITY;
-                    }
-                    if constexpr (BIAS) y = fmaf(slope, (float)(k0 - pos + 32 * q), y) + fmaxf(31.f * slope, 0.f);
-                    mt = fmaxf(mt, y);
+                    for (int g = 0; g < kGroups; ++g) mt = fmaxf(mt, fmaf(slope, 16.f * g, scored(top[g])));
+                    mt += fmaf(slope, (float)(k0 - pos), fmaxf(15.f * slope, 0.f));
+                } else {
+                    mt = scored(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
                 }
                 if (__builtin_expect(!quick, 0)) {
                     mt = -INFINITY;
