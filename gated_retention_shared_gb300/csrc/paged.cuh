@@ -131,8 +131,10 @@ struct PagedMod {
     const int32_t *doc;         // [rows], or nullptr
     float cap2;                 // cap log2(e); 0: no cap
     float qk;                   // what q.k is multiplied by: scale / cap with a cap, else scale log2(e)
-    // with a cap, for |q.k| <= quick: cap2 tanh(qk s) = s (a0 + a1 s^2 + a2 s^4 + a3 s^6)
-    float a0, a1, a2, a3, quick;
+    // with a cap, for |q.k| <= quick: cap2 tanh(qk s) = s (a[0] + a[1] s^2 + a[2] s^4 ..), to a[3] or,
+    // `wide`, to a[kWideDegree]
+    float a[6], quick;
+    bool wide;
     float hidden;  // a product whose weight comes out as 0 that way
 };
 
@@ -195,10 +197,15 @@ __device__ __forceinline__ float paged_cap(float u, float C) {
 }
 
 // what a tensor-core kernel's rows do to their scores before the softmax, beyond the plain calls'
-constexpr int kModMask = 1, kModCap = 2, kModBias = 4;
+constexpr int kModMask = 1, kModCap = 2, kModBias = 4, kModWide = 8;
 
 constexpr float kPagedLog2E = 1.4426950408889634f;
-// the tensor-core prefill's quick way (paged_prefill_tc.cu): how large scores and slopes may be, times log2(e)
+// the tensor-core prefill's quick way (paged_prefill_tc.cu): caps below kWideCap get the longer polynomial,
+// whose range is all of the cap (4096 rows, scores of deviation 2, us with the short and the long one: cap
+// 50 114 129, cap 20 126 128, cap 15 267 129, cap 10 279 140, cap 8 278 258)
+constexpr int kWideDegree = 5;
+constexpr float kWideCap = 20.f;
+// and how large scores and slopes may be, times log2(e)
 constexpr float kQuickScore = 22.f, kQuickSlope = 22.f / 15.f;
 
 // ---------------------------------------------- chunks of rows (prefill)

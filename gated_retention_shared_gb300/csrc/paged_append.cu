@@ -243,17 +243,19 @@ PagedMod paged_mod(const PagedArgs &a) {
     m.cap2 = cap * kPagedLog2E;
     if (cap > 0.f) {
         const double k = m.qk, c = m.cap2;
-        const double a[4] = {c * k * 0.999999456, -c * std::pow(k, 3) * 0.33326318, c * std::pow(k, 5) * 0.131902967,
-                             -c * std::pow(k, 7) * 0.0444022262};
-        m.a0 = (float)a[0];
-        m.a1 = (float)a[1];
-        m.a2 = (float)a[2];
-        m.a3 = (float)a[3];
-        m.quick = (float)std::min(0.5 / k, kQuickScore / (c * k));
-        m.hidden = (float)(32768.0 / k);  // (a3 < 0: the polynomial falls with s^7, here to some -2^100 C)
-        // (caps that 32 bits cannot follow that way go the exact way)
-        for (double x : a)
+        m.wide = cap < kWideCap;
+        static const double fit[2][6] = {{0.999999456, -0.33326318, 0.131902967, -0.0444022262},
+                                         {0.999999414, -0.333290425, 0.132814342, -0.0516056791, 0.016743118, -0.00306706059}};
+        const int deg = m.wide ? kWideDegree : 3;
+        m.quick = (float)std::min((m.wide ? 1.0 : 0.5) / k, kQuickScore / (c * k));
+        // (the last term is negative: the polynomial falls with s^7 or s^11, here to some -2^100 C)
+        m.hidden = (float)((m.wide ? 1024.0 : 32768.0) / k);
+        for (int i = 0; i <= deg; ++i) {
+            const double x = c * std::pow(k, 2 * i + 1) * fit[m.wide][i];
+            m.a[i] = (float)x;
+            // (caps that 32 bits cannot follow that way go the exact way)
             if (!(std::fabs(x) > 1e-36 && std::fabs(x) < 1e36)) m.quick = -1.f;
+        }
         if (!(m.quick < 1e18f)) m.quick = -1.f;
     }
     return m;

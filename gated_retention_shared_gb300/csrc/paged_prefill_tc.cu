@@ -186,10 +186,12 @@ __device__ __forceinline__ uint32_t c_below(int n) {
 // The cap and the bias are then part of the exponentials' argument,
 //     2^(s Q(s^2) + (slope (m - p) - reference)),
 // Q the polynomial of C tanh(k s) / s of degree 3 in s^2 (own minimax fit by reweighted least squares,
-// relative error 5.4e-7 up to |k s| = 0.5, a 2000th of the rounding of the weights that follows), the
-// bracket advanced by additions from every eighth column on: two scores to an instruction, 4 + 1 more
-// for two scores than without, and nothing more for the special-function unit.  That is where all
-// products of the warp's rows are within half the cap and scores within kQuickScore of 0, slopes
+// relative error 5.4e-7 up to |k s| = 0.5, a 2000th of the rounding of the weights that follows), for
+// caps below kWideCap of degree 5 (5.9e-7 up to |k s| = 1; 4096 rows, cap 15: 267 -> 129 us, as most tiles
+// went the exact way before; at cap 50, where none does, it is 114 -> 129).  The bracket is advanced by
+// additions from every eighth column on: two scores to an instruction, 4 + 1 (6 + 1) more for two scores
+// than without, and nothing more for the special-function unit.  That is where all products of the
+// warp's rows are within half the cap (all of it) and scores within kQuickScore of 0, slopes
 // below kQuickSlope and all that is seen lies behind the row: a reference is then at most 2 x 22 (cap) and
 // 22 (bias) powers of two above the maximum, and what is 2^-60 of the largest weight still is a normal
 // number (the smallest products as well took 122 us in place of 115 for 4096 rows).
@@ -228,6 +230,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         PagedPlan *plan, const typename PagedKind<(MODE > 0)>::Entry *__restrict__ entries, int cap, int rows,
                         int Hq, const PagedView pv, const PagedMod mod, float c2, int *err) {
     constexpr bool MOD = MODE > 0, CAP = MODE & kModCap, BIAS = MODE & kModBias, SCORED = CAP || BIAS;
+    constexpr int DEG = !CAP ? 0 : MODE & kModWide ? kWideDegree : 3;  // of the quick way's polynomial
     typedef typename PagedKind<MOD>::Entry Entry;
     typedef PagedPreTask<MOD> Task;
     constexpr int kWords = sizeof(Entry) / 4;
@@ -676,7 +679,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 auto scored = [&](float s0) {  // cap tanh(s0 scale / cap), times log2(e)
                     if constexpr (!CAP) return s0 * c2;
                     const float x2 = s0 * s0;
-                    return s0 == -INFINITY ? s0 : s0 * fmaf(x2, fmaf(x2, fmaf(x2, mod.a3, mod.a2), mod.a1), mod.a0);
+                    float f = mod.a[DEG];
+#pragma unroll
+                    for (int k = DEG - 1; k >= 0; --k) f = fmaf(x2, f, mod.a[k]);
+                    return s0 == -INFINITY ? s0 : s0 * f;
                 };
                 float most = 0.f;
 #pragma unroll
@@ -730,17 +736,20 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const float alpha = move ? (m_old == -INFINITY ? 0.f : c_ex2(m_old - mt)) : 1.f;
             const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
             const uint64_t c2x2 = f2_pack(c2, c2), nmu2 = f2_pack(-mu, -mu);
-            // the argument's terms: (a0 + a1 s^2 + a2 s^4 + a3 s^6) s + b0 + step c; a tile that went the
+            // the argument's terms: (a[0] + a[1] s^2 + a[2] s^4 ..) s + b0 + step c; a tile that went the
             // exact way holds arguments already
-            [[maybe_unused]] float a0 = c2, a1 = 0.f, a2 = 0.f, a3 = 0.f, b0 = -mu, step = 0.f;
+            [[maybe_unused]] float a[DEG + 1], b0 = -mu, step = 0.f;
             if constexpr (SCORED) {
-                if constexpr (CAP) a0 = mod.a0, a1 = mod.a1, a2 = mod.a2, a3 = mod.a3;
+#pragma unroll
+                for (int k = 0; k <= DEG; ++k) a[k] = CAP ? mod.a[k] : c2;
                 if constexpr (BIAS) {
                     step = slope;
                     b0 = fmaf(slope, (float)(k0 - pos), -mu);
                 }
                 if (__builtin_expect(!quick, 0)) {
-                    a0 = 1.f, a1 = a2 = a3 = b0 = step = 0.f;
+#pragma unroll
+                    for (int k = 0; k <= DEG; ++k) a[k] = k == 0 ? 1.f : 0.f;
+                    b0 = step = 0.f;
 #pragma unroll
                     for (int c = 0; c < kPagedTile; ++c)  // (s^2 stays finite)
                         sv[c] = __float_as_uint(c_max_nan(__uint_as_float(sv[c]) - mu, -1e18f));
@@ -752,7 +761,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             for (int q = 0; q < 4; ++q) {  // 32 columns at a time, each step for all of them: element by element
                                            // they come out as chains of latencies
                 if constexpr (SCORED) {
-                    const uint64_t a0x2 = f2_pack(a0, a0), a1x2 = f2_pack(a1, a1), a2x2 = f2_pack(a2, a2), a3x2 = f2_pack(a3, a3);
+                    uint64_t ax2[DEG + 1];
+#pragma unroll
+                    for (int k = 0; k <= DEG; ++k) ax2[k] = f2_pack(a[k], a[k]);
                     const uint64_t b0x2 = f2_pack(b0, b0), step2 = f2_pack(2.f * step, 2.f * step);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {  // 16 columns at a time
@@ -766,18 +777,16 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                                 const float at = fmaf(step, (float)c, b0);
                                 run[e] = e & 3 ? f2_add(run[e - 1], step2) : f2_pack(at, at + step);
                             }
-                            f2[e] = a0x2;
+                            f2[e] = ax2[DEG];
                         }
                         if constexpr (CAP) {
                             uint64_t x2[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) x2[e] = f2_mul(s2[e], s2[e]);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], a3x2, a2x2);
+                            for (int k = DEG - 1; k >= 0; --k)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], f2[e], a1x2);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], f2[e], a0x2);
+                                for (int e = 0; e < 8; ++e) f2[e] = f2_fma(x2[e], f2[e], ax2[k]);
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -987,6 +996,9 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
         return cudaErrorInvalidValue;
     if (!a.scores) return launch<0>(a, g, mq, mk, mv, st);
     const bool cap = a.scores->softcap > 0.f, bias = a.scores->slopes != nullptr;
+    if (cap && paged_mod(a).wide)
+        return bias ? launch<kModMask + kModCap + kModWide + kModBias>(a, g, mq, mk, mv, st)
+                    : launch<kModMask + kModCap + kModWide>(a, g, mq, mk, mv, st);
     if (cap) return bias ? launch<kModMask + kModCap + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask + kModCap>(a, g, mq, mk, mv, st);
     return bias ? launch<kModMask + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask>(a, g, mq, mk, mv, st);
 }

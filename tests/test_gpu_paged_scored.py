@@ -322,6 +322,16 @@ def test_calls_captured_into_a_graph_follow_the_device_values(Y):
         check(O, pool, Q, [0, 40, 120], torch.full((120,), first), pre, 15.0, slopes_of(6), 0, 0, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("dtype, d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("cap", [3.0, 7.0, 12.0, 19.99, 20.0, 60.0])
+def test_caps_about_the_size_of_the_products(Y, cap, dtype, d, decode):
+    """Products on both sides of the polynomials' ends, with and without a bias."""
+    new, ctx = ([1, 1, 1], [400, 0, 900]) if decode else ([70, 1, 130], [300, 20, 0])
+    for bias in (False, True):
+        run(Y, new, ctx, 6, 2, d, 16, dtype, cap=cap, bias=bias, decode=decode)
+
+
 def test_same_bits_every_time(Y):
     pool, Q, O, s = run(Y, [200, 300, 5], [3000, 3, 6000], 6, 2, 128, 16, "bf16", cap=20.0, bias=True, docs=500, prefix=[50, 200, 9])
     first = O.clone()
