@@ -30,8 +30,8 @@
 //
 // One block per SM; it takes entry after entry of the plan's list from a counter, longest first.
 // The next entry is chosen three tiles before this one's end, gets barriers of its own (two
-// groups in turn, set up anew while the other is in use) and its first K tile while this one's
-// rows are written; then all warps meet.
+// groups in turn, set up anew while the other is in use) and its Q and first K tile while this one's
+// last product runs and its rows are written; then all warps meet.
 //
 // Warps: 0 TMA producer, 1 issues S products, 2 issues P V products, 3 the next entry, 4-7 set
 // A, 8-11 set B (thread = TMEM lane = row).  S and P V have issuers of their own so that
@@ -39,8 +39,7 @@
 //
 // What bounds it (512 rows over 131072 keys: 586-630 us with the card's power, 1.46 us a tile of
 // 2 x 128 rows at the least; the products alone are 1.08): the softmax warps' own chain, about 2800 cycles a tile from S to P
-// with no pipe above a third; and some 6 us an entry around its tiles (first Q, K, S; last P V;
-// rows out).  What counted, each timed as the kernel then was, on the long chunk if not said:
+// with no pipe above a third; and some 5 us an entry around its tiles (first S; last P V; rows out).  What counted, each timed as the kernel then was, on the long chunk if not said:
 //   - no register spilled in the tile loop: shared memory leaves next to no L1, so each reload
 //     is an L2 round trip (140 bytes of spills: 1.5 x the time).  Hence the 120 / 192 split;
 //   - the exponentials in steps over 32 columns, not element by element (740 -> 690 us);
@@ -53,7 +52,10 @@
 //   - blocks that stay instead of one per entry: 600 short sequences 218 -> 172 us, 3 windows 129
 //     -> 123, 16 prompts of 100 to 900 rows 67 -> 62; 12 mixed sequences, about one entry to a
 //     block, 61.3 -> 62 (59 today).  The next kernel is let in when a block has found no further entry, not
-//     at once (2 us).
+//     at once (2 us);
+//   - Q and K ahead, and so rows staged in V tiles: 600 sequences of 1 to 30 rows over 10 to 400 keys 203
+//     -> 185 us, 8192 rows with a window of 500 82 -> 77, 16 prompts 47 -> 45, 8192 rows of documents
+//     100.5 -> 98.6.  The first S ahead as well: the sequences 201, and capped tiles 3 % slower.
 // Tried and slower: two warps to a row (half the columns each, 808 against 740 us), weights
 // before the maximum is known (752); S read twice by halves made no difference, nor did both
 // sets on one set's rows, tile by tile, where the rows fit one (its time is the reads').
@@ -372,14 +374,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const Entry &blk = task.blk;
             const int ntiles = blk.i1 - blk.i0;
             volatile int no_abort = 0;
+            int nk = 0, nv = 0;  // tiles whose K / V copy was issued
             bool told = false;  // warp 3 takes the next entry late: who is done first takes the longest
             auto tell = [&]() {
                 if (!told) asm volatile("bar.arrive 11, 64;\n" ::: "memory");
                 told = true;
             };
             if (ntiles > 0) {
-                if (n > 0) copy_q(task);
-                int nk = 1, nv = 0;  // tiles whose K / V copy was issued
+                nk = 1;
                 const int c_i0 = BIAS ? blk.i1 - 1 : blk.i0, c_sink = blk.range.sink_slots, c_delta = blk.range.base - c_sink, c_hk = task.hk;
                 bool ok = true;
                 auto load = [&](int i, bool is_v, int page) {
@@ -406,29 +408,46 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     pg1 = pg2;
                 }
                 tell();
+                // leave no copy in flight (only the last two of each kind can be), no tile in use, nor a commit
+                // on its way to a barrier that is set up anew: here Q and K, below V
                 if (lane == 0) {
-                    // leave no copy in flight (only the last two of each kind can be)
                     mbar_wait(&task.bar.q_full, 0, &no_abort, 200000000ull);
                     for (int k = max(0, nk - kCStages); k < nk; ++k)
                         mbar_wait(&task.bar.kfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
-                    for (int k = max(0, nv - kCStages); k < nv; ++k)
-                        mbar_wait(&task.bar.vfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
-                    // nor a tile in use, nor a commit on its way to a barrier that is set up anew
                     for (int k = max(0, nk - kCStages); k < nk && ok; ++k)
                         ok = mbar_wait(&task.bar.kempty[k % kCStages], (k / kCStages) & 1, abort_flag);
-                    for (int k = max(0, nv - kCStages); k < nv && ok; ++k)
-                        ok = mbar_wait(&task.bar.vempty[k % kCStages], (k / kCStages) & 1, abort_flag);
                     if (!ok) fail(51);
                 }
                 __syncwarp();
             }
             tell();
-            // the next entry's first K tile comes in while this one's rows are written
+            // the next entry's first K tile and Q come in while the last product runs and this one's rows
+            // are written (Q after the last product where that reads P from Q_B's place)
             asm volatile("bar.sync 10, 64;\n" ::: "memory");
             const bool ahead = next.more && next.blk.i1 > next.blk.i0 && __all_sync(0xffffffffu, !*abort_flag);
+            const bool early = blk.nrow > TS || ntiles == 0;
             if (ahead) first_k(next);
+#pragma unroll 1
+            for (int step = 0; step < 2; ++step) {
+                if (step == (early ? 0 : 1)) {
+                    if (ahead) copy_q(next);
+                } else if (ntiles > 0) {
+                    if (lane == 0) {
+                        bool ok = true;
+                        for (int k = max(0, nv - kCStages); k < nv; ++k)
+                            mbar_wait(&task.bar.vfull[k % kCStages], (k / kCStages) & 1, &no_abort, 200000000ull);
+                        for (int k = max(0, nv - kCStages); k < nv && ok; ++k)
+                            ok = mbar_wait(&task.bar.vempty[k % kCStages], (k / kCStages) & 1, abort_flag);
+                        if (!ok) fail(51);
+                    }
+                    __syncwarp();
+                }
+            }
             if (!c_end(abort_flag)) {
-                if (ahead && lane == 0) mbar_wait(&next.bar.kfull[0], 0, &no_abort, 200000000ull);
+                if (ahead && lane == 0) {
+                    mbar_wait(&next.bar.kfull[0], 0, &no_abort, 200000000ull);
+                    mbar_wait(&next.bar.q_full, 0, &no_abort, 200000000ull);
+                }
                 break;
             }
             if (!next.more) break;
@@ -479,13 +498,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const int ntiles = blk.i1 - blk.i0;
             const bool two = blk.nrow > TS;
             if (lane == 0) {
+                const uint64_t dp0 = smem_desc_sw128(smem_u32(sP), 16, 1024), dv0 = smem_desc_sw128(smem_u32(ring + kCTile), kCHalf, 1024);
                 const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);  // A = P (K-major), B = V (N-major)
                 bool ok = true;
                 for (int i = 0; i < ntiles && ok; ++i) {
                     const int s = i % kCStages;
+                    uint64_t dp = dp0 - (uint64_t)(!two && (i & 1) ? kCTile >> 4 : 0), dv = dv0 + (uint64_t)(s * (2 * kCTile >> 4));
+                    asm volatile("" : "+l"(dp), "+l"(dv));
                     if (!(ok = mbar_wait(&bar.vfull[s], (i / kCStages) & 1, abort_flag))) break;
-                    const uint64_t dp = smem_desc_sw128(smem_u32(!two && (i & 1) ? sQ + kCTile : sP), 16, 1024);
-                    const uint64_t dv = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile + kCTile), kCHalf, 1024);
                     for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
                         const int b = p_slot(two, x, i);
                         for (int hh = 0; hh < 2; ++hh) {
@@ -900,9 +920,10 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     pp[(size_t)kCD * kCRows] = m_ref;
                     pp[(size_t)(kCD + 1) * kCRows] = l;
                 } else {
-                    // o = O / l as bf16, staged in this set's Q tile (every S product is done), then rows
-                    // of 256 bytes side by side
-                    uint8_t *stg = sQ + x * kCTile;
+                    // o = O / l as bf16, staged in a V tile that no product reads any more (set B's last
+                    // comes after set A's: B takes the last tile's, A the other), then rows of 256 bytes side
+                    // by side
+                    uint8_t *stg = ring + (size_t)((ntiles + x) & 1) * 2 * kCTile + kCTile;
                     // (a row whose scores are all -inf: 0 / 0, NaN as softmax has it)
                     bool blind = pos < 0;  // sees nothing
                     if constexpr (MOD) blind = lo > pos && doc >= head;
