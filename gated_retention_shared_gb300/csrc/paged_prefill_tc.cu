@@ -20,7 +20,7 @@
 //
 // The kernel is a template: MODE 0 is the plain call's, the others are those of the scored calls
 // (masks; a cap; a bias by distance; both), whose softmax is described at c_scores.  4096 fresh rows
-// take 87 us plain, 90 with masks, 103 biased, 115 capped, 138 with both: in the tile loop the fp32 pipe
+// take 86 us plain, 90 with masks, 102 biased, 115 capped, 135 with both: in the tile loop the fp32 pipe
 // (37 % with a cap) and the chain from S to P; the products are 54.
 //
 // Pages, rows out of sight and pages that are not there: as in paged_decode_tc.cu; set A's
