@@ -131,10 +131,10 @@ struct PagedMod {
     const int32_t *doc;         // [rows], or nullptr
     float cap2;                 // cap log2(e); 0: no cap
     float qk;                   // what q.k is multiplied by: scale / cap with a cap, else scale log2(e)
-    // with a cap, for |q.k| <= quick: cap2 tanh(qk s) = s (a[0] + a[1] s^2 + a[2] s^4 ..), to a[3] or,
-    // `wide`, to a[kWideDegree]
+    // with a cap, for |q.k| <= quick: cap2 tanh(qk s) = s (a[0] + a[1] s^2 + .. + a[degree] s^(2 degree)),
+    // the others 0
     float a[6], quick;
-    bool wide;
+    int degree;
     float hidden;  // a product whose weight comes out as 0 that way
 };
 
@@ -197,14 +197,15 @@ __device__ __forceinline__ float paged_cap(float u, float C) {
 }
 
 // what a tensor-core kernel's rows do to their scores before the softmax, beyond the plain calls'
-constexpr int kModMask = 1, kModCap = 2, kModBias = 4, kModWide = 8;
+constexpr int kModMask = 1, kModCap = 2, kModBias = 4, kModWide = 8, kModShort = 16;
 
 constexpr float kPagedLog2E = 1.4426950408889634f;
-// the tensor-core prefill's quick way (paged_prefill_tc.cu): caps below kWideCap get the longer polynomial,
-// whose range is all of the cap (4096 rows, scores of deviation 2, us with the short and the long one: cap
-// 50 114 129, cap 20 126 128, cap 15 267 129, cap 10 279 140, cap 8 278 258)
-constexpr int kWideDegree = 5;
-constexpr float kWideCap = 20.f;
+// the tensor-core prefill's quick way (paged_prefill_tc.cu): the polynomial of degree 3 reaches to half the
+// cap, caps below kWideCap get one of degree 5 for all of the cap, those from kShortCap on one of degree 2
+// for 0.26 of it (4096 rows, scores of deviation 2, us with 2, 3 and 5: cap 50 110 114 129, cap 40 116 114 128,
+// cap 30 242 114 129, cap 20 273 126 128, cap 15 267 129 with 3 and 5, cap 10 279 140, cap 8 278 258)
+constexpr float kWideCap = 20.f, kShortCap = 45.f;
+__host__ __device__ constexpr int paged_cap_degree(int mode) { return mode & kModWide ? 5 : mode & kModShort ? 2 : 3; }
 // and how large scores and slopes may be, times log2(e)
 constexpr float kQuickScore = 22.f, kQuickSlope = 22.f / 15.f;
 

@@ -243,15 +243,20 @@ PagedMod paged_mod(const PagedArgs &a) {
     m.cap2 = cap * kPagedLog2E;
     if (cap > 0.f) {
         const double k = m.qk, c = m.cap2;
-        m.wide = cap < kWideCap;
-        static const double fit[2][6] = {{0.999999456, -0.33326318, 0.131902967, -0.0444022262},
-                                         {0.999999414, -0.333290425, 0.132814342, -0.0516056791, 0.016743118, -0.00306706059}};
-        const int deg = m.wide ? kWideDegree : 3;
-        m.quick = (float)std::min((m.wide ? 1.0 : 0.5) / k, kQuickScore / (c * k));
-        // (the last term is negative: the polynomial falls with s^7 or s^11, here to some -2^100 C)
-        m.hidden = (float)((m.wide ? 1024.0 : 32768.0) / k);
-        for (int i = 0; i <= deg; ++i) {
-            const double x = c * std::pow(k, 2 * i + 1) * fit[m.wide][i];
+        struct Fit {  // of tanh(x) / x in x^2: up to |x| = reach; a product of `far` / k gets weight 0
+            int degree;
+            double reach, far, a[6];
+        };
+        static const Fit fits[3] = {
+            {2, 0.26, -0x1p20, {0.999999501, -0.333200077, 0.128027106}},  // (the last term is positive: it falls towards -s^5)
+            {3, 0.5, 0x1p15, {0.999999456, -0.33326318, 0.131902967, -0.0444022262}},
+            {5, 1.0, 0x1p10, {0.999999414, -0.333290425, 0.132814342, -0.0516056791, 0.016743118, -0.00306706059}}};
+        const Fit &fit = fits[cap < kWideCap ? 2 : cap < kShortCap ? 1 : 0];
+        m.degree = fit.degree;
+        m.quick = (float)std::min(fit.reach / k, kQuickScore / (c * k));
+        m.hidden = (float)(fit.far / k);  // (there the polynomial is some -2^100 C)
+        for (int i = 0; i <= m.degree; ++i) {
+            const double x = c * std::pow(k, 2 * i + 1) * fit.a[i];
             m.a[i] = (float)x;
             // (caps that 32 bits cannot follow that way go the exact way)
             if (!(std::fabs(x) > 1e-36 && std::fabs(x) < 1e36)) m.quick = -1.f;

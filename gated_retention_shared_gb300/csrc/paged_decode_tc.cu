@@ -382,7 +382,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                         for (int n = 0; n < NQ; ++n) {
                             const float s0 = __uint_as_float(sv[n]), x2 = s0 * s0;
                             float f = fmaf(x2, mod.a[3], mod.a[2]);
-                            if (mod.wide) f = fmaf(x2, fmaf(x2, fmaf(x2, mod.a[5], mod.a[4]), mod.a[3]), mod.a[2]);
+                            if (mod.degree == 5) f = fmaf(x2, fmaf(x2, fmaf(x2, mod.a[5], mod.a[4]), mod.a[3]), mod.a[2]);
                             sc[n] = s0 * fmaf(x2, fmaf(x2, f, mod.a[1]), mod.a[0]);
                         }
                     } else {

@@ -189,11 +189,12 @@ __device__ __forceinline__ uint32_t c_below(int n) {
 //     2^(s Q(s^2) + (slope (m - p) - reference)),
 // Q the polynomial of C tanh(k s) / s of degree 3 in s^2 (own minimax fit by reweighted least squares,
 // relative error 5.4e-7 up to |k s| = 0.5, a 2000th of the rounding of the weights that follows), for
-// caps below kWideCap of degree 5 (5.9e-7 up to |k s| = 1; 4096 rows, cap 15: 267 -> 129 us, as most tiles
-// went the exact way before; at cap 50, where none does, it is 114 -> 129).  The bracket is advanced by
-// additions from every eighth column on: two scores to an instruction, 4 + 1 (6 + 1) more for two scores
-// than without, and nothing more for the special-function unit.  That is where all products of the
-// warp's rows are within half the cap (all of it) and scores within kQuickScore of 0, slopes
+// caps below kWideCap of degree 5 (5.9e-7 up to 1; 4096 rows, cap 15: 267 -> 129 us, as most tiles went the
+// exact way before; at cap 50, where none does, it is 114 -> 129), from kShortCap on of degree 2 (5.0e-7 up
+// to 0.26; cap 50 114 -> 110 us, with a bias 135 -> 126).  The bracket is advanced by additions from every eighth column on: two
+// scores to an instruction, degree + 2 more for two scores than without, and nothing more for the
+// special-function unit.  That is where all products of the warp's rows are within the polynomial's range
+// and scores within kQuickScore of 0, slopes
 // below kQuickSlope and all that is seen lies behind the row: a reference is then at most 2 x 22 (cap) and
 // 22 (bias) powers of two above the maximum, and what is 2^-60 of the largest weight still is a normal
 // number (the smallest products as well took 122 us in place of 115 for 4096 rows).
@@ -232,7 +233,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         PagedPlan *plan, const typename PagedKind<(MODE > 0)>::Entry *__restrict__ entries, int cap, int rows,
                         int Hq, const PagedView pv, const PagedMod mod, float c2, int *err) {
     constexpr bool MOD = MODE > 0, CAP = MODE & kModCap, BIAS = MODE & kModBias, SCORED = CAP || BIAS;
-    constexpr int DEG = !CAP ? 0 : MODE & kModWide ? kWideDegree : 3;  // of the quick way's polynomial
+    constexpr int DEG = CAP ? paged_cap_degree(MODE) : 0;  // of the quick way's polynomial
     typedef typename PagedKind<MOD>::Entry Entry;
     typedef PagedPreTask<MOD> Task;
     constexpr int kWords = sizeof(Entry) / 4;
@@ -1017,10 +1018,14 @@ cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_
         return cudaErrorInvalidValue;
     if (!a.scores) return launch<0>(a, g, mq, mk, mv, st);
     const bool cap = a.scores->softcap > 0.f, bias = a.scores->slopes != nullptr;
-    if (cap && paged_mod(a).wide)
-        return bias ? launch<kModMask + kModCap + kModWide + kModBias>(a, g, mq, mk, mv, st)
-                    : launch<kModMask + kModCap + kModWide>(a, g, mq, mk, mv, st);
-    if (cap) return bias ? launch<kModMask + kModCap + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask + kModCap>(a, g, mq, mk, mv, st);
+    if (cap) {
+        constexpr int both = kModMask + kModCap;
+        switch (paged_mod(a).degree) {
+            case 2: return bias ? launch<both + kModShort + kModBias>(a, g, mq, mk, mv, st) : launch<both + kModShort>(a, g, mq, mk, mv, st);
+            case 3: return bias ? launch<both + kModBias>(a, g, mq, mk, mv, st) : launch<both>(a, g, mq, mk, mv, st);
+            default: return bias ? launch<both + kModWide + kModBias>(a, g, mq, mk, mv, st) : launch<both + kModWide>(a, g, mq, mk, mv, st);
+        }
+    }
     return bias ? launch<kModMask + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask>(a, g, mq, mk, mv, st);
 }
 

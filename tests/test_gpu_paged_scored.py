@@ -332,6 +332,15 @@ def test_caps_about_the_size_of_the_products(Y, cap, dtype, d, decode):
         run(Y, new, ctx, 6, 2, d, 16, dtype, cap=cap, bias=bias, decode=decode)
 
 
+@pytest.mark.parametrize("std", [0.5, 3.0, 8.0])
+@pytest.mark.parametrize("cap", [19.99, 20.0, 44.99, 45.0, 100.0])
+def test_products_about_the_ends_of_the_polynomials(Y, cap, std):
+    """Each degree's neighbours, with products from within its range to past it; masked and whole tiles."""
+    for bias in (False, True):
+        run(Y, [130, 40], [300, 0], 6, 2, 128, 16, "bf16", cap=cap, bias=bias, std=std, docs=170)
+    run(Y, [1, 1, 1], [300, 0, 900], 6, 2, 128, 16, "bf16", cap=cap, std=std, decode=True)
+
+
 def test_same_bits_every_time(Y):
     pool, Q, O, s = run(Y, [200, 300, 5], [3000, 3, 6000], 6, 2, 128, 16, "bf16", cap=20.0, bias=True, docs=500, prefix=[50, 200, 9])
     first = O.clone()
