@@ -524,6 +524,8 @@ yoco_status yoco_rope_apply_scaled(const void *x, int64_t x_row, int64_t x_head,
     if (!aligned(positions, 4)) return fail(YOCO_ERR_INVALID_ARG, "positions must be 4-byte aligned");
     if (x == out && rows != 0 && (x_row != out_row || x_head != out_head))
         return fail(YOCO_ERR_INVALID_ARG, "in place the strides must be the same");
+    if ((rows > 1 && out_row == 0) || (H > 1 && out_head == 0))
+        return fail(YOCO_ERR_INVALID_ARG, "out's rows and heads must each have a place of their own");
     if (rows == 0) return YOCO_OK;
     YOCO_INJECTED_FAILURE("rope_apply_scaled");
     const RopeArgs a{x, x_row, x_head, out, out_row, out_head, rows, H, d, positions, pos0, dt};

@@ -375,7 +375,7 @@ typedef struct {
  * adjacent) to out [rows, H, d] with strides of its own: for instance q and k, as Hq + Hkv heads,
  * out of a fused projection.  Row i is at positions[i] (device int32 [rows], any value), or at
  * pos0 + i where positions is NULL (pos0 is not looked at otherwise); |pos0| + rows <= 2^31.
- * out may be x itself with the same strides, and must not overlap it otherwise.
+ * out may be x itself with the same strides, and must not overlap it otherwise, nor itself (x may).
  *   d in {64, 128}; pointers and strides multiples of 16 bytes; rows * H < 2^31.
  */
 YOCO_API yoco_status yoco_rope_apply_scaled(const void *x, int64_t x_row, int64_t x_head, void *out, int64_t out_row,

@@ -62,6 +62,12 @@ def test_bad_rope_arguments(Y, kw, status):
     assert rope(Y, rope_c(Y), **kw) == status
 
 
+@pytest.mark.parametrize("kw", [dict(orow=0), dict(oh=0), dict(out=F[0], xr=0, orow=0), dict(out=F[0], xh=0, oh=0)])
+def test_rows_or_heads_that_come_out_in_one_place_are_refused(Y, kw):
+    assert rope(Y, rope_c(Y), **kw) == Y.YOCO_ERR_INVALID_ARG
+    assert rope(Y, rope_c(Y), **kw, rows=0) == (Y.YOCO_ERR_INVALID_ARG if "oh" in kw else Y.YOCO_OK)
+
+
 def test_null_and_empty_rope_calls(Y):
     assert rope(Y, None) == Y.YOCO_ERR_INVALID_ARG
     assert append(Y, None) == Y.YOCO_ERR_INVALID_ARG
