@@ -346,6 +346,53 @@ def test_large_pool(Y):
     assert torch.equal(cache.page_table[:, :4000].reshape(-1).sort()[0], torch.arange(pages, dtype=torch.int32, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_pools_past_32_bits_of_elements(Y, dtype, d):
+    """Pages behind 2^31 elements of each tensor: appended to with a rotation, shared, copied, attended, moved."""
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lead = 2 ** 31 // (2 * 64 * d)
+    g = torch.Generator().manual_seed(9)
+
+    def ints(*x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def served(first):
+        """Pages before `first` are someone else's.  What every call gives, and where it was."""
+        k, v = (torch.empty(first + 9, 2, 64, d, dtype=t, device="cuda") for _ in range(2))
+        k[first:], v[first:] = 0, 0
+        cache = Y.PagedKV(k, v, torch.full((3, 4), -1, dtype=torch.int32).cuda(), ints(0, 0, 0))
+        refs = torch.zeros(first + 9, dtype=torch.int32, device="cuda")
+        refs[:first] = 1
+        ws = torch.zeros(Y.yoco_paged_pool_workspace_size(cache), dtype=torch.uint8, device="cuda")
+        Y.yoco_paged_resize(cache, refs, ints(150, 0, 40), workspace=ws)
+        rope = Y.Rope(layout="halves", rotary_dim=32, scaling="ntk", factor=4.0)
+        Y.yoco_paged_append_rope(new[0], new[1], cache, rope, cu_rows=ints(0, 150, 150, 190), workspace=ws)
+        Y.yoco_paged_fork(cache, refs, ints(0), ints(1), workspace=ws)
+        Y.yoco_paged_resize(cache, refs, ints(151, 200, 41), workspace=ws)
+        rows = new[2][:52]
+        Y.yoco_paged_append_rope(rows, rows, cache, rope, cu_rows=ints(0, 1, 51, 52), workspace=ws)
+        out = [torch.zeros(52, 6, d, dtype=t, device="cuda"), torch.zeros(3, 6, d, dtype=t, device="cuda")]
+        scores = Y.PagedScores(softcap=30.0)
+        Y.yoco_paged_attn_prefill_scored(q, cache, ints(0, 1, 51, 52), out[0], scores)
+        Y.yoco_paged_attn_decode_scored(q[:3], cache, out[1], scores)
+        assert cache.page_table[:, 0].min() >= first or first == 0
+        # without the others the pages move to the front
+        refs[:first] = 0
+        Y.yoco_paged_compact(cache, refs, workspace=ws)
+        out.append(torch.zeros(3, 6, d, dtype=t, device="cuda"))
+        Y.yoco_paged_attn_decode_scored(q[:3], cache, out[2], scores)
+        Y.yoco_workspace_status(ws)
+        assert cache.page_table.max() < 9
+        return [x.cpu() for x in out] + [cache.page_table.cpu(), refs[:9].cpu()]
+
+    new = [torch.randn(190, 2, d, generator=g).to(t).cuda() for _ in range(3)]
+    q = torch.randn(52, 6, d, generator=g).to(t).cuda()
+    far, near = served(lead + 3), served(0)
+    for a, b in zip(far, near):
+        assert torch.equal(a, b)
+    assert torch.equal(far[1], far[2]) and bool(far[0].abs().sum(-1).gt(0).all())
+
+
 def test_copy_leaves_out_what_names_no_page(Y):
     k = torch.randn(6, 2, 16, 64, device="cuda")
     v = torch.randn(6, 2, 16, 64, device="cuda")
