@@ -114,13 +114,29 @@ __device__ __forceinline__ float plan_cost(const PlanArgs &a, int B, int Hkv, in
 #pragma unroll
         for (int k = 0; k < 8; ++k) over[k] += (float)len >= part[k] * (float)most ? s.x * pc : 0;
     }
+    // (a lane to each, and the loops above not unrolled: one block that runs each line once or twice takes as
+    // long as its code takes to come.  8192 rows of documents 96.9 us; loops unrolled by two 98.0, four 99.4)
+    int n_over = 0;
+    float its_part = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const int rounds = (__reduce_add_sync(0xffffffffu, over[k]) * Hkv + a.slots - 1) / a.slots;
-        cost = max(cost, (float)rounds * (part[k] * (float)most + a.entry_cost));
+        const int sum = __reduce_add_sync(0xffffffffu, over[k]);
+        n_over = lane == k ? sum : n_over;
+        its_part = lane == k ? part[k] : its_part;
     }
+    const int rounds = (n_over * Hkv + a.slots - 1) / a.slots;
+    cost = max(cost, (float)rounds * (its_part * (float)most + a.entry_cost));
+    cost = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cost)));  // (positive: in their bits' order)
     cost += split > 0 ? .75f * a.entry_cost + (float)split * a.split_cost : 0.f;
     return split <= a.max_split ? cost : 3e38f;
+}
+
+// the Q of the least cost, the first of several (costs are positive: their bits are in their order)
+__device__ __forceinline__ int plan_best(const float *cost, const int *q) {
+    const int lane = threadIdx.x & 31;
+    const unsigned mine = lane < kPlanTries ? __float_as_uint(cost[lane]) : 0xffffffffu;
+    const unsigned least = __reduce_min_sync(0xffffffffu, mine);
+    return q[__ffs(__ballot_sync(0xffffffffu, mine == least)) - 1];
 }
 
 // what row block j of sequence b sees, number g of the call's (row bounds that overlap may pass the
@@ -201,10 +217,7 @@ paged_plan_small_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a
             }
         }
         __syncthreads();
-        // (costs are positive: their bits are in their order)
-        const unsigned mine = lane < kPlanTries ? __float_as_uint(c_cost[lane]) : 0xffffffffu;
-        const unsigned least = __reduce_min_sync(0xffffffffu, mine);
-        Q = c_q[__ffs(__ballot_sync(0xffffffffu, mine == least)) - 1];
+        Q = plan_best(c_cost, c_q);
     }
     // longest entries first: where this lane's sequence starts is what all before it take
     const int pc = plan_pieces(s.tiles, Q), len = s.blocks > 0 ? (s.tiles + pc - 1) / pc : -1;
@@ -246,7 +259,7 @@ paged_plan_small_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a
     }
 }
 
-// With documents each row block is looked at (eight lanes read its rows' document starts) and, where
+// With documents each row block is looked at (four lanes read its rows' document starts) and, where
 // there is room for them, planned by itself as if it were a sequence: what they see may differ by
 // much.  (As one sequence with the longest block's tiles 8192 rows of documents of 700 with a
 // question of 100 rows that sees all of them were not cut: 157 us.)
@@ -308,7 +321,7 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
         // (row bounds that overlap may pass what there is room for)
         single = block0[B] <= a.units;
         const int all = min(block0[B], a.cap);
-        for (int g0 = tid / 8; g0 - (tid & 31) / 8 < all; g0 += kPlanThreads / 8) {
+        for (int g0 = tid / 4; g0 - (tid & 31) / 4 < all; g0 += kPlanThreads / 4) {
             const int g = min(g0, all - 1);
             int lo = 0, hi = B;  // the sequence: block0[lo] <= g < block0[lo + 1]
             while (hi - lo > 1) {
@@ -319,11 +332,13 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
             const PlanSeq s = plan_seq<MOD>(pv, mod, a.cu, a.rows, a.T_R, lo, nullptr);
             const int j = g - block0[lo], r1 = min(s.n, (j + 1) * a.T_R);
             int least = 0x7fffffff;
-#pragma unroll 8
-            for (int r = j * a.T_R + (lane & 7); r < r1; r += 8) least = min(least, mod.doc[s.first + r]);
+            for (int r = j * a.T_R + (lane & 3); r < r1; r += 48) {  // (twelve loads on their way at a time)
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, off));
-            if ((lane & 7) == 0 && g0 < all) {
+                for (int k = 0; k < 12; ++k) least = min(least, mod.doc[s.first + min(r + 4 * k, r1 - 1)]);
+            }
+#pragma unroll
+            for (int off = 2; off > 0; off >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, off));
+            if ((lane & 3) == 0 && g0 < all) {
                 a.doc_lo[g] = least;
                 const int n = plan_range(a, pv, mod, s, lo, j, g).ntiles;
                 if (single) {
@@ -368,10 +383,7 @@ paged_plan_kernel(const PagedView pv, const PagedMod mod, const PlanArgs a) {
             }
         }
         __syncthreads();
-        int best = 0;
-        for (int k = 1; k < kPlanTries; ++k)
-            if (c_cost[k] < c_cost[best]) best = k;
-        Q = c_q[best];
+        Q = plan_best(c_cost, c_q);
     }
     // longest entries first: ranked, or, of many sequences, by 32nds of the longest (in a class
     // the order is any: it decides who runs when, not what comes out)
