@@ -251,7 +251,8 @@ PagedMod paged_mod(const PagedArgs &a) {
             {2, 0.26, -0x1p20, {0.999999501, -0.333200077, 0.128027106}},  // (the last term is positive: it falls towards -s^5)
             {3, 0.5, 0x1p15, {0.999999456, -0.33326318, 0.131902967, -0.0444022262}},
             {5, 1.0, 0x1p10, {0.999999414, -0.333290425, 0.132814342, -0.0516056791, 0.016743118, -0.00306706059}}};
-        const Fit &fit = fits[cap < kWideCap ? 2 : cap < kShortCap ? 1 : 0];
+        // (head size 64 makes do with two of them)
+        const Fit &fit = fits[cap < kWideCap ? 2 : cap < kShortCap || a.cache->d == 64 ? 1 : 0];
         m.degree = fit.degree;
         m.quick = (float)std::min(fit.reach / k, kQuickScore / (c * k));
         m.hidden = (float)(fit.far / k);  // (there the polynomial is some -2^100 C)

@@ -1,5 +1,5 @@
 // paged_prefill_tc.cu -- attention of chunks of new rows over the paged cache on the tensor
-// cores, bf16, head size 128, up to 16 query heads to a kv head.
+// cores, bf16, head size 128 (with scores 64 too), up to 16 query heads to a kv head.
 //
 // A row of the MMA is one (token, query head of the kv head's group): 128 rows are
 // TS = 128 / G tokens with their G heads, so the group reads each K and V tile once, and a
@@ -72,10 +72,9 @@ namespace yoco {
 
 using namespace tc;
 
-constexpr int kCD = 128;                       // head size
 constexpr int kCRows = 128;                    // rows of a set
 constexpr int kCStages = 2;
-constexpr int kCTile = kPagedTile * kCD * 2;   // 32 KB
+constexpr int kCTile = kPagedTile * 128 * 2;   // 32 KB (at head size 64 Q, K and V use the first half of theirs)
 constexpr int kCHalf = kCTile / 2;             // 64 channels (or keys) of 128 rows
 constexpr int kCThreads = 384;
 constexpr float kCGap = 8.f * kPagedLog2E;
@@ -226,7 +225,7 @@ __device__ __forceinline__ float c_max_nan(float a, float b) {  // NaN where one
     return r;
 }
 
-template <int MODE>
+template <int MODE, int D>
 __global__ void __launch_bounds__(kCThreads, 1)
 paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, bf16_t *__restrict__ O, float *__restrict__ part,
@@ -237,6 +236,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     typedef typename PagedKind<MOD>::Entry Entry;
     typedef PagedPreTask<MOD> Task;
     constexpr int kWords = sizeof(Entry) / 4;
+    constexpr int kHalves = D / 64, kChunks = D / 8;  // of a row: 64 channels, 16 bytes
+    static_assert(D == 64 || D == 128, "halves of 64 channels");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     uint8_t *tiles = smem_raw + pad;
@@ -290,8 +291,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     __syncthreads();
     if (!sm.task[0].more) return;
     // the TMA warp's lanes: a tile is `boxes` boxes of pages, 64 channels each
-    const int psz = min(1 << pv.shift, kPagedTile), boxes = 2 * (kPagedTile / psz);
-    const int mine = (lane >> 1) * psz;
+    const int psz = min(1 << pv.shift, kPagedTile), boxes = kHalves * (kPagedTile / psz);
+    const int mine = lane / kHalves * psz;
     // what the table says of this lane's box of tile i (fetched ahead of use, so not yet looked
     // at); -1 past the last place
     // the entry's i-th tile.  A bias takes the nearest first: from the farthest on, each tile's scores
@@ -309,7 +310,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         if (lane < boxes && tile_of(blk, i) * kPagedTile + mine < blk.range.places) paged_report(err, kErrPagedPage);
         return pv.num_pages;
     };
-    const int half = lane & 1;
+    const int half = lane % kHalves;
     auto row_of = [&](const Entry &blk, int i) -> int {  // of tile i's box in its page
         return blk.range.slot(tile_of(blk, i) * kPagedTile + mine) & ((1 << pv.shift) - 1);
     };
@@ -317,7 +318,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int s = i % kCStages;
         uint8_t *st = ring + (size_t)s * 2 * kCTile + (is_v ? kCTile : 0);
         uint64_t *full = is_v ? &task.bar.vfull[s] : &task.bar.kfull[s];
-        if (lane == 0) mbar_arrive_expect_tx(full, kCTile);
+        if (lane == 0) mbar_arrive_expect_tx(full, kHalves * kCHalf);
         __syncwarp();
         if (lane < boxes)
             tma_load_4d(st + half * kCHalf + mine * 128, is_v ? &tm_v : &tm_k, full, half * 64, row, hk, page);
@@ -325,9 +326,9 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     auto copy_q = [&](Task &task) {
         if (lane == 0) {
             const int sets = task.blk.nrow > TS ? 2 : 1;
-            mbar_arrive_expect_tx(&task.bar.q_full, (uint32_t)(sets * 2 * TS * G * 128));
+            mbar_arrive_expect_tx(&task.bar.q_full, (uint32_t)(sets * kHalves * TS * G * 128));
             for (int x = 0; x < sets; ++x)
-                for (int hf = 0; hf < 2; ++hf)
+                for (int hf = 0; hf < kHalves; ++hf)
                     tma_load_3d(sQ + x * kCTile + hf * kCHalf, &tm_q, &task.bar.q_full, hf * 64, task.hk * G,
                                 task.blk.row0 + x * TS);
         }
@@ -474,7 +475,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         const uint64_t dq = smem_desc_sw128(smem_u32(sQ + x * kCTile), 16, 1024);
                         const uint64_t dk = smem_desc_sw128(smem_u32(ring + (size_t)s * 2 * kCTile), 16, 1024);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
+                        for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t off = ((kk >> 2) * kCHalf + (kk & 3) * 32) >> 4;
                             mma_ss(tmem + 256 * x, dq + off, dk + off, id_s, kk > 0);
                         }
@@ -500,7 +501,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const bool two = blk.nrow > TS;
             if (lane == 0) {
                 const uint64_t dp0 = smem_desc_sw128(smem_u32(sP), 16, 1024), dv0 = smem_desc_sw128(smem_u32(ring + kCTile), kCHalf, 1024);
-                const uint32_t id_o = idesc_bf16_f32(kCRows, kCD, false, true);  // A = P (K-major), B = V (N-major)
+                const uint32_t id_o = idesc_bf16_f32(kCRows, D, false, true);  // A = P (K-major), B = V (N-major)
                 bool ok = true;
                 for (int i = 0; i < ntiles && ok; ++i) {
                     const int s = i % kCStages;
@@ -567,8 +568,8 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int hk = sm.task[n & 1].hk, ntiles = blk.i1 - blk.i0;
         const bool two = *(const volatile int *)&blk.nrow > TS;
         if (ntiles == 0) {  // nothing to see: zeros
-            for (int e = tid - 128; e < blk.nrow * G * (kCD / 8); e += 256)
-                *reinterpret_cast<uint4 *>(O + ((size_t)(blk.row0 + e / (G * 16)) * Hq + hk * G) * kCD + (e % (G * 16)) * 8) =
+            for (int e = tid - 128; e < blk.nrow * G * kChunks; e += 256)
+                *reinterpret_cast<uint4 *>(O + ((size_t)(blk.row0 + e / (G * kChunks)) * Hq + hk * G) * D + (e % (G * kChunks)) * 8) =
                     make_uint4(0, 0, 0, 0);
         } else if (x == 0 || two) {
         const int toks = min(TS, blk.nrow - x * TS);       // tokens of the set
@@ -846,7 +847,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tc_fence_after();
                 const uint32_t o_t = tmem + colO + lane_base;
 #pragma unroll 1
-                for (int cb = 0; cb < kCD; cb += 8) {  // (in small steps: it is rare, and registers are not)
+                for (int cb = 0; cb < D; cb += 8) {  // (in small steps: it is rare, and registers are not)
                     uint32_t ov[8];
                     c_tmem_ld8(o_t + cb, ov);
                     tmem_wait_ld();
@@ -863,7 +864,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (alive && !blk.range.seen(blk.range.slot(v0 + r), pv.sinks)) {
                     uint8_t *vr = ring + (size_t)(i % kCStages) * 2 * kCTile + kCTile + r * 128;
 #pragma unroll 1
-                    for (int ch = 0; ch < 16; ++ch)
+                    for (int ch = 0; ch < kChunks; ++ch)
                         *reinterpret_cast<uint4 *>(vr + (ch >> 3) * kCHalf + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 __syncwarp();
@@ -909,17 +910,17 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tc_fence_after();
                 const uint32_t o_t = tmem + colO + lane_base;
                 if (blk.pieces > 1) {
-                    float *pp = part + (((size_t)blk.slot * pv.Hkv + hk) * 2 + x) * (kCD + 2) * kCRows + r;
+                    float *pp = part + (((size_t)blk.slot * pv.Hkv + hk) * 2 + x) * (D + 2) * kCRows + r;
 #pragma unroll 1
-                    for (int cb = 0; cb < 4; ++cb) {
+                    for (int cb = 0; cb < D / 32; ++cb) {
                         uint32_t ov[32];
                         tmem_ld32(o_t + cb * 32, ov);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) pp[(size_t)(cb * 32 + e) * kCRows] = __uint_as_float(ov[e]);
                     }
-                    pp[(size_t)kCD * kCRows] = m_ref;
-                    pp[(size_t)(kCD + 1) * kCRows] = l;
+                    pp[(size_t)D * kCRows] = m_ref;
+                    pp[(size_t)(D + 1) * kCRows] = l;
                 } else {
                     // o = O / l as bf16, staged in a V tile that no product reads any more (set B's last
                     // comes after set A's: B takes the last tile's, A the other), then rows of 256 bytes side
@@ -930,7 +931,7 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     if constexpr (MOD) blind = lo > pos && doc >= head;
                     const float inv = blind ? 0.f : 1.f / l;
 #pragma unroll 1
-                    for (int cb = 0; cb < 4; ++cb) {
+                    for (int cb = 0; cb < D / 32; ++cb) {
                         uint32_t ov[32];
                         tmem_ld32(o_t + cb * 32, ov);
                         tmem_wait_ld();
@@ -949,14 +950,14 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         }
                     }
                     cbar(bar_id);
-                    const int ch = r & 15;
+                    const int ch = r % kChunks;
                     const uint32_t by_g = 0x10000u / (uint32_t)G + 1;  // row / G for rows below 128
 #pragma unroll 8
-                    for (int k = 0; k < kCRows / 8; ++k) {
-                        const int row = (r >> 4) + 8 * k, t = (int)((uint32_t)row * by_g >> 16);
+                    for (int k = 0; k < kChunks; ++k) {
+                        const int row = r / kChunks + kCRows / kChunks * k, t = (int)((uint32_t)row * by_g >> 16);
                         const int tok = blk.row0 + x * TS + t, h = hk * G + row - t * G;
                         if (row >= toks * G || !YOCO_DCHECK(tok < rows && h < Hq, 0x68)) continue;
-                        *reinterpret_cast<uint4 *>(O + ((size_t)tok * Hq + h) * kCD + ch * 8) =
+                        *reinterpret_cast<uint4 *>(O + ((size_t)tok * Hq + h) * D + ch * 8) =
                             *reinterpret_cast<const uint4 *>(stg + c_chunk(row, ch));
                     }
                 }
@@ -980,11 +981,11 @@ paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 namespace yoco_host {
 using namespace yoco;
 
-template <int MODE>
+template <int MODE, int D>
 static cudaError_t launch(const PagedArgs &a, const PagedGrid &g, const CUtensorMap &mq, const CUtensorMap &mk,
                           const CUtensorMap &mv, cudaStream_t st) {
     // the shared-memory opt-in is set on every launch (it belongs to the current device)
-    cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel<MODE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kCSmem<(MODE > 0)>);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1001,32 +1002,41 @@ static cudaError_t launch(const PagedArgs &a, const PagedGrid &g, const CUtensor
     cfg.numAttrs = 1;
     count_launches(1);
     const PagedMod mod = paged_mod(a);
-    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel<MODE>, mq, mk, mv, (bf16_t *)a.O, g.part, (PagedPlan *)g.plan,
+    return cudaLaunchKernelEx(&cfg, paged_prefill_tc_kernel<MODE, D>, mq, mk, mv, (bf16_t *)a.O, g.part, (PagedPlan *)g.plan,
                               (const typename PagedKind<(MODE > 0)>::Entry *)g.entries, g.cap, a.rows, a.Hq, paged_view(a), mod,
                               mod.qk, a.err);
 }
 
-cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
-    const int G = a.Hq / a.cache->Hkv, TS = kCRows / G;
-    CUtensorMap mq, mk, mv;
-    // Q [rows, Hq, 128] by boxes of TS tokens x G heads x 64 channels
-    const uint64_t dims[3] = {(uint64_t)kCD, (uint64_t)a.Hq, (uint64_t)a.rows};
-    const uint64_t strides[2] = {(uint64_t)kCD * 2, (uint64_t)a.Hq * kCD * 2};
-    const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)TS};
-    if (!paged_map(&mq, a.Q, 3, dims, strides, box) || !paged_kv_map(&mk, a.cache->k, a.cache) ||
-        !paged_kv_map(&mv, a.cache->v, a.cache))
-        return cudaErrorInvalidValue;
-    if (!a.scores) return launch<0>(a, g, mq, mk, mv, st);
+template <int D>
+static cudaError_t launch_scored(const PagedArgs &a, const PagedGrid &g, const CUtensorMap &mq, const CUtensorMap &mk,
+                                 const CUtensorMap &mv, cudaStream_t st) {
     const bool cap = a.scores->softcap > 0.f, bias = a.scores->slopes != nullptr;
     if (cap) {
         constexpr int both = kModMask + kModCap;
         switch (paged_mod(a).degree) {
-            case 2: return bias ? launch<both + kModShort + kModBias>(a, g, mq, mk, mv, st) : launch<both + kModShort>(a, g, mq, mk, mv, st);
-            case 3: return bias ? launch<both + kModBias>(a, g, mq, mk, mv, st) : launch<both>(a, g, mq, mk, mv, st);
-            default: return bias ? launch<both + kModWide + kModBias>(a, g, mq, mk, mv, st) : launch<both + kModWide>(a, g, mq, mk, mv, st);
+            case 2:
+                if constexpr (D == 128)
+                    return bias ? launch<both + kModShort + kModBias, D>(a, g, mq, mk, mv, st) : launch<both + kModShort, D>(a, g, mq, mk, mv, st);
+                return cudaErrorInvalidValue;
+            case 3: return bias ? launch<both + kModBias, D>(a, g, mq, mk, mv, st) : launch<both, D>(a, g, mq, mk, mv, st);
+            default: return bias ? launch<both + kModWide + kModBias, D>(a, g, mq, mk, mv, st) : launch<both + kModWide, D>(a, g, mq, mk, mv, st);
         }
     }
-    return bias ? launch<kModMask + kModBias>(a, g, mq, mk, mv, st) : launch<kModMask>(a, g, mq, mk, mv, st);
+    return bias ? launch<kModMask + kModBias, D>(a, g, mq, mk, mv, st) : launch<kModMask, D>(a, g, mq, mk, mv, st);
+}
+
+cudaError_t paged_prefill_tc(const PagedArgs &a, const PagedGrid &g, cudaStream_t st) {
+    const int G = a.Hq / a.cache->Hkv, TS = kCRows / G, d = a.cache->d;
+    CUtensorMap mq, mk, mv;
+    // Q [rows, Hq, d] by boxes of TS tokens x G heads x 64 channels
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)a.Hq, (uint64_t)a.rows};
+    const uint64_t strides[2] = {(uint64_t)d * 2, (uint64_t)a.Hq * d * 2};
+    const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)TS};
+    if (!paged_map(&mq, a.Q, 3, dims, strides, box) || !paged_kv_map(&mk, a.cache->k, a.cache) ||
+        !paged_kv_map(&mv, a.cache->v, a.cache))
+        return cudaErrorInvalidValue;
+    if (d == 64) return a.scores ? launch_scored<64>(a, g, mq, mk, mv, st) : cudaErrorInvalidValue;
+    return a.scores ? launch_scored<128>(a, g, mq, mk, mv, st) : launch<0, 128>(a, g, mq, mk, mv, st);
 }
 
 }  // namespace yoco_host

@@ -749,24 +749,27 @@ constexpr size_t kPagedHead = 256;
 constexpr size_t kPagedCuts = 16384;  // PagedCut per block of a decode grid
 constexpr int kMaxDecodeBlocks = (int)(kPagedCuts / sizeof(PagedCut));
 
-// the tensor-core kernels take what fits their tiles
-static bool paged_on_tc(const yoco_paged_kv *c) { return c->dtype == YOCO_BF16 && c->d == 128; }
+// the tensor-core kernels take what fits their tiles; the prefill's with scores at head size 64 too
+// (4096 rows, 16 over 4 heads, us here and there: plain 924, with masks 62, capped 72, biased 63; 4 sequences
+// of 1 to 50 rows 15.5 and 11.3).  The plain calls at 64 stay here, with the weights that they have in fp32
+static bool paged_on_tc(const yoco_paged_kv *c, bool scored_prefill = false) {
+    return c->dtype == YOCO_BF16 && (c->d == 128 || scored_prefill);
+}
 
 // blocks that a decode's grid has and a prefill's plan counts on: one per SM of the tensor-core
 // kernels, two of the CUDA-core ones.  (Two are resident at head size 64 with up to four heads at a
 // time and at 128 with up to two; the decode with more of them, and the prefill at 128, have one:
 // the grid is then two rounds, and the plan's rounds are half as many as there are.)
-static int paged_slots(const yoco_paged_kv *c) { return (paged_on_tc(c) ? 1 : 2) * device_sm_count(); }
-static int paged_decode_blocks(const yoco_paged_kv *c) { return std::min(kMaxDecodeBlocks, paged_slots(c)); }
+static int paged_slots(bool tc) { return (tc ? 1 : 2) * device_sm_count(); }
+static int paged_decode_blocks(const yoco_paged_kv *c) { return std::min(kMaxDecodeBlocks, paged_slots(paged_on_tc(c))); }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // the plan of a prefill of `rows` rows, with offsets into the workspace for pointers; its bytes
-static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &g, char *ws) {
-    const bool tc = paged_on_tc(c);
+static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, bool tc, PagedGrid &g, char *ws) {
     const int G = Hq / c->Hkv;
     g.rows = tc ? 2 * (128 / G) : kPreRows / G;
-    g.slots = paged_slots(c);
+    g.slots = paged_slots(tc);
     g.min_piece = tc ? kPagedMinPiece : kPreMinPiece;
     g.entry_cost = tc ? kPagedEntryCost : kPreEntryCost;
     g.split_cost = tc ? kPagedSplitCost : kPreSplitCost;
@@ -794,7 +797,8 @@ static size_t prefill_grid(const yoco_paged_kv *c, int Hq, int rows, PagedGrid &
 size_t paged_workspace(const yoco_paged_kv *c, int Hq, int rows) {
     PagedGrid g;
     const size_t dec = (size_t)paged_decode_blocks(c) * 2 * (Hq / c->Hkv) * (c->d + 2) * sizeof(float);
-    return std::max(kPagedHead + kPagedCuts + dec, prefill_grid(c, Hq, rows, g, nullptr));
+    return std::max({kPagedHead + kPagedCuts + dec, prefill_grid(c, Hq, rows, paged_on_tc(c), g, nullptr),
+                     prefill_grid(c, Hq, rows, paged_on_tc(c, true), g, nullptr)});
 }
 
 static void pdl_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, size_t smem,
@@ -876,10 +880,10 @@ static cudaError_t prefill_simt(const PagedArgs &a, const PagedGrid &g, cudaStre
 
 template <typename T, int D, bool MOD>
 static cudaError_t prefill_call(const PagedArgs &a, cudaStream_t st) {
-    constexpr bool tc = sizeof(T) == 2 && D == 128;
+    constexpr bool tc = sizeof(T) == 2 && (D == 128 || MOD);
     constexpr int R = tc ? 128 : kPreRows, sets = tc ? 2 : 1;
     PagedGrid g{};
-    (void)prefill_grid(a.cache, a.Hq, a.rows, g, (char *)a.ws);
+    (void)prefill_grid(a.cache, a.Hq, a.rows, tc, g, (char *)a.ws);
     cudaError_t e = paged_plan(a, g, st);
     if (e != cudaSuccess) return e;
     if constexpr (tc) e = paged_prefill_tc(a, g, st);
@@ -896,7 +900,13 @@ static cudaError_t prefill_call(const PagedArgs &a, cudaStream_t st) {
 }
 
 template <typename T, int D> static cudaError_t prefill(const PagedArgs &a, cudaStream_t st) {
-    return a.scores ? prefill_call<T, D, true>(a, st) : prefill_call<T, D, false>(a, st);
+    const yoco_paged_scores *s = a.scores;
+    if (s && !(s->softcap > 0.f) && !s->slopes && !s->prefix && !s->doc_first) {  // the plain call, and its bits
+        PagedArgs plain = a;
+        plain.scores = nullptr;
+        return prefill_call<T, D, false>(plain, st);
+    }
+    return s ? prefill_call<T, D, true>(a, st) : prefill_call<T, D, false>(a, st);
 }
 
 cudaError_t paged_decode(const PagedArgs &a, cudaStream_t st) {

@@ -5,11 +5,13 @@ The bounds are those of the plain calls (tests/test_gpu_paged.py: a score is off
 each weight by that and a few u, the sums by n u, all twice for numerator and denominator, weights
 rounded to bf16 for the tensor cores by 2^-8 at most) with, for what comes after q.k, with Y the
 largest |cap tanh(x / cap)| and B the largest slope * distance of the slots that the row sees,
-  cap    eta Y: eta = 1.5e-6 in bf16 at head size 128 (a polynomial of relative error 1.01e-6 or
+  cap    eta Y: eta = 1.5e-6 on the tensor cores (a polynomial of relative error 1.01e-6 or
          exponential and reciprocal of 2^-22 each, and six roundings), else 16 u (a polynomial of 6e-8
          or exponential and reciprocal of 4 u and 2 u, of which at most 0.76 come through, and as many).  (It does not enlarge the error of its argument: its slope is at most 1.)
   bias   8 u (Y + B): the slope times log2(e), the product, and the sum, in two steps
-each twice as well.
+each twice as well.  On the tensor cores run bf16 at head size 128 and its prefills at 64, by one kernel:
+o = sum(round(p) v) / sum(p), in which |round(p) - p| <= 2^-8 p (half a step of bf16), so o is off by at most
+2^-8 sum(p |v|) / sum(p) for it, as for the plain calls at 128.
 """
 import math
 
@@ -36,9 +38,10 @@ def slopes_of(Hq):
     return torch.tensor([2.0 ** (-8.0 * (h + 1) / Hq) for h in range(Hq)], dtype=torch.float32)
 
 
-def reference(pool, Q, b, pos, doc, prefix, cap, slopes, window, sinks, scale):
+def reference(pool, Q, b, pos, doc, prefix, cap, slopes, window, sinks, scale, decode=False):
     T, Hq, d = Q.shape
     bf16 = Q.dtype == torch.bfloat16
+    tensor = bf16 and (d == 128 or not decode)
     L = pool.lens[b]
     out, tol = torch.zeros(T, Hq, d, dtype=torch.float64), torch.zeros(T, Hq, d, dtype=torch.float64)
     m, p = torch.arange(L)[None], pos[:, None]
@@ -63,13 +66,13 @@ def reference(pool, Q, b, pos, doc, prefix, cap, slopes, window, sinks, scale):
         o = w @ v
         S = (Q[:, h].double().abs() @ k.abs().T * scale).masked_fill(~seen, 0).amax(1, keepdim=True)
         e = U * (2 * (d + 4) * S + 2 * seen.sum(1, keepdim=True) + 16)
-        e = e + (2 * (1.5e-6 if bf16 and d == 128 else 16 * U) * top if cap else 0) + (16 * U * (top + B) if slopes is not None else 0)
-        rounded, half = (2.0 ** -8 if d == 128 else 0.0, 2.0 ** -8) if bf16 else (0.0, U)
+        e = e + (2 * (1.5e-6 if tensor else 16 * U) * top if cap else 0) + (16 * U * (top + B) if slopes is not None else 0)
+        rounded, half = (2.0 ** -8 if tensor else 0.0, 2.0 ** -8) if bf16 else (0.0, U)
         out[:, h], tol[:, h] = o, half * o.abs() + (e + rounded) * (w @ v.abs()) + 1e-30
     return out, tol
 
 
-def check(got, pool, Q, cu, doc, prefix, cap, slopes, window, sinks, scale):
+def check(got, pool, Q, cu, doc, prefix, cap, slopes, window, sinks, scale, decode=False):
     got = got.cpu().double()
     for b in range(len(pool.lens)):
         T = cu[b + 1] - cu[b]
@@ -77,7 +80,7 @@ def check(got, pool, Q, cu, doc, prefix, cap, slopes, window, sinks, scale):
             continue
         rows = slice(cu[b], cu[b + 1])
         pos = torch.arange(T) + pool.lens[b] - T
-        ref, tol = reference(pool, Q[rows].cpu(), b, pos, doc[rows], prefix[b], cap, slopes, window, sinks, scale)
+        ref, tol = reference(pool, Q[rows].cpu(), b, pos, doc[rows], prefix[b], cap, slopes, window, sinks, scale, decode)
         off = (got[rows] - ref).abs()
         assert torch.isfinite(off).all(), (b, "not finite", int((~torch.isfinite(off)).sum()))
         worst = float((off / tol).max())
@@ -124,7 +127,7 @@ def run(Y, new, ctx, Hq, Hkv, d, page, dtype, cap=0.0, bias=False, prefix=None, 
     else:
         Y.yoco_paged_attn_prefill_scored(Q, pool.dev, cuda_ints(cu), O, scores, window=window, sinks=sinks, workspace=ws)
     Y.yoco_workspace_status(ws)
-    check(O, pool, Q, cu, rows_doc.clamp(min=0), [0] * len(lens) if prefix is None else prefix, cap, sl, window, sinks, d ** -0.5)
+    check(O, pool, Q, cu, rows_doc.clamp(min=0), [0] * len(lens) if prefix is None else prefix, cap, sl, window, sinks, d ** -0.5, decode)
     assert bool((O[cu[-1]:] == 7.0).all())  # rows behind the last sequence
     return pool, Q, O, scores
 
