@@ -1,5 +1,6 @@
 // paged_simt.cu -- attention over the paged cache on the CUDA cores, fp32 arithmetic: every
-// type and head size the library has (the tensor-core kernels take bf16 at head size 128),
+// type and head size the library has (the tensor-core kernels take bf16 at head size 128 and scored
+// prefills at 64),
 // and the merges of split keys that both paths share.
 //
 //   o = sum_m p_m v_m / sum_m p_m,   p_m = 2^(c q.k_m - r),  c = scale log2(e),
