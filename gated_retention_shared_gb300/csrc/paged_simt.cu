@@ -522,13 +522,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
         }
         __syncthreads();  // K read by everyone
         stage_k.issue(K, sk, at[(t + 1) & 1]);
-        // distances are taken from the step's first slot (fewer conversions)
-        [[maybe_unused]] int k0 = 0;
-        [[maybe_unused]] float to[4];
         if constexpr (MOD) {
-            k0 = blk.range.slot(v0);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) to[x] = (float)(blk.range.slot(v0 + tx + 16 * x) - k0);
             if (mod.cap2 > 0.f) {
                 float most = 0.f;
 #pragma unroll
@@ -548,11 +542,15 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
                 }
             }
             if (mod.slopes) {
+                // (distances are formed as integers: a step may hold slots on both sides of the gap between
+                // sinks and window, and positions rounded to fp32 before they are subtracted lose whole slots
+                // past 2^24.  4096 rows x 64 512 us, x 128 1025; by fp32 differences 509 and 1015)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float from = (float)(blk.pos0 + (4 * ty + i) / G - k0);
+                    const int pos = blk.pos0 + (4 * ty + i) / G;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) s[i][x] = fmaf(-slope[i], fabsf(from - to[x]), s[i][x]);
+                    for (int x = 0; x < 4; ++x)
+                        s[i][x] = fmaf(-slope[i], fabsf((float)(pos - blk.range.slot(v0 + tx + 16 * x))), s[i][x]);
                 }
             }
         }

@@ -1,0 +1,87 @@
+"""GPU checks of the scored paged calls at far positions, against the definition in 64 bits, element by
+element.
+
+Far positions: o = sum w v, so an error of e_m in the score of slot m moves o by at most
+sum w_m e_m (|v_m| + |o|).  With u = 2^-24, d channels and n slots e_m is (d + 4) u S_m for the product
+(S_m = scale sum |q_i k_i|), 8 u (|x_m| + B_m) for cap, bias B_m = slope |p - m| (the distance to fp32, the
+slope times log2(e), the product, the sum) and exponential; the sums add 2 n u.  A distance that is
+formed from two rounded numbers is off by whole slots there, far outside this.  Weights and outputs
+rounded to bf16 are off by 2^-8 of themselves at most (tests/test_gpu_paged_scored.py).
+"""
+import math
+
+import pytest
+import torch
+
+import test_gpu_paged as P
+import test_gpu_paged_scored as S
+
+pytestmark = pytest.mark.gpu
+
+U = S.U
+
+
+@pytest.fixture(scope="module")
+def Y():
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    import gated_retention_shared_gb300 as Y
+    return Y
+
+
+def far_reference(k, v, slots, Q, pos, prefix, slopes, window, sinks, tensor, half):
+    """k, v [n, Hkv, d] of the slots that are there; Q [T, Hq, d]."""
+    T, Hq, d = Q.shape
+    m, p = slots[None], pos[:, None]
+    seen = ((m <= p) & ((m > p - window) | (m < sinks))) | (m < prefix)
+    out, tol = torch.zeros(T, Hq, d, dtype=torch.float64), torch.zeros(T, Hq, d, dtype=torch.float64)
+    for h in range(Hq):
+        kh, vh = k[:, h // (Hq // k.shape[1])].double(), v[:, h // (Hq // k.shape[1])].double()
+        q = Q[:, h].double()
+        bias = float(slopes[h]) * (m - p).abs().double()
+        x = q @ kh.T * d ** -0.5 - bias
+        w = torch.softmax(x.masked_fill(~seen, -math.inf), 1)
+        e = U * ((d + 4) * (q.abs() @ kh.abs().T * d ** -0.5) + 8 * (x.abs() + bias.abs()) + 2 * seen.sum(1, keepdim=True))
+        we = w * (e + (2.0 ** -8 if tensor else 0.0))
+        o = w @ vh
+        out[:, h], tol[:, h] = o, half * o.abs() + we @ vh.abs() + we.sum(1, keepdim=True) * o.abs() + 1e-30
+    return out, tol
+
+
+@pytest.mark.parametrize("dtype,d", S.TYPES)
+@pytest.mark.parametrize("page,prefix,length", [(16, 0, 2 ** 24 + 40), (32, 0, 2 ** 25 + 77), (16, 20, 2 ** 24 + 1000), (64, 0, 2 ** 26 + 5)])
+def test_distances_past_24_bits(Y, dtype, d, page, prefix, length):
+    """A long stream behind a window, its sinks' or prefix's slots in one step with the window's first:
+    the entries between them name no page."""
+    new, Hq, Hkv, window, sinks = 45, 6, 2, 32, 4
+    front, back = -(-max(sinks, prefix) // page), (length - new - window) // page
+    entries = list(range(front)) + list(range(back, -(-length // page)))
+    g = torch.Generator().manual_seed(length + page)
+    k, v = (torch.randn(len(entries), Hkv, page, d, generator=g).to(P.DT[dtype]) for _ in range(2))
+    table = torch.full((1, entries[-1] + 1), -1, dtype=torch.int32)
+    table[0, entries] = torch.arange(len(entries), dtype=torch.int32)
+    cache = Y.PagedKV(k.cuda(), v.cuda(), table.cuda(), S.cuda_ints([length]))
+    slots = (torch.tensor(entries)[:, None] * page + torch.arange(page)).reshape(-1)
+    there = slots < length
+    rows = [t.transpose(1, 2).reshape(-1, Hkv, d)[there] for t in (k, v)]
+    slots = slots[there]
+    slopes = torch.tensor([0.5, 0.05, 1e-7, 0.0, -1e-7, 2.0])
+    scores = Y.PagedScores(slopes=slopes.cuda(), prefix=S.cuda_ints([prefix]))
+    Q = (torch.randn(new, Hq, d, generator=g) * 2).to(P.DT[dtype])
+    half = 2.0 ** -8 if dtype == "bf16" else U
+    for decode in (False, True):
+        q = Q[-1:] if decode else Q
+        O = torch.empty_like(q, device="cuda")
+        ws = torch.zeros(Y.yoco_paged_attn_workspace_size(Hq, q.shape[0], cache), dtype=torch.uint8, device="cuda")
+        if decode:
+            Y.yoco_paged_attn_decode_scored(q.cuda(), cache, O, scores, window=window, sinks=sinks, workspace=ws)
+        else:
+            Y.yoco_paged_attn_prefill_scored(q.cuda(), cache, S.cuda_ints([0, new]), O, scores, window=window, sinks=sinks,
+                                             workspace=ws)
+        Y.yoco_workspace_status(ws)
+        tensor = dtype == "bf16" and (d == 128 or not decode)
+        pos = torch.arange(length - q.shape[0], length)
+        ref, tol = far_reference(*rows, slots, q, pos, prefix, slopes, window, sinks, tensor, half)
+        off = (O.cpu().double() - ref).abs()
+        assert torch.isfinite(off).all(), "not finite"
+        worst = (off / tol).amax((0, 2))
+        assert bool((worst <= 1.0).all()), (decode, worst.tolist())
