@@ -489,7 +489,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
             const int pos = blk.pos0 + r / G;
             doc[i] = mod.doc && r < nr ? max(0, mod.doc[blk.row0 + r / G]) : 0;
             lo[i] = max(doc[i], pv.window > 0 ? pos + 1 - pv.window : 0);
-            run[i] = max(0, pos + 1 - lo[i]);
+            run[i] = lo[i] > pos ? 0 : pos + 1 - lo[i];  // (compared first: lo may be INT_MAX and pos below 0)
             head[i] = pos < 0 ? 0 : max(0, max(blk.range.pre, min(pv.sinks, pos + 1)) - doc[i]);
             slope[i] = mod.slopes && r < nr ? mod.slopes[hk * G + r % G] * kPagedLog2E : 0.f;
         }
@@ -544,7 +544,7 @@ paged_prefill_simt_kernel(const T *__restrict__ Q, T *__restrict__ O, const T *_
             if (mod.slopes) {
                 // (distances are formed as integers: a step may hold slots on both sides of the gap between
                 // sinks and window, and positions rounded to fp32 before they are subtracted lose whole slots
-                // past 2^24.  4096 rows x 64 512 us, x 128 1025; by fp32 differences 509 and 1015)
+                // past 2^24.  4096 rows x 64 510 us, x 128 1029; by fp32 differences 509 and 1015)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int pos = blk.pos0 + (4 * ty + i) / G;

@@ -1,5 +1,5 @@
-"""GPU checks of the scored paged calls at far positions, against the definition in 64 bits, element by
-element.
+"""GPU checks of the scored paged calls where positions are far or negative, against the definition in 64
+bits, element by element.
 
 Far positions: o = sum w v, so an error of e_m in the score of slot m moves o by at most
 sum w_m e_m (|v_m| + |o|).  With u = 2^-24, d channels and n slots e_m is (d + 4) u S_m for the product
@@ -19,6 +19,7 @@ import test_gpu_paged_scored as S
 pytestmark = pytest.mark.gpu
 
 U = S.U
+INT_MAX = 2147483647
 
 
 @pytest.fixture(scope="module")
@@ -85,3 +86,50 @@ def test_distances_past_24_bits(Y, dtype, d, page, prefix, length):
         assert torch.isfinite(off).all(), "not finite"
         worst = (off / tol).amax((0, 2))
         assert bool((worst <= 1.0).all()), (decode, worst.tolist())
+
+
+@pytest.mark.parametrize("dtype,d", S.TYPES)
+@pytest.mark.parametrize("mask", ["none", "prefix", "window", "cap", "bias", "all"])
+@pytest.mark.parametrize("first", [0, INT_MAX, 1 << 30, -INT_MAX - 1])
+def test_rows_before_the_first_slot(Y, dtype, d, mask, first):
+    """Sequences with more new rows than slots (padding in front): rows at negative positions are zero,
+    whatever their document start and the other rows' masks; some rows behind them see nothing either."""
+    new, ctx = [200, 40, 3, 70], [-50, -3, -2, 30]
+    lens = [a + b for a, b in zip(new, ctx)]
+    kw = dict(none={}, prefix=dict(prefix=[150, 20, 1, 0]), window=dict(window=20, sinks=3), cap=dict(cap=15.0), bias=dict(bias=True),
+              all=dict(cap=10.0, bias=True, window=30, sinks=2, prefix=[60, 7, 1, 50]))[mask]
+    pos = torch.cat([torch.arange(c, n) for c, n in zip(ctx, lens)])
+    doc = torch.where(pos < 0, first, 0)
+    doc[120:130] = first
+    _, _, O, _ = S.run(Y, new, ctx, 6, 2, d, 16, dtype, doc=doc, **kw)
+    assert bool((O[:273][(pos[:273] < 0).cuda()] == 0).all())
+
+
+@pytest.mark.parametrize("dtype,d", S.TYPES)
+@pytest.mark.parametrize("first", [0, INT_MAX])
+def test_rows_before_the_first_slot_of_cut_keys(Y, dtype, d, first):
+    """The same where the keys are cut into pieces: a prefix makes every row block see all of them."""
+    new, ctx = [2100], [-100]
+    doc = torch.full((2100,), 0)
+    doc[:100] = first
+    doc[300:310] = first
+    _, _, O, _ = S.run(Y, new, ctx, 2, 2, d, 64, dtype, doc=doc, prefix=[2000])
+    assert bool((O[:100] == 0).all())
+
+
+@pytest.mark.parametrize("dtype,d", S.TYPES)
+def test_rows_of_empty_sequences(Y, dtype, d):
+    """Sequences of length 0 with rows: zeros, beside one that is served."""
+    pool = P.Pool(Y, [100, 0, 0], 2, d, 16, dtype)
+    Q = (torch.randn(60, 6, d, generator=torch.Generator().manual_seed(2)) * 2).to(P.DT[dtype]).cuda()
+    for first in (0, INT_MAX):
+        O = torch.full_like(Q, 7.0)
+        doc = torch.zeros(60, dtype=torch.int64)
+        doc[20:] = first
+        scores = Y.PagedScores(20.0, S.slopes_of(6).cuda(), S.cuda_ints([5, 1 << 30, 9]), S.cuda_ints(doc))
+        Y.yoco_paged_attn_prefill_scored(Q, pool.dev, S.cuda_ints([0, 20, 50, 60]), O, scores, window=10, sinks=4)
+        assert bool((O[20:] == 0).all())
+        S.check(O[:20], pool, Q[:20], [0, 20, 20, 20], doc, [5, 0, 0], 20.0, S.slopes_of(6), 10, 4, d ** -0.5)
+    O = torch.full((3, 6, d), 7.0, dtype=P.DT[dtype], device="cuda")
+    Y.yoco_paged_attn_decode_scored(Q[:3], pool.dev, O, Y.PagedScores(20.0, prefix=S.cuda_ints([5, 1 << 30, 9])))
+    assert bool((O[1:] == 0).all()) and bool((O[0] != 0).any())
