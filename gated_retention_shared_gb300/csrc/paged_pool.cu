@@ -202,8 +202,10 @@ __device__ __forceinline__ int pool_before(const PoolView &v, PoolSmem &sm, int 
 
 // Of the sequences that grow: what they need and which pages have to be copied, into v's scratch and
 // the block's start and first; one block.  page[k]: the page that holds the last slot of its
-// sequence b0 + k, where that is not full.
-__device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kShareEach], const int (&N)[kShareEach],
+// sequence b0 + k, where that is not full.  Sequences whose page is counted 0, or grows in more of
+// them than it is counted, stay as they are (N becomes L) and its count is left alone: taken down for
+// their copies it would reach 0, and the page be handed out or not by when the other blocks look.
+__device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kShareEach], int (&N)[kShareEach],
                                            const int (&page)[kShareEach], int each, PoolSmem &sm, PoolShared &t) {
     const int b0 = threadIdx.x * each;
     int refs[kShareEach], slot[kShareEach];
@@ -239,7 +241,11 @@ __device__ __forceinline__ void pool_share(const PoolView &v, const int (&L)[kSh
 #pragma unroll
     for (int k = 0; k < kShareEach; ++k) {
         copy[k] = slot[k] >= 0;
-        if (copy[k] && t.grow[slot[k]] > refs[k]) paged_report(v.err, kErrPagedRefs);
+        if (page[k] >= 0 && (refs[k] <= 0 || (copy[k] && t.grow[slot[k]] > refs[k]))) {
+            paged_report(v.err, kErrPagedRefs);
+            copy[k] = false;
+            N[k] = L[k];
+        }
         if (copy[k] && t.grow[slot[k]] >= refs[k] && t.first[slot[k]] == b0 + k) copy[k] = false;
         if (copy[k]) atomicSub(v.refs + page[k], 1);
         need[k] = N[k] > L[k] ? pool_pages(v, N[k]) - pool_pages(v, L[k]) + copy[k] : 0;

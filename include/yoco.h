@@ -595,8 +595,12 @@ YOCO_API yoco_status yoco_paged_attn_decode_scored(const void *Q, int Hq, const 
  *   workspace  >= yoco_paged_pool_workspace_size(cache) bytes, 256-byte aligned; calls that share it
  *              are ordered on one stream.  Its status word (yoco_workspace_status) gets
  *              YOCO_ERR_CAPACITY where pages ran out, and YOCO_ERR_INVALID_ARG for a length that the
- *              table cannot hold, an entry outside the pool, a count of refs that is below what the
- *              table says, or an index of a sequence that cannot be used.
+ *              table cannot hold, an entry outside the pool, an index of a sequence that cannot be
+ *              used, or a count of refs below what the table says where a call comes upon it: an
+ *              entry that goes back or moves and names a page counted 0, or, where sequences that
+ *              grow would write next into a partly filled page, a count of 0, or one above 1 that is
+ *              below the number of these sequences (which then stay as they are).  Other low counts
+ *              are not looked for: a page counted 0 is free, and a page counted 1 is one sequence's.
  *   moves      NULL, or a list of the page copies that the call made, device int32, 16-byte
  *              aligned: {count, n, 0, 0}, then for each {from, to, slots, 0}: the first `slots` slots
  *              of page `from` went to `to`, in k and v of `cache`.  Where other caches (layers) share
