@@ -426,7 +426,7 @@ def yoco_rope_apply(x, base, pos0=0, stream=None):
 class Rope:
     """A rotary encoding other than pairs of the whole head at one base: `rotary_dim` channels of each
     head (None: all), in "pairs" (2i, 2i+1) or "halves" (i, i + r/2), frequencies unscaled ("none"),
-    "linear", "ntk" or "by_parts" (yoco.h has the formulas), turned channels times `magnitude`."""
+    "linear", "ntk" or "by_parts" (yoco.h has the formulas; its ramp is over turns), turned channels times `magnitude`."""
     LAYOUTS = {"pairs": 0, "halves": 1}
     SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
@@ -701,7 +701,10 @@ def _pool_moves(moves, cache, most):
 def yoco_paged_resize(cache: PagedKV, refs, new_lens, moves=None, workspace=None, stream=None):
     """The sequences' lengths become new_lens (int32 [B], below 0: unchanged): cache.page_table,
     cache.seq_lens and refs (int32 [num_pages]) are written, shared pages that are written next are
-    copied.  moves: int32 [>= B + 1, 4] for the list of copies, or None."""
+    copied.  moves: int32 [>= B + 1, 4] for the list of copies, or None.
+    A pool without room for all that grow raises nothing here (the call does not wait for the GPU):
+    no sequence grows, seq_lens stay, and the workspace's status word says so.  Pass a workspace and
+    ask yoco_workspace_status; one that the call makes itself takes its status word with it."""
     r, n = _pool_ints(refs, "refs", cache, cache.k.shape[0]), _pool_ints(new_lens, "new_lens", cache, cache._B)
     m = _pool_moves(moves, cache, cache._B)
     ws, wp, wn = _paged_workspace(lambda: yoco_paged_pool_workspace_size(cache), cache, workspace, stream)
@@ -709,7 +712,8 @@ def yoco_paged_resize(cache: PagedKV, refs, new_lens, moves=None, workspace=None
 
 
 def yoco_paged_fork(cache: PagedKV, refs, src, dst, workspace=None, stream=None):
-    """Empty sequences dst (int32 [n]) become what sequences src are, on the same pages."""
+    """Empty sequences dst (int32 [n]) become what sequences src are, on the same pages.  Pairs that
+    are left out are seen in the workspace's status word, as with yoco_paged_resize."""
     r, s = _pool_ints(refs, "refs", cache, cache.k.shape[0]), _pool_ints(src, "src", cache, None)
     d = _pool_ints(dst, "dst", cache, src.shape[0])
     ws, wp, wn = _paged_workspace(lambda: yoco_paged_pool_workspace_size(cache), cache, workspace, stream)

@@ -346,12 +346,15 @@ YOCO_API yoco_status yoco_rope_apply(void *x, int B, int N, int H, int d, int64_
  *       YOCO_ROPE_NTK       those of base * factor^(r / (r - 2))
  *       YOCO_ROPE_BY_PARTS  theta_i (w + (1 - w) / factor), w = min(1, max(0, (n_i - low) /
  *                           (high - low))), n_i = original theta_i / 2 pi the turns of pair i over
- *                           the original length ("NTK-by-parts", arXiv:2309.00071 Section 3.2)
+ *                           the original length ("NTK-by-parts", arXiv:2309.00071 Section 3.2:
+ *                           the ramp is linear in n_i.  A model whose ramp is linear in the
+ *                           channel's index has other frequencies, which no form here gives)
  *   factor      finite, >= 1;   original > 0, low < high, all finite
  *   magnitude   > 0, finite: the turned channels are multiplied by it (1: not)
  * Pair (x0, x1) of a row at position p becomes magnitude (x0 cos a - x1 sin a, x0 sin a + x1 cos a)
- * with a = p theta_i, which is kept modulo one turn to 2^-32 turns whatever the position; rounded
- * once.
+ * with a = p theta_i; rounded once.  theta_i is formed in fp64 and a kept modulo one turn in steps
+ * of 2^-32 turns, so it is off by some |p| 2^-53 + 2^-32 turns, and by up to 2^-26 turns from its
+ * rounding to fp32 for sine and cosine.
  */
 #define YOCO_ROPE_PAIRS 0
 #define YOCO_ROPE_HALVES 1
@@ -542,8 +545,9 @@ YOCO_API yoco_status yoco_paged_append_rope(const void *k, int64_t k_row, int64_
 /*
  * Scores other than scale q.k, and masks other than causal ones:
  *   softcap    0: none.  > 0: the score is softcap * tanh(scale q.k / softcap)
- *   slopes     device fp32 [Hq], finite, or NULL: slopes[h] * |p - m| is then taken off the score
- *              (after the cap) of the row at position p for slot m
+ *   slopes     device fp32 [Hq], or NULL: slopes[h] * |p - m| is then taken off the score (after the
+ *              cap) of the row at position p for slot m.  Finite, and their products with log2(e) and
+ *              with the distances as well
  *   prefix     device int32 [B], or NULL: slots m < prefix[b] of sequence b are seen by all its
  *              rows, those before them too, whatever the window (values below 0 count as 0, and
  *              the sequence's end bounds them)
@@ -567,7 +571,13 @@ typedef struct {
  * as zeros.  What the plain calls say of NaN and infinite scores holds for the scores after cap and
  * bias; the cap makes infinite products finite.  Slots before every document of a sequence's rows
  * and past every row (and prefix) may hold anything; between them each page in the table is read,
- * and values there that are not finite may make rows NaN that do not see them.
+ * and values there that are not finite may make rows NaN that do not see them.  Scores are fp32: a
+ * bias is off by a few 2^-24 of itself, which shows where the largest are weighed against each other
+ * (slopes below 0, or rows that see only what is far).
+ * bf16 prefills at head size 64: with any of the four members set they run on the tensor cores, their
+ * weights rounded to bf16 (by 2^-8 at most) before the sum over V, as all bf16 calls at 128 do.  The
+ * plain call at 64 keeps fp32 weights, on the CUDA cores, and takes 15 times as long; which of the two
+ * is a caller's choice (a prefix of zeros changes no mask).
  *   softcap    finite, >= 0, and where it is not 0: softcap and scale / softcap within
  *              [2^-64, 2^64]
  */
